@@ -17,6 +17,9 @@ import threading
 
 import torch
 
+from . import attention as _attention
+from .attention import (KvCache, kda_attn_fwd, kda_cache_alloc, kda_cache_append, kda_cache_attn,
+                        kda_cache_evict)
 from .build import LIB as _LIB_PATH
 from .build import build as _build
 
@@ -27,6 +30,8 @@ __all__ = [
     "kda_forward_host", "kda_fwd_fused", "kda_decode", "kda_forward", "kda_fwd_noalloc",
     "kda_fwd_segmented", "kda_segments_auto", "kda_segmented_workspace_size",
     "kda_validate_cu_seqlens", "REC_BYTES", "CHUNK", "HEAD_DIM",
+    "KvCache", "kda_attn_fwd", "kda_cache_alloc", "kda_cache_append", "kda_cache_attn",
+    "kda_cache_evict",
 ]
 
 CHUNK = 16
@@ -122,6 +127,7 @@ def load(build_if_missing: bool = False):
         lib.kda_selftest_timeout.restype = ctypes.c_int
         lib.kda_selftest_tcgen05.argtypes = [P, P, P, P]
         lib.kda_selftest_tcgen05.restype = ctypes.c_int
+        _attention.declare(lib)
         _lib = lib
         return lib
 

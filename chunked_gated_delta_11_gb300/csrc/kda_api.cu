@@ -108,6 +108,17 @@ kda_status error_word(int** out) {
   return s;
 }
 
+// The same with the SM count, for the softmax-attention entry points.
+kda_status device_info_for_attn(int* sm_count, int** err) {
+  DeviceInfo info;
+  const kda_status s = device_info(info);
+  if (s == KDA_OK) {
+    *sm_count = info.sm_count;
+    *err = info.err;
+  }
+  return s;
+}
+
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

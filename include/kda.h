@@ -405,6 +405,127 @@ kda_status kda_profile_phases(int32_t kernel, const void* q, const void* k, cons
                               size_t workspace_bytes, long long* stamps, int32_t max_chunks,
                               void* stream);
 
+/* ------------------------------------------------------------------------
+ * Softmax attention, for the attention layers that stand between the KDA
+ * layers of a hybrid model: over the same packed rows (prefill), and over a
+ * paged key/value cache in 8 bits (serving).  No counterpart on the pages.
+ *
+ * Score of a visible pair of query i (head h) and key j (KV head h / (H / Hk)),
+ * in this order, with p the tokens' positions:
+ *     x = scale * q_i . k_j
+ *     x = cap * tanh(x / cap)           if cap > 0
+ *     x = x - slopes[h] * |p_i - p_j|   if slopes
+ *     o_i = sum_j softmax_j(x) v_j
+ * Sums, maxima and accumulators are fp32; the softmax weights enter the
+ * products with the values in bf16 (prefill; their sum stays fp32) or fp16
+ * (cache).  D is 128.  cap is 0 (none) or a positive finite number; slopes are
+ * device fp32 [H], or NULL.  All pointers are device pointers, contiguous and
+ * row-major; rows and codes 16-byte aligned, int32 and fp32 arrays 4-byte
+ * aligned, except pos and weight (16).  Calls are asynchronous on `stream` and
+ * keep nothing between calls.
+ * ------------------------------------------------------------------------ */
+enum { KDA_MASK_FULL = 0, KDA_MASK_CAUSAL = 1, KDA_MASK_PREFIX = 2 };
+typedef struct {
+  int32_t mask;               /* KDA_MASK_*, inside each sequence: every key; keys j <= i;
+                                 keys j <= i or among the sequence's first prefix_lens[n] */
+  float cap;                  /* 0 = no cap */
+  const float* slopes;        /* fp32 [H] or NULL */
+  const int32_t* prefix_lens; /* int32 [N], KDA_MASK_PREFIX only (else NULL) */
+} kda_attn_options;
+
+/* Attention over packed rows: q, out bf16 [T_total, H, D]; k, v bf16
+ * [T_total, Hk, D], Hk dividing H; sequences as in kda_fwd (cu_seqlens, or N
+ * equal ones).  A token sees keys of its own sequence only (a document mask),
+ * among them what `mask` leaves; positions are row numbers in the sequence.
+ * Rows past the last sequence of a short cu_seqlens are not written.
+ * k and v rows of other sequences, whatever they hold, reach no result; inside
+ * a sequence a non-finite k or v row can also spoil queries that the mask
+ * hides it from (they share its tile).
+ * Errors: INVALID_ARG, UNSUPPORTED (D), LAUNCH; a wait that runs out on the
+ * device is reported by kda_device_status as KDA_ERR_TIMEOUT. */
+kda_status kda_attn_fwd(const kda_attn_options* opts, const void* q, const void* k, const void* v,
+                        float scale, const int32_t* cu_seqlens, int64_t T_total, int32_t H,
+                        int32_t Hk, int32_t N, int32_t D, void* out, void* stream);
+
+/* A pool of cache pages.  A page has page_size token slots (16, 32, 64 or 128)
+ * of every KV head; the slots of one (page, KV head) are a block of e4m3 codes
+ * with one scale, code * scale being the value.  All arrays are the caller's. */
+typedef struct {
+  void* k;        /* e4m3 [pages, Hk, page_size, D] */
+  void* v;        /* e4m3 [pages, Hk, page_size, D] */
+  float* k_scale; /* [pages, Hk] */
+  float* v_scale; /* [pages, Hk] */
+  int32_t* pos;   /* [pages, Hk, page_size]: position of the token in each slot */
+  float* weight;  /* [pages, Hk, page_size]: attention weight accumulated by each slot */
+  int32_t pages, page_size, Hk, D;
+} kda_cache;
+
+/* Sequences in a cache: block_table int32 [N, table_width], entry j of row n the
+ * page with slots j * page_size .. of sequence n (entries past what its length
+ * needs are not read); lens int32 [N], the slots in use.  The values live on the
+ * device and are not checked before the launch: an entry outside [0, pages), or
+ * a length outside [0, table_width * page_size], makes the kernels skip the page
+ * or the surplus, read and write nothing out of range, and latch
+ * KDA_ERR_INVALID_ARG for kda_device_status.  No page may stand twice in the
+ * tables of one call that writes the cache. */
+
+/* Appends bf16 rows k, v [T_total, Hk, D] of N sequences (cu_seqlens, or equal
+ * shares) at slots lens[n], lens[n] + 1, ... (lens: before the call; the caller
+ * adds the new rows to it afterwards).  positions: int32 [T_total], or NULL =
+ * the slot numbers (right while nothing was evicted); weights start at 0.
+ * Block scales are powers of two, 2^e with the smallest e in [-64, 120] such
+ * that the finite new values are at most 448 * 2^e, and at least the block's
+ * older scale; when that grows the older codes of the block are rounded again.
+ * Codes are rounded to nearest even; a non-finite value becomes NaN and does not
+ * enter the scale. */
+kda_status kda_cache_append(const kda_cache* cache, const void* k, const void* v,
+                            const int32_t* block_table, int32_t table_width, const int32_t* lens,
+                            const int32_t* positions, const int32_t* cu_seqlens, int64_t T_total,
+                            int32_t N, void* stream);
+
+typedef struct {
+  float cap;
+  const float* slopes;
+  const int32_t* positions; /* int32 [T_total]: positions of the queries, or NULL: the
+                               queries of a sequence are the newest tokens of its cache
+                               (the last one has the position of its last slot) */
+  int32_t accumulate;       /* != 0: weight[slot] += sum of the softmax weights that the
+                               slot got over the query rows of its KV head */
+} kda_cache_attn_options;
+
+/* Attention over a cache: q, out bf16 [T_total, H, D], any number of query rows
+ * per sequence (made for a few: decoding and drafted tokens), split by
+ * cu_seqlens or into equal shares; lens counts the slots in use, the query
+ * tokens' own among them.  A query sees the slots whose position is at most its
+ * own; with nothing to see (an empty cache) its output is 0.  Slots past
+ * lens[n], whatever they hold, reach no result.  Scales may be any positive
+ * finite numbers.  Sums over splits are added in a fixed order: the same call
+ * gives the same bits.
+ * workspace: kda_cache_attn_workspace_size() bytes of device memory, 16-byte
+ * aligned, or NULL (= cudaMallocAsync / cudaFreeAsync on the stream). */
+size_t kda_cache_attn_workspace_size(const kda_cache* cache, int64_t T_total, int32_t H, int32_t N,
+                                     int32_t table_width, int32_t accumulate);
+kda_status kda_cache_attn(const kda_cache_attn_options* opts, const kda_cache* cache,
+                          const void* q, float scale, const int32_t* block_table,
+                          int32_t table_width, const int32_t* lens, const int32_t* cu_seqlens,
+                          int64_t T_total, int32_t H, int32_t N, void* out, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Eviction by accumulated weight: every sequence keeps at most `budget` slots
+ * per KV head, its newest `recent` (<= budget) ones and, of the others, those of
+ * largest weight (ties: the lowest slot; a NaN weight counts as the largest), in
+ * their order.  They are written, with positions and weights, to the pages of
+ * dst_table [N, dst_width], none of which may be a page of block_table; their
+ * block scale is the largest among the rows' own (codes are rounded again where
+ * it differs).  new_lens int32 [N] receives min(lens[n], budget).  A sequence
+ * within the budget is copied whole.  The old pages are left as they are.
+ * workspace: kda_cache_evict_workspace_size() bytes, or NULL, as above. */
+size_t kda_cache_evict_workspace_size(const kda_cache* cache, int32_t N, int32_t budget);
+kda_status kda_cache_evict(const kda_cache* cache, const int32_t* block_table, int32_t table_width,
+                           const int32_t* lens, const int32_t* dst_table, int32_t dst_width,
+                           int32_t budget, int32_t recent, int32_t N, int32_t* new_lens,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
