@@ -1,9 +1,118 @@
 // kda_cache_attn.cu -- attention of a few new tokens per sequence over the
 // 8-bit paged cache (kda_cache_attn), and the weights it accumulates.
+//
+// Bound by the cache's bytes (256 per token and KV head), so the kernel is a
+// stream over them with the arithmetic kept beside it:
+//
+// Work.  A unit is (sequence, KV head, tile of 8 NT query rows); a row is a
+//   (token, head of the group).  Its slots are cut into chunks, one CTA each (4
+//   warps, a quarter of the chunk each), and joined afterwards.
+// Loads.  Every lane copies (cp.async, 16 bytes) just the codes that it will
+//   feed to the tensor core itself, into a ring of its warp: no lane waits for
+//   another, and 3 stages of 32 slots keep up to 16 KB per warp in flight.
+//   Slots past the end arrive as zeros, so what they hold reaches nothing.
+// Products.  e4m3 codes are exact in fp16, so both products run on fp16
+//   mma.m16n8k16 with fp32 sums, the slots as its M side (S^T = K Q^T) and then
+//   its K side (O^T = V^T P^T): 8 query rows fill the N side, where rows as M
+//   would leave half of it empty.  The contraction order is free, so a lane's 16
+//   consecutive channels of a key row are its operand as they lie in memory, and
+//   16 consecutive channels of 4 value rows the other's.  Queries are scaled by a
+//   power of two to [2^14, 2^15) (exact in fp16 but for channels below 2^-38 of
+//   the row's largest); P^T goes from accumulator to operand by movmatrix.
+// Softmax.  Block scales: x = acc * (k_scale * scale / fq); the value scale joins
+//   the exponent, p' = 2^(x + log2 v_scale - m) with m the running maximum of
+//   x + log2 v_scale, so p' <= 1 whatever the scales are and its fp16 rounding
+//   (2^-12) is the only one before the output's; the denominator sums p' / v_scale.
 #include "kda_attn.cuh"
 
 namespace kda {
 namespace {
+
+constexpr int CA_WARPS = 4;
+constexpr int CA_STEP = 32;                       // slots of a warp's stage
+constexpr int CA_STAGES = 3;
+constexpr int CA_STAGE_BYTES = 16 * 512 + 128 + 16;  // 16 pieces per lane, positions, scales
+constexpr int CA_WARP_BYTES = CA_STAGES * CA_STAGE_BYTES;
+constexpr int CA_SMEM = CA_WARPS * CA_WARP_BYTES;
+constexpr int CA_WCHUNK = 512;                    // slots per CTA of the weight sums
+
+// How a call is cut: `tiles` row tiles in all (tile slots, see tile_of), chunks of
+// `chunk` slots, `splits` of them for the longest possible sequence.
+struct CachePlan {
+  int nt;        // query rows per tile / 8
+  int64_t tiles;
+  int chunk, splits;
+  int64_t max_len;
+};
+
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp4(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(there ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t lo16(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w)); }
+__device__ __forceinline__ uint32_t hi16(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Power of two that takes a largest magnitude to [2^14, 2^15): 1 for 0 (and
+// non-finite rows, whose results are not finite either).
+__device__ __forceinline__ float query_factor(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+  if (!(amax > 0.f) || e > 127) return 1.f;
+  const int f = 14 - e;
+  return __uint_as_float(static_cast<uint32_t>((f > 100 ? 100 : f) + 127) << 23);
+}
+
+// Rows of a tile: tile slot s belongs to the sequence whose first slot
+// floor(bos_n group / rows) + n is the last one <= s (bounded by T group / rows + N
+// slots in all).  `tile` may be past the sequence's last.
+__device__ __forceinline__ void tile_of(const CacheAttnArgs& a, int64_t s, int rows, int& n,
+                                        int64_t& bos, int& cnt, int64_t& tile) {
+  const int group = a.H / a.c.Hk;
+  int lo = 0, hi = a.c.N - 1;
+  int64_t b, e;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    seq_bounds(a.cu, a.T, a.c.N, mid, b, e);
+    if (b * group / rows + mid <= s) lo = mid;
+    else hi = mid - 1;
+  }
+  n = lo;
+  seq_bounds(a.cu, a.T, a.c.N, n, b, e);
+  bos = b;
+  cnt = static_cast<int>(e - b);
+  tile = s - (b * group / rows + n);
+}
 
 // Position of query token i of `cnt` of sequence n, for the slots of KV head hk:
 // given, or counted back from the newest slot.
@@ -17,126 +126,582 @@ __device__ __forceinline__ int query_pos(const CacheAttnArgs& a, int n, int hk, 
   return a.c.pos[b * a.c.page + ((len - 1) & (a.c.page - 1))] - (cnt - 1 - i);
 }
 
-__device__ __forceinline__ float4 decode4(uint32_t codes) {
-  const uint32_t lo = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
-  const uint32_t hi = e4m3x2_to_f16x2(static_cast<uint16_t>(codes >> 16));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
+// A warp's view of its stretch [begin, end) of a sequence's slots.
+struct Stretch {
+  const CacheArgs& c;
+  int n, hk, end;
+  int window;  // first table column that the lanes hold
+  int ids;     // this lane's page id (-1: none)
+  int* err;
 
-__device__ __forceinline__ void load_q(const CacheAttnArgs& a, int64_t t, int h, int l, float (&q)[4]) {
-  const __nv_bfloat16* p = a.q + (t * a.H + h) * kDim + l * 4;
-  for (int i = 0; i < 4; ++i) q[i] = __bfloat162float(p[i]);
-}
+  __device__ Stretch(const CacheArgs& cc, int n_, int hk_, int end_, int* e)
+      : c(cc), n(n_), hk(hk_), end(end_), window(-64), ids(-1), err(e) {}
 
-// Score of the warp's query against slot row r of block b, in log2 units.
-__device__ __forceinline__ float score(const CacheAttnArgs& a, const float (&q)[4], int64_t b, int64_t r, int l,
-                                       float slope, int gap) {
-  const float4 k = decode4(*reinterpret_cast<const uint32_t*>(a.c.k + r * kDim + l * 4));
-  float x = q[0] * k.x + q[1] * k.y + q[2] * k.z + q[3] * k.w;
+  __device__ int page_of(int slot) {  // slot < end, the same for all lanes
+    const int j = slot >> c.lg;
+    if (j < window || j >= window + 32) {
+      window = j;
+      const int col = j + (threadIdx.x & 31);
+      ids = (static_cast<int64_t>(col) << c.lg) < end ? page_id(c, n, col, err) : -1;
+    }
+    return __shfl_sync(0xffffffffu, ids, j - window);
+  }
+
+  // Issues the copies of slots [t0, t0 + 32) into `stage`.
+  template <bool POS>
+  __device__ void issue(uint8_t* stage, int t0) {
+    const int l = threadIdx.x & 31, g = l >> 2, q = l & 3;
+    uint8_t* mine = stage + l * 16;
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  x *= a.c.ks[b] * a.scale;
-  x = a.cap > 0.f ? cap_log2(x, 2.f * kLog2e / a.cap, a.cap * kLog2e) : x * kLog2e;
-  return x - slope * static_cast<float>(gap);
-}
-
-// One warp per (query token, head): the output row, and the log2 of the softmax
-// denominator into lse[t * H + h].
-__global__ void __launch_bounds__(32) row_kernel(CacheAttnArgs a, float* __restrict__ lse, int* err) {
-  const int l = threadIdx.x, h = blockIdx.y;
-  const int64_t t = blockIdx.x;
-  int n;
-  if (a.cu) {
-    int lo = 0, hi = a.c.N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu + mid) <= t) lo = mid;
-      else hi = mid - 1;
+    for (int st = 0; st < 2; ++st) {
+      const int tb = t0 + 16 * st;
+      const int pid = tb < end ? page_of(tb) : -1;
+      const int64_t block = static_cast<int64_t>(pid < 0 ? 0 : pid) * c.Hk + hk;
+      const int in = tb & (c.page - 1);
+      const int64_t row = block * c.page + in;  // 16 slots of one page
+      const int left = pid < 0 ? 0 : end - tb;  // slots of the 16 that exist
+      const uint8_t* kp = c.k + row * kDim + q * 16;
+      const uint8_t* vp = c.v + row * kDim + g * 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // key rows g and g + 8, channels 16 q .. and 64 + 16 q ..
+        const int r = g + 8 * (i >> 1);
+        cp16(mine + (st * 8 + i) * 512, kp + r * kDim + (i & 1) * 64, r < left);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // value rows 2 q, 2 q + 1, 2 q + 8, 2 q + 9, channels 16 g ..
+        const int r = 2 * q + (i & 1) + 8 * (i >> 1);
+        cp16(mine + (st * 8 + 4 + i) * 512, vp + r * kDim, r < left);
+      }
+      if (POS && (l >> 4) == st)
+        cp4(stage + 8192 + l * 4, c.pos + row + (l & 15), (l & 15) < left);
+      if (l == st * 2) cp4(stage + 8320 + st * 8, c.ks + block, left > 0);
+      if (l == st * 2 + 1) cp4(stage + 8324 + st * 8, c.vs + block, left > 0);
     }
-    n = lo;
-  } else {
-    n = static_cast<int>(t / (a.T / a.c.N));
   }
-  int64_t bos, eos;
-  seq_bounds(a.cu, a.T, a.c.N, n, bos, eos);
-  if (t < bos || t >= eos) return;
-  const int hk = h / (a.H / a.c.Hk);
-  const int len = cached_len(a.c, n, err);
-  const int qp = query_pos(a, n, hk, bos, static_cast<int>(t - bos), static_cast<int>(eos - bos), len, err);
-  float q[4];
-  load_q(a, t, h, l, q);
-  const float slope = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-  float m = -INFINITY, sum = 0.f;
-  float o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < len; ++i) {
-    const int pid = page_id(a.c, n, i >> a.c.lg, err);
-    if (pid < 0) continue;
-    const int64_t b = static_cast<int64_t>(pid) * a.c.Hk + hk;
-    const int64_t r = b * a.c.page + (i & (a.c.page - 1));
-    const int gap = qp - a.c.pos[r];
-    if (gap < 0) continue;
-    const float x = score(a, q, b, r, l, slope, gap);
-    const float4 v = decode4(*reinterpret_cast<const uint32_t*>(a.c.v + r * kDim + l * 4));
-    const float mn = fmaxf(m, x), f = ex2_approx(m - mn), p = ex2_approx(x - mn);
-    const float pv = p * a.c.vs[b];
-    sum = sum * f + p;
-    o[0] = o[0] * f + pv * v.x;
-    o[1] = o[1] * f + pv * v.y;
-    o[2] = o[2] * f + pv * v.z;
-    o[3] = o[3] * f + pv * v.w;
-    m = mn;
-  }
-  const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-  *reinterpret_cast<uint2*>(a.out + (t * a.H + h) * kDim + l * 4) =
-      make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-  if (lse && l == 0) lse[t * a.H + h] = m + log2f(sum);
-}
+};
 
-// One warp per (slot, sequence, KV head): the weights of the slot, summed over
-// the query rows of the head in order and added to the cache once.
-__global__ void __launch_bounds__(32) weight_kernel(CacheAttnArgs a, const float* __restrict__ lse, int* err) {
-  const int l = threadIdx.x, hk = blockIdx.y % a.c.Hk, n = blockIdx.y / a.c.Hk;
-  const int len = cached_len(a.c, n, err), i = blockIdx.x;
-  if (i >= len) return;
-  int64_t bos, eos;
-  seq_bounds(a.cu, a.T, a.c.N, n, bos, eos);
-  const int pid = page_id(a.c, n, i >> a.c.lg, err);
-  if (pid < 0) return;
-  const int64_t b = static_cast<int64_t>(pid) * a.c.Hk + hk;
-  const int64_t r = b * a.c.page + (i & (a.c.page - 1));
+template <int NT, bool POS, bool CAP>
+__global__ void __launch_bounds__(CA_WARPS * 32, 2)
+cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
+                  float2* __restrict__ part_ml, float* __restrict__ scores, int* err) {
+  constexpr int RT = 8 * NT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5, g = l >> 2, q = l & 3;
+  const int chunk = blockIdx.y, hk = blockIdx.x % a.c.Hk;
+  const int64_t slot = blockIdx.x / a.c.Hk;
   const int group = a.H / a.c.Hk;
-  float w = 0.f;
-  for (int64_t t = bos; t < eos; ++t) {
-    const int gap = query_pos(a, n, hk, bos, static_cast<int>(t - bos), static_cast<int>(eos - bos), len, err) - a.c.pos[r];
-    if (gap < 0) continue;
-    for (int h = hk * group; h < (hk + 1) * group; ++h) {
-      float q[4];
-      load_q(a, t, h, l, q);
-      w += ex2_approx(score(a, q, b, r, l, a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f, gap) - lse[t * a.H + h]);
+  int n, cnt;
+  int64_t bos, tile;
+  tile_of(a, slot, RT, n, bos, cnt, tile);
+  const int64_t rows = static_cast<int64_t>(cnt) * group - tile * RT;  // of this tile
+  if (rows <= 0) return;
+  const int len = cached_len(a.c, n, err);
+  const int begin = chunk * plan.chunk;
+  if (begin >= len && chunk > 0) return;
+  const int end = len < begin + plan.chunk ? len : begin + plan.chunk;
+
+  // query rows tile * RT + 8 t + g as operand words, channels as the keys' bytes
+  uint32_t qf[NT][16];
+  float fac[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = 8 * t + g;
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const int64_t rr = tile * RT + r;
+      const int64_t at = ((bos + rr / group) * a.H + hk * group + rr % group) * kDim + q * 16;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = *reinterpret_cast<const uint4*>(a.q + at + (i >> 1) * 64 + (i & 1) * 8);
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(ws[j] << 16)), fabsf(__uint_as_float(ws[j] & 0xffff0000u))));
+    }
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float f = query_factor(m);
+    fac[t] = 1.f / f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        qf[t][i * 4 + j] = pack_f16(__uint_as_float(ws[j] << 16) * f, __uint_as_float(ws[j] & 0xffff0000u) * f);
     }
   }
-  if (l == 0) a.c.weight[r] += w;
+  // what the lane's columns (query rows 8 t + 2 q + e) need
+  float mul[NT][2], slope[NT][2], m[NT][2], sum[NT][2];
+  int qpos[NT][2];
+  float o[NT][8][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * t + 2 * q + e;
+      mul[t][e] = __shfl_sync(0xffffffffu, fac[t], (2 * q + e) * 4) * a.scale * (CAP ? 1.f : kLog2e);
+      slope[t][e] = 0.f;
+      qpos[t][e] = -1;
+      if (POS && r < rows) {
+        const int64_t rr = tile * RT + r;
+        qpos[t][e] = query_pos(a, n, hk, bos, static_cast<int>(rr / group), cnt, len, err);
+        if (a.slopes) slope[t][e] = __ldg(a.slopes + hk * group + rr % group) * kLog2e;
+      }
+      m[t][e] = -INFINITY;
+      sum[t][e] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+  }
+  const float c1 = CAP ? 2.f * kLog2e / a.cap : 0.f, c2 = CAP ? a.cap * kLog2e : 0.f;
+
+  // the warp's quarter of the chunk, in whole stages
+  const int quarter = plan.chunk / CA_WARPS;
+  const int wb = begin + w * quarter;
+  const int we = end < wb + quarter ? end : wb + quarter;
+  const int steps = we > wb ? (we - wb + CA_STEP - 1) / CA_STEP : 0;
+  uint8_t* ring = smem + w * CA_WARP_BYTES;
+  Stretch src(a.c, n, hk, we, err);
+#pragma unroll
+  for (int i = 0; i < CA_STAGES - 1; ++i) {
+    if (i < steps) src.issue<POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
+    cp_commit();
+  }
+  float* srow = scores ? scores + (static_cast<int64_t>(blockIdx.x) * RT) * plan.max_len : nullptr;
+  int buf = 0;
+  for (int it = 0; it < steps; ++it) {
+    cp_wait<CA_STAGES - 2>();
+    __syncwarp();  // positions and scales come from other lanes; the buffer refilled below is free
+    const int nb = buf == 0 ? CA_STAGES - 1 : buf - 1;
+    if (it + CA_STAGES - 1 < steps)
+      src.issue<POS>(ring + nb * CA_STAGE_BYTES, wb + (it + CA_STAGES - 1) * CA_STEP);
+    cp_commit();
+    const uint8_t* stage = ring + buf * CA_STAGE_BYTES;
+    buf = buf + 1 == CA_STAGES ? 0 : buf + 1;
+    const uint8_t* mine = stage + l * 16;
+    const int t0 = wb + it * CA_STEP;
+
+    float s[2][NT][4];
+    float lvs[2], ivs[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      uint4 kk[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kk[i] = *reinterpret_cast<const uint4*>(mine + (st * 8 + i) * 512);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[st][t][e] = 0.f;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t r0[4] = {kk[half].x, kk[half].y, kk[half].z, kk[half].w};
+        const uint32_t r1[4] = {kk[2 + half].x, kk[2 + half].y, kk[2 + half].z, kk[2 + half].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = lo16(r0[j]), a1 = lo16(r1[j]), a2 = hi16(r0[j]), a3 = hi16(r1[j]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma_f16(s[st][t], a0, a1, a2, a3, qf[t][half * 8 + 2 * j], qf[t][half * 8 + 2 * j + 1]);
+        }
+      }
+      const float2 sc = *reinterpret_cast<const float2*>(stage + 8320 + st * 8);
+      const bool page_ok = sc.y > 0.f;
+      lvs[st] = page_ok ? __log2f(sc.y) : 0.f;
+      ivs[st] = page_ok ? ex2_approx(-lvs[st]) : 0.f;  // undoes what the exponent adds
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int tok = t0 + 16 * st + 8 * r + g;
+        const bool there = tok < we && page_ok;
+        const int p = POS ? *reinterpret_cast<const int*>(stage + 8192 + (16 * st + 8 * r + g) * 4) : 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = s[st][t][2 * r + e] * (mul[t][e] * sc.x);
+            if (CAP) x = cap_log2(x, c1, c2);
+            bool see = there;
+            if (POS) {
+              const int gap = qpos[t][e] - p;
+              x = fmaf(-slope[t][e], static_cast<float>(gap), x);
+              see = see && gap >= 0;
+            }
+            x = see ? x : -INFINITY;
+            if (srow && tok < we && 8 * t + 2 * q + e < rows)
+              srow[(8 * t + 2 * q + e) * plan.max_len + tok] = x;
+            s[st][t][2 * r + e] = x + lvs[st];
+          }
+        }
+      }
+    }
+    // running maximum of x + log2 v_scale
+    uint32_t pf[2][NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float mx[2], f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+        mx[e] = fmaxf(mx[e], m[t][e]);
+        f[e] = mx[e] == m[t][e] ? 1.f : ex2_approx(m[t][e] - mx[e]);
+        m[t][e] = mx[e];
+        sum[t][e] *= f[e];
+      }
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[t][i][0] *= f[0];
+          o[t][i][1] *= f[1];
+          o[t][i][2] *= f[0];
+          o[t][i][3] *= f[1];
+        }
+      }
+      const float ref0 = m[t][0] == -INFINITY ? 0.f : m[t][0], ref1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const float p0 = ex2_approx(s[st][t][0] - ref0), p1 = ex2_approx(s[st][t][1] - ref1);
+        const float p2 = ex2_approx(s[st][t][2] - ref0), p3 = ex2_approx(s[st][t][3] - ref1);
+        sum[t][0] = fmaf(p0 + p2, ivs[st], sum[t][0]);
+        sum[t][1] = fmaf(p1 + p3, ivs[st], sum[t][1]);
+        pf[st][t][0] = transpose8x8(pack_f16(p0, p1));
+        pf[st][t][1] = transpose8x8(pack_f16(p2, p3));
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      uint32_t v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + (st * 8 + 4 + i) * 512);
+        v[i][0] = x.x;
+        v[i][1] = x.y;
+        v[i][2] = x.z;
+        v[i][3] = x.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // channels 4 j .. 4 j + 3 of the lane's 16
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // bytes 2 half, 2 half + 1 of the rows' words, interleaved
+          const uint32_t x = __byte_perm(v[0][j], v[1][j], half ? 0x7362 : 0x5140);
+          const uint32_t y = __byte_perm(v[2][j], v[3][j], half ? 0x7362 : 0x5140);
+          const uint32_t a0 = lo16(x), a1 = hi16(x), a2 = lo16(y), a3 = hi16(y);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma_f16(o[t][2 * j + half], a0, a1, a2, a3, pf[st][t][0], pf[st][t][1]);
+        }
+      }
+    }
+  }
+
+  // join the warps: the ring is done with
+  cp_wait<0>();
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      sum[t][e] += __shfl_xor_sync(0xffffffffu, sum[t][e], 4);
+      sum[t][e] += __shfl_xor_sync(0xffffffffu, sum[t][e], 8);
+      sum[t][e] += __shfl_xor_sync(0xffffffffu, sum[t][e], 16);
+    }
+  __syncthreads();
+  float* so = reinterpret_cast<float*>(smem);             // [warp][row][128]
+  float2* sml = reinterpret_cast<float2*>(so + CA_WARPS * RT * kDim);  // [warp][row]
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * t + 2 * q + e;
+      if (g == 0) sml[w * RT + r] = make_float2(m[t][e], sum[t][e]);
+      float* dst = so + (w * RT + r) * kDim + g * 16;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dst[2 * i] = o[t][i][e];
+        dst[2 * i + 1] = o[t][i][2 + e];
+      }
+    }
+  }
+  __syncthreads();
+  const bool direct = part_o == nullptr;
+  for (int r = w; r < RT && r < rows; r += CA_WARPS) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < CA_WARPS; ++i) top = fmaxf(top, sml[i * RT + r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float tot = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < CA_WARPS; ++i) {
+      const float2 ml = sml[i * RT + r];
+      const float f = ex2_approx(ml.x - ref);
+      const float4 x = *reinterpret_cast<const float4*>(so + (i * RT + r) * kDim + l * 4);
+      tot = fmaf(ml.y, f, tot);
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z);
+      acc.w = fmaf(x.w, f, acc.w);
+    }
+    const int64_t rr = tile * RT + r;
+    if (direct) {
+      const float inv = tot == 0.f ? 0.f : 1.f / tot;
+      const int64_t at = ((bos + rr / group) * a.H + hk * group + rr % group) * kDim + l * 4;
+      *reinterpret_cast<uint2*>(a.out + at) =
+          make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    } else {
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * plan.splits + chunk) * RT + r;
+      *reinterpret_cast<float4*>(part_o + at * kDim + l * 4) = acc;
+      if (l == 0) part_ml[at] = make_float2(top, tot);
+    }
+  }
+}
+
+// Joins the chunks.  The first T H CTAs take one output row each: 4 warps over
+// the row's chunks, then over the warps, in a fixed order.  With `scores` the
+// other CTAs add the weights of 512 slots of a (sequence, KV head) each, the rows
+// in order; a row's denominator they work out again from the chunks' pairs.
+__global__ void __launch_bounds__(128)
+join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
+            const float2* __restrict__ part_ml, const float* __restrict__ scores, int* err) {
+  __shared__ float so[4][kDim];
+  __shared__ float2 sml[4];
+  __shared__ float lse[32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int group = a.H / a.c.Hk, rt = 8 * plan.nt;
+  const int64_t out_rows = a.T * a.H;
+  if (blockIdx.x < out_rows) {
+    const int64_t t = blockIdx.x / a.H;
+    const int h = static_cast<int>(blockIdx.x - t * a.H), hk = h / group;
+    int n = 0;
+    if (a.cu) {
+      int lo = 0, hi = a.c.N - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(a.cu + mid) <= t) lo = mid;
+        else hi = mid - 1;
+      }
+      n = lo;
+    } else {
+      n = static_cast<int>(t / (a.T / a.c.N));
+    }
+    int64_t bos, eos;
+    seq_bounds(a.cu, a.T, a.c.N, n, bos, eos);
+    if (t < bos || t >= eos) return;
+    const int len = cached_len(a.c, n, err);
+    const int chunks = len > plan.chunk ? (len + plan.chunk - 1) / plan.chunk : 1;
+    const int64_t rr = (t - bos) * group + (h - hk * group);
+    const int64_t unit = ((bos * group / rt + n) + rr / rt) * a.c.Hk + hk;
+    const int64_t base = unit * plan.splits * rt + rr % rt;
+    float top = -INFINITY, tot = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = w; c0 < chunks; c0 += 16) {
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ml[i] = make_float2(-INFINITY, 0.f);
+        x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c0 + 4 * i < chunks) {
+          const int64_t at = base + static_cast<int64_t>(c0 + 4 * i) * rt;
+          ml[i] = part_ml[at];
+          x[i] = *reinterpret_cast<const float4*>(part_o + at * kDim + l * 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float mn = fmaxf(top, ml[i].x), ref = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2_approx(top - ref), e = ex2_approx(ml[i].x - ref);
+        top = mn;
+        tot = tot * f + ml[i].y * e;
+        acc.x = acc.x * f + x[i].x * e;
+        acc.y = acc.y * f + x[i].y * e;
+        acc.z = acc.z * f + x[i].z * e;
+        acc.w = acc.w * f + x[i].w * e;
+      }
+    }
+    *reinterpret_cast<float4*>(&so[w][l * 4]) = acc;
+    if (l == 0) sml[w] = make_float2(top, tot);
+    __syncthreads();
+    if (w != 0) return;
+    top = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
+    const float ref = top == -INFINITY ? 0.f : top;
+    tot = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = ex2_approx(sml[i].x - ref);
+      const float4 x = *reinterpret_cast<const float4*>(&so[i][l * 4]);
+      tot = fmaf(sml[i].y, e, tot);
+      acc.x = fmaf(x.x, e, acc.x);
+      acc.y = fmaf(x.y, e, acc.y);
+      acc.z = fmaf(x.z, e, acc.z);
+      acc.w = fmaf(x.w, e, acc.w);
+    }
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    *reinterpret_cast<uint2*>(a.out + (t * a.H + h) * kDim + l * 4) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    return;
+  }
+  const int64_t b = blockIdx.x - out_rows;
+  const int64_t per = (plan.max_len + CA_WCHUNK - 1) / CA_WCHUNK;
+  const int64_t unit0 = b / per;
+  const int first = static_cast<int>(b - unit0 * per) * CA_WCHUNK;
+  const int n = static_cast<int>(unit0 / a.c.Hk), hk = static_cast<int>(unit0 - static_cast<int64_t>(n) * a.c.Hk);
+  const int len = cached_len(a.c, n, err);
+  if (first >= len) return;
+  int64_t bos, eos;
+  seq_bounds(a.cu, a.T, a.c.N, n, bos, eos);
+  const int64_t rows = (eos - bos) * group;
+  const int chunks = len > plan.chunk ? (len + plan.chunk - 1) / plan.chunk : 1;
+  const int64_t slot = bos * group / rt + n;
+  float wsum[CA_WCHUNK / 128];
+#pragma unroll
+  for (int j = 0; j < CA_WCHUNK / 128; ++j) wsum[j] = 0.f;
+  for (int64_t r0 = 0; r0 < rows; r0 += rt) {
+    const int64_t unit = (slot + r0 / rt) * a.c.Hk + hk;
+    const int here = rows - r0 < rt ? static_cast<int>(rows - r0) : rt;
+    __syncthreads();
+    for (int r = w; r < here; r += 4) {
+      float top = -INFINITY, tot = 0.f;
+      for (int c0 = l; c0 < chunks; c0 += 32) {
+        const float2 ml = part_ml[(unit * plan.splits + c0) * rt + r];
+        const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+        tot = tot * ex2_approx(top - ref) + ml.y * ex2_approx(ml.x - ref);
+        top = mn;
+      }
+      float all = top;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+      tot *= ex2_approx(top - (all == -INFINITY ? 0.f : all));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      // nothing seen: every score of the row is -inf and gives 0 against 0
+      if (l == 0) lse[r] = all == -INFINITY ? 0.f : all + log2f(tot);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < CA_WCHUNK / 128; ++j) {
+      const int tok = first + j * 128 + threadIdx.x;
+      if (tok >= len) continue;
+      const float* s = scores + unit * rt * plan.max_len + tok;
+      for (int r = 0; r < here; ++r) wsum[j] += ex2_approx(s[r * plan.max_len] - lse[r]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < CA_WCHUNK / 128; ++j) {
+    const int tok = first + j * 128 + threadIdx.x;
+    if (tok >= len) continue;
+    const int pid = page_id(a.c, n, tok >> a.c.lg, err);
+    if (pid < 0) continue;
+    float* at = a.c.weight + (static_cast<int64_t>(pid) * a.c.Hk + hk) * a.c.page + (tok & (a.c.page - 1));
+    *at += wsum[j];
+  }
+}
+
+// Two tile heights: 8 rows keep 32 accumulators per lane and read the cache
+// once for up to 8 rows; 16 rows halve the passes over it for more.
+CachePlan make_plan(int64_t T, int H, int Hk, int N, int64_t max_len) {
+  CachePlan p{};
+  const int64_t group = H / Hk;
+  p.nt = T * group > 8 * static_cast<int64_t>(N) ? 2 : 1;
+  const int64_t rt = 8 * p.nt;
+  p.tiles = T * group / rt + N;
+  p.max_len = max_len;
+  // Two CTAs fit an SM.  One sequence: the chunks fill the GPU once, evenly.
+  // More of them are ragged: chunks of at most 1024 slots keep the last ones short.
+  const int64_t slots = 2 * 152;
+  const int64_t units = (T * group + rt - 1) / rt > N ? (T * group + rt - 1) / rt * Hk : static_cast<int64_t>(N) * Hk;
+  int64_t chunk = (max_len * units + slots - 1) / slots;
+  if (N > 1 && chunk > 1024) chunk = 1024;
+  const int64_t step = CA_WARPS * CA_STEP;
+  chunk = (chunk + step - 1) / step * step;
+  const int64_t least = (max_len + 65534) / 65535;  // grid.y
+  if (chunk < least) chunk = (least + step - 1) / step * step;
+  p.chunk = static_cast<int>(chunk);
+  p.splits = static_cast<int>((max_len + chunk - 1) / chunk);
+  return p;
+}
+
+struct CacheScratch {
+  size_t o, ml, scores, total;
+};
+
+CacheScratch scratch_of(const CachePlan& p, int Hk, bool accumulate) {
+  CacheScratch s{};
+  const size_t rows = static_cast<size_t>(p.tiles) * Hk * 8 * p.nt;
+  if (p.splits > 1 || accumulate) {
+    s.ml = rows * p.splits * kDim * 4;
+    s.scores = s.ml + rows * p.splits * 8;
+    s.total = s.scores + (accumulate ? rows * static_cast<size_t>(p.max_len) * 4 : 0);
+  }
+  return s;
+}
+
+template <int NT, bool POS, bool CAP>
+cudaError_t launch_one(const CacheAttnArgs& a, const CachePlan& p, float* o, float2* ml,
+                       float* scores, int* err, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = cache_attn_kernel<NT, POS, CAP>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), CA_SMEM, done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.tiles * a.c.Hk), static_cast<unsigned>(p.splits));
+  return launch_pdl(kernel, grid, dim3(CA_WARPS * 32), CA_SMEM, stream, a, p, o, ml, scores, err);
+}
+
+template <int NT>
+cudaError_t launch_variant(bool pos, bool cap, const CacheAttnArgs& a, const CachePlan& p, float* o,
+                           float2* ml, float* scores, int* err, cudaStream_t stream) {
+  if (pos) return cap ? launch_one<NT, true, true>(a, p, o, ml, scores, err, stream)
+                      : launch_one<NT, true, false>(a, p, o, ml, scores, err, stream);
+  return cap ? launch_one<NT, false, true>(a, p, o, ml, scores, err, stream)
+             : launch_one<NT, false, false>(a, p, o, ml, scores, err, stream);
 }
 
 }  // namespace
 
 size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, int64_t max_len, bool accumulate) {
-  (void)Hk;
-  (void)N;
-  (void)max_len;
-  return accumulate ? static_cast<size_t>(T) * H * 4 : 0;
+  return scratch_of(make_plan(T, H, Hk, N, max_len), Hk, accumulate).total;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, int* err,
                               cudaStream_t stream) {
   (void)sm_count;
-  float* lse = static_cast<float*>(ws);
-  row_kernel<<<dim3(static_cast<unsigned>(a.T), a.H), 32, 0, stream>>>(a, lse, err);
-  if (a.accumulate)
-    weight_kernel<<<dim3(static_cast<unsigned>(a.c.width) << a.c.lg, a.c.N * a.c.Hk), 32, 0, stream>>>(a, lse, err);
-  return cudaGetLastError();
+  const int64_t max_len = static_cast<int64_t>(a.c.width) << a.c.lg;
+  const CachePlan p = make_plan(a.T, a.H, a.c.Hk, a.c.N, max_len);
+  if (p.tiles * a.c.Hk > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const CacheScratch s = scratch_of(p, a.c.Hk, a.accumulate != 0);
+  float *o = nullptr, *scores = nullptr;
+  float2* ml = nullptr;
+  if (s.total) {
+    o = static_cast<float*>(ws);
+    ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + s.ml);
+    if (a.accumulate) scores = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + s.scores);
+  }
+  // positions matter for the bias, and where a query is not its sequence's newest token
+  const bool pos = a.slopes || a.positions || a.cu || a.T != a.c.N;
+  cudaError_t e = p.nt == 1 ? launch_variant<1>(pos, a.cap > 0.f, a, p, o, ml, scores, err, stream)
+                            : launch_variant<2>(pos, a.cap > 0.f, a, p, o, ml, scores, err, stream);
+  if (e != cudaSuccess || !s.total) return e;
+  const int64_t weights = a.accumulate
+                              ? (max_len + CA_WCHUNK - 1) / CA_WCHUNK * a.c.N * a.c.Hk : 0;
+  const int64_t blocks = a.T * a.H + weights;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, a, p,
+                    static_cast<const float*>(o), static_cast<const float2*>(ml),
+                    static_cast<const float*>(scores), err);
 }
 
 }  // namespace kda
