@@ -1,81 +1,450 @@
-// kda_attn.cu -- softmax attention over packed rows (kda_attn_fwd).
+// kda_attn.cu -- softmax attention over packed rows (kda_attn_fwd) on tcgen05.
 //
-// One warp per (token, head): the four channels of a lane in registers, the
-// visible keys one after the other with a running maximum and sum.
+// One CTA per (256 query rows of a sequence, head), 12 warps:
+//   warps 0-3, 4-7  the softmax of query tiles 0 and 1 (128 rows each, one thread
+//                   a row, tensor-memory lane = row)
+//   warp 8          TMA: the two query tiles once, then key and value tiles of
+//                   128 rows through two stages each
+//   warp 9          the MMAs, issued by one lane (warps 10, 11 fill the warpgroup)
+// Per key tile j and query tile t:  S = Q_t K_j^T (A, B in shared memory) into
+// tensor memory; the row's thread reads it, takes the running maximum and sum,
+// and writes P = 2^(S - m) in bf16 over S; O_t += P V_j (A in tensor memory, B =
+// V in its own row order, an MN-major operand).  The two query tiles alternate:
+// while the tensor core works for one, the softmax of the other runs.
+// Tensor memory: S0 | S1 | O0 | O1, 128 columns each, all 512.
+//
+// Softmax.  m moves only when a row's maximum grows by more than 2^8 over it (P
+// then stays below 2^8, in bf16's range, and the sum in fp32), so O is rarely
+// rescaled; a row thread rescales its own row of O in tensor memory.  P is
+// rounded to bf16 (2^-9 relative, as the output once more); its sum is taken in
+// fp32 before that rounding.
+//
+// Masks.  Every row sees a prefix of its sequence's keys: all of them, up to
+// itself, or up to max(itself, prefix_len).  Tiles past a query tile's last
+// visible key are skipped, and only tiles that cross a row's limit select.
+// Rows of V past the sequence's end (another sequence's, whatever they hold)
+// are overwritten with zeros in shared memory before the product.
 #include "kda_attn.cuh"
+#include "kda_tma.cuh"
 
 namespace kda {
+
 namespace {
 
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 b = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
-                     __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u));
+constexpr int AT_ROWS = 128;                   // rows of a query or key tile
+constexpr int AT_TILE = AT_ROWS * kDim * 2;    // bytes of a tile (two boxes of 64 channels)
+constexpr int AT_BOX = AT_TILE / 2;
+constexpr int AT_THREADS = 384;
+// three warpgroups of 168 registers a thread at launch; the softmax ones (a row of
+// 128 scores in registers) take from the third: 2 x 232 + 40 = 3 x 168
+constexpr int AT_REGS_SOFTMAX = 232, AT_REGS_ISSUE = 40;
+constexpr int AT_Q = 0, AT_K = 2 * AT_TILE, AT_V = 4 * AT_TILE, AT_CTL = 6 * AT_TILE;
+constexpr int AT_SMEM = AT_CTL + 256 + 1024;
+constexpr float AT_GROW = 8.0f;                // how far a maximum may outgrow the reference
+
+struct AttnMaps {
+  CUtensorMap q, k, v;
+};
+
+struct AttnCtl {
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], drained;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(AttnCtl) <= 256, "control block");
+
+// A bounded wait that also gives up when another role has.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, AttnCtl* ctl, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_sleep(bar, parity, kSleepHintNs)) {
+    if (*reinterpret_cast<volatile int*>(&ctl->abort)) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *reinterpret_cast<volatile int*>(&ctl->abort) = 1;
+      atomicCAS(err, 0, static_cast<int>(KDA_ERR_TIMEOUT));
+      return false;
+    }
+  }
+  return true;
 }
 
-__global__ void __launch_bounds__(128) attn_kernel(AttnArgs a) {
-  const int l = threadIdx.x & 31;
-  const int h = blockIdx.y;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (t >= a.T) return;
-  int64_t bos = 0, eos = 0;
-  int n = 0;
-  if (a.cu) {
-    int lo = 0, hi = a.N - 1;  // last sequence that starts at or before t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu + mid) <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    n = lo;
-  } else {
-    n = static_cast<int>(t / (a.T / a.N));
+// The same for a whole warp: true if every lane's wait ended.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, AttnCtl* ctl, int* err) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, ctl, err));
+}
+
+template <int REGS>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// D (tmem, fp32) (+)= A (smem) * B (smem); bf16, one K = 16 step.
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// What a query tile of a sequence sees.
+struct TileView {
+  int len, prefix, mask;
+  // keys that row i (of the sequence) sees: the first limit(i)
+  __device__ __forceinline__ int limit(int i) const {
+    if (mask == KDA_MASK_FULL) return len;
+    const int own = i + 1 > prefix ? i + 1 : prefix;
+    return own < len ? own : len;
   }
-  seq_bounds(a.cu, a.T, a.N, n, bos, eos);
-  if (t < bos || t >= eos) return;
-  int64_t end = eos;
-  if (a.mask != KDA_MASK_FULL) {
-    end = t + 1;
-    if (a.mask == KDA_MASK_PREFIX) {
-      const int64_t p = bos + __ldg(a.prefix + n);
-      end = p > end ? (p < eos ? p : eos) : end;
-    }
+  // key tiles of the 128 rows from i0 on; 0 past the sequence's end
+  __device__ __forceinline__ int tiles(int i0) const {
+    if (i0 >= len) return 0;
+    const int last = i0 + AT_ROWS < len ? i0 + AT_ROWS - 1 : len - 1;
+    return (limit(last) + AT_ROWS - 1) / AT_ROWS;
   }
-  const int64_t row = (t * a.H + h) * kDim + l * 4;
-  const float4 q = load4(a.q + row);
-  const float slope = a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
+};
+
+template <bool CAP, bool BIAS>
+__global__ void __launch_bounds__(AT_THREADS, 1)
+attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, int* err) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  AttnCtl* ctl = reinterpret_cast<AttnCtl*>(smem + AT_CTL);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
+  // long causal rows come last in a sequence: start from the last slot
+  const int h = blockIdx.x % a.H;
+  const int64_t slot = slots - 1 - blockIdx.x / a.H;
   const int hk = h / (a.H / a.Hk);
-  float m = -INFINITY, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int64_t j = bos; j < end; ++j) {
-    const int64_t at = (j * a.Hk + hk) * kDim + l * 4;
-    const float4 k = load4(a.k + at), v = load4(a.v + at);
-    float x = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    x *= a.scale;
-    x = a.cap > 0.f ? cap_log2(x, 2.f * kLog2e / a.cap, a.cap * kLog2e) : x * kLog2e;
-    x -= slope * fabsf(static_cast<float>(t - j));
-    const float mn = fmaxf(m, x), r = ex2_approx(m - mn), p = ex2_approx(x - mn);
-    sum = sum * r + p;
-    o.x = o.x * r + p * v.x;
-    o.y = o.y * r + p * v.y;
-    o.z = o.z * r + p * v.z;
-    o.w = o.w * r + p * v.w;
-    m = mn;
+  const int n = seq_of_slot(a.cu, a.T, a.N, 2 * AT_ROWS, 1, slot);
+  int64_t bos, eos;
+  seq_bounds(a.cu, a.T, a.N, n, bos, eos);
+  const int64_t i_first = (slot - (bos / (2 * AT_ROWS) + n)) * (2 * AT_ROWS);
+  if (i_first >= eos - bos) return;
+  const int i0 = static_cast<int>(i_first);
+  TileView view{static_cast<int>(eos - bos), 0, a.mask};
+  if (a.mask == KDA_MASK_PREFIX) {
+    const int p = __ldg(a.prefix + n);
+    view.prefix = p < 0 ? 0 : (p < view.len ? p : view.len);
   }
-  const float inv = 1.f / sum;
-  *reinterpret_cast<uint2*>(a.out + row) =
-      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  const int n0 = view.tiles(i0), n1 = view.tiles(i0 + AT_ROWS);
+  const int nj = n0 > n1 ? n0 : n1;
+
+  if (tid == 0) {
+    mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->k_full[i], 1);
+      mbar_init(&ctl->k_empty[i], 1);
+      mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->v_empty[i], 1);
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], AT_ROWS);
+    }
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (w == 9) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (w >= 8) {
+    regs_give<AT_REGS_ISSUE>();
+    if (w == 8) {
+      if (l == 0) {
+        auto tile = [&](int off, const CUtensorMap* map, int head, int64_t tok, uint64_t* bar) {
+          tma_box(smem + off, map, 0, head, static_cast<int>(tok), bar);
+          tma_box(smem + off + AT_BOX, map, 64, head, static_cast<int>(tok), bar);
+        };
+        mbar_arrive_expect_tx(&ctl->k_full[0], AT_TILE);
+        tile(AT_K, &maps.k, hk, bos, &ctl->k_full[0]);
+        mbar_arrive_expect_tx(&ctl->q_full, n1 > 0 ? 2 * AT_TILE : AT_TILE);
+        tile(AT_Q, &maps.q, h, bos + i0, &ctl->q_full);
+        if (n1 > 0) tile(AT_Q + AT_TILE, &maps.q, h, bos + i0 + AT_ROWS, &ctl->q_full);
+        int ks = 1, vs = 0;  // tiles issued
+        bool ok = true;
+        while (ok && (ks < nj || vs < nj)) {
+          if (vs < nj) {
+            if (vs >= 2) ok = wait_for(&ctl->v_empty[vs & 1], ((vs >> 1) - 1) & 1, ctl, err);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ctl->v_full[vs & 1], AT_TILE);
+            tile(AT_V + (vs & 1) * AT_TILE, &maps.v, hk, bos + static_cast<int64_t>(vs) * AT_ROWS, &ctl->v_full[vs & 1]);
+            ++vs;
+          }
+          if (ks < nj) {
+            if (ks >= 2) ok = wait_for(&ctl->k_empty[ks & 1], ((ks >> 1) - 1) & 1, ctl, err);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&ctl->k_full[ks & 1], AT_TILE);
+            tile(AT_K + (ks & 1) * AT_TILE, &maps.k, hk, bos + static_cast<int64_t>(ks) * AT_ROWS, &ctl->k_full[ks & 1]);
+            ++ks;
+          }
+        }
+        // after a wait that ran out, copies may be in flight: let them land first
+        if (!ok) {
+          mbar_wait(&ctl->q_full, 0);
+          for (int i = ks > 2 ? ks - 2 : 0; i < ks; ++i) mbar_wait(&ctl->k_full[i & 1], (i >> 1) & 1);
+          for (int i = vs > 2 ? vs - 2 : 0; i < vs; ++i) mbar_wait(&ctl->v_full[i & 1], (i >> 1) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (w == 9) {
+      const uint32_t sb = smem_u32(smem);
+      constexpr uint32_t id_s = make_idesc(1, AT_ROWS, AT_ROWS);
+      constexpr uint32_t id_o = make_idesc(1, AT_ROWS, kDim) | (1u << 16);  // B is MN-major
+      auto issue_s = [&](int t, int j) {
+        if (l == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t off = (k >> 2) * AT_BOX + (k & 3) * 32;
+            mma_bf16_ss(tmem + t * 128, make_sdesc(sb + AT_Q + t * AT_TILE + off, 16, 1024, 2),
+                        make_sdesc(sb + AT_K + (j & 1) * AT_TILE + off, 16, 1024, 2), id_s, k > 0);
+          }
+        }
+      };
+      // 16 keys a step: two groups of 8 rows of 128 bytes; channels 64.. one box further
+      auto issue_o = [&](int t, int j, int steps) {
+        if (l == 0) {
+          for (int k = 0; k < steps; ++k)
+            mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
+                        make_sdesc(sb + AT_V + (j & 1) * AT_TILE + k * 2048, AT_BOX, 1024, 2), id_o, j > 0 || k > 0);
+        }
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (l == 0) tc_commit(bar);
+        __syncwarp();
+      };
+      bool ok = warp_wait(&ctl->k_full[0], 0, ctl, err) && warp_wait(&ctl->q_full, 0, ctl, err);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        commit(&ctl->s_full[0]);
+        if (n1 > 0) {
+          issue_s(1, 0);
+          commit(&ctl->s_full[1]);
+        }
+        commit(&ctl->k_empty[0]);
+        for (int j = 0; j < nj; ++j) {
+          ok = warp_wait(&ctl->v_full[j & 1], (j >> 1) & 1, ctl, err);
+          if (!ok) break;
+          const int left = view.len - j * AT_ROWS;
+          const int steps = left >= AT_ROWS ? AT_ROWS / 16 : (left + 15) / 16;
+          if (left < steps * 16) {
+            // zeros in the rows between the sequence's end and the last step's
+            for (int e = l; e < (steps * 16 - left) * 16; e += 32) {
+              const int off = (e & 8 ? AT_BOX : 0) + (left + (e >> 4)) * 128 + (e & 7) * 16;
+              *reinterpret_cast<uint4*>(smem + AT_V + (j & 1) * AT_TILE + off) = make_uint4(0, 0, 0, 0);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+          }
+          if (j + 1 < nj) {
+            ok = warp_wait(&ctl->k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, ctl, err);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t == 0 ? n0 : n1;
+            if (j < nt) {
+              ok = warp_wait(&ctl->p_full[t], j & 1, ctl, err);
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(t, j, steps);
+              // the tensor core runs these in order: S may follow into the columns P is read from
+              if (j + 1 < nt) issue_s(t, j + 1);
+              commit(&ctl->s_full[t]);
+            }
+          }
+          if (!ok) break;
+          commit(&ctl->v_empty[j & 1]);
+          if (j + 1 < nj) commit(&ctl->k_empty[(j + 1) & 1]);
+        }
+      }
+      // nothing may be running in tensor memory when it is freed
+      commit(&ctl->drained);
+      mbar_wait(&ctl->drained, 0);
+    }
+  } else {
+    regs_take<AT_REGS_SOFTMAX>();
+    const int t = w >> 2;
+    const int nt = t == 0 ? n0 : n1;
+    const int i = i0 + t * AT_ROWS + (tid & 127);  // row of the sequence
+    const uint32_t lane = static_cast<uint32_t>((w & 3) * 32) << 16;
+    const uint32_t S = tmem + t * 128 + lane, O = tmem + 256 + t * 128 + lane;
+    const int limit = view.limit(i);
+    const int tile_lo = view.limit(i0 + t * AT_ROWS);  // least limit of the tile's rows
+    const float slope = BIAS && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
+    // CAP: x log2 e = c2 - 2 c2 / (1 + 2^(c1 s)); the constant c2 cancels in the softmax
+    const float c1 = CAP ? a.scale * 2.f * kLog2e / a.cap : a.scale * kLog2e;
+    const float c2 = CAP ? -2.f * a.cap * kLog2e : 0.f;
+    float ref = -INFINITY, sum = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      ok = warp_wait(&ctl->s_full[t], j & 1, ctl, err);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(S + c * 32, s[c]);
+      tmem_wait_ld();
+      const int j0 = j * AT_ROWS;
+      float base = 0.f;  // added to every score of the row
+      if (CAP) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            s[c][e] = __float_as_uint(c2 * rcp_approx(1.0f + ex2_approx(__uint_as_float(s[c][e]) * c1)));
+      }
+      if (BIAS) {
+        const float mul = CAP ? 1.f : c1;
+        const int d = i - j0;
+        const int lo = i0 + t * AT_ROWS - j0;  // the same for the warp
+        if (lo >= AT_ROWS - 1 || lo + AT_ROWS - 1 <= 0) {
+          // one side of the diagonal: the distance is linear in the column
+          const float step = lo > 0 ? slope : -slope;
+          base = lo > 0 ? -slope * static_cast<float>(d) : slope * static_cast<float>(d);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), mul, step * static_cast<float>(c * 32 + e)));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              s[c][e] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(d - (c * 32 + e))),
+                                             __uint_as_float(s[c][e]) * mul));
+        }
+      }
+      if (j0 + AT_ROWS > tile_lo) {
+        const int left = limit - j0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= left) s[c][e] = 0xff800000u;  // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[c][e]));
+      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      constexpr bool SCALED = !CAP && !BIAS;  // scores still to be multiplied by c1 (> 0)
+      top = SCALED ? top * c1 : top + base;
+      const bool grow = top > ref + AT_GROW;  // ref = -inf: any finite maximum
+      if (__any_sync(0xffffffffu, grow)) {
+        const float now = grow ? top : ref;
+        const float f = grow ? ex2_approx(ref - now) : 1.f;
+        sum *= f;
+        ref = now;
+        if (j > 0) {  // the products of the tiles before are complete (S came after them)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(O + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(O + c * 32, o);
+          }
+        }
+      }
+      // nothing seen yet: every weight is 0
+      const float sub = (ref == -INFINITY ? 0.f : ref) - base;
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
+          const float p0 = ex2_approx(SCALED ? fmaf(x, c1, -sub) : x - sub);
+          const float p1 = ex2_approx(SCALED ? fmaf(y, c1, -sub) : y - sub);
+          part[e & 2] += p0;
+          part[(e & 2) + 1] += p1;
+          pk[e >> 1] = pack_bf16(p0, p1);
+        }
+        tmem_st16(S + c * 16, pk);
+      }
+      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&ctl->p_full[t]);
+    }
+    if (ok && nt > 0) {
+      ok = warp_wait(&ctl->s_full[t], nt & 1, ctl, err);  // the last product
+      tc_fence_after();
+      if (ok) {
+        const float inv = 1.f / sum;
+        const bool store = i < view.len;
+        __nv_bfloat16* dst = a.out + ((bos + (store ? i : 0)) * a.H + h) * kDim;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(O + c * 32, o);
+          tmem_wait_ld();
+          if (store) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t p[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                p[x] = pack_bf16(__uint_as_float(o[e * 8 + 2 * x]) * inv, __uint_as_float(o[e * 8 + 2 * x + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + c * 32 + e * 8) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == 9) tmem_dealloc(tmem, 512);
+}
+
+template <bool CAP, bool BIAS>
+cudaError_t launch_one(const AttnMaps& maps, const AttnArgs& a, int* err, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = attn_kernel<CAP, BIAS>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), AT_SMEM, done);
+  if (e != cudaSuccess) return e;
+  // sequence n owns the slots of 256 rows from floor(bos_n / 256) + n on
+  const int64_t slots = a.cu ? a.T / (2 * AT_ROWS) + a.N
+                             : (a.T - a.T / a.N) / (2 * AT_ROWS) + a.N - 1 + (a.T / a.N + 2 * AT_ROWS - 1) / (2 * AT_ROWS);
+  if (slots * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(slots * a.H)), dim3(AT_THREADS), AT_SMEM, stream,
+                    maps, a, slots, err);
 }
 
 }  // namespace
 
 cudaError_t launch_attn(const AttnArgs& a, int sm_count, int* err, cudaStream_t stream) {
   (void)sm_count;
-  (void)err;
-  attn_kernel<<<dim3(static_cast<unsigned>((a.T + 3) / 4), a.H), 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  AttnMaps maps;
+  cudaError_t e = make_tile_map(&maps.q, a.q, a.T, a.H, AT_ROWS);
+  if (e == cudaSuccess) e = make_tile_map(&maps.k, a.k, a.T, a.Hk, AT_ROWS);
+  if (e == cudaSuccess) e = make_tile_map(&maps.v, a.v, a.T, a.Hk, AT_ROWS);
+  if (e != cudaSuccess) return e;
+  // the plain kernel takes its maximum before the scale, which has to be positive for that
+  const bool bias = a.slopes || !(a.scale > 0.f);
+  if (a.cap > 0.f)
+    return bias ? launch_one<true, true>(maps, a, err, stream) : launch_one<true, false>(maps, a, err, stream);
+  return bias ? launch_one<false, true>(maps, a, err, stream) : launch_one<false, false>(maps, a, err, stream);
 }
 
 }  // namespace kda

@@ -47,6 +47,25 @@ cudaError_t make_raw_map(CUtensorMap* map, const void* base, int64_t T_total, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Tiles of `rows` tokens of one head in two boxes of 64 channels (128 bytes, the
+// span of the 128-byte swizzle), for tcgen05 operands (kda_attn.cu).
+cudaError_t make_tile_map(CUtensorMap* map, const void* base, int64_t T_total, int H, int rows) {
+  if (T_total < 1 || T_total >= (static_cast<int64_t>(1) << 31) || H < 1) return cudaErrorInvalidValue;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kDim), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(T_total)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kDim) * 2,
+                                 static_cast<cuuint64_t>(H) * kDim * 2};
+  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_raw_maps(RawMaps* maps, const void* q, const void* k, const void* v,
                           const void* g, int64_t T_total, int H, bool gate_scalar) {
   std::memset(maps, 0, sizeof(RawMaps));

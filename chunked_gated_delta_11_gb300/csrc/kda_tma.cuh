@@ -60,4 +60,8 @@ cudaError_t make_raw_map(CUtensorMap* map, const void* base, int64_t T_total, in
 cudaError_t make_raw_maps(RawMaps* maps, const void* q, const void* k, const void* v,
                           const void* g, int64_t T_total, int H, bool gate_scalar);
 
+// Host: a map whose boxes are 64 channels x 1 head x `rows` tokens, 128-byte
+// swizzled.  The x coordinates used with it are 0 and 64 channels.
+cudaError_t make_tile_map(CUtensorMap* map, const void* base, int64_t T_total, int H, int rows);
+
 }  // namespace kda
