@@ -126,7 +126,7 @@ struct CacheAttnArgs {
   float scale, cap;
   int accumulate;
 };
-size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, int64_t max_len, bool accumulate);
+size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len, bool accumulate);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, int* err,
                               cudaStream_t stream);
 

@@ -75,6 +75,13 @@ CacheArgs cache_args(const kda_cache* c, const int32_t* table, int32_t width, co
   return a;
 }
 
+// The larger need of the two ways to give the sequences (cu_seqlens or equal shares).
+size_t cached_need(const kda_cache* c, int64_t T, int H, int N, int64_t max_len, bool accumulate) {
+  const size_t a = cache_attn_workspace(T, H, c->Hk, N, true, max_len, accumulate);
+  const size_t b = T % N == 0 ? cache_attn_workspace(T, H, c->Hk, N, false, max_len, accumulate) : 0;
+  return a > b ? a : b;
+}
+
 // A workspace of the caller's, or one allocated on the stream for this call.
 class Workspace {
  public:
@@ -173,8 +180,8 @@ extern "C" size_t kda_cache_attn_workspace_size(const kda_cache* cache, int64_t 
   if (check_rows(T_total, H, cache->Hk, N, cache->D, reinterpret_cast<const int32_t*>(4)) != KDA_OK)
     return 0;
   const int64_t max_len = static_cast<int64_t>(table_width) * cache->page_size;
-  if (max_len > 0x7fffff00LL) return 0;
-  return T_total == 0 ? 0 : cache_attn_workspace(T_total, H, cache->Hk, N, max_len, accumulate != 0);
+  if (max_len > 0x7fffff00LL || T_total > 0x7fffffffLL / H) return 0;
+  return T_total == 0 ? 0 : cached_need(cache, T_total, H, N, max_len, accumulate != 0);
 }
 
 extern "C" kda_status kda_cache_attn(const kda_cache_attn_options* opts, const kda_cache* cache,
@@ -190,12 +197,13 @@ extern "C" kda_status kda_cache_attn(const kda_cache_attn_options* opts, const k
   if ((s = check_rows(T_total, H, cache->Hk, N, cache->D, cu_seqlens)) != KDA_OK) return s;
   if (!good_scores(scale, opts->cap, opts->slopes) || !aligned(opts->positions, 4))
     return KDA_ERR_INVALID_ARG;
+  if (T_total > 0x7fffffffLL / H) return KDA_ERR_INVALID_ARG;  // (token, head) rows are int32
   if (T_total == 0) return KDA_OK;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return KDA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t need = cache_attn_workspace(T_total, H, cache->Hk, N,
-                                           static_cast<int64_t>(table_width) * cache->page_size,
-                                           opts->accumulate != 0);
+  const size_t need = cached_need(cache, T_total, H, N,
+                                  static_cast<int64_t>(table_width) * cache->page_size,
+                                  opts->accumulate != 0);
   if (workspace && (!aligned(workspace, 16) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   int sms = 0, *err = nullptr;
   if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;

@@ -29,19 +29,31 @@ namespace kda {
 namespace {
 
 constexpr int CA_WARPS = 4;
-constexpr int CA_STEP = 32;                       // slots of a warp's stage
-constexpr int CA_STAGES = 3;
+constexpr int CA_STEP = 32;                          // slots of a warp's stage
 constexpr int CA_STAGE_BYTES = 16 * 512 + 128 + 16;  // 16 pieces per lane, positions, scales
-constexpr int CA_WARP_BYTES = CA_STAGES * CA_STAGE_BYTES;
-constexpr int CA_SMEM = CA_WARPS * CA_WARP_BYTES;
-constexpr int CA_WCHUNK = 512;                    // slots per CTA of the weight sums
+constexpr int CA_PIECE = 18, CA_ROW = 8 * CA_PIECE;  // floats: a warp's output rows in shared memory
+constexpr int CA_WCHUNK = 2048;                      // slots per CTA of the weight sums
 
-// How a call is cut: `tiles` row tiles in all (tile slots, see tile_of), chunks of
-// `chunk` slots, `splits` of them for the longest possible sequence.
+// 8 rows: 3 CTAs per SM, two stages each.  16 and 32 rows (more registers): 2
+// CTAs, three stages.  32 rows keep the queries' operand words in shared memory.
+constexpr int ca_stages(int nt) { return nt == 1 ? 2 : 3; }
+constexpr int ca_ctas(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int ca_qbytes(int nt) { return nt == 4 ? nt * 16 * 32 * 4 : 0; }
+constexpr int ca_smem(int nt) {
+  const int ring = CA_WARPS * ca_stages(nt) * CA_STAGE_BYTES;
+  const int join = CA_WARPS * 8 * nt * (CA_ROW * 4 + 8);
+  return ca_qbytes(nt) + (ring > join ? ring : join);
+}
+
+// How a call is cut.  Row tiles of the sequences: without cu_seqlens each has the
+// same number `per_tiles`; with it sequence n owns the tile slots from
+// floor(bos_n group / rows) + n on, T group / rows + N in all.
 struct CachePlan {
-  int nt;        // query rows per tile / 8
-  int64_t tiles;
-  int chunk, splits;
+  int nt;         // query rows per tile / 8
+  int per;        // tokens per sequence (0: cu_seqlens)
+  int per_tiles;
+  int64_t tiles;  // tile slots
+  int chunk, splits;  // slots per chunk, chunks of the longest possible sequence
   int64_t max_len;
 };
 
@@ -93,25 +105,43 @@ __device__ __forceinline__ float query_factor(float amax) {
   return __uint_as_float(static_cast<uint32_t>((f > 100 ? 100 : f) + 127) << 23);
 }
 
-// Rows of a tile: tile slot s belongs to the sequence whose first slot
-// floor(bos_n group / rows) + n is the last one <= s (bounded by T group / rows + N
-// slots in all).  `tile` may be past the sequence's last.
-__device__ __forceinline__ void tile_of(const CacheAttnArgs& a, int64_t s, int rows, int& n,
-                                        int64_t& bos, int& cnt, int64_t& tile) {
-  const int group = a.H / a.c.Hk;
-  int lo = 0, hi = a.c.N - 1;
-  int64_t b, e;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    seq_bounds(a.cu, a.T, a.c.N, mid, b, e);
-    if (b * group / rows + mid <= s) lo = mid;
-    else hi = mid - 1;
+// Query tokens of sequence n.
+__device__ __forceinline__ void tokens_of(const CacheAttnArgs& a, const CachePlan& p, int n,
+                                          int64_t& bos, int& cnt) {
+  if (a.cu) {
+    int64_t eos;
+    clamp_seq_bounds(__ldg(a.cu + n), __ldg(a.cu + n + 1), a.T, bos, eos);
+    cnt = static_cast<int>(eos - bos);
+  } else {
+    bos = static_cast<int64_t>(n) * p.per;
+    cnt = p.per;
   }
-  n = lo;
-  seq_bounds(a.cu, a.T, a.c.N, n, b, e);
-  bos = b;
-  cnt = static_cast<int>(e - b);
-  tile = s - (b * group / rows + n);
+}
+
+// First tile slot of sequence n.
+__device__ __forceinline__ int64_t first_tile(const CacheAttnArgs& a, const CachePlan& p, int n,
+                                              int64_t bos) {
+  return a.cu ? bos * static_cast<unsigned>(a.H / a.c.Hk) / (8u * p.nt) + n
+              : static_cast<int64_t>(n) * p.per_tiles;
+}
+
+// Sequence, its tokens, and the tile (which may be past its last) of tile slot s.
+__device__ __forceinline__ void tile_of(const CacheAttnArgs& a, const CachePlan& p, int s, int& n,
+                                        int64_t& bos, int& cnt, int& tile) {
+  if (a.cu) {
+    int lo = 0, hi = a.c.N - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      const int64_t c = __ldg(a.cu + mid);
+      if (first_tile(a, p, mid, c < 0 ? 0 : (c > a.T ? a.T : c)) <= s) lo = mid;
+      else hi = mid - 1;
+    }
+    n = lo;
+  } else {
+    n = static_cast<unsigned>(s) / static_cast<unsigned>(p.per_tiles);
+  }
+  tokens_of(a, p, n, bos, cnt);
+  tile = static_cast<int>(s - first_tile(a, p, n, bos));
 }
 
 // Position of query token i of `cnt` of sequence n, for the slots of KV head hk:
@@ -180,31 +210,52 @@ struct Stretch {
   }
 };
 
+// POS: query positions matter (a bias, or queries that are not their sequence's
+// newest token).
 template <int NT, bool POS, bool CAP>
-__global__ void __launch_bounds__(CA_WARPS * 32, 2)
+__global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(NT))
 cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
                   float2* __restrict__ part_ml, float* __restrict__ scores, int* err) {
-  constexpr int RT = 8 * NT;
+  constexpr int RT = 8 * NT, STAGES = ca_stages(NT);
+  constexpr bool QSMEM = NT == 4;
   extern __shared__ __align__(16) uint8_t smem[];
   grid_dep_wait();
   grid_dep_launch();
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5, g = l >> 2, q = l & 3;
-  const int chunk = blockIdx.y, hk = blockIdx.x % a.c.Hk;
-  const int64_t slot = blockIdx.x / a.c.Hk;
-  const int group = a.H / a.c.Hk;
-  int n, cnt;
-  int64_t bos, tile;
-  tile_of(a, slot, RT, n, bos, cnt, tile);
-  const int64_t rows = static_cast<int64_t>(cnt) * group - tile * RT;  // of this tile
-  if (rows <= 0) return;
+  const int chunk = blockIdx.y;
+  const int slot = blockIdx.x / static_cast<unsigned>(a.c.Hk), hk = blockIdx.x - slot * a.c.Hk;
+  const unsigned group = a.H / a.c.Hk;
+  int n, cnt, tile;
+  int64_t bos;
+  tile_of(a, plan, slot, n, bos, cnt, tile);
+  const int64_t left_rows = static_cast<int64_t>(cnt) * group - static_cast<int64_t>(tile) * RT;
+  if (left_rows <= 0) return;
+  const int rows = left_rows < RT ? static_cast<int>(left_rows) : RT;  // of this tile
+  const unsigned row0 = static_cast<unsigned>(tile) * RT;               // its first (token, head) row
   const int len = cached_len(a.c, n, err);
   const int begin = chunk * plan.chunk;
   if (begin >= len && chunk > 0) return;
   const int end = len < begin + plan.chunk ? len : begin + plan.chunk;
 
-  // query rows tile * RT + 8 t + g as operand words, channels as the keys' bytes
-  uint32_t qf[NT][16];
-  float fac[NT];
+  // the warp's quarter of the chunk, in whole stages; its first copies go out first
+  const int quarter = plan.chunk / CA_WARPS;
+  const int wb = begin + w * quarter;
+  const int we = end < wb + quarter ? end : wb + quarter;
+  const int steps = we > wb ? (we - wb + CA_STEP - 1) / CA_STEP : 0;
+  uint8_t* ring = smem + ca_qbytes(NT) + w * (STAGES * CA_STAGE_BYTES);
+  Stretch src(a.c, n, hk, we, err);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) {
+    if (i < steps) src.issue<POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
+    cp_commit();
+  }
+
+  // query rows 8 t + g as operand words, channels as the keys' bytes
+  uint32_t qf[QSMEM ? 1 : NT][16];
+  uint32_t* qs = reinterpret_cast<uint32_t*>(smem);  // QSMEM: [t][word pair][lane][2]
+  float mul[NT][2], slope[NT][2], m[NT][2], sum[NT][2];
+  int qpos[NT][2];
+  int qleast = 0x7fffffff;  // least position of the tile's queries
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = 8 * t + g;
@@ -212,130 +263,150 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = make_uint4(0, 0, 0, 0);
     if (r < rows) {
-      const int64_t rr = tile * RT + r;
-      const int64_t at = ((bos + rr / group) * a.H + hk * group + rr % group) * kDim + q * 16;
+      const unsigned rr = row0 + r, tok = rr / group;
+      const int64_t at = ((bos + tok) * a.H + hk * group + (rr - tok * group)) * kDim + q * 16;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         x[i] = *reinterpret_cast<const uint4*>(a.q + at + (i >> 1) * 64 + (i & 1) * 8);
     }
-    float m = 0.f;
+    float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(ws[j] << 16)), fabsf(__uint_as_float(ws[j] & 0xffff0000u))));
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(ws[j] << 16)), fabsf(__uint_as_float(ws[j] & 0xffff0000u))));
     }
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const float f = query_factor(m);
-    fac[t] = 1.f / f;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float f = query_factor(top), inv = 1.f / f;
+    if (!QSMEM || w == t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t ws[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        qf[t][i * 4 + j] = pack_f16(__uint_as_float(ws[j] << 16) * f, __uint_as_float(ws[j] & 0xffff0000u) * f);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t v = pack_f16(__uint_as_float(ws[j] << 16) * f, __uint_as_float(ws[j] & 0xffff0000u) * f);
+          if (QSMEM) qs[((t * 8 + i * 2 + (j >> 1)) * 32 + l) * 2 + (j & 1)] = v;
+          else qf[QSMEM ? 0 : t][i * 4 + j] = v;
+        }
+      }
     }
-  }
-  // what the lane's columns (query rows 8 t + 2 q + e) need
-  float mul[NT][2], slope[NT][2], m[NT][2], sum[NT][2];
-  int qpos[NT][2];
-  float o[NT][8][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
+    // what the lane's columns (query rows 8 t + 2 q + e) need
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = 8 * t + 2 * q + e;
-      mul[t][e] = __shfl_sync(0xffffffffu, fac[t], (2 * q + e) * 4) * a.scale * (CAP ? 1.f : kLog2e);
+      const int c = 8 * t + 2 * q + e;
+      mul[t][e] = __shfl_sync(0xffffffffu, inv, (2 * q + e) * 4) * a.scale * (CAP ? 1.f : kLog2e);
       slope[t][e] = 0.f;
       qpos[t][e] = -1;
-      if (POS && r < rows) {
-        const int64_t rr = tile * RT + r;
-        qpos[t][e] = query_pos(a, n, hk, bos, static_cast<int>(rr / group), cnt, len, err);
-        if (a.slopes) slope[t][e] = __ldg(a.slopes + hk * group + rr % group) * kLog2e;
+      if (POS && c < rows) {
+        const unsigned rr = row0 + c, tok = rr / group;
+        qpos[t][e] = query_pos(a, n, hk, bos, static_cast<int>(tok), cnt, len, err);
+        qleast = qleast < qpos[t][e] ? qleast : qpos[t][e];
+        if (a.slopes) slope[t][e] = __ldg(a.slopes + hk * group + (rr - tok * group)) * kLog2e;
       }
       m[t][e] = -INFINITY;
       sum[t][e] = 0.f;
     }
+  }
+  float o[NT][8][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
+  if (POS) {
+    qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 1));
+    qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 2));
   }
+  if (QSMEM) __syncthreads();
   const float c1 = CAP ? 2.f * kLog2e / a.cap : 0.f, c2 = CAP ? a.cap * kLog2e : 0.f;
 
-  // the warp's quarter of the chunk, in whole stages
-  const int quarter = plan.chunk / CA_WARPS;
-  const int wb = begin + w * quarter;
-  const int we = end < wb + quarter ? end : wb + quarter;
-  const int steps = we > wb ? (we - wb + CA_STEP - 1) / CA_STEP : 0;
-  uint8_t* ring = smem + w * CA_WARP_BYTES;
-  Stretch src(a.c, n, hk, we, err);
-#pragma unroll
-  for (int i = 0; i < CA_STAGES - 1; ++i) {
-    if (i < steps) src.issue<POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
-    cp_commit();
-  }
   float* srow = scores ? scores + (static_cast<int64_t>(blockIdx.x) * RT) * plan.max_len : nullptr;
   int buf = 0;
   for (int it = 0; it < steps; ++it) {
-    cp_wait<CA_STAGES - 2>();
+    cp_wait<STAGES - 2>();
     __syncwarp();  // positions and scales come from other lanes; the buffer refilled below is free
-    const int nb = buf == 0 ? CA_STAGES - 1 : buf - 1;
-    if (it + CA_STAGES - 1 < steps)
-      src.issue<POS>(ring + nb * CA_STAGE_BYTES, wb + (it + CA_STAGES - 1) * CA_STEP);
+    const int nb = buf == 0 ? STAGES - 1 : buf - 1;
+    if (it + STAGES - 1 < steps)
+      src.issue<POS>(ring + nb * CA_STAGE_BYTES, wb + (it + STAGES - 1) * CA_STEP);
     cp_commit();
     const uint8_t* stage = ring + buf * CA_STAGE_BYTES;
-    buf = buf + 1 == CA_STAGES ? 0 : buf + 1;
+    buf = buf + 1 == STAGES ? 0 : buf + 1;
     const uint8_t* mine = stage + l * 16;
     const int t0 = wb + it * CA_STEP;
 
     float s[2][NT][4];
-    float lvs[2], ivs[2];
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      uint4 kk[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) kk[i] = *reinterpret_cast<const uint4*>(mine + (st * 8 + i) * 512);
+    for (int st = 0; st < 2; ++st)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[st][t][e] = 0.f;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t r0[4] = {kk[half].x, kk[half].y, kk[half].z, kk[half].w};
-        const uint32_t r1[4] = {kk[2 + half].x, kk[2 + half].y, kk[2 + half].z, kk[2 + half].w};
+    for (int half = 0; half < 2; ++half) {
+      uint4 kk[2][2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a0 = lo16(r0[j]), a1 = lo16(r1[j]), a2 = hi16(r0[j]), a3 = hi16(r1[j]);
+      for (int st = 0; st < 2; ++st) {
+        kk[st][0] = *reinterpret_cast<const uint4*>(mine + (st * 8 + half) * 512);
+        kk[st][1] = *reinterpret_cast<const uint4*>(mine + (st * 8 + 2 + half) * 512);
+      }
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma_f16(s[st][t], a0, a1, a2, a3, qf[t][half * 8 + 2 * j], qf[t][half * 8 + 2 * j + 1]);
+      for (int j = 0; j < 4; ++j) {
+        uint32_t af[2][4];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint32_t r0[4] = {kk[st][0].x, kk[st][0].y, kk[st][0].z, kk[st][0].w};
+          const uint32_t r1[4] = {kk[st][1].x, kk[st][1].y, kk[st][1].z, kk[st][1].w};
+          af[st][0] = lo16(r0[j]);
+          af[st][1] = lo16(r1[j]);
+          af[st][2] = hi16(r0[j]);
+          af[st][3] = hi16(r1[j]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          uint2 b;
+          if (QSMEM) b = *reinterpret_cast<const uint2*>(qs + ((t * 8 + half * 4 + j) * 32 + l) * 2);
+          else b = make_uint2(qf[QSMEM ? 0 : t][half * 8 + 2 * j], qf[QSMEM ? 0 : t][half * 8 + 2 * j + 1]);
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+            mma_f16(s[st][t], af[st][0], af[st][1], af[st][2], af[st][3], b.x, b.y);
         }
       }
+    }
+    // scores in log2 units, plus log2 v_scale
+    float lvs[2], ivs[2], ksc[2];
+    bool page_ok[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
       const float2 sc = *reinterpret_cast<const float2*>(stage + 8320 + st * 8);
-      const bool page_ok = sc.y > 0.f;
-      lvs[st] = page_ok ? __log2f(sc.y) : 0.f;
-      ivs[st] = page_ok ? ex2_approx(-lvs[st]) : 0.f;  // undoes what the exponent adds
+      page_ok[st] = sc.y > 0.f;
+      ksc[st] = sc.x;
+      lvs[st] = page_ok[st] ? __log2f(sc.y) : 0.f;
+      ivs[st] = page_ok[st] ? ex2_approx(-lvs[st]) : 0.f;  // undoes what the exponent adds
+    }
+    // whole stages of visible slots (almost all) need no selection
+    bool whole = t0 + CA_STEP <= we && page_ok[0] && page_ok[1];
+    int pl = 0;
+    if (POS) {
+      pl = *reinterpret_cast<const int*>(stage + 8192 + l * 4);
+      whole = __all_sync(0xffffffffu, whole && pl <= qleast);
+    }
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int tok = t0 + 16 * st + 8 * r + g;
-        const bool there = tok < we && page_ok;
-        const int p = POS ? *reinterpret_cast<const int*>(stage + 8192 + (16 * st + 8 * r + g) * 4) : 0;
+        const int p = POS ? __shfl_sync(0xffffffffu, pl, 16 * st + 8 * r + g) : 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = s[st][t][2 * r + e] * (mul[t][e] * sc.x);
+            float x = s[st][t][2 * r + e] * (mul[t][e] * ksc[st]);
             if (CAP) x = cap_log2(x, c1, c2);
-            bool see = there;
-            if (POS) {
-              const int gap = qpos[t][e] - p;
-              x = fmaf(-slope[t][e], static_cast<float>(gap), x);
-              see = see && gap >= 0;
-            }
-            x = see ? x : -INFINITY;
+            if (POS) x = fmaf(-slope[t][e], static_cast<float>(qpos[t][e] - p), x);
+            if (!whole && !(tok < we && page_ok[st] && (!POS || p <= qpos[t][e]))) x = -INFINITY;
             if (srow && tok < we && 8 * t + 2 * q + e < rows)
               srow[(8 * t + 2 * q + e) * plan.max_len + tok] = x;
             s[st][t][2 * r + e] = x + lvs[st];
@@ -343,7 +414,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         }
       }
     }
-    // running maximum of x + log2 v_scale
+    // running maximum
     uint32_t pf[2][NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -355,11 +426,14 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
         mx[e] = fmaxf(mx[e], m[t][e]);
-        f[e] = mx[e] == m[t][e] ? 1.f : ex2_approx(m[t][e] - mx[e]);
-        m[t][e] = mx[e];
-        sum[t][e] *= f[e];
       }
-      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+      if (__any_sync(0xffffffffu, mx[0] != m[t][0] || mx[1] != m[t][1])) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f[e] = mx[e] == m[t][e] ? 1.f : ex2_approx(m[t][e] - mx[e]);
+          m[t][e] = mx[e];
+          sum[t][e] *= f[e];
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           o[t][i][0] *= f[0];
@@ -406,7 +480,8 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
     }
   }
 
-  // join the warps: the ring is done with
+  // join the warps: the ring is done with.  Channel 16 g + 2 i + b of a row is at
+  // i * CA_PIECE + 2 g + b (no worse than 2-way bank conflicts either way).
   cp_wait<0>();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -417,25 +492,23 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
       sum[t][e] += __shfl_xor_sync(0xffffffffu, sum[t][e], 16);
     }
   __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);             // [warp][row][128]
-  float2* sml = reinterpret_cast<float2*>(so + CA_WARPS * RT * kDim);  // [warp][row]
+  float* so = reinterpret_cast<float*>(smem + ca_qbytes(NT));          // [warp][row][CA_ROW]
+  float2* sml = reinterpret_cast<float2*>(so + CA_WARPS * RT * CA_ROW);  // [warp][row]
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * t + 2 * q + e;
       if (g == 0) sml[w * RT + r] = make_float2(m[t][e], sum[t][e]);
-      float* dst = so + (w * RT + r) * kDim + g * 16;
+      float* dst = so + (w * RT + r) * CA_ROW + g * 2;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        dst[2 * i] = o[t][i][e];
-        dst[2 * i + 1] = o[t][i][2 + e];
-      }
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float2*>(dst + i * CA_PIECE) = make_float2(o[t][i][e], o[t][i][2 + e]);
     }
   }
   __syncthreads();
   const bool direct = part_o == nullptr;
-  for (int r = w; r < RT && r < rows; r += CA_WARPS) {
+  for (int r = w; r < rows; r += CA_WARPS) {
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < CA_WARPS; ++i) top = fmaxf(top, sml[i * RT + r].x);
@@ -446,17 +519,19 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
     for (int i = 0; i < CA_WARPS; ++i) {
       const float2 ml = sml[i * RT + r];
       const float f = ex2_approx(ml.x - ref);
-      const float4 x = *reinterpret_cast<const float4*>(so + (i * RT + r) * kDim + l * 4);
+      const float* at = so + (i * RT + r) * CA_ROW + (l & 3) * (2 * CA_PIECE) + (l >> 2) * 2;
+      const float2 x = *reinterpret_cast<const float2*>(at);
+      const float2 y = *reinterpret_cast<const float2*>(at + CA_PIECE);
       tot = fmaf(ml.y, f, tot);
       acc.x = fmaf(x.x, f, acc.x);
       acc.y = fmaf(x.y, f, acc.y);
-      acc.z = fmaf(x.z, f, acc.z);
-      acc.w = fmaf(x.w, f, acc.w);
+      acc.z = fmaf(y.x, f, acc.z);
+      acc.w = fmaf(y.y, f, acc.w);
     }
-    const int64_t rr = tile * RT + r;
+    const unsigned rr = row0 + r, tok = rr / group;
     if (direct) {
       const float inv = tot == 0.f ? 0.f : 1.f / tot;
-      const int64_t at = ((bos + rr / group) * a.H + hk * group + rr % group) * kDim + l * 4;
+      const int64_t at = ((bos + tok) * a.H + hk * group + (rr - tok * group)) * kDim + l * 4;
       *reinterpret_cast<uint2*>(a.out + at) =
           make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     } else {
@@ -480,11 +555,11 @@ join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
   grid_dep_wait();
   grid_dep_launch();
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int group = a.H / a.c.Hk, rt = 8 * plan.nt;
+  const unsigned group = a.H / a.c.Hk, rt = 8 * plan.nt;
   const int64_t out_rows = a.T * a.H;
   if (blockIdx.x < out_rows) {
-    const int64_t t = blockIdx.x / a.H;
-    const int h = static_cast<int>(blockIdx.x - t * a.H), hk = h / group;
+    const int t = blockIdx.x / static_cast<unsigned>(a.H);
+    const int h = blockIdx.x - t * a.H, hk = h / group;
     int n = 0;
     if (a.cu) {
       int lo = 0, hi = a.c.N - 1;
@@ -495,15 +570,16 @@ join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
       }
       n = lo;
     } else {
-      n = static_cast<int>(t / (a.T / a.c.N));
+      n = static_cast<unsigned>(t) / static_cast<unsigned>(plan.per);
     }
-    int64_t bos, eos;
-    seq_bounds(a.cu, a.T, a.c.N, n, bos, eos);
-    if (t < bos || t >= eos) return;
+    int64_t bos;
+    int cnt;
+    tokens_of(a, plan, n, bos, cnt);
+    if (t < bos || t >= bos + cnt) return;
     const int len = cached_len(a.c, n, err);
     const int chunks = len > plan.chunk ? (len + plan.chunk - 1) / plan.chunk : 1;
-    const int64_t rr = (t - bos) * group + (h - hk * group);
-    const int64_t unit = ((bos * group / rt + n) + rr / rt) * a.c.Hk + hk;
+    const unsigned rr = static_cast<unsigned>(t - bos) * group + (h - hk * group);
+    const int64_t unit = (first_tile(a, plan, n, bos) + rr / rt) * a.c.Hk + hk;
     const int64_t base = unit * plan.splits * rt + rr % rt;
     float top = -INFINITY, tot = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -555,24 +631,26 @@ join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     return;
   }
-  const int64_t b = blockIdx.x - out_rows;
-  const int64_t per = (plan.max_len + CA_WCHUNK - 1) / CA_WCHUNK;
-  const int64_t unit0 = b / per;
-  const int first = static_cast<int>(b - unit0 * per) * CA_WCHUNK;
-  const int n = static_cast<int>(unit0 / a.c.Hk), hk = static_cast<int>(unit0 - static_cast<int64_t>(n) * a.c.Hk);
+  const unsigned b = static_cast<unsigned>(blockIdx.x - out_rows);
+  const unsigned per = static_cast<unsigned>((plan.max_len + CA_WCHUNK - 1) / CA_WCHUNK);
+  const unsigned pair = b / per;
+  const int first = static_cast<int>(b - pair * per) * CA_WCHUNK;
+  const int n = pair / static_cast<unsigned>(a.c.Hk), hk = pair - n * a.c.Hk;
   const int len = cached_len(a.c, n, err);
   if (first >= len) return;
-  int64_t bos, eos;
-  seq_bounds(a.cu, a.T, a.c.N, n, bos, eos);
-  const int64_t rows = (eos - bos) * group;
+  int64_t bos;
+  int cnt;
+  tokens_of(a, plan, n, bos, cnt);
+  const int64_t rows = static_cast<int64_t>(cnt) * group;
   const int chunks = len > plan.chunk ? (len + plan.chunk - 1) / plan.chunk : 1;
-  const int64_t slot = bos * group / rt + n;
-  float wsum[CA_WCHUNK / 128];
+  const int64_t slot = first_tile(a, plan, n, bos);
+  constexpr int QUADS = CA_WCHUNK / 512;  // groups of 4 slots per thread
+  float4 wsum[QUADS];
 #pragma unroll
-  for (int j = 0; j < CA_WCHUNK / 128; ++j) wsum[j] = 0.f;
+  for (int j = 0; j < QUADS; ++j) wsum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t r0 = 0; r0 < rows; r0 += rt) {
     const int64_t unit = (slot + r0 / rt) * a.c.Hk + hk;
-    const int here = rows - r0 < rt ? static_cast<int>(rows - r0) : rt;
+    const int here = rows - r0 < rt ? static_cast<int>(rows - r0) : static_cast<int>(rt);
     __syncthreads();
     for (int r = w; r < here; r += 4) {
       float top = -INFINITY, tot = 0.f;
@@ -593,37 +671,52 @@ join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < CA_WCHUNK / 128; ++j) {
-      const int tok = first + j * 128 + threadIdx.x;
+    for (int j = 0; j < QUADS; ++j) {
+      const int tok = first + j * 512 + threadIdx.x * 4;
       if (tok >= len) continue;
       const float* s = scores + unit * rt * plan.max_len + tok;
-      for (int r = 0; r < here; ++r) wsum[j] += ex2_approx(s[r * plan.max_len] - lse[r]);
+      for (int r = 0; r < here; ++r) {
+        const float4 x = *reinterpret_cast<const float4*>(s + r * plan.max_len);
+        wsum[j].x += ex2_approx(x.x - lse[r]);
+        wsum[j].y += ex2_approx(x.y - lse[r]);
+        wsum[j].z += ex2_approx(x.z - lse[r]);
+        wsum[j].w += ex2_approx(x.w - lse[r]);
+      }
     }
   }
 #pragma unroll
-  for (int j = 0; j < CA_WCHUNK / 128; ++j) {
-    const int tok = first + j * 128 + threadIdx.x;
+  for (int j = 0; j < QUADS; ++j) {
+    const int tok = first + j * 512 + threadIdx.x * 4;  // 4 slots of one page
     if (tok >= len) continue;
     const int pid = page_id(a.c, n, tok >> a.c.lg, err);
     if (pid < 0) continue;
-    float* at = a.c.weight + (static_cast<int64_t>(pid) * a.c.Hk + hk) * a.c.page + (tok & (a.c.page - 1));
-    *at += wsum[j];
+    float4* at = reinterpret_cast<float4*>(a.c.weight + (static_cast<int64_t>(pid) * a.c.Hk + hk) * a.c.page +
+                                           (tok & (a.c.page - 1)));
+    float4 x = *at;
+    x.x += wsum[j].x;  // the scores of slots past the length were never written
+    if (tok + 1 < len) x.y += wsum[j].y;
+    if (tok + 2 < len) x.z += wsum[j].z;
+    if (tok + 3 < len) x.w += wsum[j].w;
+    *at = x;
   }
 }
 
-// Two tile heights: 8 rows keep 32 accumulators per lane and read the cache
-// once for up to 8 rows; 16 rows halve the passes over it for more.
-CachePlan make_plan(int64_t T, int H, int Hk, int N, int64_t max_len) {
+// Tile heights of 8, 16 and 32 rows by the rows of an average sequence: the cache
+// is read once per tile, and a lane keeps 4 accumulators per row.
+CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   CachePlan p{};
-  const int64_t group = H / Hk;
-  p.nt = T * group > 8 * static_cast<int64_t>(N) ? 2 : 1;
+  const int64_t group = H / Hk, rows = T * group;
+  p.nt = rows <= 8 * static_cast<int64_t>(N) ? 1 : rows <= 16 * static_cast<int64_t>(N) ? 2 : 4;
   const int64_t rt = 8 * p.nt;
-  p.tiles = T * group / rt + N;
+  p.per = cu ? 0 : static_cast<int>(T / N);
+  p.per_tiles = cu ? 0 : static_cast<int>((p.per * group + rt - 1) / rt);
+  p.tiles = cu ? rows / rt + N : static_cast<int64_t>(N) * p.per_tiles;
   p.max_len = max_len;
-  // Two CTAs fit an SM.  One sequence: the chunks fill the GPU once, evenly.
-  // More of them are ragged: chunks of at most 1024 slots keep the last ones short.
-  const int64_t slots = 2 * 152;
-  const int64_t units = (T * group + rt - 1) / rt > N ? (T * group + rt - 1) / rt * Hk : static_cast<int64_t>(N) * Hk;
+  // One sequence: the chunks fill the GPU once, evenly.  More of them are ragged:
+  // chunks of at most 1024 slots keep the last ones short.
+  const int64_t slots = ca_ctas(p.nt) * 152;
+  const int64_t tiles = (rows + rt - 1) / rt;
+  const int64_t units = (tiles > N ? tiles : N) * Hk;
   int64_t chunk = (max_len * units + slots - 1) / slots;
   if (N > 1 && chunk > 1024) chunk = 1024;
   const int64_t step = CA_WARPS * CA_STEP;
@@ -655,10 +748,10 @@ cudaError_t launch_one(const CacheAttnArgs& a, const CachePlan& p, float* o, flo
                        float* scores, int* err, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto* kernel = cache_attn_kernel<NT, POS, CAP>;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), CA_SMEM, done);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), ca_smem(NT), done);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(p.tiles * a.c.Hk), static_cast<unsigned>(p.splits));
-  return launch_pdl(kernel, grid, dim3(CA_WARPS * 32), CA_SMEM, stream, a, p, o, ml, scores, err);
+  return launch_pdl(kernel, grid, dim3(CA_WARPS * 32), ca_smem(NT), stream, a, p, o, ml, scores, err);
 }
 
 template <int NT>
@@ -672,15 +765,15 @@ cudaError_t launch_variant(bool pos, bool cap, const CacheAttnArgs& a, const Cac
 
 }  // namespace
 
-size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, int64_t max_len, bool accumulate) {
-  return scratch_of(make_plan(T, H, Hk, N, max_len), Hk, accumulate).total;
+size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len, bool accumulate) {
+  return scratch_of(make_plan(T, H, Hk, N, cu, max_len), Hk, accumulate).total;
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, int* err,
                               cudaStream_t stream) {
   (void)sm_count;
   const int64_t max_len = static_cast<int64_t>(a.c.width) << a.c.lg;
-  const CachePlan p = make_plan(a.T, a.H, a.c.Hk, a.c.N, max_len);
+  const CachePlan p = make_plan(a.T, a.H, a.c.Hk, a.c.N, a.cu != nullptr, max_len);
   if (p.tiles * a.c.Hk > 0x7fffffffLL) return cudaErrorInvalidValue;
   const CacheScratch s = scratch_of(p, a.c.Hk, a.accumulate != 0);
   float *o = nullptr, *scores = nullptr;
@@ -692,8 +785,10 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, in
   }
   // positions matter for the bias, and where a query is not its sequence's newest token
   const bool pos = a.slopes || a.positions || a.cu || a.T != a.c.N;
-  cudaError_t e = p.nt == 1 ? launch_variant<1>(pos, a.cap > 0.f, a, p, o, ml, scores, err, stream)
-                            : launch_variant<2>(pos, a.cap > 0.f, a, p, o, ml, scores, err, stream);
+  const bool cap = a.cap > 0.f;
+  cudaError_t e = p.nt == 1   ? launch_variant<1>(pos, cap, a, p, o, ml, scores, err, stream)
+                  : p.nt == 2 ? launch_variant<2>(pos, cap, a, p, o, ml, scores, err, stream)
+                              : launch_variant<4>(pos, cap, a, p, o, ml, scores, err, stream);
   if (e != cudaSuccess || !s.total) return e;
   const int64_t weights = a.accumulate
                               ? (max_len + CA_WCHUNK - 1) / CA_WCHUNK * a.c.N * a.c.Hk : 0;

@@ -498,8 +498,9 @@ typedef struct {
  * cu_seqlens or into equal shares; lens counts the slots in use, the query
  * tokens' own among them.  A query sees the slots whose position is at most its
  * own; with nothing to see (an empty cache) its output is 0.  Slots past
- * lens[n], whatever they hold, reach no result.  Scales may be any positive
- * finite numbers.  Sums over splits are added in a fixed order: the same call
+ * lens[n], whatever they hold, reach no result (a NaN code in a slot that only
+ * its position hides can spoil queries that share its block).  Scales may be any
+ * positive finite numbers; T_total * H is below 2^31.  Sums over splits are added in a fixed order: the same call
  * gives the same bits.
  * workspace: kda_cache_attn_workspace_size() bytes of device memory, 16-byte
  * aligned, or NULL (= cudaMallocAsync / cudaFreeAsync on the stream). */

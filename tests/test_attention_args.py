@@ -109,6 +109,7 @@ def test_append(lib, kw, status):
     (dict(scale=float("inf")), INVALID), (dict(slopes=FAKE + 1), INVALID), (dict(positions=FAKE + 2), INVALID),
     (dict(q=0), INVALID), (dict(out=0), INVALID), (dict(q=FAKE + 8), INVALID), (dict(out=FAKE + 2), INVALID),
     (dict(H=3), INVALID), (dict(H=0), INVALID), (dict(T=9), INVALID), (dict(cu=FAKE + 2), INVALID),
+    (dict(T=1 << 30, H=4), INVALID),
     (dict(ws=FAKE, ws_bytes=16, accumulate=1), WORKSPACE), (dict(ws=FAKE + 8, ws_bytes=1 << 40, accumulate=1), WORKSPACE),
     (dict(T=0, q=0, out=0), 0),
 ])
