@@ -20,9 +20,10 @@
 //   power of two to [2^14, 2^15) (exact in fp16 but for channels below 2^-38 of
 //   the row's largest); P^T goes from accumulator to operand by movmatrix.
 // Softmax.  Block scales: x = acc * (k_scale * scale / fq); the value scale joins
-//   the exponent, p' = 2^(x + log2 v_scale - m) with m the running maximum of
-//   x + log2 v_scale, so p' <= 1 whatever the scales are and its fp16 rounding
-//   (2^-12) is the only one before the output's; the denominator sums p' / v_scale.
+//   the exponent, p' = 2^(x + log2 v_scale - m) with m within 2^6 of the running
+//   maximum of x + log2 v_scale, so p' <= 2^6 whatever the scales are and its fp16
+//   rounding (2^-12) is the only one before the output's; the denominator sums
+//   p' / v_scale.
 #include "kda_attn.cuh"
 
 namespace kda {
@@ -62,6 +63,9 @@ __device__ __forceinline__ void cp16(void* dst, const void* src, bool there) {
                "r"(there ? 16 : 0)
                : "memory");
 }
+__device__ __forceinline__ void cp16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp4(void* dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
                "r"(there ? 4 : 0)
@@ -88,8 +92,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t lo16(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w)); }
-__device__ __forceinline__ uint32_t hi16(uint32_t w) { return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16)); }
+// Four e4m3 codes -> two words of two fp16 values (exact).
+__device__ __forceinline__ void unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -144,16 +155,13 @@ __device__ __forceinline__ void tile_of(const CacheAttnArgs& a, const CachePlan&
   tile = static_cast<int>(s - first_tile(a, p, n, bos));
 }
 
-// Position of query token i of `cnt` of sequence n, for the slots of KV head hk:
-// given, or counted back from the newest slot.
-__device__ __forceinline__ int query_pos(const CacheAttnArgs& a, int n, int hk, int64_t bos, int i,
-                                         int cnt, int len, int* err) {
-  if (a.positions) return __ldg(a.positions + bos + i);
+// Position of the newest slot, for the slots of KV head hk.
+__device__ __forceinline__ int newest_pos(const CacheAttnArgs& a, int n, int hk, int len, int* err) {
   if (len == 0) return 0;
   const int pid = page_id(a.c, n, (len - 1) >> a.c.lg, err);
   if (pid < 0) return 0;
   const int64_t b = static_cast<int64_t>(pid) * a.c.Hk + hk;
-  return a.c.pos[b * a.c.page + ((len - 1) & (a.c.page - 1))] - (cnt - 1 - i);
+  return a.c.pos[b * a.c.page + ((len - 1) & (a.c.page - 1))];
 }
 
 // A warp's view of its stretch [begin, end) of a sequence's slots.
@@ -192,15 +200,21 @@ struct Stretch {
       const int left = pid < 0 ? 0 : end - tb;  // slots of the 16 that exist
       const uint8_t* kp = c.k + row * kDim + q * 16;
       const uint8_t* vp = c.v + row * kDim + g * 16;
+      // key rows g and g + 8, channels 16 q .. and 64 + 16 q ..; value rows 2 q,
+      // 2 q + 1, 2 q + 8 and 2 q + 9, channels 16 g ..
+      if (left >= 16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // key rows g and g + 8, channels 16 q .. and 64 + 16 q ..
-        const int r = g + 8 * (i >> 1);
-        cp16(mine + (st * 8 + i) * 512, kp + r * kDim + (i & 1) * 64, r < left);
-      }
+        for (int i = 0; i < 4; ++i) {
+          cp16(mine + (st * 8 + i) * 512, kp + (g + 8 * (i >> 1)) * kDim + (i & 1) * 64);
+          cp16(mine + (st * 8 + 4 + i) * 512, vp + (2 * q + (i & 1) + 8 * (i >> 1)) * kDim);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // value rows 2 q, 2 q + 1, 2 q + 8, 2 q + 9, channels 16 g ..
-        const int r = 2 * q + (i & 1) + 8 * (i >> 1);
-        cp16(mine + (st * 8 + 4 + i) * 512, vp + r * kDim, r < left);
+        for (int i = 0; i < 4; ++i) {
+          const int kr = g + 8 * (i >> 1), vr = 2 * q + (i & 1) + 8 * (i >> 1);
+          cp16(mine + (st * 8 + i) * 512, kp + kr * kDim + (i & 1) * 64, kr < left);
+          cp16(mine + (st * 8 + 4 + i) * 512, vp + vr * kDim, vr < left);
+        }
       }
       if (POS && (l >> 4) == st)
         cp4(stage + 8192 + l * 4, c.pos + row + (l & 15), (l & 15) < left);
@@ -233,12 +247,16 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
   const int rows = left_rows < RT ? static_cast<int>(left_rows) : RT;  // of this tile
   const unsigned row0 = static_cast<unsigned>(tile) * RT;               // its first (token, head) row
   const int len = cached_len(a.c, n, err);
-  const int begin = chunk * plan.chunk;
-  if (begin >= len && chunk > 0) return;
-  const int end = len < begin + plan.chunk ? len : begin + plan.chunk;
+  // the sequence's chunks are equal, in steps of 128 slots, and so are the warps' shares
+  const int chunks = len > plan.chunk ? (len + plan.chunk - 1) / plan.chunk : 1;
+  if (chunk >= chunks) return;
+  constexpr int WHOLE = CA_WARPS * CA_STEP;
+  const int size = ((len + chunks - 1) / chunks + WHOLE - 1) / WHOLE * WHOLE;
+  const int begin = len < chunk * size ? len : chunk * size;
+  const int end = len - begin < size ? len : begin + size;
 
-  // the warp's quarter of the chunk, in whole stages; its first copies go out first
-  const int quarter = plan.chunk / CA_WARPS;
+  // the warp's quarter of the chunk; its first copies go out first
+  const int quarter = (end - begin + WHOLE - 1) / WHOLE * CA_STEP;
   const int wb = begin + w * quarter;
   const int we = end < wb + quarter ? end : wb + quarter;
   const int steps = we > wb ? (we - wb + CA_STEP - 1) / CA_STEP : 0;
@@ -256,6 +274,8 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
   float mul[NT][2], slope[NT][2], m[NT][2], sum[NT][2];
   int qpos[NT][2];
   int qleast = 0x7fffffff;  // least position of the tile's queries
+  // without given positions the queries are the newest tokens
+  const int newest = POS && !a.positions ? newest_pos(a, n, hk, len, err) : 0;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int r = 8 * t + g;
@@ -301,7 +321,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
       qpos[t][e] = -1;
       if (POS && c < rows) {
         const unsigned rr = row0 + c, tok = rr / group;
-        qpos[t][e] = query_pos(a, n, hk, bos, static_cast<int>(tok), cnt, len, err);
+        qpos[t][e] = a.positions ? __ldg(a.positions + bos + tok) : newest - (cnt - 1 - static_cast<int>(tok));
         qleast = qleast < qpos[t][e] ? qleast : qpos[t][e];
         if (a.slopes) slope[t][e] = __ldg(a.slopes + hk * group + (rr - tok * group)) * kLog2e;
       }
@@ -320,6 +340,11 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
     qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 1));
     qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 2));
   }
+  float qfar[NT][2];  // positions relative to that
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) qfar[t][e] = POS ? static_cast<float>(qpos[t][e] - qleast) : 0.f;
   if (QSMEM) __syncthreads();
   const float c1 = CAP ? 2.f * kLog2e / a.cap : 0.f, c2 = CAP ? a.cap * kLog2e : 0.f;
 
@@ -359,10 +384,8 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         for (int st = 0; st < 2; ++st) {
           const uint32_t r0[4] = {kk[st][0].x, kk[st][0].y, kk[st][0].z, kk[st][0].w};
           const uint32_t r1[4] = {kk[st][1].x, kk[st][1].y, kk[st][1].z, kk[st][1].w};
-          af[st][0] = lo16(r0[j]);
-          af[st][1] = lo16(r1[j]);
-          af[st][2] = hi16(r0[j]);
-          af[st][3] = hi16(r1[j]);
+          unpack4(r0[j], af[st][0], af[st][2]);
+          unpack4(r1[j], af[st][1], af[st][3]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -393,26 +416,63 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
       pl = *reinterpret_cast<const int*>(stage + 8192 + l * 4);
       whole = __all_sync(0xffffffffu, whole && pl <= qleast);
     }
+    const bool bias = POS && a.slopes != nullptr;
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
+    for (int st = 0; st < 2; ++st)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int tok = t0 + 16 * st + 8 * r + g;
-        const int p = POS ? __shfl_sync(0xffffffffu, pl, 16 * st + 8 * r + g) : 0;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int e = 0; e < 2; ++e) {
+          const float f = mul[t][e] * ksc[st];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = s[st][t][2 * r + e] * (mul[t][e] * ksc[st]);
-            if (CAP) x = cap_log2(x, c1, c2);
-            if (POS) x = fmaf(-slope[t][e], static_cast<float>(qpos[t][e] - p), x);
-            if (!whole && !(tok < we && page_ok[st] && (!POS || p <= qpos[t][e]))) x = -INFINITY;
-            if (srow && tok < we && 8 * t + 2 * q + e < rows)
-              srow[(8 * t + 2 * q + e) * plan.max_len + tok] = x;
-            s[st][t][2 * r + e] = x + lvs[st];
+          for (int r = 0; r < 2; ++r) {
+            float& x = s[st][t][2 * r + e];
+            x = CAP ? cap_log2(x * f, c1, c2) + lvs[st] : fmaf(x, f, lvs[st]);
           }
         }
-      }
+    if (bias) {
+      const float far = static_cast<float>(pl - qleast);
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p = __shfl_sync(0xffffffffu, far, 16 * st + 8 * r + g);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              s[st][t][2 * r + e] = fmaf(-slope[t][e], qfar[t][e] - p, s[st][t][2 * r + e]);
+        }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int p = POS ? __shfl_sync(0xffffffffu, pl, 16 * st + 8 * r + g) : 0;
+          const bool there = t0 + 16 * st + 8 * r + g < we && page_ok[st];
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!there || (POS && p > qpos[t][e])) s[st][t][2 * r + e] = -INFINITY;
+        }
+    }
+    if (srow) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int tok = t0 + 16 * st + 8 * r + g;
+          if (tok < we) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (8 * t + 2 * q + e < rows)
+                  srow[(8 * t + 2 * q + e) * plan.max_len + tok] = s[st][t][2 * r + e] - lvs[st];
+          }
+        }
     }
     // running maximum
     uint32_t pf[2][NT][2];
@@ -425,15 +485,17 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
-        mx[e] = fmaxf(mx[e], m[t][e]);
       }
-      if (__any_sync(0xffffffffu, mx[0] != m[t][0] || mx[1] != m[t][1])) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f[e] = mx[e] == m[t][e] ? 1.f : ex2_approx(m[t][e] - mx[e]);
-          m[t][e] = mx[e];
-          sum[t][e] *= f[e];
-        }
+      // the reference moves only when the maximum outgrows it by 2^6: p' stays in
+      // fp16's range, and its rounding below 2^-25 of the largest weight
+      const bool g0 = mx[0] > m[t][0] + 6.f, g1 = mx[1] > m[t][1] + 6.f;
+      if (__any_sync(0xffffffffu, g0 || g1)) {
+        f[0] = g0 ? ex2_approx(m[t][0] - mx[0]) : 1.f;
+        f[1] = g1 ? ex2_approx(m[t][1] - mx[1]) : 1.f;
+        if (g0) m[t][0] = mx[0];
+        if (g1) m[t][1] = mx[1];
+        sum[t][0] *= f[0];
+        sum[t][1] *= f[1];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           o[t][i][0] *= f[0];
@@ -471,7 +533,9 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
           // bytes 2 half, 2 half + 1 of the rows' words, interleaved
           const uint32_t x = __byte_perm(v[0][j], v[1][j], half ? 0x7362 : 0x5140);
           const uint32_t y = __byte_perm(v[2][j], v[3][j], half ? 0x7362 : 0x5140);
-          const uint32_t a0 = lo16(x), a1 = hi16(x), a2 = lo16(y), a3 = hi16(y);
+          uint32_t a0, a1, a2, a3;
+          unpack4(x, a0, a1);
+          unpack4(y, a2, a3);
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             mma_f16(o[t][2 * j + half], a0, a1, a2, a3, pf[st][t][0], pf[st][t][1]);
@@ -542,12 +606,13 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
   }
 }
 
-// Joins the chunks.  The first T H CTAs take one output row each: 4 warps over
-// the row's chunks, then over the warps, in a fixed order.  With `scores` the
-// other CTAs add the weights of 512 slots of a (sequence, KV head) each, the rows
-// in order; a row's denominator they work out again from the chunks' pairs.
+// Joins the chunks.  The first CTAs take output rows: 4 each, a warp a row, or
+// (plan.splits > 16) one each, 4 warps over its chunks; always in a fixed order.
+// With `scores` the other CTAs add the weights of 2048 slots of a (sequence, KV
+// head) each, the rows in order; a row's denominator they work out again from the
+// chunks' pairs.
 __global__ void __launch_bounds__(128)
-join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
+join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __restrict__ part_o,
             const float2* __restrict__ part_ml, const float* __restrict__ scores, int* err) {
   __shared__ float so[4][kDim];
   __shared__ float2 sml[4];
@@ -556,10 +621,12 @@ join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
   grid_dep_launch();
   const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned group = a.H / a.c.Hk, rt = 8 * plan.nt;
-  const int64_t out_rows = a.T * a.H;
-  if (blockIdx.x < out_rows) {
-    const int t = blockIdx.x / static_cast<unsigned>(a.H);
-    const int h = blockIdx.x - t * a.H, hk = h / group;
+  if (blockIdx.x < row_ctas) {
+    const bool spread = plan.splits > 16;
+    const unsigned row = spread ? blockIdx.x : blockIdx.x * 4 + w;
+    const int t = row / static_cast<unsigned>(a.H);
+    const int h = row - t * a.H, hk = h / group;
+    if (t >= a.T) return;  // a whole warp, or the whole CTA
     int n = 0;
     if (a.cu) {
       int lo = 0, hi = a.c.N - 1;
@@ -581,57 +648,67 @@ join_kernel(CacheAttnArgs a, CachePlan plan, const float* __restrict__ part_o,
     const unsigned rr = static_cast<unsigned>(t - bos) * group + (h - hk * group);
     const int64_t unit = (first_tile(a, plan, n, bos) + rr / rt) * a.c.Hk + hk;
     const int64_t base = unit * plan.splits * rt + rr % rt;
+    const int stride = spread ? 4 : 1;
     float top = -INFINITY, tot = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = w; c0 < chunks; c0 += 16) {
+    for (int c0 = spread ? w : 0; c0 < chunks; c0 += 4 * stride) {
       float2 ml[4];
       float4 x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         ml[i] = make_float2(-INFINITY, 0.f);
         x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c0 + 4 * i < chunks) {
-          const int64_t at = base + static_cast<int64_t>(c0 + 4 * i) * rt;
+        if (c0 + stride * i < chunks) {
+          const int64_t at = base + static_cast<int64_t>(c0 + stride * i) * rt;
           ml[i] = part_ml[at];
           x[i] = *reinterpret_cast<const float4*>(part_o + at * kDim + l * 4);
         }
       }
+      const float mn = fmaxf(fmaxf(fmaxf(top, ml[0].x), ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2_approx(top - ref);
+      top = mn;
+      tot *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float mn = fmaxf(top, ml[i].x), ref = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2_approx(top - ref), e = ex2_approx(ml[i].x - ref);
-        top = mn;
-        tot = tot * f + ml[i].y * e;
-        acc.x = acc.x * f + x[i].x * e;
-        acc.y = acc.y * f + x[i].y * e;
-        acc.z = acc.z * f + x[i].z * e;
-        acc.w = acc.w * f + x[i].w * e;
+        const float e = ex2_approx(ml[i].x - ref);
+        tot = fmaf(ml[i].y, e, tot);
+        acc.x = fmaf(x[i].x, e, acc.x);
+        acc.y = fmaf(x[i].y, e, acc.y);
+        acc.z = fmaf(x[i].z, e, acc.z);
+        acc.w = fmaf(x[i].w, e, acc.w);
       }
     }
-    *reinterpret_cast<float4*>(&so[w][l * 4]) = acc;
-    if (l == 0) sml[w] = make_float2(top, tot);
-    __syncthreads();
-    if (w != 0) return;
-    top = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
-    const float ref = top == -INFINITY ? 0.f : top;
-    tot = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (spread) {
+      *reinterpret_cast<float4*>(&so[w][l * 4]) = acc;
+      if (l == 0) sml[w] = make_float2(top, tot);
+      __syncthreads();
+      if (w != 0) return;
+      top = fmaxf(fmaxf(sml[0].x, sml[1].x), fmaxf(sml[2].x, sml[3].x));
+      const float ref = top == -INFINITY ? 0.f : top;
+      tot = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float e = ex2_approx(sml[i].x - ref);
-      const float4 x = *reinterpret_cast<const float4*>(&so[i][l * 4]);
-      tot = fmaf(sml[i].y, e, tot);
-      acc.x = fmaf(x.x, e, acc.x);
-      acc.y = fmaf(x.y, e, acc.y);
-      acc.z = fmaf(x.z, e, acc.z);
-      acc.w = fmaf(x.w, e, acc.w);
+      for (int i = 0; i < 4; ++i) {
+        const float e = ex2_approx(sml[i].x - ref);
+        const float4 x = *reinterpret_cast<const float4*>(&so[i][l * 4]);
+        tot = fmaf(sml[i].y, e, tot);
+        acc.x = fmaf(x.x, e, acc.x);
+        acc.y = fmaf(x.y, e, acc.y);
+        acc.z = fmaf(x.z, e, acc.z);
+        acc.w = fmaf(x.w, e, acc.w);
+      }
     }
     const float inv = tot == 0.f ? 0.f : 1.f / tot;
-    *reinterpret_cast<uint2*>(a.out + (t * a.H + h) * kDim + l * 4) =
+    *reinterpret_cast<uint2*>(a.out + static_cast<int64_t>(row) * kDim + l * 4) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     return;
   }
-  const unsigned b = static_cast<unsigned>(blockIdx.x - out_rows);
+  const unsigned b = static_cast<unsigned>(blockIdx.x - row_ctas);
   const unsigned per = static_cast<unsigned>((plan.max_len + CA_WCHUNK - 1) / CA_WCHUNK);
   const unsigned pair = b / per;
   const int first = static_cast<int>(b - pair * per) * CA_WCHUNK;
@@ -792,11 +869,12 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, in
   if (e != cudaSuccess || !s.total) return e;
   const int64_t weights = a.accumulate
                               ? (max_len + CA_WCHUNK - 1) / CA_WCHUNK * a.c.N * a.c.Hk : 0;
-  const int64_t blocks = a.T * a.H + weights;
+  const int64_t rows = a.T * a.H, row_ctas = p.splits > 16 ? rows : (rows + 3) / 4;
+  const int64_t blocks = row_ctas + weights;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, a, p,
-                    static_cast<const float*>(o), static_cast<const float2*>(ml),
-                    static_cast<const float*>(scores), err);
+                    static_cast<unsigned>(row_ctas), static_cast<const float*>(o),
+                    static_cast<const float2*>(ml), static_cast<const float*>(scores), err);
 }
 
 }  // namespace kda
