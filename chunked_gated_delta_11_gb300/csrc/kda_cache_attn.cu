@@ -9,7 +9,8 @@
 //   warps, a quarter of the chunk each), and joined afterwards.
 // Loads.  Every lane copies (cp.async, 16 bytes) just the codes that it will
 //   feed to the tensor core itself, into a ring of its warp: no lane waits for
-//   another, and 3 stages of 32 slots keep up to 16 KB per warp in flight.
+//   another.  A stage is 32 slots; its keys are refilled as soon as they are in
+//   registers, its values at the end, so three quarters of the ring is in flight.
 //   Slots past the end arrive as zeros, so what they hold reaches nothing.
 // Products.  e4m3 codes are exact in fp16, so both products run on fp16
 //   mma.m16n8k16 with fp32 sums, the slots as its M side (S^T = K Q^T) and then
@@ -79,7 +80,7 @@ __device__ __forceinline__ void cp_wait() {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -88,7 +89,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 
@@ -185,8 +186,9 @@ struct Stretch {
     return __shfl_sync(0xffffffffu, ids, j - window);
   }
 
-  // Issues the copies of slots [t0, t0 + 32) into `stage`.
-  template <bool POS>
+  // Issues the copies of slots [t0, t0 + 32) into `stage`: the keys (with the
+  // positions and both scales), or the values.
+  template <bool VALUES, bool POS>
   __device__ void issue(uint8_t* stage, int t0) {
     const int l = threadIdx.x & 31, g = l >> 2, q = l & 3;
     uint8_t* mine = stage + l * 16;
@@ -195,27 +197,20 @@ struct Stretch {
       const int tb = t0 + 16 * st;
       const int pid = tb < end ? page_of(tb) : -1;
       const int64_t block = static_cast<int64_t>(pid < 0 ? 0 : pid) * c.Hk + hk;
-      const int in = tb & (c.page - 1);
-      const int64_t row = block * c.page + in;  // 16 slots of one page
-      const int left = pid < 0 ? 0 : end - tb;  // slots of the 16 that exist
-      const uint8_t* kp = c.k + row * kDim + q * 16;
-      const uint8_t* vp = c.v + row * kDim + g * 16;
+      const int64_t row = block * c.page + (tb & (c.page - 1));  // 16 slots of one page
+      const int left = pid < 0 ? 0 : end - tb;                   // slots of the 16 that exist
       // key rows g and g + 8, channels 16 q .. and 64 + 16 q ..; value rows 2 q,
       // 2 q + 1, 2 q + 8 and 2 q + 9, channels 16 g ..
-      if (left >= 16) {
+      const uint8_t* from = (VALUES ? c.v + g * 16 : c.k + q * 16) + row * kDim;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cp16(mine + (st * 8 + i) * 512, kp + (g + 8 * (i >> 1)) * kDim + (i & 1) * 64);
-          cp16(mine + (st * 8 + 4 + i) * 512, vp + (2 * q + (i & 1) + 8 * (i >> 1)) * kDim);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int kr = g + 8 * (i >> 1), vr = 2 * q + (i & 1) + 8 * (i >> 1);
-          cp16(mine + (st * 8 + i) * 512, kp + kr * kDim + (i & 1) * 64, kr < left);
-          cp16(mine + (st * 8 + 4 + i) * 512, vp + vr * kDim, vr < left);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int r = VALUES ? 2 * q + (i & 1) + 8 * (i >> 1) : g + 8 * (i >> 1);
+        const uint8_t* at = from + r * kDim + (VALUES ? 0 : (i & 1) * 64);
+        uint8_t* to = mine + (VALUES ? 4096 : 0) + (st * 4 + i) * 512;
+        if (left >= 16) cp16(to, at);
+        else cp16(to, at, r < left);
       }
+      if (VALUES) continue;
       if (POS && (l >> 4) == st)
         cp4(stage + 8192 + l * 4, c.pos + row + (l & 15), (l & 15) < left);
       if (l == st * 2) cp4(stage + 8320 + st * 8, c.ks + block, left > 0);
@@ -263,8 +258,10 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
   uint8_t* ring = smem + ca_qbytes(NT) + w * (STAGES * CA_STAGE_BYTES);
   Stretch src(a.c, n, hk, we, err);
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) {
-    if (i < steps) src.issue<POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
+  for (int i = 0; i < STAGES; ++i) {
+    if (i < steps) src.issue<false, POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
+    cp_commit();
+    if (i < steps) src.issue<true, POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
     cp_commit();
   }
 
@@ -351,13 +348,11 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
   float* srow = scores ? scores + (static_cast<int64_t>(blockIdx.x) * RT) * plan.max_len : nullptr;
   int buf = 0;
   for (int it = 0; it < steps; ++it) {
-    cp_wait<STAGES - 2>();
-    __syncwarp();  // positions and scales come from other lanes; the buffer refilled below is free
-    const int nb = buf == 0 ? STAGES - 1 : buf - 1;
-    if (it + STAGES - 1 < steps)
-      src.issue<POS>(ring + nb * CA_STAGE_BYTES, wb + (it + STAGES - 1) * CA_STEP);
-    cp_commit();
-    const uint8_t* stage = ring + buf * CA_STAGE_BYTES;
+    // one group for the keys and one for the values of each stage: 2 STAGES - 1
+    // younger ones may be in flight
+    cp_wait<2 * STAGES - 1>();
+    __syncwarp();  // positions and scales come from other lanes
+    uint8_t* stage = ring + buf * CA_STAGE_BYTES;
     buf = buf + 1 == STAGES ? 0 : buf + 1;
     const uint8_t* mine = stage + l * 16;
     const int t0 = wb + it * CA_STEP;
@@ -374,8 +369,8 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
       uint4 kk[2][2];
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        kk[st][0] = *reinterpret_cast<const uint4*>(mine + (st * 8 + half) * 512);
-        kk[st][1] = *reinterpret_cast<const uint4*>(mine + (st * 8 + 2 + half) * 512);
+        kk[st][0] = *reinterpret_cast<const uint4*>(mine + (st * 4 + half) * 512);
+        kk[st][1] = *reinterpret_cast<const uint4*>(mine + (st * 4 + 2 + half) * 512);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -416,6 +411,10 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
       pl = *reinterpret_cast<const int*>(stage + 8192 + l * 4);
       whole = __all_sync(0xffffffffu, whole && pl <= qleast);
     }
+    // the keys have been read by every lane: refill them while the rest goes on
+    __syncwarp();
+    if (it + STAGES < steps) src.issue<false, POS>(stage, t0 + STAGES * CA_STEP);
+    cp_commit();
     const bool bias = POS && a.slopes != nullptr;
 #pragma unroll
     for (int st = 0; st < 2; ++st)
@@ -515,12 +514,13 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         pf[st][t][1] = transpose8x8(pack_f16(p2, p3));
       }
     }
+    cp_wait<2 * STAGES - 1>();
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       uint32_t v[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(mine + (st * 8 + 4 + i) * 512);
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + 4096 + (st * 4 + i) * 512);
         v[i][0] = x.x;
         v[i][1] = x.y;
         v[i][2] = x.z;
@@ -542,6 +542,8 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         }
       }
     }
+    if (it + STAGES < steps) src.issue<true, POS>(stage, t0 + STAGES * CA_STEP);
+    cp_commit();
   }
 
   // join the warps: the ring is done with.  Channel 16 g + 2 i + b of a row is at
@@ -790,12 +792,12 @@ CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   p.tiles = cu ? rows / rt + N : static_cast<int64_t>(N) * p.per_tiles;
   p.max_len = max_len;
   // One sequence: the chunks fill the GPU once, evenly.  More of them are ragged:
-  // chunks of at most 1024 slots keep the last ones short.
+  // chunks of at most 2048 slots keep the last ones short.
   const int64_t slots = ca_ctas(p.nt) * 152;
   const int64_t tiles = (rows + rt - 1) / rt;
   const int64_t units = (tiles > N ? tiles : N) * Hk;
   int64_t chunk = (max_len * units + slots - 1) / slots;
-  if (N > 1 && chunk > 1024) chunk = 1024;
+  if (N > 1 && chunk > 2048) chunk = 2048;
   const int64_t step = CA_WARPS * CA_STEP;
   chunk = (chunk + step - 1) / step * step;
   const int64_t least = (max_len + 65534) / 65535;  // grid.y
