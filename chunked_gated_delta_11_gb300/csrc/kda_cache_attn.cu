@@ -7,11 +7,10 @@
 // Work.  A unit is (sequence, KV head, tile of 8 NT query rows); a row is a
 //   (token, head of the group).  Its slots are cut into chunks, one CTA each (4
 //   warps, a quarter of the chunk each), and joined afterwards.
-// Loads.  Every lane copies (cp.async, 16 bytes) just the codes that it will
-//   feed to the tensor core itself, into a ring of its warp: no lane waits for
-//   another.  A stage is 32 slots; its keys are refilled as soon as they are in
-//   registers, its values at the end, so three quarters of the ring is in flight.
-//   Slots past the end arrive as zeros, so what they hold reaches nothing.
+// Loads.  cp.async, 16 bytes a lane, into a ring of the warp's own: no warp waits
+//   for another.  A stage is 32 slots; its keys are refilled as soon as they are
+//   in registers, its values at the end, so three quarters of the ring is in
+//   flight.  Slots past the end arrive as zeros, so what they hold reaches nothing.
 // Products.  e4m3 codes are exact in fp16, so both products run on fp16
 //   mma.m16n8k16 with fp32 sums, the slots as its M side (S^T = K Q^T) and then
 //   its K side (O^T = V^T P^T): 8 query rows fill the N side, where rows as M
@@ -172,6 +171,9 @@ struct Stretch {
   int window;  // first table column that the lanes hold
   int ids;     // this lane's page id (-1: none)
   int* err;
+  int pid[2], left[2];  // of the located slots: pages, and how many of each 16 exist (may be more)
+  int64_t row[2];
+  bool whole;
 
   __device__ Stretch(const CacheArgs& cc, int n_, int hk_, int end_, int* e)
       : c(cc), n(n_), hk(hk_), end(end_), window(-64), ids(-1), err(e) {}
@@ -186,36 +188,55 @@ struct Stretch {
     return __shfl_sync(0xffffffffu, ids, j - window);
   }
 
-  // Issues the copies of slots [t0, t0 + 32) into `stage`: the keys (with the
-  // positions and both scales), or the values.
-  template <bool VALUES, bool POS>
-  __device__ void issue(uint8_t* stage, int t0) {
-    const int l = threadIdx.x & 31, g = l >> 2, q = l & 3;
-    uint8_t* mine = stage + l * 16;
+  // Finds the slots [t0, t0 + 32): their two blocks, or block 0 and nothing left.
+  __device__ __forceinline__ void locate(int t0) {
+    pid[0] = page_of(t0);
+    pid[1] = c.lg > 4 || t0 + 16 >= end ? pid[0] : page_of(t0 + 16);
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
-      const int tb = t0 + 16 * st;
-      const int pid = tb < end ? page_of(tb) : -1;
-      const int64_t block = static_cast<int64_t>(pid < 0 ? 0 : pid) * c.Hk + hk;
-      const int64_t row = block * c.page + (tb & (c.page - 1));  // 16 slots of one page
-      const int left = pid < 0 ? 0 : end - tb;                   // slots of the 16 that exist
-      // key rows g and g + 8, channels 16 q .. and 64 + 16 q ..; value rows 2 q,
-      // 2 q + 1, 2 q + 8 and 2 q + 9, channels 16 g ..
-      const uint8_t* from = (VALUES ? c.v + g * 16 : c.k + q * 16) + row * kDim;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = VALUES ? 2 * q + (i & 1) + 8 * (i >> 1) : g + 8 * (i >> 1);
-        const uint8_t* at = from + r * kDim + (VALUES ? 0 : (i & 1) * 64);
-        uint8_t* to = mine + (VALUES ? 4096 : 0) + (st * 4 + i) * 512;
-        if (left >= 16) cp16(to, at);
-        else cp16(to, at, r < left);
-      }
-      if (VALUES) continue;
-      if (POS && (l >> 4) == st)
-        cp4(stage + 8192 + l * 4, c.pos + row + (l & 15), (l & 15) < left);
-      if (l == st * 2) cp4(stage + 8320 + st * 8, c.ks + block, left > 0);
-      if (l == st * 2 + 1) cp4(stage + 8324 + st * 8, c.vs + block, left > 0);
+      left[st] = pid[st] < 0 ? 0 : end - t0 - 16 * st;
+      const int64_t block = static_cast<int64_t>(pid[st] < 0 ? 0 : pid[st]) * c.Hk + hk;
+      row[st] = block * c.page + ((t0 + 16 * st) & (c.page - 1));
     }
+    whole = left[0] >= 32 && left[1] >= 16;
+  }
+
+  // Issues the copies of the located slots into `stage`: the keys (with the
+  // positions and both scales), or the values.  For the keys a lane copies what it
+  // reads itself, rows g and g + 8, channels 16 q .. and 64 + 16 q ..: four lanes
+  // take 64 bytes of a row.  Value rows are read by lanes with the rows across the
+  // four, so they are copied whole, 8 lanes a row, and their 16-byte pieces stored
+  // in the order c ^ (row & 6), where reads of 8 lanes meet no bank conflict.
+  template <bool VALUES, bool POS>
+  __device__ __forceinline__ void issue(uint8_t* stage) {
+    const int l = threadIdx.x & 31;
+    const int r0 = VALUES ? l >> 3 : l >> 2, c0 = VALUES ? l & 7 : l & 3;
+    const uint8_t* from = (VALUES ? c.v : c.k) + r0 * kDim + c0 * 16;
+    uint8_t* mine = VALUES ? stage + 4096 + r0 * kDim : stage + l * 16;
+    auto at = [&](int st, int i) {
+      return from + (st ? row[1] : row[0]) * kDim + (VALUES ? 4 * i * kDim : 8 * (i >> 1) * kDim + (i & 1) * 64);
+    };
+    auto to = [&](int st, int i) {  // rows r0 + 4 i: (r & 6) is r0 & 2 and 4 (i & 1)
+      return VALUES ? mine + (st * 16 + 4 * i) * kDim + ((c0 ^ (r0 & 2)) ^ (4 * (i & 1))) * 16 : mine + (st * 4 + i) * 512;
+    };
+    if (whole) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp16(to(st, i), at(st, i));
+    } else {
+#pragma unroll 1
+      for (int st = 0; st < 2; ++st)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i)
+          cp16(to(st, i), at(st, i), r0 + (VALUES ? 4 * i : 8 * (i >> 1)) < (st ? left[1] : left[0]));
+    }
+    if (VALUES) return;
+    const int half = l >> 4;
+    const int64_t mine_row = half ? row[1] : row[0];
+    const int mine_left = half ? left[1] : left[0];
+    if (POS) cp4(stage + 8192 + l * 4, c.pos + mine_row + (l & 15), (l & 15) < mine_left);
+    if ((l & 15) < 2) cp4(stage + 8320 + half * 8 + (l & 1) * 4, (l & 1 ? c.vs : c.ks) + (mine_row >> c.lg), mine_left > 0);
   }
 };
 
@@ -259,9 +280,12 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
   Stretch src(a.c, n, hk, we, err);
 #pragma unroll
   for (int i = 0; i < STAGES; ++i) {
-    if (i < steps) src.issue<false, POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
+    if (i < steps) {
+      src.locate(wb + i * CA_STEP);
+      src.issue<false, POS>(ring + i * CA_STAGE_BYTES);
+    }
     cp_commit();
-    if (i < steps) src.issue<true, POS>(ring + i * CA_STAGE_BYTES, wb + i * CA_STEP);
+    if (i < steps) src.issue<true, POS>(ring + i * CA_STAGE_BYTES);
     cp_commit();
   }
 
@@ -358,12 +382,15 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
     const int t0 = wb + it * CA_STEP;
 
     float s[2][NT][4];
+    float s2[2][4];  // NT = 1: the second half of the channels, for two shorter chains
 #pragma unroll
     for (int st = 0; st < 2; ++st)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int e = 0; e < 4; ++e) {
+        s2[st][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[st][t][e] = 0.f;
+        for (int t = 0; t < NT; ++t) s[st][t][e] = 0.f;
+      }
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint4 kk[2][2];
@@ -389,9 +416,15 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
           else b = make_uint2(qf[QSMEM ? 0 : t][half * 8 + 2 * j], qf[QSMEM ? 0 : t][half * 8 + 2 * j + 1]);
 #pragma unroll
           for (int st = 0; st < 2; ++st)
-            mma_f16(s[st][t], af[st][0], af[st][1], af[st][2], af[st][3], b.x, b.y);
+            mma_f16(NT == 1 && half ? s2[st] : s[st][t], af[st][0], af[st][1], af[st][2], af[st][3], b.x, b.y);
         }
       }
+    }
+    if (NT == 1) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[st][0][e] += s2[st][e];
     }
     // scores in log2 units, plus log2 v_scale
     float lvs[2], ivs[2], ksc[2];
@@ -413,7 +446,10 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
     }
     // the keys have been read by every lane: refill them while the rest goes on
     __syncwarp();
-    if (it + STAGES < steps) src.issue<false, POS>(stage, t0 + STAGES * CA_STEP);
+    if (it + STAGES < steps) {
+      src.locate(t0 + STAGES * CA_STEP);
+      src.issue<false, POS>(stage);
+    }
     cp_commit();
     const bool bias = POS && a.slopes != nullptr;
 #pragma unroll
@@ -479,20 +515,20 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
     for (int t = 0; t < NT; ++t) {
       float mx[2], f[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 2; ++e)
         mx[e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
-      }
       // the reference moves only when the maximum outgrows it by 2^6: p' stays in
       // fp16's range, and its rounding below 2^-25 of the largest weight
-      const bool g0 = mx[0] > m[t][0] + 6.f, g1 = mx[1] > m[t][1] + 6.f;
-      if (__any_sync(0xffffffffu, g0 || g1)) {
-        f[0] = g0 ? ex2_approx(m[t][0] - mx[0]) : 1.f;
-        f[1] = g1 ? ex2_approx(m[t][1] - mx[1]) : 1.f;
-        if (g0) m[t][0] = mx[0];
-        if (g1) m[t][1] = mx[1];
+      if (__any_sync(0xffffffffu, mx[0] > m[t][0] + 6.f || mx[1] > m[t][1] + 6.f)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
+          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
+          const bool grow = mx[e] > m[t][e] + 6.f;
+          f[e] = grow ? ex2_approx(m[t][e] - mx[e]) : 1.f;
+          if (grow) m[t][e] = mx[e];
+        }
         sum[t][0] *= f[0];
         sum[t][1] *= f[1];
 #pragma unroll
@@ -515,12 +551,14 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
       }
     }
     cp_wait<2 * STAGES - 1>();
+    __syncwarp();
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       uint32_t v[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(mine + 4096 + (st * 4 + i) * 512);
+        const int r = 2 * q + (i & 1) + 8 * (i >> 1);  // r & 6 = 2 q
+        const uint4 x = *reinterpret_cast<const uint4*>(stage + 4096 + (st * 16 + r) * kDim + ((g ^ (2 * q)) * 16));
         v[i][0] = x.x;
         v[i][1] = x.y;
         v[i][2] = x.z;
@@ -542,7 +580,8 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, float* __restrict__ part_o,
         }
       }
     }
-    if (it + STAGES < steps) src.issue<true, POS>(stage, t0 + STAGES * CA_STEP);
+    __syncwarp();
+    if (it + STAGES < steps) src.issue<true, POS>(stage);
     cp_commit();
   }
 
