@@ -67,16 +67,21 @@ def _api():
     return load(), KdaError
 
 
-def _tensor(t, name, dtype, shape, device):
-    """Checks one argument (None in `shape` stands for any size) and returns its address."""
+def _tensor(t, name, dtype, shape, index):
+    """Checks one argument (None in `shape` stands for any size; index: the CUDA
+    device) and returns its address.  These checks are a good part of a small call's
+    time, so the usual case is one line."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index and t.is_contiguous() and index >= 0):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     got = t.shape
     if len(got) != len(shape) or any(s is not None and s != g for s, g in zip(shape, got)):
         raise ValueError(f"{name} has shape {tuple(got)}, expected {tuple(shape)}")
@@ -85,33 +90,38 @@ def _tensor(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-def _optional(t, name, dtype, shape, device):
-    return None if t is None else _tensor(t, name, dtype, shape, device)
-
-
-def _device(t, name):
+def _sizes(t, name, dims, what):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    return t.device
+    if t.dim() != dims:
+        raise ValueError(f"{name} must be {what}, got {tuple(t.shape)}")
+    return t.shape
 
 
-def _cache(cache, device):
-    k = cache.k
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("cache.k must be a tensor [pages, Hk, page_size, 128]")
-    pages, Hk, page, _ = shape = tuple(k.shape)
+def _rows(t, name):
+    return _sizes(t, name, 3, "[T_total, heads, 128]")
+
+
+def _table(t, name):
+    return _sizes(t, name, 2, "[N, width]")
+
+
+def _cache(cache, index):
+    pages, Hk, page, D = shape = _sizes(cache.k, "cache.k", 4, "[pages, Hk, page_size, 128]")
     f8, f32 = torch.float8_e4m3fn, torch.float32
-    return _Cache(_tensor(k, "cache.k", f8, shape, device),
-                  _tensor(cache.v, "cache.v", f8, shape, device),
-                  _tensor(cache.k_scale, "cache.k_scale", f32, shape[:2], device),
-                  _tensor(cache.v_scale, "cache.v_scale", f32, shape[:2], device),
-                  _tensor(cache.pos, "cache.pos", torch.int32, shape[:3], device),
-                  _tensor(cache.weight, "cache.weight", f32, shape[:3], device),
-                  pages, page, Hk, shape[3])
+    blocks, slots = (pages, Hk), (pages, Hk, page)
+    return _Cache(_tensor(cache.k, "cache.k", f8, shape, index),
+                  _tensor(cache.v, "cache.v", f8, shape, index),
+                  _tensor(cache.k_scale, "cache.k_scale", f32, blocks, index),
+                  _tensor(cache.v_scale, "cache.v_scale", f32, blocks, index),
+                  _tensor(cache.pos, "cache.pos", torch.int32, slots, index),
+                  _tensor(cache.weight, "cache.weight", f32, slots, index),
+                  pages, page, Hk, D)
 
 
-def _on(stream, device):
-    return torch.cuda.current_stream(device) if stream is None else stream
+def _on(stream, index):
+    # the address of torch's current stream, without building a Stream object for it
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -122,26 +132,23 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace(workspace, need, device, stream):
+def _workspace(workspace, need, like, stream):
+    """(tensor to keep, its address, its bytes)"""
     if workspace is None:
-        return _empty(need, torch.uint8, device, stream) if need else None
-    _tensor(workspace, "workspace", torch.uint8, (None,), device)
-    return workspace
+        if not need:
+            return None, None, 0
+        workspace = _empty(need, torch.uint8, like.device, stream)
+        return workspace, workspace.data_ptr(), need
+    return workspace, _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), like.get_device()), workspace.numel()
 
 
-def _sequences(cu_seqlens, N, device):
+def _sequences(cu_seqlens, N, index):
     if cu_seqlens is None:
         return None, 1 if N is None else int(N)
-    at = _tensor(cu_seqlens, "cu_seqlens", torch.int32, (None,), device)
-    if N is not None and N != cu_seqlens.shape[0] - 1:
-        raise ValueError(f"N is {N}, cu_seqlens has {cu_seqlens.shape[0] - 1} sequences")
-    return at, cu_seqlens.shape[0] - 1
-
-
-def _rows(t, name):
-    if _device(t, name) is not None and t.dim() != 3:
-        raise ValueError(f"{name} must be [T_total, heads, 128], got {tuple(t.shape)}")
-    return t.shape
+    count = _sizes(cu_seqlens, "cu_seqlens", 1, "[N + 1]")[0]
+    if N is not None and N != count - 1:
+        raise ValueError(f"N is {N}, cu_seqlens has {count - 1} sequences")
+    return _tensor(cu_seqlens, "cu_seqlens", torch.int32, (count,), index), count - 1
 
 
 def kda_attn_fwd(q, k, v, scale, mask="causal", cap=0.0, slopes=None, prefix_lens=None,
@@ -153,19 +160,23 @@ def kda_attn_fwd(q, k, v, scale, mask="causal", cap=0.0, slopes=None, prefix_len
     lib, error = _api()
     T, H, D = _rows(q, "q")
     Hk = _rows(k, "k")[1]
-    dev = q.device
-    bf = torch.bfloat16
-    cu, N = _sequences(cu_seqlens, N, dev)
     if mask not in MASKS:
         raise ValueError(f"mask must be one of {tuple(MASKS)}, got {mask!r}")
+    dev, bf = q.get_device(), torch.bfloat16
+    rows, kv = (T, H, D), (T, Hk, D)
+    qp = _tensor(q, "q", bf, rows, dev)
+    kp = _tensor(k, "k", bf, kv, dev)
+    vp = _tensor(v, "v", bf, kv, dev)
+    cu, N = _sequences(cu_seqlens, N, dev)
     if out is None:
-        out = _empty((T, H, D), bf, dev, stream)
-    opts = _AttnOptions(MASKS[mask], cap, _optional(slopes, "slopes", torch.float32, (H,), dev),
-                        _optional(prefix_lens, "prefix_lens", torch.int32, (N,), dev))
-    st = lib.kda_attn_fwd(ctypes.byref(opts), _tensor(q, "q", bf, (T, H, D), dev),
-                          _tensor(k, "k", bf, (T, Hk, D), dev), _tensor(v, "v", bf, (T, Hk, D), dev),
-                          scale, cu, T, H, Hk, N, D, _tensor(out, "out", bf, (T, H, D), dev),
-                          _on(stream, dev).cuda_stream)
+        out = _empty(rows, bf, q.device, stream)
+    op = _tensor(out, "out", bf, rows, dev)
+    opts = _AttnOptions(
+        MASKS[mask], cap,
+        None if slopes is None else _tensor(slopes, "slopes", torch.float32, (H,), dev),
+        None if prefix_lens is None else _tensor(prefix_lens, "prefix_lens", torch.int32, (N,), dev))
+    st = lib.kda_attn_fwd(ctypes.byref(opts), qp, kp, vp, scale, cu, T, H, Hk, N, D, op,
+                          _on(stream, dev))
     if st:
         raise error(st, "kda_attn_fwd")
     return out
@@ -190,20 +201,21 @@ def kda_cache_append(cache, k, v, block_table, lens, cu_seqlens=None, positions=
     slots in use (lens is not changed: add the new rows yourself).  positions:
     int32 [T_total], default the slot numbers.  Returns cache."""
     lib, error = _api()
-    T, Hk, D = _rows(k, "k")
-    dev = k.device
-    bf, i32 = torch.bfloat16, torch.int32
+    T, Hk, D = rows = _rows(k, "k")
+    N, width = _table(block_table, "block_table")
+    dev, bf, i32 = k.get_device(), torch.bfloat16, torch.int32
     c = _cache(cache, dev)
     if Hk != c.Hk:
         raise ValueError(f"k has {Hk} heads, the cache {c.Hk}")
-    table = _tensor(block_table, "block_table", i32, (None, None), dev)
-    N, width = block_table.shape
+    kp, vp = _tensor(k, "k", bf, rows, dev), _tensor(v, "v", bf, rows, dev)
+    table = _tensor(block_table, "block_table", i32, (N, width), dev)
+    lp = _tensor(lens, "lens", i32, (N,), dev)
+    pp = None if positions is None else _tensor(positions, "positions", i32, (T,), dev)
     cu, N = _sequences(cu_seqlens, N, dev)
-    st = lib.kda_cache_append(ctypes.byref(c), _tensor(k, "k", bf, (T, Hk, c.D), dev),
-                              _tensor(v, "v", bf, (T, Hk, c.D), dev), table, width,
-                              _tensor(lens, "lens", i32, (N,), dev),
-                              _optional(positions, "positions", i32, (T,), dev), cu, T, N,
-                              _on(stream, dev).cuda_stream)
+    if D != c.D:
+        raise ValueError(f"k has {D} channels, the cache {c.D}")
+    st = lib.kda_cache_append(ctypes.byref(c), kp, vp, table, width, lp, pp, cu, T, N,
+                              _on(stream, dev))
     if st:
         raise error(st, "kda_cache_append")
     return cache
@@ -218,25 +230,28 @@ def kda_cache_attn(cache, q, block_table, lens, scale, cap=0.0, slopes=None, cu_
     accumulate: adds the softmax weight of every slot to cache.weight.
     Returns out [T_total, H, 128]."""
     lib, error = _api()
-    T, H, D = _rows(q, "q")
-    dev = q.device
-    bf, i32 = torch.bfloat16, torch.int32
+    T, H, D = rows = _rows(q, "q")
+    N, width = _table(block_table, "block_table")
+    dev, bf, i32 = q.get_device(), torch.bfloat16, torch.int32
     c = _cache(cache, dev)
-    table = _tensor(block_table, "block_table", i32, (None, None), dev)
-    N, width = block_table.shape
+    if D != c.D:
+        raise ValueError(f"q has {D} channels, the cache {c.D}")
+    qp = _tensor(q, "q", bf, rows, dev)
+    table = _tensor(block_table, "block_table", i32, (N, width), dev)
+    lp = _tensor(lens, "lens", i32, (N,), dev)
     cu, N = _sequences(cu_seqlens, N, dev)
     if out is None:
-        out = _empty((T, H, D), bf, dev, stream)
-    opts = _CacheAttnOptions(cap, _optional(slopes, "slopes", torch.float32, (H,), dev),
-                             _optional(positions, "positions", i32, (T,), dev), 1 if accumulate else 0)
+        out = _empty(rows, bf, q.device, stream)
+    op = _tensor(out, "out", bf, rows, dev)
+    opts = _CacheAttnOptions(
+        cap, None if slopes is None else _tensor(slopes, "slopes", torch.float32, (H,), dev),
+        None if positions is None else _tensor(positions, "positions", i32, (T,), dev),
+        1 if accumulate else 0)
     ref = ctypes.byref(c)
     need = lib.kda_cache_attn_workspace_size(ref, T, H, N, width, opts.accumulate)
-    ws = _workspace(workspace, need, dev, stream)
-    st = lib.kda_cache_attn(ctypes.byref(opts), ref, _tensor(q, "q", bf, (T, H, c.D), dev), scale,
-                            table, width, _tensor(lens, "lens", i32, (N,), dev), cu, T, H, N,
-                            _tensor(out, "out", bf, (T, H, D), dev),
-                            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                            _on(stream, dev).cuda_stream)
+    keep, ws, nbytes = _workspace(workspace, need, q, stream)
+    st = lib.kda_cache_attn(ctypes.byref(opts), ref, qp, scale, table, width, lp, cu, T, H, N, op,
+                            ws, nbytes, _on(stream, dev))
     if st:
         raise error(st, "kda_cache_attn")
     return out
@@ -249,22 +264,21 @@ def kda_cache_evict(cache, block_table, lens, dst_table, budget, recent, new_len
     dst_table int32 [N, dst_width] (other pages than block_table's).  Returns
     new_lens int32 [N] = min(lens, budget); the old pages are free afterwards."""
     lib, error = _api()
-    i32 = torch.int32
-    dev = _device(block_table, "block_table")
+    N, width = _table(block_table, "block_table")
+    dst_width = _table(dst_table, "dst_table")[1]
+    dev, i32 = block_table.get_device(), torch.int32
     c = _cache(cache, dev)
-    table = _tensor(block_table, "block_table", i32, (None, None), dev)
-    N, width = block_table.shape
-    dst = _tensor(dst_table, "dst_table", i32, (N, None), dev)
+    table = _tensor(block_table, "block_table", i32, (N, width), dev)
+    dst = _tensor(dst_table, "dst_table", i32, (N, dst_width), dev)
+    lp = _tensor(lens, "lens", i32, (N,), dev)
     if new_lens is None:
-        new_lens = _empty((N,), i32, dev, stream)
+        new_lens = _empty((N,), i32, block_table.device, stream)
+    np_ = _tensor(new_lens, "new_lens", i32, (N,), dev)
     ref = ctypes.byref(c)
     need = lib.kda_cache_evict_workspace_size(ref, N, budget)
-    ws = _workspace(workspace, need, dev, stream)
-    st = lib.kda_cache_evict(ref, table, width, _tensor(lens, "lens", i32, (N,), dev), dst,
-                             dst_table.shape[1], budget, recent, N,
-                             _tensor(new_lens, "new_lens", i32, (N,), dev),
-                             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                             _on(stream, dev).cuda_stream)
+    keep, ws, nbytes = _workspace(workspace, need, block_table, stream)
+    st = lib.kda_cache_evict(ref, table, width, lp, dst, dst_width, budget, recent, N, np_, ws,
+                             nbytes, _on(stream, dev))
     if st:
         raise error(st, "kda_cache_evict")
     return new_lens
