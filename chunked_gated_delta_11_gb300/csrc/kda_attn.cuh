@@ -90,19 +90,34 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Sequence of slot s where sequence n owns the slots from floor(bos_n / unit) +
-// extra * n on (strictly increasing in n): the last n whose first slot is <= s.
-__device__ __forceinline__ int seq_of_slot(const int32_t* cu, int64_t T, int N, int unit, int extra,
-                                           int64_t s) {
+// The last n in [0, N) with first(n) <= s, for a function that does not decrease;
+// 0 if there is none.  All lanes of a warp call it with the same arguments; each
+// round tries 32 places, so a thousand sequences take two dependent loads.
+template <class F>
+__device__ __forceinline__ int warp_search(int N, int64_t s, F first) {
   int lo = 0, hi = N - 1;
+  const int lane = threadIdx.x & 31;
   while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    int64_t bos, eos;
-    seq_bounds(cu, T, N, mid, bos, eos);
-    if (bos / unit + static_cast<int64_t>(extra) * mid <= s) lo = mid;
-    else hi = mid - 1;
+    const int step = (hi - lo + 31) / 32;
+    const int64_t at = lo + static_cast<int64_t>(lane + 1) * step;
+    const bool below = at <= hi && first(static_cast<int>(at)) <= s;
+    const int took = __popc(__ballot_sync(0xffffffffu, below)) * step;
+    lo = lo + took < hi ? lo + took : hi;
+    hi = hi < lo + step - 1 ? hi : lo + step - 1;
   }
   return lo;
+}
+
+// Sequence of slot s where sequence n owns the slots from floor(bos_n / unit) +
+// extra * n on.  All lanes of a warp call it.
+__device__ __forceinline__ int seq_of_slot(const int32_t* cu, int64_t T, int N, int unit, int extra,
+                                           int64_t s) {
+  const int64_t per = cu ? 0 : T / N;
+  return warp_search(N, s, [&](int n) -> int64_t {
+    int64_t bos = cu ? __ldg(cu + n) : n * per;
+    bos = bos < 0 ? 0 : (bos > T ? T : bos);
+    return bos / unit + static_cast<int64_t>(extra) * n;
+  });
 }
 
 cudaError_t launch_attn(const AttnArgs& a, int sm_count, int* err, cudaStream_t stream);

@@ -33,41 +33,25 @@ __device__ __forceinline__ float block_scale(float amax) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// largest finite magnitude of 8 bf16 values
-__device__ __forceinline__ float amax8(const uint4& x) {
-  float m = 0.f;
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = fabsf(__uint_as_float(w[i] << 16));
-    const float hi = fabsf(__uint_as_float(w[i] & 0xffff0000u));
-    // fmaxf drops NaN; infinities are left out here
-    m = fmaxf(m, lo < INFINITY ? lo : 0.f);
-    m = fmaxf(m, hi < INFINITY ? hi : 0.f);
-  }
-  return m;
-}
-
 __device__ __forceinline__ float finite_or_nan(float x) {
   return fabsf(x) < INFINITY ? x : __uint_as_float(0x7fffffffu);
 }
 
-// 8 bf16 values -> 8 codes of value * inv
+// largest finite magnitude of 2 bf16 values, and their codes
+__device__ __forceinline__ float amax2(uint32_t w) {
+  const float lo = fabsf(__uint_as_float(w << 16)), hi = fabsf(__uint_as_float(w & 0xffff0000u));
+  return fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f);
+}
+__device__ __forceinline__ uint32_t encode2(uint32_t w, float inv) {
+  return f32x2_to_e4m3x2(finite_or_nan(__uint_as_float(w << 16)) * inv,
+                         finite_or_nan(__uint_as_float(w & 0xffff0000u)) * inv);
+}
+
+__device__ __forceinline__ float amax8(const uint4& x) {
+  return fmaxf(fmaxf(amax2(x.x), amax2(x.y)), fmaxf(amax2(x.z), amax2(x.w)));
+}
 __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t r[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t c[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float lo = finite_or_nan(__uint_as_float(w[2 * i + j] << 16));
-      const float hi = finite_or_nan(__uint_as_float(w[2 * i + j] & 0xffff0000u));
-      c[j] = f32x2_to_e4m3x2(lo * inv, hi * inv);
-    }
-    r[i] = c[0] | (c[1] << 16);
-  }
-  return make_uint2(r[0], r[1]);
+  return make_uint2(encode2(x.x, inv) | (encode2(x.y, inv) << 16), encode2(x.z, inv) | (encode2(x.w, inv) << 16));
 }
 
 // 4 codes times `ratio`, rounded to codes again
@@ -82,10 +66,41 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
   return r[0] | (r[1] << 16);
 }
 
-// One CTA per (page that gets rows, KV head).  Its page is slot blockIdx.x of
-// the list in which sequence n owns the slots from floor(bos_n / page) + 2 n on:
-// n new rows touch at most floor(n / page) + 2 pages.  A row is 16 threads of 8
-// elements; the new rows stay in registers between the maximum and the codes.
+// A page that gets rows: its id, its rows [lo, hi) that are new, the sequence slot
+// of its row 0, and the input row that goes to row lo.
+struct Touched {
+  int pid, lo, hi;
+  int64_t first, row0;
+};
+
+// Page slot s of the list in which sequence n owns the slots from floor(bos_n /
+// page) + 2 n on (r new rows touch at most floor(r / page) + 2 pages).  False if
+// there is no such page.  The same for all threads of a warp.
+template <int PAGE>
+__device__ __forceinline__ bool touched_page(const CacheArgs& c, const int32_t* cu, int64_t T,
+                                             int64_t s, int* err, Touched& p) {
+  const int n = seq_of_slot(cu, T, c.N, PAGE, 2, s);
+  int64_t bos, eos;
+  seq_bounds(cu, T, c.N, n, bos, eos);
+  const int64_t len = cached_len(c, n, err), most = static_cast<int64_t>(c.width) * PAGE;
+  const int64_t fresh = eos - bos;
+  int64_t end = len + fresh;
+  if (end > most) {
+    atomicCAS(err, 0, static_cast<int>(KDA_ERR_INVALID_ARG));
+    end = most;
+  }
+  const int64_t pj = len / PAGE + (s - (bos / PAGE + 2 * static_cast<int64_t>(n)));
+  p.first = pj * PAGE;
+  if (fresh == 0 || p.first >= end) return false;
+  p.pid = page_id(c, n, static_cast<int>(pj), err);
+  p.lo = static_cast<int>(len > p.first ? len - p.first : 0);
+  p.hi = static_cast<int>(end - p.first < PAGE ? end - p.first : PAGE);
+  p.row0 = bos + p.first + p.lo - len;
+  return p.pid >= 0;
+}
+
+// One CTA per (page that gets rows, KV head).  A row is 16 threads of 8 elements;
+// the new rows stay in registers between the maximum and the codes.
 template <int PAGE>
 __global__ void __launch_bounds__(256)
 append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
@@ -93,26 +108,13 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
               int* __restrict__ err) {
   constexpr int PASSES = PAGE / 16;
   __shared__ float red[2][8];
+  grid_dep_wait();
+  grid_dep_launch();
   const int t = threadIdx.x, sub = t & 15, row0 = t >> 4, h = blockIdx.y;
-  const int64_t slot = blockIdx.x;
-  const int n = seq_of_slot(cu, T, c.N, PAGE, 2, slot);
-  int64_t bos, eos;
-  seq_bounds(cu, T, c.N, n, bos, eos);
-  const int64_t len = cached_len(c, n, err), most = static_cast<int64_t>(c.width) * PAGE;
-  const int64_t fresh = eos - bos;
-  int64_t end = len + fresh;
-  if (end > most) {
-    if (t == 0) atomicCAS(err, 0, static_cast<int>(KDA_ERR_INVALID_ARG));
-    end = most;
-  }
-  const int64_t pj = len / PAGE + (slot - (bos / PAGE + 2 * static_cast<int64_t>(n)));
-  if (fresh == 0 || pj * PAGE >= end) return;
-  const int pid = page_id(c, n, static_cast<int>(pj), err);
-  if (pid < 0) return;
-  const int64_t first = pj * PAGE;  // sequence slot of the page's row 0
-  const int lo = static_cast<int>(len > first ? len - first : 0);
-  const int hi = static_cast<int>(end - first < PAGE ? end - first : PAGE);
-  const int64_t block = static_cast<int64_t>(pid) * c.Hk + h;
+  Touched pg;
+  if (!touched_page<PAGE>(c, cu, T, blockIdx.x, err, pg)) return;
+  const int lo = pg.lo, hi = pg.hi;
+  const int64_t block = static_cast<int64_t>(pg.pid) * c.Hk + h;
 
   uint4 xk[PASSES], xv[PASSES];
   float mk = 0.f, mv = 0.f;
@@ -121,7 +123,7 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
     const int r = p * 16 + row0;
     xk[p] = xv[p] = make_uint4(0, 0, 0, 0);
     if (r >= lo && r < hi) {
-      const int64_t at = ((bos + first + r - len) * c.Hk + h) * kDim + sub * 8;
+      const int64_t at = ((pg.row0 + r - lo) * c.Hk + h) * kDim + sub * 8;
       xk[p] = *reinterpret_cast<const uint4*>(k + at);
       xv[p] = *reinterpret_cast<const uint4*>(v + at);
       mk = fmaxf(mk, amax8(xk[p]));
@@ -169,12 +171,70 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
     }
   }
   if (t >= lo && t < hi) {
-    const int64_t row = first + t - len;
-    c.pos[block * PAGE + t] = positions ? __ldg(positions + bos + row) : static_cast<int32_t>(first + t);
+    c.pos[block * PAGE + t] = positions ? __ldg(positions + pg.row0 + t - lo) : static_cast<int32_t>(pg.first + t);
     c.weight[block * PAGE + t] = 0.f;
   }
   // the old scales were read before the barrier above
   if (t == 0) {
+    c.ks[block] = sk;
+    c.vs[block] = sv;
+  }
+}
+
+// The same for few new rows (serving steps): a warp per (page, KV head), 8 heads
+// of a page per CTA.  A lane has 4 channels of a row; rows are read twice.
+template <int PAGE>
+__global__ void __launch_bounds__(256)
+append_few_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
+                  const int32_t* __restrict__ positions, const int32_t* __restrict__ cu, int64_t T,
+                  int* __restrict__ err) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int l = threadIdx.x & 31, h = blockIdx.y * 8 + (threadIdx.x >> 5);
+  if (h >= c.Hk) return;
+  Touched p;
+  if (!touched_page<PAGE>(c, cu, T, blockIdx.x, err, p)) return;
+  const int64_t block = static_cast<int64_t>(p.pid) * c.Hk + h;
+  const float oldk = p.lo > 0 ? c.ks[block] : 0.f, oldv = p.lo > 0 ? c.vs[block] : 0.f;
+  const int64_t at0 = (p.row0 * c.Hk + h) * kDim + l * 4, step = static_cast<int64_t>(c.Hk) * kDim;
+  const int rows = p.hi - p.lo;
+  float mk = 0.f, mv = 0.f;
+  for (int i = 0; i < rows; ++i) {
+    const uint2 x = *reinterpret_cast<const uint2*>(k + at0 + i * step);
+    const uint2 y = *reinterpret_cast<const uint2*>(v + at0 + i * step);
+    mk = fmaxf(mk, fmaxf(amax2(x.x), amax2(x.y)));
+    mv = fmaxf(mv, fmaxf(amax2(y.x), amax2(y.y)));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
+  }
+  const float sk = fmaxf(block_scale(mk), oldk), sv = fmaxf(block_scale(mv), oldv);
+  const float ik = 1.0f / sk, iv = 1.0f / sv;
+  uint8_t* dk = c.k + block * (PAGE * kDim);
+  uint8_t* dv = c.v + block * (PAGE * kDim);
+  for (int i = 0; i < rows; ++i) {
+    const uint2 x = *reinterpret_cast<const uint2*>(k + at0 + i * step);
+    const uint2 y = *reinterpret_cast<const uint2*>(v + at0 + i * step);
+    *reinterpret_cast<uint32_t*>(dk + (p.lo + i) * kDim + l * 4) = encode2(x.x, ik) | (encode2(x.y, ik) << 16);
+    *reinterpret_cast<uint32_t*>(dv + (p.lo + i) * kDim + l * 4) = encode2(y.x, iv) | (encode2(y.y, iv) << 16);
+  }
+  // older rows under a grown scale, 16 codes a lane
+  auto again = [&](uint8_t* d, float ratio) {
+    for (int e = l; e < p.lo * 8; e += 32) {
+      uint4* q = reinterpret_cast<uint4*>(d) + e;
+      const uint4 x = *q;
+      *q = make_uint4(rescale4(x.x, ratio), rescale4(x.y, ratio), rescale4(x.z, ratio), rescale4(x.w, ratio));
+    }
+  };
+  if (p.lo > 0 && sk != oldk) again(dk, oldk * ik);
+  if (p.lo > 0 && sv != oldv) again(dv, oldv * iv);
+  for (int i = l; i < rows; i += 32) {
+    c.pos[block * PAGE + p.lo + i] = positions ? __ldg(positions + p.row0 + i) : static_cast<int32_t>(p.first + p.lo + i);
+    c.weight[block * PAGE + p.lo + i] = 0.f;
+  }
+  if (l == 0) {
     c.ks[block] = sk;
     c.vs[block] = sv;
   }
@@ -188,58 +248,149 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 constexpr int SEL_THREADS = 1024;
+constexpr int SEL_BINS = 2048;
+constexpr int SEL_KEYS = 32768;  // keys that a CTA can hold
+constexpr int SEL_SMEM = SEL_KEYS * 4;
+constexpr int SEL_MAX_CLUSTER = 8;
 
-// The kept slots of one (sequence, head), in order, into kept[unit * budget].
-// A radix selection finds the key of the last slot to be kept (four passes of 8
-// bits over the weights), then one ordered pass writes the slots.
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// Word at `local` (this CTA's shared memory) in the CTA of `rank`.
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* local, unsigned rank) {
+  uint32_t at, x;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
+// The kept slots of one (sequence, head), in order, into kept[unit * budget]: a
+// radix selection finds the key of the last slot to be kept (three passes of 11,
+// 11 and 10 bits), then one ordered pass writes the slots.  A cluster of CTAs
+// shares a unit, each with a stretch of its slots, whose keys stay in shared
+// memory (the first SEL_KEYS of them; the rest are read again); the histograms
+// and counts are summed through distributed shared memory.  What bounds it is the
+// latency of the passes, so few long sequences get the largest cluster.
 __global__ void __launch_bounds__(SEL_THREADS)
-select_kernel(CacheArgs c, int budget, int recent, int32_t* __restrict__ new_lens,
+select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restrict__ new_lens,
               int32_t* __restrict__ kept, int* __restrict__ err) {
-  __shared__ uint32_t hist[256];
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ uint32_t hist[2][SEL_BINS];  // alternate, so that a pass can be cleared while others read the last
   __shared__ uint32_t warp_n[2][32];
-  __shared__ uint32_t pick[2];  // digit chosen, how many of its slots are still to be kept
+  __shared__ uint32_t pick[2];   // digit chosen, how many of its slots are still to be kept
+  __shared__ uint32_t count[2];  // this CTA's slots above and at the last key
+  grid_dep_wait();
+  grid_dep_launch();
   const int t = threadIdx.x, l = t & 31, w = t >> 5;
-  const int n = blockIdx.x / c.Hk, h = blockIdx.x - n * c.Hk;
+  const int unit = blockIdx.x / static_cast<unsigned>(cluster);
+  const unsigned rank = cluster > 1 ? cluster_rank() : 0u;
+  const int n = unit / c.Hk, h = unit - n * c.Hk;
   const int len = cached_len(c, n, err);
-  if (h == 0 && t == 0) new_lens[n] = len < budget ? len : budget;
-  if (len <= budget) return;  // everything stays, in place: no list
+  if (h == 0 && t == 0 && rank == 0) new_lens[n] = len < budget ? len : budget;
+  if (len <= budget) return;  // everything stays, in place: no list (the same for the whole cluster)
   const int old = len - recent, want = budget - recent;
-  int32_t* list = kept + static_cast<int64_t>(blockIdx.x) * budget;
-  for (int i = t; i < recent; i += SEL_THREADS) list[want + i] = old + i;
+  int32_t* list = kept + static_cast<int64_t>(unit) * budget;
+  for (int i = rank * SEL_THREADS + t; i < recent; i += cluster * SEL_THREADS) list[want + i] = old + i;
   if (want == 0) return;
-  auto key_at = [&](int i) -> uint32_t {
-    const int pid = page_id(c, n, i >> c.lg, err);
+  const int share = (old + cluster - 1) / cluster;
+  const int begin = old < static_cast<int>(rank) * share ? old : static_cast<int>(rank) * share;
+  const int mine = old - begin < share ? old - begin : share;
+  auto read = [&](int i) -> uint32_t {
+    const int pid = page_id(c, n, (begin + i) >> c.lg, err);
     if (pid < 0) return 0u;
-    return weight_key(__ldg(c.weight + (static_cast<int64_t>(pid) * c.Hk + h) * c.page + (i & (c.page - 1))));
+    return weight_key(__ldg(c.weight + (static_cast<int64_t>(pid) * c.Hk + h) * c.page + ((begin + i) & (c.page - 1))));
   };
-  uint32_t prefix = 0, need = static_cast<uint32_t>(want);
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (t < 256) hist[t] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = t; i < old; i += SEL_THREADS) {
+  auto key_at = [&](int i) -> uint32_t { return i < SEL_KEYS ? keys[i] : read(i); };
+  for (int i = t; i < 2 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
+#pragma unroll 4
+  for (int i = t; i < mine && i < SEL_KEYS; i += SEL_THREADS) keys[i] = read(i);
+  if (t < 2) count[t] = 0;
+  __syncthreads();
+  uint32_t last = 0, need = static_cast<uint32_t>(want);
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : 2048;
+    uint32_t* hs = hist[pass & 1];
+    const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 1 ? 11 : 10));
+    for (int i = t; i < mine; i += SEL_THREADS) {
       const uint32_t key = key_at(i);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+      if ((key & mask) == last) atomicAdd(&hs[(key >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
-    if (t == 0) {
-      uint32_t left = need;
-      int d = 255;
-      while (d > 0 && hist[d] < left) left -= hist[d--];
-      pick[0] = static_cast<uint32_t>(d);
-      pick[1] = left;
+    if (cluster > 1) cluster_sync_all();
+    // two bins per thread, from the top: thread t has bins - 1 - 2 t and the one below
+    const int hi = SEL_BINS - 1 - 2 * t;
+    uint32_t a = hs[hi], b = hs[hi - 1];
+    for (int r = 1; r < cluster; ++r) {
+      const unsigned other = (rank + r) % static_cast<unsigned>(cluster);
+      a += cluster_load(&hs[hi], other);
+      b += cluster_load(&hs[hi - 1], other);
+    }
+    uint32_t sum = a + b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (l >= o) sum += x;
+    }
+    if (l == 31) warp_n[0][w] = sum;
+    __syncthreads();
+    uint32_t before = warp_n[0][l];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
+      if (l >= o) before += x;
+    }
+    before = w ? __shfl_sync(0xffffffffu, before, w - 1) : 0u;
+    const uint32_t above = before + sum - a - b;  // slots in bins above this thread's
+    if (above < need && need <= above + a) {
+      pick[0] = hi;
+      pick[1] = need - above;
+    } else if (above + a < need && need <= above + a + b) {
+      pick[0] = hi - 1;
+      pick[1] = need - above - a;
     }
     __syncthreads();
-    prefix |= pick[0] << shift;
+    last |= pick[0] << shift;
     need = pick[1];
+    // the last pass uses hist[0] again: the others read it before this pass's barrier
+    if (pass == 1)
+      for (int i = t; i < SEL_BINS; i += SEL_THREADS) hist[0][i] = 0;
     __syncthreads();
   }
-  // keep key > prefix, and the first `need` slots with key == prefix
-  uint32_t base = 0, ties = 0;
-  for (int i0 = 0; i0 < old; i0 += SEL_THREADS) {
+  // keep the slots with key > last, and the first `need` with key == last
+  uint32_t above0 = 0, ties0 = 0;  // in the stretches of lower ranks
+  if (cluster > 1) {
+    uint32_t g = 0, e = 0;
+    for (int i = t; i < mine; i += SEL_THREADS) {
+      const uint32_t key = key_at(i);
+      g += key > last;
+      e += key == last;
+    }
+    g = __reduce_add_sync(0xffffffffu, g);
+    e = __reduce_add_sync(0xffffffffu, e);
+    if (l == 0) {
+      atomicAdd(&count[0], g);
+      atomicAdd(&count[1], e);
+    }
+    __syncthreads();
+    cluster_sync_all();
+    for (unsigned r = 0; r < rank; ++r) {
+      above0 += cluster_load(&count[0], r);
+      ties0 += cluster_load(&count[1], r);
+    }
+    cluster_sync_all();  // nobody leaves while its counts are read
+  }
+  uint32_t ties = ties0, base = above0 + (ties0 < need ? ties0 : need);
+  for (int i0 = 0; i0 < mine; i0 += SEL_THREADS) {
     const int i = i0 + t;
-    const uint32_t key = i < old ? key_at(i) : 0u;
-    const bool eq = i < old && key == prefix, gt = i < old && key > prefix;
+    const uint32_t key = i < mine ? key_at(i) : 0u;
+    const bool eq = i < mine && key == last, gt = i < mine && key > last;
     const uint32_t be = __ballot_sync(0xffffffffu, eq), bg = __ballot_sync(0xffffffffu, gt);
     if (l == 0) {
       warp_n[0][w] = __popc(be);
@@ -258,13 +409,13 @@ select_kernel(CacheArgs c, int budget, int recent, int32_t* __restrict__ new_len
     const uint32_t etot = __shfl_sync(0xffffffffu, e, 31), gtot = __shfl_sync(0xffffffffu, g, 31);
     const uint32_t ew = __shfl_sync(0xffffffffu, e, (w + 31) & 31), gw = __shfl_sync(0xffffffffu, g, (w + 31) & 31);
     const uint32_t below = (1u << l) - 1u;
-    const uint32_t er = ties + (w ? ew : 0u) + __popc(be & below);    // ties before this slot
+    const uint32_t er = ties + (w ? ew : 0u) + __popc(be & below);  // ties before this slot
     const uint32_t gr = (w ? gw : 0u) + __popc(bg & below);
     const uint32_t eq_kept = er < need ? er : need;
-    const uint32_t ties0 = ties < need ? ties : need;
-    if (gt || (eq && er < need)) list[base + gr + (eq_kept - ties0)] = i;
+    const uint32_t ties_kept = ties < need ? ties : need;
+    if (gt || (eq && er < need)) list[base + gr + (eq_kept - ties_kept)] = begin + i;
     const uint32_t ties1 = ties + etot < need ? ties + etot : need;
-    base += gtot + (ties1 - ties0);
+    base += gtot + (ties1 - ties_kept);
     ties += etot;
     __syncthreads();
   }
@@ -277,6 +428,8 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
             const int32_t* __restrict__ kept, int* __restrict__ err) {
   __shared__ int64_t src[128];  // source row (block * page + row), -1: bad page
   __shared__ float sks[128], svs[128];
+  grid_dep_wait();
+  grid_dep_launch();
   const int t = threadIdx.x, unit = blockIdx.x;
   const int n = unit / c.Hk, h = unit - n * c.Hk;
   const int len = cached_len(c, n, err), now = len < budget ? len : budget;
@@ -329,38 +482,64 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
   }
 }
 
+template <int PAGE>
+cudaError_t append_page(const CacheArgs& c, const void* k, const void* v, const int32_t* positions,
+                        const int32_t* cu, int64_t T, int* err, cudaStream_t stream) {
+  const int64_t slots = T / PAGE + 2 * static_cast<int64_t>(c.N);
+  if (slots > 0x7fffffffLL) return cudaErrorInvalidValue;
+  // a few rows per sequence leave most of a CTA's threads idle: a warp does them
+  const bool few = T <= 4 * static_cast<int64_t>(c.N);
+  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(few ? (c.Hk + 7) / 8 : c.Hk));
+  return launch_pdl(few ? append_few_kernel<PAGE> : append_kernel<PAGE>, grid, dim3(256), 0, stream, c,
+                    static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), positions, cu,
+                    T, err);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheArgs& c, const void* k, const void* v,
                                 const int32_t* positions, const int32_t* cu, int64_t T, int* err,
                                 cudaStream_t stream) {
-  const int64_t slots = T / c.page + 2 * static_cast<int64_t>(c.N);
-  if (slots > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(c.Hk));
-  const auto* kk = static_cast<const __nv_bfloat16*>(k);
-  const auto* vv = static_cast<const __nv_bfloat16*>(v);
   switch (c.page) {
-    case 16: append_kernel<16><<<grid, 256, 0, stream>>>(c, kk, vv, positions, cu, T, err); break;
-    case 32: append_kernel<32><<<grid, 256, 0, stream>>>(c, kk, vv, positions, cu, T, err); break;
-    case 64: append_kernel<64><<<grid, 256, 0, stream>>>(c, kk, vv, positions, cu, T, err); break;
-    default: append_kernel<128><<<grid, 256, 0, stream>>>(c, kk, vv, positions, cu, T, err); break;
+    case 16: return append_page<16>(c, k, v, positions, cu, T, err, stream);
+    case 32: return append_page<32>(c, k, v, positions, cu, T, err, stream);
+    case 64: return append_page<64>(c, k, v, positions, cu, T, err, stream);
+    default: return append_page<128>(c, k, v, positions, cu, T, err, stream);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_cache_evict(const CacheArgs& c, const int32_t* dst, int dst_width, int budget,
                                int recent, int32_t* new_lens, int32_t* kept, int* err,
                                cudaStream_t stream) {
-  const unsigned units = static_cast<unsigned>(c.N) * static_cast<unsigned>(c.Hk);
-  select_kernel<<<units, SEL_THREADS, 0, stream>>>(c, budget, recent, new_lens, kept, err);
-  cudaError_t e = cudaGetLastError();
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(select_kernel), SEL_SMEM, done);
   if (e != cudaSuccess) return e;
-  // pages that the kept rows can need, whatever the destination table's width
+  const unsigned units = static_cast<unsigned>(c.N) * static_cast<unsigned>(c.Hk);
   const int64_t most = static_cast<int64_t>(c.width) << c.lg;
+  // CTAs per unit: up to 8 while that leaves SMs idle and gives each 2048 slots
+  int cluster = 1;
+  while (cluster < SEL_MAX_CLUSTER && units * 2u * cluster <= 2u * 152u && most > 4096LL * cluster) cluster *= 2;
+  const int64_t share = (most + cluster - 1) / cluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(units * cluster);
+  cfg.blockDim = dim3(SEL_THREADS);
+  cfg.dynamicSmemBytes = static_cast<size_t>(share < SEL_KEYS ? share : SEL_KEYS) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if ((e = cudaLaunchKernelEx(&cfg, select_kernel, c, budget, recent, cluster, new_lens, kept, err)) != cudaSuccess)
+    return e;
+  // pages that the kept rows can need, whatever the destination table's width
   const int64_t rows = budget < most ? budget : most;
   const unsigned pages = static_cast<unsigned>((rows + c.page - 1) >> c.lg);
-  pack_kernel<<<dim3(units, pages < 65535u ? pages : 65535u), 256, 0, stream>>>(c, dst, dst_width, budget, kept, err);
-  return cudaGetLastError();
+  return launch_pdl(pack_kernel, dim3(units, pages < 65535u ? pages : 65535u), dim3(256), 0, stream, c, dst,
+                    dst_width, budget, static_cast<const int32_t*>(kept), err);
 }
 
 }  // namespace kda

@@ -140,14 +140,10 @@ __device__ __forceinline__ int64_t first_tile(const CacheAttnArgs& a, const Cach
 __device__ __forceinline__ void tile_of(const CacheAttnArgs& a, const CachePlan& p, int s, int& n,
                                         int64_t& bos, int& cnt, int& tile) {
   if (a.cu) {
-    int lo = 0, hi = a.c.N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      const int64_t c = __ldg(a.cu + mid);
-      if (first_tile(a, p, mid, c < 0 ? 0 : (c > a.T ? a.T : c)) <= s) lo = mid;
-      else hi = mid - 1;
-    }
-    n = lo;
+    n = warp_search(a.c.N, s, [&](int i) -> int64_t {
+      const int64_t c = __ldg(a.cu + i);
+      return first_tile(a, p, i, c < 0 ? 0 : (c > a.T ? a.T : c));
+    });
   } else {
     n = static_cast<unsigned>(s) / static_cast<unsigned>(p.per_tiles);
   }
@@ -670,13 +666,7 @@ join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __r
     if (t >= a.T) return;  // a whole warp, or the whole CTA
     int n = 0;
     if (a.cu) {
-      int lo = 0, hi = a.c.N - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(a.cu + mid) <= t) lo = mid;
-        else hi = mid - 1;
-      }
-      n = lo;
+      n = warp_search(a.c.N, t, [&](int i) -> int64_t { return __ldg(a.cu + i); });
     } else {
       n = static_cast<unsigned>(t) / static_cast<unsigned>(plan.per);
     }

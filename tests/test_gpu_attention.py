@@ -529,6 +529,28 @@ def test_evict(page, lens, budget, recent, ties):
     same_cache(dev, want)
 
 
+@pytest.mark.parametrize("n,budget,recent", [(20_000, 150, 20), (300_000, 200, 7), (70_000, 60_000, 30_000)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_evict_long_sequences(n, budget, recent, ties):
+    """Several CTAs share a sequence, with more slots than they keep in shared memory."""
+    page = 128
+    cache, table = filled([n], 1, page, n)
+    w = torch.rand(cache.weight.shape, generator=gen(3))
+    w = torch.round(w * 40) if ties else w
+    pages, need = cache.k.shape[0], -(-budget // page)
+    dst = torch.arange(pages, pages + need, dtype=torch.int32)[None].contiguous()
+    more = lambda t: torch.cat([t, torch.zeros((need, *t.shape[1:]), dtype=t.dtype)])  # noqa: E731
+    dev = kda.KvCache(*(more(t.view(torch.uint8)).view(t.dtype) if t.dtype == torch.float8_e4m3fn else more(t)
+                        for t in cache._replace(weight=w)))
+    dev = to(dev, "cuda")
+    kda.kda_cache_evict(dev, table.cuda(), torch.tensor([n], dtype=torch.int32).cuda(), dst.cuda(), budget, recent)
+    ok()
+    flat = w[table[0, : -(-n // page)].long(), 0].reshape(-1)[:n]
+    keep = torch.tensor(ref.kept_slots(flat.tolist(), budget, recent), dtype=torch.int32)
+    assert torch.equal(dev.pos[pages:, 0].reshape(-1)[:budget].cpu(), keep)
+    assert torch.equal(dev.weight[pages:, 0].reshape(-1)[:budget].cpu(), flat[keep.long()])
+
+
 def test_evict_bad_pages_and_narrow_tables_are_reported():
     cache, table = filled([100], 1, 16, 1)
     lens = torch.tensor([100], dtype=torch.int32).cuda()
