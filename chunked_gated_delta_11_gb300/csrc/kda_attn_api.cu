@@ -35,8 +35,8 @@ kda_status check_cache(const kda_cache* c) {
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return KDA_ERR_UNSUPPORTED;
   if (c->pages <= 0 || c->Hk <= 0 || c->Hk > 65535) return KDA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(c->pages) > kMaxElems / (static_cast<int64_t>(c->Hk) * c->page_size * c->D))
-    return KDA_ERR_INVALID_ARG;
+  // rows of the pool are int32
+  if (static_cast<int64_t>(c->pages) * c->Hk > 0x7fffffffLL / c->page_size) return KDA_ERR_INVALID_ARG;
   if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->pos || !c->weight)
     return KDA_ERR_INVALID_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||

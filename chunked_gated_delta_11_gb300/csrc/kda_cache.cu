@@ -66,6 +66,10 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float ratio) {
   return r[0] | (r[1] << 16);
 }
 
+__device__ __forceinline__ uint4 rescale16(const uint4& x, float ratio) {
+  return make_uint4(rescale4(x.x, ratio), rescale4(x.y, ratio), rescale4(x.z, ratio), rescale4(x.w, ratio));
+}
+
 // A page that gets rows: its id, its rows [lo, hi) that are new, the sequence slot
 // of its row 0, and the input row that goes to row lo.
 struct Touched {
@@ -224,8 +228,7 @@ append_few_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_b
   auto again = [&](uint8_t* d, float ratio) {
     for (int e = l; e < p.lo * 8; e += 32) {
       uint4* q = reinterpret_cast<uint4*>(d) + e;
-      const uint4 x = *q;
-      *q = make_uint4(rescale4(x.x, ratio), rescale4(x.y, ratio), rescale4(x.z, ratio), rescale4(x.w, ratio));
+      *q = rescale16(*q, ratio);
     }
   };
   if (p.lo > 0 && sk != oldk) again(dk, oldk * ik);
@@ -269,7 +272,8 @@ __device__ __forceinline__ uint32_t cluster_load(const uint32_t* local, unsigned
   return x;
 }
 
-// The kept slots of one (sequence, head), in order, into kept[unit * budget]: a
+// The rows (block * page + slot in it, -1: bad page) of the kept slots of one
+// (sequence, head), in order, into kept[unit * budget]: a
 // radix selection finds the key of the last slot to be kept (three passes of 11,
 // 11 and 10 bits), then one ordered pass writes the slots.  A cluster of CTAs
 // shares a unit, each with a stretch of its slots, whose keys stay in shared
@@ -281,7 +285,7 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
               int32_t* __restrict__ kept, int* __restrict__ err) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[2][SEL_BINS];  // alternate, so that a pass can be cleared while others read the last
-  __shared__ uint32_t warp_n[2][32];
+  __shared__ uint32_t warp_n[32];
   __shared__ uint32_t pick[2];   // digit chosen, how many of its slots are still to be kept
   __shared__ uint32_t count[2];  // this CTA's slots above and at the last key
   grid_dep_wait();
@@ -292,23 +296,31 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
   const int n = unit / c.Hk, h = unit - n * c.Hk;
   const int len = cached_len(c, n, err);
   if (h == 0 && t == 0 && rank == 0) new_lens[n] = len < budget ? len : budget;
-  if (len <= budget) return;  // everything stays, in place: no list (the same for the whole cluster)
-  const int old = len - recent, want = budget - recent;
   int32_t* list = kept + static_cast<int64_t>(unit) * budget;
-  for (int i = rank * SEL_THREADS + t; i < recent; i += cluster * SEL_THREADS) list[want + i] = old + i;
+  auto row_of = [&](int slot) -> int {
+    const int pid = page_id(c, n, slot >> c.lg, err);
+    return pid < 0 ? -1 : ((pid * c.Hk + h) << c.lg) + (slot & (c.page - 1));
+  };
+  // the newest, or everything (the same for the whole cluster)
+  const int old = len <= budget ? 0 : len - recent, want = len <= budget ? 0 : budget - recent;
+  for (int i = rank * SEL_THREADS + t; i < len - old; i += cluster * SEL_THREADS) list[want + i] = row_of(old + i);
   if (want == 0) return;
-  const int share = (old + cluster - 1) / cluster;
+  const int share = ((old + cluster - 1) / cluster + 3) & ~3;
   const int begin = old < static_cast<int>(rank) * share ? old : static_cast<int>(rank) * share;
   const int mine = old - begin < share ? old - begin : share;
-  auto read = [&](int i) -> uint32_t {
+  // keys of the 4 slots from i on (a multiple of 4: one page; those past `mine` are
+  // the page's own, and not used)
+  auto read4 = [&](int i) -> uint4 {
     const int pid = page_id(c, n, (begin + i) >> c.lg, err);
-    if (pid < 0) return 0u;
-    return weight_key(__ldg(c.weight + (static_cast<int64_t>(pid) * c.Hk + h) * c.page + ((begin + i) & (c.page - 1))));
+    if (pid < 0) return make_uint4(0u, 0u, 0u, 0u);
+    const float4 x = __ldg(reinterpret_cast<const float4*>(
+        c.weight + (static_cast<int64_t>(pid) * c.Hk + h) * c.page + ((begin + i) & (c.page - 1))));
+    return make_uint4(weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w));
   };
-  auto key_at = [&](int i) -> uint32_t { return i < SEL_KEYS ? keys[i] : read(i); };
+  auto keys4 = [&](int i) -> uint4 { return i < SEL_KEYS ? *reinterpret_cast<const uint4*>(keys + i) : read4(i); };
   for (int i = t; i < 2 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
 #pragma unroll 4
-  for (int i = t; i < mine && i < SEL_KEYS; i += SEL_THREADS) keys[i] = read(i);
+  for (int i = 4 * t; i < mine && i < SEL_KEYS; i += 4 * SEL_THREADS) *reinterpret_cast<uint4*>(keys + i) = read4(i);
   if (t < 2) count[t] = 0;
   __syncthreads();
   uint32_t last = 0, need = static_cast<uint32_t>(want);
@@ -318,9 +330,12 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
     const int bins = pass == 2 ? 1024 : 2048;
     uint32_t* hs = hist[pass & 1];
     const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + (pass == 1 ? 11 : 10));
-    for (int i = t; i < mine; i += SEL_THREADS) {
-      const uint32_t key = key_at(i);
-      if ((key & mask) == last) atomicAdd(&hs[(key >> shift) & (bins - 1)], 1u);
+    for (int i = 4 * t; i < mine; i += 4 * SEL_THREADS) {
+      const uint4 k = keys4(i);
+      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < mine && (key[e] & mask) == last) atomicAdd(&hs[(key[e] >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
     if (cluster > 1) cluster_sync_all();
@@ -338,9 +353,9 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
       const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
       if (l >= o) sum += x;
     }
-    if (l == 31) warp_n[0][w] = sum;
+    if (l == 31) warp_n[w] = sum;
     __syncthreads();
-    uint32_t before = warp_n[0][l];
+    uint32_t before = warp_n[l];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
@@ -367,10 +382,14 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
   uint32_t above0 = 0, ties0 = 0;  // in the stretches of lower ranks
   if (cluster > 1) {
     uint32_t g = 0, e = 0;
-    for (int i = t; i < mine; i += SEL_THREADS) {
-      const uint32_t key = key_at(i);
-      g += key > last;
-      e += key == last;
+    for (int i = 4 * t; i < mine; i += 4 * SEL_THREADS) {
+      const uint4 k = keys4(i);
+      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g += i + j < mine && key[j] > last;
+        e += i + j < mine && key[j] == last;
+      }
     }
     g = __reduce_add_sync(0xffffffffu, g);
     e = __reduce_add_sync(0xffffffffu, e);
@@ -386,96 +405,135 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
     }
     cluster_sync_all();  // nobody leaves while its counts are read
   }
-  uint32_t ties = ties0, base = above0 + (ties0 < need ? ties0 : need);
-  for (int i0 = 0; i0 < mine; i0 += SEL_THREADS) {
-    const int i = i0 + t;
-    const uint32_t key = i < mine ? key_at(i) : 0u;
-    const bool eq = i < mine && key == last, gt = i < mine && key > last;
-    const uint32_t be = __ballot_sync(0xffffffffu, eq), bg = __ballot_sync(0xffffffffu, gt);
-    if (l == 0) {
-      warp_n[0][w] = __popc(be);
-      warp_n[1][w] = __popc(bg);
+  // 4 slots a thread; (slots above, ties) of a stretch packed as 16 + 16 bits
+  uint32_t ties = ties0, base = above0;  // before the stretch: ties met, slots above
+  for (int i0 = 0; i0 < mine; i0 += 4 * SEL_THREADS) {
+    const int i = i0 + 4 * t;
+    uint32_t above4 = 0, tie4 = 0, own = 0;
+    if (i < mine) {
+      const uint4 k = keys4(i);
+      const uint32_t key[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        above4 |= (i + j < mine && key[j] > last ? 1u : 0u) << j;
+        tie4 |= (i + j < mine && key[j] == last ? 1u : 0u) << j;
+      }
+      own = (__popc(above4) << 16) | __popc(tie4);
     }
-    __syncthreads();
-    uint32_t e = warp_n[0][l], g = warp_n[1][l];
+    uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t a = __shfl_up_sync(0xffffffffu, e, o), b = __shfl_up_sync(0xffffffffu, g, o);
-      if (l >= o) {
-        e += a;
-        g += b;
-      }
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (l >= o) sum += x;
     }
-    const uint32_t etot = __shfl_sync(0xffffffffu, e, 31), gtot = __shfl_sync(0xffffffffu, g, 31);
-    const uint32_t ew = __shfl_sync(0xffffffffu, e, (w + 31) & 31), gw = __shfl_sync(0xffffffffu, g, (w + 31) & 31);
-    const uint32_t below = (1u << l) - 1u;
-    const uint32_t er = ties + (w ? ew : 0u) + __popc(be & below);  // ties before this slot
-    const uint32_t gr = (w ? gw : 0u) + __popc(bg & below);
-    const uint32_t eq_kept = er < need ? er : need;
-    const uint32_t ties_kept = ties < need ? ties : need;
-    if (gt || (eq && er < need)) list[base + gr + (eq_kept - ties_kept)] = begin + i;
-    const uint32_t ties1 = ties + etot < need ? ties + etot : need;
-    base += gtot + (ties1 - ties_kept);
-    ties += etot;
+    if (l == 31) warp_n[w] = sum;
+    __syncthreads();
+    uint32_t all = warp_n[l];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, all, o);
+      if (l >= o) all += x;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, all, 31);
+    const uint32_t before = (w ? __shfl_sync(0xffffffffu, all, w - 1) : 0u) + sum - own;
+    uint32_t g = base + (before >> 16), e = ties + (before & 0xffffu);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool gt = above4 >> j & 1u, eq = tie4 >> j & 1u;
+      if (gt || (eq && e < need)) list[g + (e < need ? e : need)] = row_of(begin + i + j);
+      g += gt;
+      e += eq;
+    }
+    base += total >> 16;
+    ties += total & 0xffffu;
     __syncthreads();
   }
 }
 
-// One CTA per (destination page, sequence, head), the page along grid.y: gathers
-// the page's rows.  A row is 8 threads of 16 codes.
-__global__ void __launch_bounds__(256)
+// A warp per (destination page, sequence, head), 4 pages of a unit per CTA: gathers
+// the page's rows, 8 lanes a row, 4 groups of 4 rows under way at a time.  What
+// bounds it is how many bytes are in flight, so the chain of lookups before the
+// rows (length, kept row) is short and shared by a whole page.
+template <int PAGE>
+__global__ void __launch_bounds__(128)
 pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int budget,
             const int32_t* __restrict__ kept, int* __restrict__ err) {
-  __shared__ int64_t src[128];  // source row (block * page + row), -1: bad page
-  __shared__ float sks[128], svs[128];
+  constexpr int LOOKS = (PAGE + 31) / 32;  // rows a lane looks up: lane, lane + 32, ..
+  constexpr int BATCH = PAGE / 4 < 4 ? PAGE / 4 : 4;
   grid_dep_wait();
   grid_dep_launch();
-  const int t = threadIdx.x, unit = blockIdx.x;
-  const int n = unit / c.Hk, h = unit - n * c.Hk;
+  const int l = threadIdx.x & 31, unit = blockIdx.x;
+  const int n = unit / static_cast<unsigned>(c.Hk), h = unit - n * c.Hk;
   const int len = cached_len(c, n, err), now = len < budget ? len : budget;
-  for (int j = blockIdx.y; (static_cast<int64_t>(j) << c.lg) < now; j += gridDim.y) {
-    const int first = j << c.lg;
-    const int rows = now - first < c.page ? now - first : c.page;
+  for (int j = blockIdx.y * 4 + (threadIdx.x >> 5); static_cast<int64_t>(j) * PAGE < now; j += gridDim.y * 4) {
+    const int first = j * PAGE;
+    const int rows = now - first < PAGE ? now - first : PAGE;
+    int from[LOOKS];  // source row (block * PAGE + row), -1: none
+#pragma unroll
+    for (int i = 0; i < LOOKS; ++i) {
+      const int r = l + 32 * i;
+      from[i] = r < rows ? __ldg(kept + static_cast<int64_t>(unit) * budget + first + r) : -1;
+    }
     const int dp = j < dst_width ? __ldg(dst + static_cast<int64_t>(n) * dst_width + j) : -1;
     if (dp < 0 || dp >= c.pages) {
-      if (t == 0) atomicCAS(err, 0, static_cast<int>(KDA_ERR_INVALID_ARG));
+      if (l == 0) atomicCAS(err, 0, static_cast<int>(KDA_ERR_INVALID_ARG));
       continue;
     }
     const int64_t block = static_cast<int64_t>(dp) * c.Hk + h;
-    __syncthreads();  // the last page's rows are no longer read
-    if (t < rows) {
-      const int i = len <= budget ? first + t : kept[static_cast<int64_t>(unit) * budget + first + t];
-      const int pid = page_id(c, n, i >> c.lg, err);
-      src[t] = -1;
-      sks[t] = svs[t] = 0.f;
-      if (pid >= 0) {
-        const int64_t b = static_cast<int64_t>(pid) * c.Hk + h;
-        const int64_t r = b * c.page + (i & (c.page - 1));
-        src[t] = r;
-        sks[t] = c.ks[b];
-        svs[t] = c.vs[b];
-        c.pos[block * c.page + t] = c.pos[r];
-        c.weight[block * c.page + t] = c.weight[r];
+    float fk[LOOKS], fv[LOOKS], mk = 0.f, mv = 0.f;
+#pragma unroll
+    for (int i = 0; i < LOOKS; ++i) {
+      fk[i] = from[i] < 0 ? 0.f : c.ks[from[i] / PAGE];
+      fv[i] = from[i] < 0 ? 0.f : c.vs[from[i] / PAGE];
+      mk = fmaxf(mk, fk[i]);
+      mv = fmaxf(mv, fv[i]);
+    }
+    const uint8_t* ck = c.k + (l & 7) * 16;
+    const uint8_t* cv = c.v + (l & 7) * 16;
+#pragma unroll
+    for (int g0 = 0; g0 < PAGE / 4; g0 += BATCH) {
+      if (g0 * 4 >= rows) break;
+      uint4 a[BATCH], b[BATCH];
+      int sr[BATCH];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int r = 4 * (g0 + i) + (l >> 3);  // looked up by lane r & 31
+        sr[i] = __shfl_sync(0xffffffffu, from[(4 * (g0 + i)) / 32], r & 31);
+        if (sr[i] >= 0) {
+          a[i] = *reinterpret_cast<const uint4*>(ck + static_cast<int64_t>(sr[i]) * kDim);
+          b[i] = *reinterpret_cast<const uint4*>(cv + static_cast<int64_t>(sr[i]) * kDim);
+        }
+      }
+      if (g0 == 0) {
+        // the maxima are not negative: their order is that of their bits
+        mk = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mk)));
+        mv = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mv)));
+#pragma unroll
+        for (int i = 0; i < LOOKS; ++i) {
+          fk[i] = fk[i] == mk ? 1.f : fk[i] / mk;
+          fv[i] = fv[i] == mv ? 1.f : fv[i] / mv;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int r = 4 * (g0 + i) + (l >> 3);
+        const float rk = __shfl_sync(0xffffffffu, fk[(4 * (g0 + i)) / 32], r & 31);
+        const float rv = __shfl_sync(0xffffffffu, fv[(4 * (g0 + i)) / 32], r & 31);
+        if (sr[i] < 0) continue;
+        if (rk != 1.f) a[i] = rescale16(a[i], rk);
+        if (rv != 1.f) b[i] = rescale16(b[i], rv);
+        const int64_t to = (block * PAGE + r) * kDim + (l & 7) * 16;
+        *reinterpret_cast<uint4*>(c.k + to) = a[i];
+        *reinterpret_cast<uint4*>(c.v + to) = b[i];
       }
     }
-    __syncthreads();
-    float mk = 0.f, mv = 0.f;
-    for (int r = 0; r < rows; ++r) {
-      mk = fmaxf(mk, sks[r]);
-      mv = fmaxf(mv, svs[r]);
+#pragma unroll
+    for (int i = 0; i < LOOKS; ++i) {
+      if (from[i] < 0) continue;
+      c.pos[block * PAGE + l + 32 * i] = c.pos[from[i]];
+      c.weight[block * PAGE + l + 32 * i] = c.weight[from[i]];
     }
-    const int sub = (t & 7) * 16;
-    for (int r = t >> 3; r < rows; r += 32) {
-      if (src[r] < 0) continue;
-      const uint4 a = *reinterpret_cast<const uint4*>(c.k + src[r] * kDim + sub);
-      const uint4 b = *reinterpret_cast<const uint4*>(c.v + src[r] * kDim + sub);
-      const float fk = mk > 0.f ? sks[r] / mk : 1.f, fv = mv > 0.f ? svs[r] / mv : 1.f;
-      uint4* ok = reinterpret_cast<uint4*>(c.k + (block * c.page + r) * kDim + sub);
-      uint4* ov = reinterpret_cast<uint4*>(c.v + (block * c.page + r) * kDim + sub);
-      *ok = fk == 1.f ? a : make_uint4(rescale4(a.x, fk), rescale4(a.y, fk), rescale4(a.z, fk), rescale4(a.w, fk));
-      *ov = fv == 1.f ? b : make_uint4(rescale4(b.x, fv), rescale4(b.y, fv), rescale4(b.z, fv), rescale4(b.w, fv));
-    }
-    if (t == 0) {
+    if (l == 0) {
       c.ks[block] = mk;
       c.vs[block] = mv;
     }
@@ -519,7 +577,7 @@ cudaError_t launch_cache_evict(const CacheArgs& c, const int32_t* dst, int dst_w
   // CTAs per unit: up to 8 while that leaves SMs idle and gives each 2048 slots
   int cluster = 1;
   while (cluster < SEL_MAX_CLUSTER && units * 2u * cluster <= 2u * 152u && most > 4096LL * cluster) cluster *= 2;
-  const int64_t share = (most + cluster - 1) / cluster;
+  const int64_t share = ((most + cluster - 1) / cluster + 3) & ~3LL;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * cluster);
   cfg.blockDim = dim3(SEL_THREADS);
@@ -538,8 +596,10 @@ cudaError_t launch_cache_evict(const CacheArgs& c, const int32_t* dst, int dst_w
   // pages that the kept rows can need, whatever the destination table's width
   const int64_t rows = budget < most ? budget : most;
   const unsigned pages = static_cast<unsigned>((rows + c.page - 1) >> c.lg);
-  return launch_pdl(pack_kernel, dim3(units, pages < 65535u ? pages : 65535u), dim3(256), 0, stream, c, dst,
-                    dst_width, budget, static_cast<const int32_t*>(kept), err);
+  auto pack = c.page == 16 ? pack_kernel<16> : c.page == 32 ? pack_kernel<32>
+              : c.page == 64 ? pack_kernel<64> : pack_kernel<128>;
+  return launch_pdl(pack, dim3(units, (pages + 3) / 4 < 65535u ? (pages + 3) / 4 : 65535u), dim3(128), 0, stream, c, dst, dst_width,
+                    budget, static_cast<const int32_t*>(kept), err);
 }
 
 }  // namespace kda

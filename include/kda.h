@@ -449,7 +449,8 @@ kda_status kda_attn_fwd(const kda_attn_options* opts, const void* q, const void*
 
 /* A pool of cache pages.  A page has page_size token slots (16, 32, 64 or 128)
  * of every KV head; the slots of one (page, KV head) are a block of e4m3 codes
- * with one scale, code * scale being the value.  All arrays are the caller's. */
+ * with one scale, code * scale being the value.  pages * Hk * page_size is below
+ * 2^31.  All arrays are the caller's. */
 typedef struct {
   void* k;        /* e4m3 [pages, Hk, page_size, D] */
   void* v;        /* e4m3 [pages, Hk, page_size, D] */
