@@ -250,8 +250,9 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-constexpr int SEL_THREADS = 1024;
+constexpr int SEL_THREADS = 512;
 constexpr int SEL_BINS = 2048;
+constexpr int SEL_PER = SEL_BINS / SEL_THREADS;  // bins per thread
 constexpr int SEL_KEYS = 32768;  // keys that a CTA can hold
 constexpr int SEL_SMEM = SEL_KEYS * 4;
 constexpr int SEL_MAX_CLUSTER = 8;
@@ -280,7 +281,7 @@ __device__ __forceinline__ uint32_t cluster_load(const uint32_t* local, unsigned
 // memory (the first SEL_KEYS of them; the rest are read again); the histograms
 // and counts are summed through distributed shared memory.  What bounds it is the
 // latency of the passes, so few long sequences get the largest cluster.
-__global__ void __launch_bounds__(SEL_THREADS)
+__global__ void __launch_bounds__(SEL_THREADS, 2)
 select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restrict__ new_lens,
               int32_t* __restrict__ kept, int* __restrict__ err) {
   extern __shared__ __align__(16) uint32_t keys[];
@@ -339,15 +340,19 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
     }
     __syncthreads();
     if (cluster > 1) cluster_sync_all();
-    // two bins per thread, from the top: thread t has bins - 1 - 2 t and the one below
-    const int hi = SEL_BINS - 1 - 2 * t;
-    uint32_t a = hs[hi], b = hs[hi - 1];
+    // SEL_PER bins per thread, from the top
+    const int hi = SEL_BINS - 1 - SEL_PER * t;
+    uint32_t bin[SEL_PER], own = 0;
+#pragma unroll
+    for (int i = 0; i < SEL_PER; ++i) bin[i] = hs[hi - i];
     for (int r = 1; r < cluster; ++r) {
       const unsigned other = (rank + r) % static_cast<unsigned>(cluster);
-      a += cluster_load(&hs[hi], other);
-      b += cluster_load(&hs[hi - 1], other);
+#pragma unroll
+      for (int i = 0; i < SEL_PER; ++i) bin[i] += cluster_load(&hs[hi - i], other);
     }
-    uint32_t sum = a + b;
+#pragma unroll
+    for (int i = 0; i < SEL_PER; ++i) own += bin[i];
+    uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -355,20 +360,21 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
     }
     if (l == 31) warp_n[w] = sum;
     __syncthreads();
-    uint32_t before = warp_n[l];
+    uint32_t before = l < SEL_THREADS / 32 ? warp_n[l] : 0u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
       if (l >= o) before += x;
     }
     before = w ? __shfl_sync(0xffffffffu, before, w - 1) : 0u;
-    const uint32_t above = before + sum - a - b;  // slots in bins above this thread's
-    if (above < need && need <= above + a) {
-      pick[0] = hi;
-      pick[1] = need - above;
-    } else if (above + a < need && need <= above + a + b) {
-      pick[0] = hi - 1;
-      pick[1] = need - above - a;
+    uint32_t above = before + sum - own;  // slots in bins above this one
+#pragma unroll
+    for (int i = 0; i < SEL_PER; ++i) {
+      if (above < need && need <= above + bin[i]) {
+        pick[0] = hi - i;
+        pick[1] = need - above;
+      }
+      above += bin[i];
     }
     __syncthreads();
     last |= pick[0] << shift;
@@ -428,7 +434,7 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
     }
     if (l == 31) warp_n[w] = sum;
     __syncthreads();
-    uint32_t all = warp_n[l];
+    uint32_t all = l < SEL_THREADS / 32 ? warp_n[l] : 0u;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, all, o);
@@ -453,19 +459,23 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
 // A warp per (destination page, sequence, head), 4 pages of a unit per CTA: gathers
 // the page's rows, 8 lanes a row, 4 groups of 4 rows under way at a time.  What
 // bounds it is how many bytes are in flight, so the chain of lookups before the
-// rows (length, kept row) is short and shared by a whole page.
-template <int PAGE>
+// rows (length, kept row) is short and shared by a whole page.  SPLIT = 4: the 4
+// warps share a page, for calls with fewer pages than warps that fit the GPU.
+template <int PAGE, int SPLIT>
 __global__ void __launch_bounds__(128)
 pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int budget,
             const int32_t* __restrict__ kept, int* __restrict__ err) {
   constexpr int LOOKS = (PAGE + 31) / 32;  // rows a lane looks up: lane, lane + 32, ..
-  constexpr int BATCH = PAGE / 4 < 4 ? PAGE / 4 : 4;
+  constexpr int GROUPS = PAGE / 4 / SPLIT;  // of 4 rows: the warp's part, + SPLIT, ..
+  constexpr int BATCH = GROUPS < 4 ? GROUPS : 4;
   grid_dep_wait();
   grid_dep_launch();
   const int l = threadIdx.x & 31, unit = blockIdx.x;
   const int n = unit / static_cast<unsigned>(c.Hk), h = unit - n * c.Hk;
   const int len = cached_len(c, n, err), now = len < budget ? len : budget;
-  for (int j = blockIdx.y * 4 + (threadIdx.x >> 5); static_cast<int64_t>(j) * PAGE < now; j += gridDim.y * 4) {
+  const int w = threadIdx.x >> 5, part = SPLIT == 1 ? 0 : w;
+  const int step = gridDim.y * (4 / SPLIT);
+  for (int j = blockIdx.y * (4 / SPLIT) + (SPLIT == 1 ? w : 0); static_cast<int64_t>(j) * PAGE < now; j += step) {
     const int first = j * PAGE;
     const int rows = now - first < PAGE ? now - first : PAGE;
     int from[LOOKS];  // source row (block * PAGE + row), -1: none
@@ -491,14 +501,14 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
     const uint8_t* ck = c.k + (l & 7) * 16;
     const uint8_t* cv = c.v + (l & 7) * 16;
 #pragma unroll
-    for (int g0 = 0; g0 < PAGE / 4; g0 += BATCH) {
-      if (g0 * 4 >= rows) break;
+    for (int g0 = 0; g0 < GROUPS; g0 += BATCH) {
+      if (g0 * SPLIT * 4 >= rows) break;
       uint4 a[BATCH], b[BATCH];
       int sr[BATCH];
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int r = 4 * (g0 + i) + (l >> 3);  // looked up by lane r & 31
-        sr[i] = __shfl_sync(0xffffffffu, from[(4 * (g0 + i)) / 32], r & 31);
+        const int r = 4 * ((g0 + i) * SPLIT + part) + (l >> 3);  // looked up by lane r & 31
+        sr[i] = __shfl_sync(0xffffffffu, from[4 * (g0 + i) * SPLIT / 32], r & 31);
         if (sr[i] >= 0) {
           a[i] = *reinterpret_cast<const uint4*>(ck + static_cast<int64_t>(sr[i]) * kDim);
           b[i] = *reinterpret_cast<const uint4*>(cv + static_cast<int64_t>(sr[i]) * kDim);
@@ -516,9 +526,9 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
       }
 #pragma unroll
       for (int i = 0; i < BATCH; ++i) {
-        const int r = 4 * (g0 + i) + (l >> 3);
-        const float rk = __shfl_sync(0xffffffffu, fk[(4 * (g0 + i)) / 32], r & 31);
-        const float rv = __shfl_sync(0xffffffffu, fv[(4 * (g0 + i)) / 32], r & 31);
+        const int r = 4 * ((g0 + i) * SPLIT + part) + (l >> 3);
+        const float rk = __shfl_sync(0xffffffffu, fk[4 * (g0 + i) * SPLIT / 32], r & 31);
+        const float rv = __shfl_sync(0xffffffffu, fv[4 * (g0 + i) * SPLIT / 32], r & 31);
         if (sr[i] < 0) continue;
         if (rk != 1.f) a[i] = rescale16(a[i], rk);
         if (rv != 1.f) b[i] = rescale16(b[i], rv);
@@ -529,15 +539,30 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
     }
 #pragma unroll
     for (int i = 0; i < LOOKS; ++i) {
-      if (from[i] < 0) continue;
+      if (from[i] < 0 || part != 0) continue;
       c.pos[block * PAGE + l + 32 * i] = c.pos[from[i]];
       c.weight[block * PAGE + l + 32 * i] = c.weight[from[i]];
     }
-    if (l == 0) {
+    if (l == 0 && part == 0) {
       c.ks[block] = mk;
       c.vs[block] = mv;
     }
   }
+}
+
+template <int PAGE>
+cudaError_t launch_pack(const CacheArgs& c, const int32_t* dst, int dst_width, int budget,
+                        const int32_t* kept, int* err, cudaStream_t stream) {
+  // pages that the kept rows can need, whatever the destination table's width
+  const int64_t most = static_cast<int64_t>(c.width) << c.lg;
+  const int64_t rows = budget < most ? budget : most;
+  const int64_t pages = (rows + PAGE - 1) / PAGE;
+  const unsigned units = static_cast<unsigned>(c.N) * static_cast<unsigned>(c.Hk);
+  const bool split = pages * units < 152 * 24;  // 24 warps of 80 registers per SM
+  const int64_t y = split ? pages : (pages + 3) / 4;
+  return launch_pdl(split ? pack_kernel<PAGE, 4> : pack_kernel<PAGE, 1>,
+                    dim3(units, static_cast<unsigned>(y < 65535 ? y : 65535)), dim3(128), 0, stream, c, dst, dst_width,
+                    budget, kept, err);
 }
 
 template <int PAGE>
@@ -593,13 +618,12 @@ cudaError_t launch_cache_evict(const CacheArgs& c, const int32_t* dst, int dst_w
   cfg.numAttrs = 2;
   if ((e = cudaLaunchKernelEx(&cfg, select_kernel, c, budget, recent, cluster, new_lens, kept, err)) != cudaSuccess)
     return e;
-  // pages that the kept rows can need, whatever the destination table's width
-  const int64_t rows = budget < most ? budget : most;
-  const unsigned pages = static_cast<unsigned>((rows + c.page - 1) >> c.lg);
-  auto pack = c.page == 16 ? pack_kernel<16> : c.page == 32 ? pack_kernel<32>
-              : c.page == 64 ? pack_kernel<64> : pack_kernel<128>;
-  return launch_pdl(pack, dim3(units, (pages + 3) / 4 < 65535u ? (pages + 3) / 4 : 65535u), dim3(128), 0, stream, c, dst, dst_width,
-                    budget, static_cast<const int32_t*>(kept), err);
+  switch (c.page) {
+    case 16: return launch_pack<16>(c, dst, dst_width, budget, kept, err, stream);
+    case 32: return launch_pack<32>(c, dst, dst_width, budget, kept, err, stream);
+    case 64: return launch_pack<64>(c, dst, dst_width, budget, kept, err, stream);
+    default: return launch_pack<128>(c, dst, dst_width, budget, kept, err, stream);
+  }
 }
 
 }  // namespace kda
