@@ -93,6 +93,75 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// Pairs of fp32 in one operation (same rate per value, half the issue slots).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 pair(const uint32_t& lo, const uint32_t& hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(f2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ void unpair(f2 x, uint32_t& lo, uint32_t& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(x));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+      m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+__device__ __forceinline__ float row_min(const uint32_t (&s)[4][32]) {
+  float m[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int e = 0; e < 32; e += 2)
+      m[(e >> 1) & 3] = min3(m[(e >> 1) & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+  return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
+}
+
+// tanh(y) = y Q(y^2) for |y| <= 1, Q of degree 5, fitted for the least maximum
+// error of y Q (2.4e-7; 3.2e-7 with fp32 rounding): the error of the form with an
+// exponential and a reciprocal, without their 3 slots of the special-function
+// unit, which a capped score otherwise spends most of its time on.
+__device__ constexpr float kTanh[6] = {0.99999685f, -0.33324004f, 0.13253525f,
+                                       -0.05097286f, 0.01611418f, -0.00283946f};
+
 // What a query tile of a sequence sees.
 struct TileView {
   int len, prefix, mask;
@@ -285,9 +354,8 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     const int limit = view.limit(i);
     const int tile_lo = view.limit(i0 + t * AT_ROWS);  // least limit of the tile's rows
     const float slope = BIAS && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
-    // CAP: x log2 e = c2 - 2 c2 / (1 + 2^(c1 s)); the constant c2 cancels in the softmax
-    const float c1 = CAP ? a.scale * 2.f * kLog2e / a.cap : a.scale * kLog2e;
-    const float c2 = CAP ? -2.f * a.cap * kLog2e : 0.f;
+    const float c1 = a.scale * kLog2e;
+    const float cap2 = CAP ? a.cap * kLog2e : 0.f, per_cap = CAP ? a.scale / a.cap : 0.f;
     float ref = -INFINITY, sum = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -299,13 +367,39 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       for (int c = 0; c < 4; ++c) tmem_ld32(S + c * 32, s[c]);
       tmem_wait_ld();
       const int j0 = j * AT_ROWS;
-      float base = 0.f;  // added to every score of the row
+      const bool masked = j0 + AT_ROWS > tile_lo;  // the same for the warp
+      float base = 0.f, top = 0.f;                 // base: added to every score of the row
       if (CAP) {
+        bool small = false;  // all of the warp's scores below the cap: the polynomial holds
+        if (!masked) {
+          top = row_max(s);
+          const float low = row_min(s);
+          small = __all_sync(0xffffffffu, fmaxf(fabsf(top), fabsf(low)) * fabsf(per_cap) <= 1.0f);
+        }
+        const f2 pc = pair(per_cap, per_cap);
+        f2 q[6];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int k = 0; k < 6; ++k) q[k] = pair(kTanh[k] * cap2, kTanh[k] * cap2);
+        const float e1 = per_cap * 2.f * kLog2e;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            s[c][e] = __float_as_uint(c2 * rcp_approx(1.0f + ex2_approx(__uint_as_float(s[c][e]) * c1)));
+        for (int c = 0; c < 4; ++c) {
+          // one quarter by the special-function unit, so that both have work
+          if (small && c < 3) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const f2 y = mul2(pair(s[c][e], s[c][e + 1]), pc), u = mul2(y, y);
+              f2 p = fma2(u, q[5], q[4]);
+#pragma unroll
+              for (int k = 3; k >= 0; --k) p = fma2(u, p, q[k]);
+              unpair(mul2(y, p), s[c][e], s[c][e + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              s[c][e] = __float_as_uint(cap_log2(__uint_as_float(s[c][e]), e1, cap2));
+          }
+        }
+        top = cap_log2(top, e1, cap2);  // rises with the score (scale > 0 unless BIAS)
       }
       if (BIAS) {
         const float mul = CAP ? 1.f : c1;
@@ -315,11 +409,16 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           // one side of the diagonal: the distance is linear in the column
           const float step = lo > 0 ? slope : -slope;
           base = lo > 0 ? -slope * static_cast<float>(d) : slope * static_cast<float>(d);
+          const f2 m2 = pair(mul, mul), up = pair(2.f * step, 2.f * step);
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            f2 at = pair(step * (32.f * c), step * (32.f * c + 1.f));
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[c][e] = __float_as_uint(fmaf(__uint_as_float(s[c][e]), mul, step * static_cast<float>(c * 32 + e)));
+            for (int e = 0; e < 32; e += 2) {
+              unpair(fma2(pair(s[c][e], s[c][e + 1]), m2, at), s[c][e], s[c][e + 1]);
+              at = add2(at, up);
+            }
+          }
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -329,7 +428,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
                                              __uint_as_float(s[c][e]) * mul));
         }
       }
-      if (j0 + AT_ROWS > tile_lo) {
+      if (masked) {
         const int left = limit - j0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -337,13 +436,8 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           for (int e = 0; e < 32; ++e)
             if (c * 32 + e >= left) s[c][e] = 0xff800000u;  // -inf
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[c][e]));
-      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       constexpr bool SCALED = !CAP && !BIAS;  // scores still to be multiplied by c1 (> 0)
+      if (!CAP || BIAS || masked) top = row_max(s);
       top = SCALED ? top * c1 : top + base;
       const bool grow = top > ref + AT_GROW;  // ref = -inf: any finite maximum
       if (__any_sync(0xffffffffu, grow)) {
@@ -365,22 +459,26 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       }
       // nothing seen yet: every weight is 0
       const float sub = (ref == -INFINITY ? 0.f : ref) - base;
-      float part[4] = {0.f, 0.f, 0.f, 0.f};
+      const f2 mul = pair(SCALED ? c1 : 1.f, SCALED ? c1 : 1.f), off = pair(-sub, -sub);
+      f2 part[2] = {0ull, 0ull};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float x = __uint_as_float(s[c][e]), y = __uint_as_float(s[c][e + 1]);
-          const float p0 = ex2_approx(SCALED ? fmaf(x, c1, -sub) : x - sub);
-          const float p1 = ex2_approx(SCALED ? fmaf(y, c1, -sub) : y - sub);
-          part[e & 2] += p0;
-          part[(e & 2) + 1] += p1;
+          const f2 x = pair(s[c][e], s[c][e + 1]);
+          float p0, p1;
+          unpair(SCALED ? fma2(x, mul, off) : add2(x, off), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pair(p0, p1));
           pk[e >> 1] = pack_bf16(p0, p1);
         }
         tmem_st16(S + c * 16, pk);
       }
-      sum += (part[0] + part[1]) + (part[2] + part[3]);
+      float s0, s1;
+      unpair(add2(part[0], part[1]), s0, s1);
+      sum += s0 + s1;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&ctl->p_full[t]);
