@@ -24,6 +24,8 @@
 // visible key are skipped, and only tiles that cross a row's limit select.
 // Rows of V past the sequence's end (another sequence's, whatever they hold)
 // are overwritten with zeros in shared memory before the product.
+#include <type_traits>
+
 #include "kda_attn.cuh"
 #include "kda_tma.cuh"
 
@@ -36,8 +38,8 @@ constexpr int AT_TILE = AT_ROWS * kDim * 2;    // bytes of a tile (two boxes of 
 constexpr int AT_BOX = AT_TILE / 2;
 constexpr int AT_THREADS = 384;
 // three warpgroups of 168 registers a thread at launch; the softmax ones (a row of
-// 128 scores in registers) take from the third: 2 x 232 + 40 = 3 x 168
-constexpr int AT_REGS_SOFTMAX = 232, AT_REGS_ISSUE = 40;
+// 128 scores in registers) take from the third: 2 x 224 + 56 = 3 x 168
+constexpr int AT_REGS_SOFTMAX = 224, AT_REGS_ISSUE = 56;
 constexpr int AT_Q = 0, AT_K = 2 * AT_TILE, AT_V = 4 * AT_TILE, AT_CTL = 6 * AT_TILE;
 constexpr int AT_SMEM = AT_CTL + 256 + 1024;
 constexpr float AT_GROW = 8.0f;                // how far a maximum may outgrow the reference
@@ -82,14 +84,46 @@ __device__ __forceinline__ void regs_give() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-// D (tmem, fp32) (+)= A (smem) * B (smem); bf16, one K = 16 step.
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// One K = 16 step, bf16: D (tmem, fp32) (+)= A * B with B in shared memory and A in
+// shared memory (ss) or tensor memory (ts).  A descriptor is a low word (address
+// and leading offset) plus a constant step, and a high word; putting it together
+// inside keeps 16 steps' descriptors from being held in registers (or spilled).
+template <uint32_t STEP_A, uint32_t STEP_B>
+__device__ __forceinline__ void mma_ss_step(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "add.u32 x, %1, %2;\n\t"
+      "add.u32 y, %3, %4;\n\t"
+      "mov.b64 a, {x, %5};\n\t"
+      "mov.b64 b, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %6, p;\n\t}\n" ::"r"(d),
+      "r"(a_lo), "n"(STEP_A), "r"(b_lo), "n"(STEP_B), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <uint32_t STEP_A, uint32_t STEP_B>
+__device__ __forceinline__ void mma_ts_step(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %7, 0;\n\t"
+      "add.u32 x, %1, %2;\n\t"
+      "add.u32 y, %3, %4;\n\t"
+      "mov.b64 b, {y, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %6, p;\n\t}\n" ::"r"(d),
+      "r"(a_tmem), "n"(STEP_A), "r"(b_lo), "n"(STEP_B), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -272,72 +306,92 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       const uint32_t sb = smem_u32(smem);
       constexpr uint32_t id_s = make_idesc(1, AT_ROWS, AT_ROWS);
       constexpr uint32_t id_o = make_idesc(1, AT_ROWS, kDim) | (1u << 16);  // B is MN-major
-      auto issue_s = [&](int t, int j) {
-        if (l == 0) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t off = (k >> 2) * AT_BOX + (k & 3) * 32;
-            mma_bf16_ss(tmem + t * 128, make_sdesc(sb + AT_Q + t * AT_TILE + off, 16, 1024, 2),
-                        make_sdesc(sb + AT_K + (j & 1) * AT_TILE + off, 16, 1024, 2), id_s, k > 0);
-          }
-        }
+      // One lane issues.  Descriptors are stepped by constants (stage and tile are
+      // template values): worked out from the loop's variables they take the lane
+      // twice as long as the products themselves.
+      const bool one = elect_one();
+      const uint64_t qk_desc = make_sdesc(sb, 16, 1024, 2), v_desc = make_sdesc(sb + AT_V, AT_BOX, 1024, 2);
+      const uint32_t qk_lo = static_cast<uint32_t>(qk_desc), v_lo = static_cast<uint32_t>(v_desc);
+      const uint32_t desc_hi = static_cast<uint32_t>(qk_desc >> 32);  // the same for both
+      auto issue_s = [&](auto tile, auto stage) {
+        constexpr uint32_t q = (AT_Q + tile.value * AT_TILE) >> 4, k = (AT_K + stage.value * AT_TILE) >> 4;
+        constexpr uint32_t B = AT_BOX >> 4;
+        const uint32_t d = tmem + tile.value * 128;
+        mma_ss_step<q, k>(d, qk_lo, qk_lo, desc_hi, id_s, 0);
+        mma_ss_step<q + 2, k + 2>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
+        mma_ss_step<q + 4, k + 4>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
+        mma_ss_step<q + 6, k + 6>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
+        mma_ss_step<q + B, k + B>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
+        mma_ss_step<q + B + 2, k + B + 2>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
+        mma_ss_step<q + B + 4, k + B + 4>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
+        mma_ss_step<q + B + 6, k + B + 6>(d, qk_lo, qk_lo, desc_hi, id_s, 1);
       };
       // 16 keys a step: two groups of 8 rows of 128 bytes; channels 64.. one box further
-      auto issue_o = [&](int t, int j, int steps) {
-        if (l == 0) {
-          for (int k = 0; k < steps; ++k)
-            mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8,
-                        make_sdesc(sb + AT_V + (j & 1) * AT_TILE + k * 2048, AT_BOX, 1024, 2), id_o, j > 0 || k > 0);
-        }
+      auto issue_o = [&](auto tile, auto stage, bool add, int steps) {
+        constexpr uint32_t p = tile.value * 128, v = stage.value * (AT_TILE >> 4);
+        const uint32_t o = tmem + 256 + p;
+        mma_ts_step<p, v>(o, tmem, v_lo, desc_hi, id_o, add);
+        if (steps > 1) mma_ts_step<p + 8, v + 128>(o, tmem, v_lo, desc_hi, id_o, 1);
+        if (steps > 2) mma_ts_step<p + 16, v + 256>(o, tmem, v_lo, desc_hi, id_o, 1);
+        if (steps > 3) mma_ts_step<p + 24, v + 384>(o, tmem, v_lo, desc_hi, id_o, 1);
+        if (steps > 4) mma_ts_step<p + 32, v + 512>(o, tmem, v_lo, desc_hi, id_o, 1);
+        if (steps > 5) mma_ts_step<p + 40, v + 640>(o, tmem, v_lo, desc_hi, id_o, 1);
+        if (steps > 6) mma_ts_step<p + 48, v + 768>(o, tmem, v_lo, desc_hi, id_o, 1);
+        if (steps > 7) mma_ts_step<p + 56, v + 896>(o, tmem, v_lo, desc_hi, id_o, 1);
       };
       auto commit = [&](uint64_t* bar) {
-        if (l == 0) tc_commit(bar);
+        if (one) tc_commit(bar);
         __syncwarp();
       };
+      using N0 = std::integral_constant<uint32_t, 0>;
+      using N1 = std::integral_constant<uint32_t, 1>;
       bool ok = warp_wait(&ctl->k_full[0], 0, ctl, err) && warp_wait(&ctl->q_full, 0, ctl, err);
       if (ok) {
         tc_fence_after();
-        issue_s(0, 0);
+        if (one) issue_s(N0{}, N0{});
         commit(&ctl->s_full[0]);
         if (n1 > 0) {
-          issue_s(1, 0);
+          if (one) issue_s(N1{}, N0{});
           commit(&ctl->s_full[1]);
         }
         commit(&ctl->k_empty[0]);
-        for (int j = 0; j < nj; ++j) {
-          ok = warp_wait(&ctl->v_full[j & 1], (j >> 1) & 1, ctl, err);
-          if (!ok) break;
+        // key tile j in stage `stage`; false once a wait has run out
+        auto body = [&](int j, auto stage, auto next) -> bool {
+          constexpr uint32_t st = stage.value;
+          if (!warp_wait(&ctl->v_full[st], (j >> 1) & 1, ctl, err)) return false;
           const int left = view.len - j * AT_ROWS;
           const int steps = left >= AT_ROWS ? AT_ROWS / 16 : (left + 15) / 16;
           if (left < steps * 16) {
             // zeros in the rows between the sequence's end and the last step's
             for (int e = l; e < (steps * 16 - left) * 16; e += 32) {
               const int off = (e & 8 ? AT_BOX : 0) + (left + (e >> 4)) * 128 + (e & 7) * 16;
-              *reinterpret_cast<uint4*>(smem + AT_V + (j & 1) * AT_TILE + off) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(smem + AT_V + st * AT_TILE + off) = make_uint4(0, 0, 0, 0);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
           }
-          if (j + 1 < nj) {
-            ok = warp_wait(&ctl->k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, ctl, err);
-            if (!ok) break;
-          }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int nt = t == 0 ? n0 : n1;
-            if (j < nt) {
-              ok = warp_wait(&ctl->p_full[t], j & 1, ctl, err);
-              if (!ok) break;
-              tc_fence_after();
-              issue_o(t, j, steps);
+          if (j + 1 < nj && !warp_wait(&ctl->k_full[next.value], ((j + 1) >> 1) & 1, ctl, err)) return false;
+          auto tile = [&](auto which, int nt) -> bool {
+            if (j >= nt) return true;
+            constexpr uint32_t t = which.value;
+            if (!warp_wait(&ctl->p_full[t], j & 1, ctl, err)) return false;
+            tc_fence_after();
+            if (one) {
+              issue_o(which, stage, j > 0, steps);
               // the tensor core runs these in order: S may follow into the columns P is read from
-              if (j + 1 < nt) issue_s(t, j + 1);
-              commit(&ctl->s_full[t]);
+              if (j + 1 < nt) issue_s(which, next);
             }
-          }
-          if (!ok) break;
-          commit(&ctl->v_empty[j & 1]);
-          if (j + 1 < nj) commit(&ctl->k_empty[(j + 1) & 1]);
+            commit(&ctl->s_full[t]);
+            return true;
+          };
+          if (!tile(N0{}, n0) || !tile(N1{}, n1)) return false;
+          commit(&ctl->v_empty[st]);
+          if (j + 1 < nj) commit(&ctl->k_empty[next.value]);
+          return true;
+        };
+        for (int j = 0; j < nj; j += 2) {
+          if (!body(j, N0{}, N1{})) break;
+          if (j + 1 < nj && !body(j + 1, N1{}, N0{})) break;
         }
       }
       // nothing may be running in tensor memory when it is freed
