@@ -189,12 +189,12 @@ __device__ __forceinline__ float row_min(const uint32_t (&s)[4][32]) {
   return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
 }
 
-// tanh(y) = y Q(y^2) for |y| <= 1, Q of degree 5, fitted for the least maximum
-// error of y Q (2.4e-7; 3.2e-7 with fp32 rounding): the error of the form with an
-// exponential and a reciprocal, without their 3 slots of the special-function
-// unit, which a capped score otherwise spends most of its time on.
-__device__ constexpr float kTanh[6] = {0.99999685f, -0.33324004f, 0.13253525f,
-                                       -0.05097286f, 0.01611418f, -0.00283946f};
+// tanh(y) = y Q(y^2) for |y| <= 1, Q of degree 4, fitted for the least maximum
+// error of y Q: 2.8e-6, which moves a capped score by 1.4e-4 at a cap of 50 and so a
+// weight by a sixteenth of its bf16 rounding.  Six paired multiply-adds for two
+// scores, where an exponential and a reciprocal take 24 cycles of a special-function
+// unit that a tile's 128 weights keep busy already.
+__device__ constexpr float kTanh[5] = {0.999968469f, -0.33265823f, 0.12922066f, -0.0432998512f, 0.00836588039f};
 
 // What a query tile of a sequence sees.
 struct TileView {
@@ -267,12 +267,13 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     regs_give<AT_REGS_ISSUE>();
     if (w == 8) {
       if (l == 0) {
-        auto tile = [&](int off, const CUtensorMap* map, int head, int64_t tok, uint64_t* bar) {
+        auto key_row = [&](int j) { return bos + static_cast<int64_t>(nj - 1 - j) * AT_ROWS; };
+      auto tile = [&](int off, const CUtensorMap* map, int head, int64_t tok, uint64_t* bar) {
           tma_box(smem + off, map, 0, head, static_cast<int>(tok), bar);
           tma_box(smem + off + AT_BOX, map, 64, head, static_cast<int>(tok), bar);
         };
         mbar_arrive_expect_tx(&ctl->k_full[0], AT_TILE);
-        tile(AT_K, &maps.k, hk, bos, &ctl->k_full[0]);
+        tile(AT_K, &maps.k, hk, key_row(0), &ctl->k_full[0]);
         mbar_arrive_expect_tx(&ctl->q_full, n1 > 0 ? 2 * AT_TILE : AT_TILE);
         tile(AT_Q, &maps.q, h, bos + i0, &ctl->q_full);
         if (n1 > 0) tile(AT_Q + AT_TILE, &maps.q, h, bos + i0 + AT_ROWS, &ctl->q_full);
@@ -283,14 +284,14 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
             if (vs >= 2) ok = wait_for(&ctl->v_empty[vs & 1], ((vs >> 1) - 1) & 1, ctl, err);
             if (!ok) break;
             mbar_arrive_expect_tx(&ctl->v_full[vs & 1], AT_TILE);
-            tile(AT_V + (vs & 1) * AT_TILE, &maps.v, hk, bos + static_cast<int64_t>(vs) * AT_ROWS, &ctl->v_full[vs & 1]);
+            tile(AT_V + (vs & 1) * AT_TILE, &maps.v, hk, key_row(vs), &ctl->v_full[vs & 1]);
             ++vs;
           }
           if (ks < nj) {
             if (ks >= 2) ok = wait_for(&ctl->k_empty[ks & 1], ((ks >> 1) - 1) & 1, ctl, err);
             if (!ok) break;
             mbar_arrive_expect_tx(&ctl->k_full[ks & 1], AT_TILE);
-            tile(AT_K + (ks & 1) * AT_TILE, &maps.k, hk, bos + static_cast<int64_t>(ks) * AT_ROWS, &ctl->k_full[ks & 1]);
+            tile(AT_K + (ks & 1) * AT_TILE, &maps.k, hk, key_row(ks), &ctl->k_full[ks & 1]);
             ++ks;
           }
         }
@@ -339,64 +340,68 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         if (steps > 6) mma_ts_step<p + 48, v + 768>(o, tmem, v_lo, desc_hi, id_o, 1);
         if (steps > 7) mma_ts_step<p + 56, v + 896>(o, tmem, v_lo, desc_hi, id_o, 1);
       };
-      auto commit = [&](uint64_t* bar) {
-        if (one) tc_commit(bar);
-        __syncwarp();
-      };
       using N0 = std::integral_constant<uint32_t, 0>;
       using N1 = std::integral_constant<uint32_t, 1>;
-      bool ok = warp_wait(&ctl->k_full[0], 0, ctl, err) && warp_wait(&ctl->q_full, 0, ctl, err);
-      if (ok) {
-        tc_fence_after();
-        if (one) issue_s(N0{}, N0{});
-        commit(&ctl->s_full[0]);
-        if (n1 > 0) {
-          if (one) issue_s(N1{}, N0{});
-          commit(&ctl->s_full[1]);
-        }
-        commit(&ctl->k_empty[0]);
-        // key tile j in stage `stage`; false once a wait has run out
-        auto body = [&](int j, auto stage, auto next) -> bool {
-          constexpr uint32_t st = stage.value;
-          if (!warp_wait(&ctl->v_full[st], (j >> 1) & 1, ctl, err)) return false;
-          const int left = view.len - j * AT_ROWS;
-          const int steps = left >= AT_ROWS ? AT_ROWS / 16 : (left + 15) / 16;
-          if (left < steps * 16) {
-            // zeros in the rows between the sequence's end and the last step's
-            for (int e = l; e < (steps * 16 - left) * 16; e += 32) {
-              const int off = (e & 8 ? AT_BOX : 0) + (left + (e >> 4)) * 128 + (e & 7) * 16;
-              *reinterpret_cast<uint4*>(smem + AT_V + st * AT_TILE + off) = make_uint4(0, 0, 0, 0);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
+      if (one) {
+        bool ok = wait_for(&ctl->k_full[0], 0, ctl, err) && wait_for(&ctl->q_full, 0, ctl, err);
+        if (ok) {
+          // a query tile that sees fewer key tiles joins in at step nj - nt
+          if (n0 == nj) {
+            issue_s(N0{}, N0{});
+            tc_commit(&ctl->s_full[0]);
           }
-          if (j + 1 < nj && !warp_wait(&ctl->k_full[next.value], ((j + 1) >> 1) & 1, ctl, err)) return false;
-          auto tile = [&](auto which, int nt) -> bool {
-            if (j >= nt) return true;
-            constexpr uint32_t t = which.value;
-            if (!warp_wait(&ctl->p_full[t], j & 1, ctl, err)) return false;
-            tc_fence_after();
-            if (one) {
-              issue_o(which, stage, j > 0, steps);
-              // the tensor core runs these in order: S may follow into the columns P is read from
-              if (j + 1 < nt) issue_s(which, next);
+          if (n1 == nj) {
+            issue_s(N1{}, N0{});
+            tc_commit(&ctl->s_full[1]);
+          }
+          tc_commit(&ctl->k_empty[0]);
+          // step j: key tile nj - 1 - j, in stage `stage`; false once a wait has run out
+          auto body = [&](int j, auto stage, auto next) -> bool {
+            constexpr uint32_t st = stage.value;
+            if (!wait_for(&ctl->v_full[st], (j >> 1) & 1, ctl, err)) return false;
+            int steps = AT_ROWS / 16;
+            if (j == 0) {
+              // the sequence's last keys: zeros in the rows between their end and the last step's
+              const int left = view.len - (nj - 1) * AT_ROWS;
+              steps = left >= AT_ROWS ? AT_ROWS / 16 : (left + 15) / 16;
+              if (left < steps * 16) {
+                for (int r = left; r < steps * 16; ++r)
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    *reinterpret_cast<uint4*>(smem + AT_V + (e & 8 ? AT_BOX : 0) + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              }
             }
-            commit(&ctl->s_full[t]);
+            if (j + 1 < nj && !wait_for(&ctl->k_full[next.value], ((j + 1) >> 1) & 1, ctl, err)) return false;
+            auto tile = [&](auto which, int nt) -> bool {
+              constexpr uint32_t t = which.value;
+              const int mine = j - (nj - nt);  // the query tile's own step
+              const bool more = j + 1 < nj && mine + 1 >= 0;
+              if (mine >= 0) {
+                if (!wait_for(&ctl->p_full[t], mine & 1, ctl, err)) return false;
+                tc_fence_after();
+                issue_o(which, stage, mine > 0, steps);
+              }
+              // the tensor core runs these in order: S may follow into the columns P is read from
+              if (more) issue_s(which, next);
+              if (mine >= 0 || more) tc_commit(&ctl->s_full[t]);
+              return true;
+            };
+            if (!tile(N0{}, n0) || (n1 > 0 && !tile(N1{}, n1))) return false;
+            tc_commit(&ctl->v_empty[st]);
+            if (j + 1 < nj) tc_commit(&ctl->k_empty[next.value]);
             return true;
           };
-          if (!tile(N0{}, n0) || !tile(N1{}, n1)) return false;
-          commit(&ctl->v_empty[st]);
-          if (j + 1 < nj) commit(&ctl->k_empty[next.value]);
-          return true;
-        };
-        for (int j = 0; j < nj; j += 2) {
-          if (!body(j, N0{}, N1{})) break;
-          if (j + 1 < nj && !body(j + 1, N1{}, N0{})) break;
+          for (int j = 0; j < nj; j += 2) {
+            if (!body(j, N0{}, N1{})) break;
+            if (j + 1 < nj && !body(j + 1, N1{}, N0{})) break;
+          }
         }
+        // nothing may be running in tensor memory when it is freed
+        tc_commit(&ctl->drained);
+        mbar_wait(&ctl->drained, 0);
       }
-      // nothing may be running in tensor memory when it is freed
-      commit(&ctl->drained);
-      mbar_wait(&ctl->drained, 0);
+      __syncwarp();
     }
   } else {
     regs_take<AT_REGS_SOFTMAX>();
@@ -410,6 +415,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     const float slope = BIAS && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.f;
     const float c1 = a.scale * kLog2e;
     const float cap2 = CAP ? a.cap * kLog2e : 0.f, per_cap = CAP ? a.scale / a.cap : 0.f;
+    const float e1 = per_cap * 2.f * kLog2e;
     float ref = -INFINITY, sum = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -420,79 +426,45 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(S + c * 32, s[c]);
       tmem_wait_ld();
-      const int j0 = j * AT_ROWS;
-      const bool masked = j0 + AT_ROWS > tile_lo;  // the same for the warp
-      float base = 0.f, top = 0.f;                 // base: added to every score of the row
-      if (CAP) {
-        bool small = false;  // all of the warp's scores below the cap: the polynomial holds
-        if (!masked) {
-          top = row_max(s);
+      const int j0 = (nt - 1 - j) * AT_ROWS;
+      const int lo = i0 + t * AT_ROWS - j0;  // first row less first column
+      // The usual tile: no row's limit in it, a bias linear in the column, no score
+      // over the cap.  Then an upper bound of the row's scores comes from the largest
+      // product alone, and where it does not outgrow the reference the scores go from
+      // products to weights in one pass.  The choice is the warp's.
+      bool fast = j0 + AT_ROWS <= tile_lo;
+      float top = 0.f, base = 0.f, step = 0.f;
+      if (fast) {
+        top = row_max(s);
+        if (CAP) {
           const float low = row_min(s);
-          small = __all_sync(0xffffffffu, fmaxf(fabsf(top), fabsf(low)) * fabsf(per_cap) <= 1.0f);
-        }
-        const f2 pc = pair(per_cap, per_cap);
-        f2 q[6];
-#pragma unroll
-        for (int k = 0; k < 6; ++k) q[k] = pair(kTanh[k] * cap2, kTanh[k] * cap2);
-        const float e1 = per_cap * 2.f * kLog2e;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          // one quarter by the special-function unit, so that both have work
-          if (small && c < 3) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const f2 y = mul2(pair(s[c][e], s[c][e + 1]), pc), u = mul2(y, y);
-              f2 p = fma2(u, q[5], q[4]);
-#pragma unroll
-              for (int k = 3; k >= 0; --k) p = fma2(u, p, q[k]);
-              unpair(mul2(y, p), s[c][e], s[c][e + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[c][e] = __float_as_uint(cap_log2(__uint_as_float(s[c][e]), e1, cap2));
-          }
-        }
-        top = cap_log2(top, e1, cap2);  // rises with the score (scale > 0 unless BIAS)
-      }
-      if (BIAS) {
-        const float mul = CAP ? 1.f : c1;
-        const int d = i - j0;
-        const int lo = i0 + t * AT_ROWS - j0;  // the same for the warp
-        if (lo >= AT_ROWS - 1 || lo + AT_ROWS - 1 <= 0) {
-          // one side of the diagonal: the distance is linear in the column
-          const float step = lo > 0 ? slope : -slope;
-          base = lo > 0 ? -slope * static_cast<float>(d) : slope * static_cast<float>(d);
-          const f2 m2 = pair(mul, mul), up = pair(2.f * step, 2.f * step);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            f2 at = pair(step * (32.f * c), step * (32.f * c + 1.f));
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              unpair(fma2(pair(s[c][e], s[c][e + 1]), m2, at), s[c][e], s[c][e + 1]);
-              at = add2(at, up);
-            }
-          }
+          fast = fmaxf(fabsf(top), fabsf(low)) * fabsf(per_cap) <= 1.0f;
+          top = cap_log2(per_cap >= 0.f ? top : low, e1, cap2);
         } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[c][e] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(d - (c * 32 + e))),
-                                             __uint_as_float(s[c][e]) * mul));
+          top *= c1;
+          fast = !BIAS || c1 > 0.f;
         }
+        if (BIAS) {
+          step = lo >= 0 ? slope : -slope;
+          base = -step * static_cast<float>(i - j0);
+          top += base + fmaxf(step * (AT_ROWS - 1.f), 0.f);
+          fast = fast && (lo >= AT_ROWS - 1 || lo + AT_ROWS - 1 <= 0) && !(top > ref + AT_GROW);
+        }
+        fast = __all_sync(0xffffffffu, fast);
       }
-      if (masked) {
+      if (!fast) {
         const int left = limit - j0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= left) s[c][e] = 0xff800000u;  // -inf
+          for (int e = 0; e < 32; ++e) {
+            const float x = __uint_as_float(s[c][e]);
+            float y = CAP ? cap_log2(x, e1, cap2) : x * c1;
+            if (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), y);
+            s[c][e] = c * 32 + e < left ? __float_as_uint(y) : 0xff800000u;  // -inf
+          }
+        top = row_max(s);
       }
-      constexpr bool SCALED = !CAP && !BIAS;  // scores still to be multiplied by c1 (> 0)
-      if (!CAP || BIAS || masked) top = row_max(s);
-      top = SCALED ? top * c1 : top + base;
       const bool grow = top > ref + AT_GROW;  // ref = -inf: any finite maximum
       if (__any_sync(0xffffffffu, grow)) {
         const float now = grow ? top : ref;
@@ -512,23 +484,61 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         }
       }
       // nothing seen yet: every weight is 0
-      const float sub = (ref == -INFINITY ? 0.f : ref) - base;
-      const f2 mul = pair(SCALED ? c1 : 1.f, SCALED ? c1 : 1.f), off = pair(-sub, -sub);
+      const float sub = ref == -INFINITY ? 0.f : ref;
       f2 part[2] = {0ull, 0ull};
+      // weights of a pair of scores, into their sum and a word of P
+      auto weigh = [&](f2 x, f2& acc) -> uint32_t {
+        float p0, p1;
+        unpair(x, p0, p1);
+        p0 = ex2_approx(p0);
+        p1 = ex2_approx(p1);
+        acc = add2(acc, pair(p0, p1));
+        return pack_bf16(p0, p1);
+      };
+      if (fast) {
+        const f2 m2 = pair(CAP ? per_cap : c1, CAP ? per_cap : c1), up = pair(2.f * step, 2.f * step);
+        f2 q[5];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int k = 0; k < 5; ++k) q[k] = pair(kTanh[k] * cap2, kTanh[k] * cap2);
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const f2 x = pair(s[c][e], s[c][e + 1]);
-          float p0, p1;
-          unpair(SCALED ? fma2(x, mul, off) : add2(x, off), p0, p1);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pair(p0, p1));
-          pk[e >> 1] = pack_bf16(p0, p1);
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          const float off0 = base - sub + step * (32.f * c);
+          f2 off = pair(off0, off0 + step);  // what the column's score is off by
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const f2 x = pair(s[c][e], s[c][e + 1]);
+            f2 z;
+            if (!CAP) {
+              z = fma2(x, m2, off);
+            } else if (c < 3) {
+              const f2 y = mul2(x, m2), u = mul2(y, y);
+              f2 p = fma2(u, q[4], q[3]);
+#pragma unroll
+              for (int k = 2; k >= 0; --k) p = fma2(u, p, q[k]);
+              z = fma2(y, p, off);
+            } else {
+              // a quarter by the special-function unit, so that both have work
+              float a0, a1;
+              unpair(mul2(x, pair(e1, e1)), a0, a1);
+              unpair(add2(pair(ex2_approx(a0), ex2_approx(a1)), pair(1.f, 1.f)), a0, a1);
+              z = fma2(pair(rcp_approx(a0), rcp_approx(a1)), pair(-2.f * cap2, -2.f * cap2), add2(off, pair(cap2, cap2)));
+            }
+            pk[e >> 1] = weigh(z, part[(e >> 1) & 1]);
+            if (BIAS) off = add2(off, up);
+          }
+          tmem_st16(S + c * 16, pk);
         }
-        tmem_st16(S + c * 16, pk);
+      } else {
+        const f2 off = pair(-sub, -sub);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            pk[e >> 1] = weigh(add2(pair(s[c][e], s[c][e + 1]), off), part[(e >> 1) & 1]);
+          tmem_st16(S + c * 16, pk);
+        }
       }
       float s0, s1;
       unpair(add2(part[0], part[1]), s0, s1);
