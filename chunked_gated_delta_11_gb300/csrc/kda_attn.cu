@@ -13,8 +13,8 @@
 // while the tensor core works for one, the softmax of the other runs.
 // Tensor memory: S0 | S1 | O0 | O1, 128 columns each, all 512.
 //
-// Softmax.  m moves only when a row's maximum grows by more than 2^8 over it (P
-// then stays below 2^8, in bf16's range, and the sum in fp32), so O is rarely
+// Softmax.  m moves only when a row's maximum may grow by more than 2^16 over it (P
+// then stays below 2^16, in bf16's range, and the sum in fp32), so O is rarely
 // rescaled; a row thread rescales its own row of O in tensor memory.  P is
 // rounded to bf16 (2^-9 relative, as the output once more); its sum is taken in
 // fp32 before that rounding.
@@ -42,7 +42,7 @@ constexpr int AT_THREADS = 384;
 constexpr int AT_REGS_SOFTMAX = 224, AT_REGS_ISSUE = 56;
 constexpr int AT_Q = 0, AT_K = 2 * AT_TILE, AT_V = 4 * AT_TILE, AT_CTL = 6 * AT_TILE;
 constexpr int AT_SMEM = AT_CTL + 256 + 1024;
-constexpr float AT_GROW = 8.0f;                // how far a maximum may outgrow the reference
+constexpr float AT_GROW = 16.0f;               // how far a maximum may outgrow the reference
 
 struct AttnMaps {
   CUtensorMap q, k, v;
@@ -165,11 +165,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -179,22 +174,13 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {
       m[(e >> 1) & 3] = max3(m[(e >> 1) & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-__device__ __forceinline__ float row_min(const uint32_t (&s)[4][32]) {
-  float m[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-#pragma unroll
-    for (int e = 0; e < 32; e += 2)
-      m[(e >> 1) & 3] = min3(m[(e >> 1) & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-  return fminf(fminf(m[0], m[1]), fminf(m[2], m[3]));
-}
-
-// tanh(y) = y Q(y^2) for |y| <= 1, Q of degree 4, fitted for the least maximum
-// error of y Q: 2.8e-6, which moves a capped score by 1.4e-4 at a cap of 50 and so a
-// weight by a sixteenth of its bf16 rounding.  Six paired multiply-adds for two
-// scores, where an exponential and a reciprocal take 24 cycles of a special-function
-// unit that a tile's 128 weights keep busy already.
-__device__ constexpr float kTanh[5] = {0.999968469f, -0.33265823f, 0.12922066f, -0.0432998512f, 0.00836588039f};
+// tanh(y) = y (c0 + c1 y^2 + c2 y^4 + c3 y^6) for |y| <= 0.7, fitted for the least
+// maximum error: 2.1e-6, which moves a capped score by 1.5e-4 (in units of log2) at
+// a cap of 50 and so a weight by a twentieth of its bf16 rounding.  Five
+// multiply-adds a score, where an exponential and a reciprocal take 12 cycles of a
+// special-function unit that a tile's weights keep busy already.
+constexpr float kTanhMost = 0.7f;
+__device__ constexpr float kTanh[4] = {0.999972696f, -0.332557463f, 0.127291387f, -0.0357217971f};
 
 // What a query tile of a sequence sees.
 struct TileView {
@@ -416,6 +402,13 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     const float c1 = a.scale * kLog2e;
     const float cap2 = CAP ? a.cap * kLog2e : 0.f, per_cap = CAP ? a.scale / a.cap : 0.f;
     const float e1 = per_cap * 2.f * kLog2e;
+    // multipliers of the one-pass scores: s (k0 + k1 s^2 + k2 s^4 + k3 s^6), or s k0
+    const float pc2 = per_cap * per_cap;
+    const float w0 = CAP ? kTanh[0] * c1 : c1, w1 = kTanh[1] * c1 * pc2, w2 = kTanh[2] * c1 * pc2 * pc2,
+                w3 = kTanh[3] * c1 * pc2 * pc2 * pc2;
+    const f2 k0 = pair(w0, w0), k1 = pair(w1, w1), k2 = pair(w2, w2), k3 = pair(w3, w3);
+    // a positive scale; with a cap, powers of scale / cap that fp32 holds
+    const bool usual = c1 > 0.f && (!CAP || (per_cap > 1e-5f && per_cap < 1e5f));
     float ref = -INFINITY, sum = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
@@ -428,63 +421,6 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       tmem_wait_ld();
       const int j0 = (nt - 1 - j) * AT_ROWS;
       const int lo = i0 + t * AT_ROWS - j0;  // first row less first column
-      // The usual tile: no row's limit in it, a bias linear in the column, no score
-      // over the cap.  Then an upper bound of the row's scores comes from the largest
-      // product alone, and where it does not outgrow the reference the scores go from
-      // products to weights in one pass.  The choice is the warp's.
-      bool fast = j0 + AT_ROWS <= tile_lo;
-      float top = 0.f, base = 0.f, step = 0.f;
-      if (fast) {
-        top = row_max(s);
-        if (CAP) {
-          const float low = row_min(s);
-          fast = fmaxf(fabsf(top), fabsf(low)) * fabsf(per_cap) <= 1.0f;
-          top = cap_log2(per_cap >= 0.f ? top : low, e1, cap2);
-        } else {
-          top *= c1;
-          fast = !BIAS || c1 > 0.f;
-        }
-        if (BIAS) {
-          step = lo >= 0 ? slope : -slope;
-          base = -step * static_cast<float>(i - j0);
-          top += base + fmaxf(step * (AT_ROWS - 1.f), 0.f);
-          fast = fast && (lo >= AT_ROWS - 1 || lo + AT_ROWS - 1 <= 0) && !(top > ref + AT_GROW);
-        }
-        fast = __all_sync(0xffffffffu, fast);
-      }
-      if (!fast) {
-        const int left = limit - j0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float x = __uint_as_float(s[c][e]);
-            float y = CAP ? cap_log2(x, e1, cap2) : x * c1;
-            if (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), y);
-            s[c][e] = c * 32 + e < left ? __float_as_uint(y) : 0xff800000u;  // -inf
-          }
-        top = row_max(s);
-      }
-      const bool grow = top > ref + AT_GROW;  // ref = -inf: any finite maximum
-      if (__any_sync(0xffffffffu, grow)) {
-        const float now = grow ? top : ref;
-        const float f = grow ? ex2_approx(ref - now) : 1.f;
-        sum *= f;
-        ref = now;
-        if (j > 0) {  // the products of the tiles before are complete (S came after them)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(O + c * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(O + c * 32, o);
-          }
-        }
-      }
-      // nothing seen yet: every weight is 0
-      const float sub = ref == -INFINITY ? 0.f : ref;
       f2 part[2] = {0ull, 0ull};
       // weights of a pair of scores, into their sum and a word of P
       auto weigh = [&](f2 x, f2& acc) -> uint32_t {
@@ -495,42 +431,77 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         acc = add2(acc, pair(p0, p1));
         return pack_bf16(p0, p1);
       };
-      if (fast) {
-        const f2 m2 = pair(CAP ? per_cap : c1, CAP ? per_cap : c1), up = pair(2.f * step, 2.f * step);
-        f2 q[5];
-#pragma unroll
-        for (int k = 0; k < 5; ++k) q[k] = pair(kTanh[k] * cap2, kTanh[k] * cap2);
+      // The usual tile: no row's limit in it, a bias linear in the column, scores well
+      // under the cap, none far above the reference.  From products to weights in one
+      // pass, with the largest product found on the way; if that shows that the
+      // reference had to move or the polynomial does not hold, the warp does the tile
+      // again below.
+      bool done = false;
+      if (j > 0 && j0 + AT_ROWS <= tile_lo && usual && (!BIAS || lo >= AT_ROWS - 1 || lo + AT_ROWS - 1 <= 0)) {
+        const float step = lo >= 0 ? slope : -slope;
+        const float base = BIAS ? -step * static_cast<float>(i - j0) : 0.f;
+        const f2 up = pair(2.f * step, 2.f * step);
+        float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
-          const float off0 = base - sub + step * (32.f * c);
+          const float off0 = base - ref + step * (32.f * c);
           f2 off = pair(off0, off0 + step);  // what the column's score is off by
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const f2 x = pair(s[c][e], s[c][e + 1]);
-            f2 z;
-            if (!CAP) {
-              z = fma2(x, m2, off);
-            } else if (c < 3) {
-              const f2 y = mul2(x, m2), u = mul2(y, y);
-              f2 p = fma2(u, q[4], q[3]);
-#pragma unroll
-              for (int k = 2; k >= 0; --k) p = fma2(u, p, q[k]);
-              z = fma2(y, p, off);
-            } else {
-              // a quarter by the special-function unit, so that both have work
-              float a0, a1;
-              unpair(mul2(x, pair(e1, e1)), a0, a1);
-              unpair(add2(pair(ex2_approx(a0), ex2_approx(a1)), pair(1.f, 1.f)), a0, a1);
-              z = fma2(pair(rcp_approx(a0), rcp_approx(a1)), pair(-2.f * cap2, -2.f * cap2), add2(off, pair(cap2, cap2)));
+            const float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
+            float& mx = m[(e >> 1) & 3];
+            mx = CAP ? fmaxf(fmaxf(mx, fabsf(x0)), fabsf(x1)) : max3(mx, x0, x1);
+            const f2 x = pair(x0, x1);
+            f2 f = k0;
+            if (CAP) {
+              const f2 u = mul2(x, x);
+              f = fma2(u, fma2(u, fma2(u, k3, k2), k1), k0);
             }
-            pk[e >> 1] = weigh(z, part[(e >> 1) & 1]);
+            pk[e >> 1] = weigh(fma2(x, f, off), part[(e >> 1) & 1]);
             if (BIAS) off = add2(off, up);
           }
           tmem_st16(S + c * 16, pk);
         }
-      } else {
+        const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+        // tanh(y) <= y: c1 is the slope of the capped score at 0 too
+        const float bound = most * c1 + base + (BIAS ? fmaxf(step * (AT_ROWS - 1.f), 0.f) : 0.f);
+        done = __all_sync(0xffffffffu, bound <= ref + AT_GROW && (!CAP || most * per_cap <= kTanhMost));
+      }
+      if (!done) {
+        const int left = limit - j0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = __uint_as_float(s[c][e]);
+            float y = CAP ? cap_log2(x, e1, cap2) : x * c1;
+            if (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), y);
+            s[c][e] = c * 32 + e < left ? __float_as_uint(y) : 0xff800000u;  // -inf
+          }
+        const float top = row_max(s);
+        const bool grow = top > ref;  // ref = -inf: any finite maximum
+        if (__any_sync(0xffffffffu, grow)) {
+          const float now = grow ? top : ref;
+          const float f = grow ? ex2_approx(ref - now) : 1.f;
+          sum *= f;
+          ref = now;
+          if (j > 0) {  // the products of the tiles before are complete (S came after them)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(O + c * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(O + c * 32, o);
+            }
+          }
+        }
+        // nothing seen yet: every weight is 0
+        const float sub = ref == -INFINITY ? 0.f : ref;
         const f2 off = pair(-sub, -sub);
+        part[0] = part[1] = 0ull;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
