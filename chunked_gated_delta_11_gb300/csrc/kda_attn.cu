@@ -415,12 +415,18 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       ok = warp_wait(&ctl->s_full[t], j & 1, ctl, err);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(S + c * 32, s[c]);
-      tmem_wait_ld();
       const int j0 = (nt - 1 - j) * AT_ROWS;
       const int lo = i0 + t * AT_ROWS - j0;  // first row less first column
+      // Without a cap the row's 128 scores stay in registers.  With one the usual tile
+      // takes them 64 at a time in a loop that stays rolled: unrolled, its code
+      // outgrows the instruction caches that the SM's warps share.
+      uint32_t s[4][32];
+      auto load = [&]() {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(S + c * 32, s[c]);
+        tmem_wait_ld();
+      };
+      if (!CAP) load();
       f2 part[2] = {0ull, 0ull};
       // weights of a pair of scores, into their sum and a word of P
       auto weigh = [&](f2 x, f2& acc) -> uint32_t {
@@ -442,42 +448,92 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         const float base = BIAS ? -step * static_cast<float>(i - j0) : 0.f;
         const f2 up = pair(2.f * step, 2.f * step);
         float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-          const float off0 = base - ref + step * (32.f * c);
+        // weights of 32 columns from column col on
+        auto columns = [&](const uint32_t (&x)[32], uint32_t* pk, float col) {
+          const float off0 = base - ref + step * col;
           f2 off = pair(off0, off0 + step);  // what the column's score is off by
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float x0 = __uint_as_float(s[c][e]), x1 = __uint_as_float(s[c][e + 1]);
+            const float x0 = __uint_as_float(x[e]), x1 = __uint_as_float(x[e + 1]);
             float& mx = m[(e >> 1) & 3];
             mx = CAP ? fmaxf(fmaxf(mx, fabsf(x0)), fabsf(x1)) : max3(mx, x0, x1);
-            const f2 x = pair(x0, x1);
+            const f2 xx = pair(x0, x1);
             f2 f = k0;
             if (CAP) {
-              const f2 u = mul2(x, x);
+              const f2 u = mul2(xx, xx);
               f = fma2(u, fma2(u, fma2(u, k3, k2), k1), k0);
             }
-            pk[e >> 1] = weigh(fma2(x, f, off), part[(e >> 1) & 1]);
+            pk[e >> 1] = weigh(fma2(xx, f, off), part[(e >> 1) & 1]);
             if (BIAS) off = add2(off, up);
           }
-          tmem_st16(S + c * 16, pk);
+        };
+        uint32_t pk[32], first[32];  // CAP: P is written at the end, over scores still needed if it fails
+        if (CAP) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) pk[e] = 0u;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) first[e] = pk[e];
+            tmem_ld32(S + half * 64, s[0]);
+            tmem_ld32(S + half * 64 + 32, s[1]);
+            tmem_wait_ld();
+            columns(s[0], pk, 64.f * half);
+            columns(s[1], pk + 16, 64.f * half + 32.f);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t p16[16];
+            columns(s[c], p16, 32.f * c);
+            tmem_st16(S + c * 16, p16);
+          }
         }
         const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         // tanh(y) <= y: c1 is the slope of the capped score at 0 too
         const float bound = most * c1 + base + (BIAS ? fmaxf(step * (AT_ROWS - 1.f), 0.f) : 0.f);
         done = __all_sync(0xffffffffu, bound <= ref + AT_GROW && (!CAP || most * per_cap <= kTanhMost));
+        if (CAP && done) {
+          tmem_st32(S, first);
+          tmem_st32(S + 32, pk);
+        }
       }
       if (!done) {
+        if (CAP) load();
+        bool small = false;  // the polynomial holds for the warp's scores
+        if (CAP) {
+          float m[2] = {0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              m[(e >> 1) & 1] = fmaxf(fmaxf(m[(e >> 1) & 1], fabsf(__uint_as_float(s[c][e]))), fabsf(__uint_as_float(s[c][e + 1])));
+          small = __all_sync(0xffffffffu, usual && fmaxf(m[0], m[1]) * per_cap <= kTanhMost);
+        }
+        // scores in log2 units, -inf where the row does not see
+        if (CAP && small) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const f2 x = pair(s[c][e], s[c][e + 1]), u = mul2(x, x);
+              unpair(mul2(x, fma2(u, fma2(u, fma2(u, k3, k2), k1), k0)), s[c][e], s[c][e + 1]);
+            }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              s[c][e] = __float_as_uint(CAP ? cap_log2(__uint_as_float(s[c][e]), e1, cap2) : __uint_as_float(s[c][e]) * c1);
+        }
         const int left = limit - j0;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
-            const float x = __uint_as_float(s[c][e]);
-            float y = CAP ? cap_log2(x, e1, cap2) : x * c1;
+            float y = __uint_as_float(s[c][e]);
             if (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), y);
-            s[c][e] = c * 32 + e < left ? __float_as_uint(y) : 0xff800000u;  // -inf
+            s[c][e] = c * 32 + e < left ? __float_as_uint(y) : 0xff800000u;
           }
         const float top = row_max(s);
         const bool grow = top > ref;  // ref = -inf: any finite maximum
@@ -487,7 +543,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           sum *= f;
           ref = now;
           if (j > 0) {  // the products of the tiles before are complete (S came after them)
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t o[32];
               tmem_ld32(O + c * 32, o);
@@ -525,7 +581,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         const float inv = 1.f / sum;
         const bool store = i < view.len;
         __nv_bfloat16* dst = a.out + ((bos + (store ? i : 0)) * a.H + h) * kDim;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           uint32_t o[32];
           tmem_ld32(O + c * 32, o);
