@@ -526,16 +526,28 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
             for (int e = 0; e < 32; ++e)
               s[c][e] = __float_as_uint(CAP ? cap_log2(__uint_as_float(s[c][e]), e1, cap2) : __uint_as_float(s[c][e]) * c1);
         }
-        const int left = limit - j0;
+        if (BIAS) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float y = __uint_as_float(s[c][e]);
-            if (BIAS) y = fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), y);
-            s[c][e] = c * 32 + e < left ? __float_as_uint(y) : 0xff800000u;
-          }
-        const float top = row_max(s);
+            for (int e = 0; e < 32; ++e)
+              s[c][e] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), __uint_as_float(s[c][e])));
+        }
+        float top = row_max(s);
+        if (j0 + AT_ROWS > tile_lo) {
+          const float all = top;
+          const int left = limit - j0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= left) s[c][e] = 0xff800000u;
+          top = row_max(s);
+          // A row that sees few keys of its first tile would move its reference again
+          // in the next: the hidden keys' scores say how far it is likely to go.  Up
+          // to 2^60 over the row's maximum costs no accuracy (its weight is then 2^-60).
+          top = top == -INFINITY ? top : fmaxf(top, fminf(all, top + 60.f));
+        }
         const bool grow = top > ref;  // ref = -inf: any finite maximum
         if (__any_sync(0xffffffffu, grow)) {
           const float now = grow ? top : ref;
