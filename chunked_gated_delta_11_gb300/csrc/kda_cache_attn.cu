@@ -754,8 +754,15 @@ join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __r
   const int64_t slot = first_tile(a, plan, n, bos);
   constexpr int QUADS = CA_WCHUNK / 512;  // groups of 4 slots per thread
   float4 wsum[QUADS];
+  int at[QUADS], pid[QUADS];
+  const int last = (len - 1) & ~3;
 #pragma unroll
-  for (int j = 0; j < QUADS; ++j) wsum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j = 0; j < QUADS; ++j) {
+    const int tok = first + j * 512 + threadIdx.x * 4;
+    wsum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    at[j] = tok < len ? tok : last;
+    pid[j] = tok < len ? page_id(a.c, n, tok >> a.c.lg, err) : -1;
+  }
   for (int64_t r0 = 0; r0 < rows; r0 += rt) {
     const int64_t unit = (slot + r0 / rt) * a.c.Hk + hk;
     const int here = rows - r0 < rt ? static_cast<int>(rows - r0) : static_cast<int>(rt);
@@ -778,34 +785,45 @@ join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __r
       if (l == 0) lse[r] = all == -INFINITY ? 0.f : all + log2f(tot);
     }
     __syncthreads();
+    // two rows' scores of all the thread's slots are under way at a time; a quad past
+    // the length reads the last one instead, and drops what it gets
+    const float* row = scores + unit * rt * plan.max_len;
+    for (int r = 0; r < here; r += 2) {
+      const int rr = r + 1 < here ? r + 1 : r;
+      float4 x[2][QUADS];
 #pragma unroll
-    for (int j = 0; j < QUADS; ++j) {
-      const int tok = first + j * 512 + threadIdx.x * 4;
-      if (tok >= len) continue;
-      const float* s = scores + unit * rt * plan.max_len + tok;
-      for (int r = 0; r < here; ++r) {
-        const float4 x = *reinterpret_cast<const float4*>(s + r * plan.max_len);
-        wsum[j].x += ex2_approx(x.x - lse[r]);
-        wsum[j].y += ex2_approx(x.y - lse[r]);
-        wsum[j].z += ex2_approx(x.z - lse[r]);
-        wsum[j].w += ex2_approx(x.w - lse[r]);
+      for (int j = 0; j < QUADS; ++j) {
+        x[0][j] = *reinterpret_cast<const float4*>(row + r * plan.max_len + at[j]);
+        x[1][j] = *reinterpret_cast<const float4*>(row + rr * plan.max_len + at[j]);
+      }
+      const float l0 = lse[r], l1 = rr > r ? lse[rr] : INFINITY;
+#pragma unroll
+      for (int j = 0; j < QUADS; ++j) {
+        wsum[j].x += ex2_approx(x[0][j].x - l0);
+        wsum[j].y += ex2_approx(x[0][j].y - l0);
+        wsum[j].z += ex2_approx(x[0][j].z - l0);
+        wsum[j].w += ex2_approx(x[0][j].w - l0);
+        if (rr > r) {
+          wsum[j].x += ex2_approx(x[1][j].x - l1);
+          wsum[j].y += ex2_approx(x[1][j].y - l1);
+          wsum[j].z += ex2_approx(x[1][j].z - l1);
+          wsum[j].w += ex2_approx(x[1][j].w - l1);
+        }
       }
     }
   }
 #pragma unroll
   for (int j = 0; j < QUADS; ++j) {
     const int tok = first + j * 512 + threadIdx.x * 4;  // 4 slots of one page
-    if (tok >= len) continue;
-    const int pid = page_id(a.c, n, tok >> a.c.lg, err);
-    if (pid < 0) continue;
-    float4* at = reinterpret_cast<float4*>(a.c.weight + (static_cast<int64_t>(pid) * a.c.Hk + hk) * a.c.page +
+    if (tok >= len || pid[j] < 0) continue;
+    float4* to = reinterpret_cast<float4*>(a.c.weight + (static_cast<int64_t>(pid[j]) * a.c.Hk + hk) * a.c.page +
                                            (tok & (a.c.page - 1)));
-    float4 x = *at;
+    float4 x = *to;
     x.x += wsum[j].x;  // the scores of slots past the length were never written
     if (tok + 1 < len) x.y += wsum[j].y;
     if (tok + 2 < len) x.z += wsum[j].z;
     if (tok + 3 < len) x.w += wsum[j].w;
-    *at = x;
+    *to = x;
   }
 }
 
