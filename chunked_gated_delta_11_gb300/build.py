@@ -2,13 +2,16 @@
 
 Each .cu under csrc/ compiles to an object in parallel, then nvcc links them
 into ``chunked_gated_delta_11_gb300/_build/libkda.so``.  ``-Xptxas -v``
-register and shared-memory reports go to ``_build/ptxas.log``.
+register and shared-memory reports go to ``_build/ptxas.log``.  The Python
+extension of the softmax-attention calls, ``_build/attn_binding.so``, is compiled
+beside them with g++ against torch's headers and linked to libkda.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
+BINDING = os.path.join(BUILD, "attn_binding.so")
+BINDING_SRC = os.path.join(CSRC, "attn_binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -37,16 +42,44 @@ def sources():
 def _deps():
     deps = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                         if f.endswith((".cuh", ".h"))]
-    deps.append(os.path.join(INCLUDE, "kda.h"))
+    deps += [os.path.join(INCLUDE, "kda.h"), BINDING_SRC]
     deps.append(os.path.abspath(__file__))
     return deps
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def _compile_binding() -> str:
+    import torch  # noqa: F401  (its headers and libraries belong to this interpreter's torch)
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    obj = os.path.join(BUILD, "attn_binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in inc for x in ("-I", d)], "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-lkda", "-Wl,-rpath,$ORIGIN", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,8 +96,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, sources()))
+        binding_obj = binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for obj, log in results:
             f.write(f"== {os.path.basename(obj)}\n{log}\n")
@@ -74,6 +109,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         print(open(os.path.join(BUILD, "ptxas.log")).read())
     return LIB
