@@ -42,16 +42,26 @@ __device__ __forceinline__ float amax2(uint32_t w) {
   const float lo = fabsf(__uint_as_float(w << 16)), hi = fabsf(__uint_as_float(w & 0xffff0000u));
   return fmaxf(lo < INFINITY ? lo : 0.f, hi < INFINITY ? hi : 0.f);
 }
+// CHECK: non-finite values become NaN.
+template <bool CHECK = true>
 __device__ __forceinline__ uint32_t encode2(uint32_t w, float inv) {
-  return f32x2_to_e4m3x2(finite_or_nan(__uint_as_float(w << 16)) * inv,
-                         finite_or_nan(__uint_as_float(w & 0xffff0000u)) * inv);
+  const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+  return f32x2_to_e4m3x2((CHECK ? finite_or_nan(lo) : lo) * inv, (CHECK ? finite_or_nan(hi) : hi) * inv);
 }
-
+// The larger magnitudes, two bf16 at a time as integers (their order is the same).
+__device__ __forceinline__ uint32_t larger2(uint32_t m, const uint4& x) {
+  m = __vmaxu2(m, x.x & 0x7fff7fffu);
+  m = __vmaxu2(m, x.y & 0x7fff7fffu);
+  m = __vmaxu2(m, x.z & 0x7fff7fffu);
+  return __vmaxu2(m, x.w & 0x7fff7fffu);
+}
 __device__ __forceinline__ float amax8(const uint4& x) {
   return fmaxf(fmaxf(amax2(x.x), amax2(x.y)), fmaxf(amax2(x.z), amax2(x.w)));
 }
+template <bool CHECK>
 __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
-  return make_uint2(encode2(x.x, inv) | (encode2(x.y, inv) << 16), encode2(x.z, inv) | (encode2(x.w, inv) << 16));
+  return make_uint2(encode2<CHECK>(x.x, inv) | (encode2<CHECK>(x.y, inv) << 16),
+                    encode2<CHECK>(x.z, inv) | (encode2<CHECK>(x.w, inv) << 16));
 }
 
 // 4 codes times `ratio`, rounded to codes again
@@ -111,7 +121,7 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
               const int32_t* __restrict__ positions, const int32_t* __restrict__ cu, int64_t T,
               int* __restrict__ err) {
   constexpr int PASSES = PAGE / 16;
-  __shared__ float red[2][8];
+  __shared__ uint32_t red[2][8];
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x, sub = t & 15, row0 = t >> 4, h = blockIdx.y;
@@ -121,7 +131,7 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
   const int64_t block = static_cast<int64_t>(pg.pid) * c.Hk + h;
 
   uint4 xk[PASSES], xv[PASSES];
-  float mk = 0.f, mv = 0.f;
+  uint32_t pk = 0u, pv = 0u;  // largest magnitudes, two bf16 at a time as integers
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int r = p * 16 + row0;
@@ -130,27 +140,47 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
       const int64_t at = ((pg.row0 + r - lo) * c.Hk + h) * kDim + sub * 8;
       xk[p] = *reinterpret_cast<const uint4*>(k + at);
       xv[p] = *reinterpret_cast<const uint4*>(v + at);
-      mk = fmaxf(mk, amax8(xk[p]));
-      mv = fmaxf(mv, amax8(xv[p]));
+      pk = larger2(pk, xk[p]);
+      pv = larger2(pv, xv[p]);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-  }
+  pk = __reduce_max_sync(0xffffffffu, max(pk & 0xffffu, pk >> 16));
+  pv = __reduce_max_sync(0xffffffffu, max(pv & 0xffffu, pv >> 16));
   if ((t & 31) == 0) {
-    red[0][t >> 5] = mk;
-    red[1][t >> 5] = mv;
+    red[0][t >> 5] = pk;
+    red[1][t >> 5] = pv;
   }
   const float oldk = lo > 0 ? c.ks[block] : 0.f, oldv = lo > 0 ? c.vs[block] : 0.f;
   __syncthreads();
-  mk = mv = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    mk = fmaxf(mk, red[0][i]);
-    mv = fmaxf(mv, red[1][i]);
+    pk = max(pk, red[0][i]);
+    pv = max(pv, red[1][i]);
   }
+  const bool finite = max(pk, pv) < 0x7f80u;  // the same for the CTA
+  if (!finite) {
+    // infinities or NaN among the rows: the largest finite value, after all
+    float mk = 0.f, mv = 0.f;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      mk = fmaxf(mk, amax8(xk[p]));
+      mv = fmaxf(mv, amax8(xv[p]));
+    }
+    __syncthreads();
+    const uint32_t bk = __reduce_max_sync(0xffffffffu, __float_as_uint(mk)), bv = __reduce_max_sync(0xffffffffu, __float_as_uint(mv));
+    if ((t & 31) == 0) {
+      red[0][t >> 5] = bk >> 16;
+      red[1][t >> 5] = bv >> 16;
+    }
+    __syncthreads();
+    pk = pv = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pk = max(pk, red[0][i]);
+      pv = max(pv, red[1][i]);
+    }
+  }
+  const float mk = __uint_as_float(pk << 16), mv = __uint_as_float(pv << 16);
   const float sk = fmaxf(block_scale(mk), oldk), sv = fmaxf(block_scale(mv), oldv);
   const float ik = 1.0f / sk, iv = 1.0f / sv;
   uint8_t* dk = c.k + block * (PAGE * kDim) + sub * 8;
@@ -159,8 +189,8 @@ append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloa
   for (int p = 0; p < PASSES; ++p) {
     const int r = p * 16 + row0;
     if (r >= lo && r < hi) {
-      *reinterpret_cast<uint2*>(dk + r * kDim) = encode8(xk[p], ik);
-      *reinterpret_cast<uint2*>(dv + r * kDim) = encode8(xv[p], iv);
+      *reinterpret_cast<uint2*>(dk + r * kDim) = finite ? encode8<false>(xk[p], ik) : encode8<true>(xk[p], ik);
+      *reinterpret_cast<uint2*>(dv + r * kDim) = finite ? encode8<false>(xv[p], iv) : encode8<true>(xv[p], iv);
     } else if (r < lo) {
       if (sk != oldk) {
         uint2* at = reinterpret_cast<uint2*>(dk + r * kDim);
@@ -462,7 +492,7 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
 // rows (length, kept row) is short and shared by a whole page.  SPLIT = 4: the 4
 // warps share a page, for calls with fewer pages than warps that fit the GPU.
 template <int PAGE, int SPLIT>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 8)
 pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int budget,
             const int32_t* __restrict__ kept, int* __restrict__ err) {
   constexpr int LOOKS = (PAGE + 31) / 32;  // rows a lane looks up: lane, lane + 32, ..
