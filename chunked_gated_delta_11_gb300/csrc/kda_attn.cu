@@ -216,7 +216,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
   int64_t bos, eos;
   seq_bounds(a.cu, a.T, a.N, n, bos, eos);
   const int64_t i_first = (slot - (bos / (2 * AT_ROWS) + n)) * (2 * AT_ROWS);
-  if (i_first >= eos - bos) return;
+  if (i_first < 0 || i_first >= eos - bos) return;  // (a malformed cu_seqlens can give the former)
   const int i0 = static_cast<int>(i_first);
   TileView view{static_cast<int>(eos - bos), 0, a.mask};
   if (a.mask == KDA_MASK_PREFIX) {

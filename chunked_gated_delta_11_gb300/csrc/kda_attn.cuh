@@ -90,7 +90,8 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// The last n in [0, N) with first(n) <= s, for a function that does not decrease;
+// The last n in [0, N) with first(n) <= s, for a function that does not decrease
+// (for another, as a malformed cu_seqlens gives, any n: first(n) may be over s);
 // 0 if there is none.  All lanes of a warp call it with the same arguments; each
 // round tries 32 places, so a thousand sequences take two dependent loads.
 template <class F>

@@ -181,7 +181,9 @@ extern "C" size_t kda_cache_attn_workspace_size(const kda_cache* cache, int64_t 
     return 0;
   const int64_t max_len = static_cast<int64_t>(table_width) * cache->page_size;
   if (max_len > 0x7fffff00LL || T_total > 0x7fffffffLL / H) return 0;
-  return T_total == 0 ? 0 : cached_need(cache, T_total, H, N, max_len, accumulate != 0);
+  if (T_total == 0) return 0;
+  const size_t need = cached_need(cache, T_total, H, N, max_len, accumulate != 0);
+  return need == SIZE_MAX ? 0 : need;
 }
 
 extern "C" kda_status kda_cache_attn(const kda_cache_attn_options* opts, const kda_cache* cache,
@@ -204,6 +206,7 @@ extern "C" kda_status kda_cache_attn(const kda_cache_attn_options* opts, const k
   const size_t need = cached_need(cache, T_total, H, N,
                                   static_cast<int64_t>(table_width) * cache->page_size,
                                   opts->accumulate != 0);
+  if (need == SIZE_MAX) return KDA_ERR_WORKSPACE;  // no device has as much
   if (workspace && (!aligned(workspace, 16) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   int sms = 0, *err = nullptr;
   if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;

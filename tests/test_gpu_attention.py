@@ -327,6 +327,36 @@ def test_cached_wide_table_and_same_bits():
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("H,Hk,counts", [(8, 8, 1), (12, 4, 1), (16, 2, None), (32, 2, 3)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_cached_many_short_sequences_in_a_very_wide_table(H, Hk, counts, bias):
+    """The grid of all possible chunks would be mostly empty: a list of the real ones is used."""
+    r = random.Random(H)
+    lens = [r.choice([0, 1, 3, 16, 20, 40]) for _ in range(699)] + [5000]
+    cache, table = filled(lens, Hk, 16, 24 + H)
+    wide = torch.full((700, 4000), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    each = [counts] * 700 if counts else [r.choice([0, 1, 2, 5]) for _ in range(700)]
+    check_cached(cache, wide, lens, H, each, 25, bias=bias)
+
+
+@pytest.mark.parametrize("H,Hk", [(4, 4), (32, 2)])
+def test_cached_malformed_cu_seqlens_stays_in_bounds(H, Hk):
+    lens = [100, 50, 7, 300]
+    cache, table = filled(lens, Hk, 16, 26)
+    wide = torch.full((4, 4000), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    q = randn(gen(5), 40, H, D).cuda()
+    pad = torch.full((60, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    for tab in (table, wide):
+        for cu in ([0, 40, 0, 40, 40], [-3, 100, 7, 2, 1 << 30]):
+            kda.kda_cache_attn(to(cache, "cuda"), q, tab.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), SCALE,
+                               cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(), accumulate=True, out=pad[10:50])
+            torch.cuda.synchronize()
+            assert (pad[:10] == 7).all() and (pad[50:] == 7).all()
+    ok()
+
+
 def test_cached_streams_graphs_and_own_workspace():
     lens = [900, 33]
     cache, table = filled(lens, 2, 64, 22)
@@ -582,6 +612,46 @@ def test_evict_infinite_and_nan_weights():
     kda.kda_cache_evict(dev, table.cuda(), torch.tensor([50], dtype=torch.int32).cuda(), dst.cuda(), 5, 2)
     ok()
     assert dev.pos[-1, 0, :5].tolist() == [3, 8, 30, 48, 49]
+
+
+# ------------------------------------------------------------------ arguments
+
+def test_tensors_are_checked_and_views_at_odd_places_taken():
+    lens = [40, 9]
+    cache, table = filled(lens, 2, 16, 30)
+    q = randn(gen(8), 2, 4, D)
+    want, tol, _, _ = ref.cached(cache, q, table, lens, SCALE, [1, 1])
+    dev = to(cache, "cuda")
+    # arrays that start 4 bytes into theirs, rows that start in the middle of theirs
+    shift = lambda t: torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)  # noqa: E731
+    qd = torch.cat([q, q, q]).cuda()[2:4]
+    tab, n = shift(table.cuda()), shift(torch.tensor(lens, dtype=torch.int32).cuda())
+    assert tab.data_ptr() % 16 == 4
+    out = kda.kda_cache_attn(dev, qd, tab, n, SCALE)
+    ok()
+    within(out, want, tol, "out")
+    good = dict(q=qd, block_table=tab, lens=n, scale=SCALE)
+    for change, error in ((dict(q=qd.float()), TypeError), (dict(q=qd.transpose(0, 1)), ValueError),
+                          (dict(q=torch.zeros((2, 8, D), dtype=torch.bfloat16, device="cuda")[:, ::2]), ValueError),
+                          (dict(lens=n.long()), TypeError), (dict(lens=n[:1]), ValueError),
+                          (dict(block_table=tab[0]), ValueError), (dict(lens=n.cpu()), ValueError),
+                          (dict(out=torch.empty((2, 4, 64), dtype=torch.bfloat16, device="cuda")), ValueError),
+                          (dict(slopes=torch.zeros(3, device="cuda")), ValueError), (dict(scale="x"), TypeError),
+                          (dict(workspace=torch.empty(4, device="cuda")), TypeError)):
+        with pytest.raises(error):
+            kda.kda_cache_attn(dev, **{**good, **change})
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_cache_attn(dev, **good, cap=-1.0)
+    assert e.value.status == 1
+    with pytest.raises(kda.KdaError) as e:  # 3 heads over 2 KV heads
+        kda.kda_cache_attn(dev, **{**good, "q": torch.zeros((2, 3, D), dtype=torch.bfloat16, device="cuda")})
+    assert e.value.status == 1
+    with pytest.raises(kda.KdaError) as e:
+        kda.kda_attn_fwd(qd, qd, qd, SCALE, mask="prefix")
+    assert e.value.status == 1
+    with pytest.raises(ValueError, match="N is 3"):
+        kda.kda_attn_fwd(qd, qd, qd, SCALE, N=3, cu_seqlens=cu_of([1, 1]).cuda())
+    ok()
 
 
 # ------------------------------------------------------------------ together
