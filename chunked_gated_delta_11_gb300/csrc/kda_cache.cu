@@ -284,10 +284,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_BINS = 2048;
-constexpr int SEL_PER = SEL_BINS / SEL_THREADS;  // bins per thread
 constexpr int SEL_KEYS = 32768;  // keys that a CTA can hold
 constexpr int SEL_SMEM = SEL_KEYS * 4;
 constexpr int SEL_MAX_CLUSTER = 8;
+constexpr int SEL_GROUPS = SEL_BINS / 32;
+static_assert(SEL_GROUPS * SEL_MAX_CLUSTER == SEL_THREADS, "one word of the cluster's sums a thread");
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
@@ -301,8 +302,33 @@ __device__ __forceinline__ void cluster_sync_all() {
 __device__ __forceinline__ uint32_t cluster_load(const uint32_t* local, unsigned rank) {
   uint32_t at, x;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at));
   return x;
+}
+
+__device__ __forceinline__ uint32_t sum8(uint32_t x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  x += __shfl_xor_sync(0xffffffffu, x, 2);
+  return x + __shfl_xor_sync(0xffffffffu, x, 4);
+}
+// One warp: `a` and `b` are the counts of digits top - 2 lane and top - 2 lane - 1;
+// finds the digit with the need-th slot from the top, and which of the digit's it is.
+__device__ __forceinline__ void pick_digit(uint32_t a, uint32_t b, uint32_t need, int top, uint32_t* pick) {
+  const int l = threadIdx.x & 31;
+  uint32_t sum = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+    if (l >= o) sum += x;
+  }
+  const uint32_t above = sum - a - b;
+  if (above < need && need <= above + a) {
+    pick[0] = top - 2 * l;
+    pick[1] = need - above;
+  } else if (above + a < need && need <= sum) {
+    pick[0] = top - 2 * l - 1;
+    pick[1] = need - above - a;
+  }
 }
 
 // The rows (block * page + slot in it, -1: bad page) of the kept slots of one
@@ -318,6 +344,8 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
               int32_t* __restrict__ kept, int* __restrict__ err) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[2][SEL_BINS];  // alternate, so that a pass can be cleared while others read the last
+  __shared__ uint32_t coarse[2][SEL_GROUPS];  // sums of 32 bins of each
+  __shared__ uint32_t totals[SEL_GROUPS];     // over the cluster
   __shared__ uint32_t warp_n[32];
   __shared__ uint32_t pick[2];   // digit chosen, how many of its slots are still to be kept
   __shared__ uint32_t count[2];  // this CTA's slots above and at the last key
@@ -352,8 +380,32 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
   };
   auto keys4 = [&](int i) -> uint4 { return i < SEL_KEYS ? *reinterpret_cast<const uint4*>(keys + i) : read4(i); };
   for (int i = t; i < 2 * SEL_BINS; i += SEL_THREADS) (&hist[0][0])[i] = 0;
-#pragma unroll 4
-  for (int i = 4 * t; i < mine && i < SEL_KEYS; i += 4 * SEL_THREADS) *reinterpret_cast<uint4*>(keys + i) = read4(i);
+  // 4 groups of 4 slots a thread at a time: table entries, then weights, then keys
+  for (int i0 = 4 * t; i0 < mine && i0 < SEL_KEYS; i0 += 16 * SEL_THREADS) {
+    int id[4];
+    float4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 4 * SEL_THREADS;
+      id[j] = i < mine && i < SEL_KEYS ? __ldg(c.table + static_cast<int64_t>(n) * c.width + ((begin + i) >> c.lg)) : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 4 * SEL_THREADS;
+      if (id[j] >= 0 && id[j] < c.pages)
+        x[j] = __ldg(reinterpret_cast<const float4*>(
+            c.weight + (static_cast<int64_t>(id[j]) * c.Hk + h) * c.page + ((begin + i) & (c.page - 1))));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * 4 * SEL_THREADS;
+      if (i >= mine || i >= SEL_KEYS) continue;
+      const bool good = id[j] >= 0 && id[j] < c.pages;
+      if (!good) atomicCAS(err, 0, static_cast<int>(KDA_ERR_INVALID_ARG));
+      *reinterpret_cast<uint4*>(keys + i) =
+          good ? make_uint4(weight_key(x[j].x), weight_key(x[j].y), weight_key(x[j].z), weight_key(x[j].w)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
   if (t < 2) count[t] = 0;
   __syncthreads();
   uint32_t last = 0, need = static_cast<uint32_t>(want);
@@ -371,44 +423,41 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
         if (i + e < mine && (key[e] & mask) == last) atomicAdd(&hs[(key[e] >> shift) & (bins - 1)], 1u);
     }
     __syncthreads();
+    // The digit of the last kept slot in two steps, groups of 32 bins and then the
+    // group's own: of the other CTAs' histograms (all of them would be 57 KB) only 64
+    // sums and 32 bins are read, one word a thread.
+    uint32_t* cs = coarse[pass & 1];
+#pragma unroll
+    for (int i = 0; i < SEL_GROUPS * 32 / SEL_THREADS; ++i) {
+      const int g = w * (SEL_GROUPS * 32 / SEL_THREADS) + i;
+      const uint32_t x = __reduce_add_sync(0xffffffffu, hs[g * 32 + l]);
+      if (l == 0) cs[g] = x;
+    }
+    __syncthreads();
     if (cluster > 1) cluster_sync_all();
-    // SEL_PER bins per thread, from the top
-    const int hi = SEL_BINS - 1 - SEL_PER * t;
-    uint32_t bin[SEL_PER], own = 0;
-#pragma unroll
-    for (int i = 0; i < SEL_PER; ++i) bin[i] = hs[hi - i];
-    for (int r = 1; r < cluster; ++r) {
-      const unsigned other = (rank + r) % static_cast<unsigned>(cluster);
-#pragma unroll
-      for (int i = 0; i < SEL_PER; ++i) bin[i] += cluster_load(&hs[hi - i], other);
-    }
-#pragma unroll
-    for (int i = 0; i < SEL_PER; ++i) own += bin[i];
-    uint32_t sum = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
-      if (l >= o) sum += x;
-    }
-    if (l == 31) warp_n[w] = sum;
+    // lanes t & 7 of group SEL_GROUPS - 1 - t / 8: the CTAs
+    const unsigned r = t & 7;
+    uint32_t x = r == rank ? cs[SEL_GROUPS - 1 - (t >> 3)]
+                 : r < static_cast<unsigned>(cluster) ? cluster_load(&cs[SEL_GROUPS - 1 - (t >> 3)], r) : 0u;
+    x = sum8(x);
+    if (r == 0) totals[t >> 3] = x;
     __syncthreads();
-    uint32_t before = l < SEL_THREADS / 32 ? warp_n[l] : 0u;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
-      if (l >= o) before += x;
-    }
-    before = w ? __shfl_sync(0xffffffffu, before, w - 1) : 0u;
-    uint32_t above = before + sum - own;  // slots in bins above this one
-#pragma unroll
-    for (int i = 0; i < SEL_PER; ++i) {
-      if (above < need && need <= above + bin[i]) {
-        pick[0] = hi - i;
-        pick[1] = need - above;
-      }
-      above += bin[i];
-    }
+    if (w == 0) pick_digit(totals[2 * l], totals[2 * l + 1], need, SEL_GROUPS - 1, pick);
     __syncthreads();
+    const int group = pick[0] * 32;
+    const uint32_t rest = pick[1];
+    x = 0u;
+    if (t < 256) {
+      const uint32_t* at = &hs[group + 31 - (t >> 3)];
+      x = r == rank ? *at : r < static_cast<unsigned>(cluster) ? cluster_load(at, r) : 0u;
+    }
+    x = sum8(x);
+    __syncthreads();
+    if (r == 0 && t < 256) totals[t >> 3] = x;
+    __syncthreads();
+    if (w == 0) pick_digit(l < 16 ? totals[2 * l] : 0u, l < 16 ? totals[2 * l + 1] : 0u, rest, 31, pick);
+    __syncthreads();
+    last |= static_cast<uint32_t>(group) << shift;
     last |= pick[0] << shift;
     need = pick[1];
     // the last pass uses hist[0] again: the others read it before this pass's barrier
@@ -437,9 +486,15 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
     }
     __syncthreads();
     cluster_sync_all();
-    for (unsigned r = 0; r < rank; ++r) {
-      above0 += cluster_load(&count[0], r);
-      ties0 += cluster_load(&count[1], r);
+    uint32_t theirs[SEL_MAX_CLUSTER - 1][2];
+#pragma unroll
+    for (unsigned r = 0; r < SEL_MAX_CLUSTER - 1; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) theirs[r][i] = r < rank ? cluster_load(&count[i], r) : 0u;
+#pragma unroll
+    for (unsigned r = 0; r < SEL_MAX_CLUSTER - 1; ++r) {
+      above0 += theirs[r][0];
+      ties0 += theirs[r][1];
     }
     cluster_sync_all();  // nobody leaves while its counts are read
   }

@@ -33,7 +33,7 @@ constexpr int CA_WARPS = 4;
 constexpr int CA_STEP = 32;                          // slots of a warp's stage
 constexpr int CA_STAGE_BYTES = 16 * 512 + 128 + 16;  // 16 pieces per lane, positions, scales
 constexpr int CA_PIECE = 18, CA_ROW = 8 * CA_PIECE;  // floats: a warp's output rows in shared memory
-constexpr int CA_WCHUNK = 2048;                      // slots per CTA of the weight sums
+constexpr int CA_WCHUNK = 512;                       // slots per CTA of the weight sums
 
 // 8 rows: 3 CTAs per SM, two stages each.  16 and 32 rows (more registers): 2
 // CTAs, three stages.  32 rows keep the queries' operand words in shared memory.
@@ -726,7 +726,7 @@ __device__ __forceinline__ void add_weights(const CacheAttnArgs& a, const CacheP
                                             const float2* __restrict__ part_ml,
                                             const float* __restrict__ scores, float* lse, int n,
                                             int hk, int len, int first, int* err) {
-  const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int l = threadIdx.x & 31;
   const unsigned group = a.H / a.c.Hk, rt = 8 * plan.nt;
   int64_t bos;
   int cnt;
@@ -734,84 +734,66 @@ __device__ __forceinline__ void add_weights(const CacheAttnArgs& a, const CacheP
   const int64_t rows = static_cast<int64_t>(cnt) * group;
   const int chunks = chunks_of(plan, len);
   const int64_t slot = first_tile(a, plan, n, bos);
-  constexpr int QUADS = CA_WCHUNK / 512;  // groups of 4 slots per thread
-  float4 wsum[QUADS];
-  int at[QUADS], pid[QUADS];
-  const int last = (len - 1) & ~3;
-#pragma unroll
-  for (int j = 0; j < QUADS; ++j) {
-    const int tok = first + j * 512 + threadIdx.x * 4;
-    wsum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    at[j] = tok < len ? tok : last;
-    pid[j] = tok < len ? page_id(a.c, n, tok >> a.c.lg, err) : -1;
-  }
+  const int tok = first + threadIdx.x * 4;         // the thread's 4 slots, of one page
+  const int at = tok < len ? tok : (len - 1) & ~3;  // past the length: reads the last, drops it
+  const int pid = tok < len ? page_id(a.c, n, tok >> a.c.lg, err) : -1;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t r0 = 0; r0 < rows; r0 += rt) {
     const int64_t unit = (slot + r0 / rt) * a.c.Hk + hk;
     const int here = rows - r0 < rt ? static_cast<int>(rows - r0) : static_cast<int>(rt);
     __syncthreads();
-    for (int r = w; r < here; r += 4) {
+    {
+      // denominators: row threadIdx / 4, its chunks over 4 lanes
+      const int r = threadIdx.x >> 2;
       float top = -INFINITY, tot = 0.f;
-      for (int c0 = l; c0 < chunks; c0 += 32) {
-        const float2 ml = part_ml[(unit * plan.splits + c0) * rt + r];
-        const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-        tot = tot * ex2_approx(top - ref) + ml.y * ex2_approx(ml.x - ref);
-        top = mn;
-      }
-      float all = top;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-      tot *= ex2_approx(top - (all == -INFINITY ? 0.f : all));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-      // nothing seen: every score of the row is -inf and gives 0 against 0
-      if (l == 0) lse[r] = all == -INFINITY ? 0.f : all + log2f(tot);
-    }
-    __syncthreads();
-    // two rows' scores of all the thread's slots are under way at a time; a quad past
-    // the length reads the last one instead, and drops what it gets
-    const float* row = scores + unit * rt * plan.max_len;
-    for (int r = 0; r < here; r += 2) {
-      const int rr = r + 1 < here ? r + 1 : r;
-      float4 x[2][QUADS];
-#pragma unroll
-      for (int j = 0; j < QUADS; ++j) {
-        x[0][j] = *reinterpret_cast<const float4*>(row + r * plan.max_len + at[j]);
-        x[1][j] = *reinterpret_cast<const float4*>(row + rr * plan.max_len + at[j]);
-      }
-      const float l0 = lse[r], l1 = rr > r ? lse[rr] : INFINITY;
-#pragma unroll
-      for (int j = 0; j < QUADS; ++j) {
-        wsum[j].x += ex2_approx(x[0][j].x - l0);
-        wsum[j].y += ex2_approx(x[0][j].y - l0);
-        wsum[j].z += ex2_approx(x[0][j].z - l0);
-        wsum[j].w += ex2_approx(x[0][j].w - l0);
-        if (rr > r) {
-          wsum[j].x += ex2_approx(x[1][j].x - l1);
-          wsum[j].y += ex2_approx(x[1][j].y - l1);
-          wsum[j].z += ex2_approx(x[1][j].z - l1);
-          wsum[j].w += ex2_approx(x[1][j].w - l1);
+      if (r < here) {
+        for (int c0 = l & 3; c0 < chunks; c0 += 4) {
+          const float2 ml = part_ml[(unit * plan.splits + c0) * rt + r];
+          const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+          tot = tot * ex2_approx(top - ref) + ml.y * ex2_approx(ml.x - ref);
+          top = mn;
         }
       }
+      float all = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, 2));
+      tot *= ex2_approx(top - (all == -INFINITY ? 0.f : all));
+      tot += __shfl_xor_sync(0xffffffffu, tot, 1);
+      tot += __shfl_xor_sync(0xffffffffu, tot, 2);
+      // nothing seen: every score of the row is -inf and gives 0 against 0; rows that
+      // are not there give 0 against infinity
+      if ((l & 3) == 0) lse[r] = r >= here ? INFINITY : all == -INFINITY ? 0.f : all + log2f(tot);
+    }
+    __syncthreads();
+    const float* row = scores + unit * rt * plan.max_len + at;
+    for (int r = 0; r < here; r += 8) {  // 8 rows under way at a time, added in order
+      float4 x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = r + i < here ? *reinterpret_cast<const float4*>(row + (r + i) * plan.max_len) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = lse[r + i];
+        sum.x += ex2_approx(x[i].x - d);
+        sum.y += ex2_approx(x[i].y - d);
+        sum.z += ex2_approx(x[i].z - d);
+        sum.w += ex2_approx(x[i].w - d);
+      }
     }
   }
-#pragma unroll
-  for (int j = 0; j < QUADS; ++j) {
-    const int tok = first + j * 512 + threadIdx.x * 4;  // 4 slots of one page
-    if (tok >= len || pid[j] < 0) continue;
-    float4* to = reinterpret_cast<float4*>(a.c.weight + (static_cast<int64_t>(pid[j]) * a.c.Hk + hk) * a.c.page +
-                                           (tok & (a.c.page - 1)));
-    float4 x = *to;
-    x.x += wsum[j].x;  // the scores of slots past the length were never written
-    if (tok + 1 < len) x.y += wsum[j].y;
-    if (tok + 2 < len) x.z += wsum[j].z;
-    if (tok + 3 < len) x.w += wsum[j].w;
-    *to = x;
-  }
+  if (pid < 0) return;
+  float4* to = reinterpret_cast<float4*>(a.c.weight + (static_cast<int64_t>(pid) * a.c.Hk + hk) * a.c.page +
+                                         (tok & (a.c.page - 1)));
+  float4 x = *to;
+  x.x += sum.x;  // the scores of slots past the length were never written
+  if (tok + 1 < len) x.y += sum.y;
+  if (tok + 2 < len) x.z += sum.z;
+  if (tok + 3 < len) x.w += sum.w;
+  *to = x;
 }
 
 // Joins the chunks.  The first CTAs take output rows: 4 each, a warp a row, or
 // (plan.splits > 16) one each, 4 warps over its chunks; always in a fixed order.
-// With `scores` the other CTAs add the weights of 2048 slots of a (sequence, KV
+// With `scores` the other CTAs add the weights of 512 slots of a (sequence, KV
 // head) each, the rows in order; a row's denominator they work out again from the
 // chunks' pairs.
 __global__ void __launch_bounds__(128)
@@ -947,7 +929,7 @@ CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   // us), so it is for far more places than that.
   p.ctas = p.splits > 1 && p.tiles * Hk * p.splits > 64 * slots ? static_cast<int>(slots) : 0;
   const int64_t ranges = (max_len + CA_WCHUNK - 1) / CA_WCHUNK, pairs = static_cast<int64_t>(N) * Hk;
-  const int64_t fill = (16384 + pairs - 1) / pairs;
+  const int64_t fill = (32768 + pairs - 1) / pairs;
   p.weight_per = static_cast<int>(ranges < fill ? ranges : fill);
   return p;
 }
