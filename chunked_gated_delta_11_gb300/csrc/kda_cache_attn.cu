@@ -22,8 +22,15 @@
 // Softmax.  Block scales: x = acc * (k_scale * scale / fq); the value scale joins
 //   the exponent, p' = 2^(x + log2 v_scale - m) with m within 2^6 of the running
 //   maximum of x + log2 v_scale, so p' <= 2^6 whatever the scales are and its fp16
-//   rounding (2^-12) is the only one before the output's; the denominator sums
-//   p' / v_scale.
+//   rounding (2^-11 of the value at most) is the only one before the output's; the
+//   denominator sums p' / v_scale.
+//
+// Measured (GB300, replayed from a graph): one sequence of 131072 slots, 8 KV heads
+// of 4 rows, capped and biased, 56 us = 4.8 TB/s (the cap's instructions and one
+// round of chunks); 256 sequences (498,000 slots) with weights 185 us = 5.5 TB/s and 32 us for the
+// join; one of 4096 slots 7.8 us, three launches' worth.  32 sequences x 4 tokens (32
+// rows per KV head) 132 us = 2.2 TB/s: 8 warps per SM with 255 registers each, which
+// neither the copies nor the products keep busy.
 #include "kda_attn.cuh"
 
 namespace kda {
