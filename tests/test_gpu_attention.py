@@ -139,6 +139,50 @@ def test_prefill_other_sequences_reach_no_result(bad, mask):
         within(out[rows], want[rows], tol[rows], "out")
 
 
+# more (256 rows, head) pieces of work than SMs, so that a CTA takes several
+MANY = [random.Random(7).choice([0, 1, 17, 64, 128, 129, 250, 257, 300]) for _ in range(60)]
+
+
+@pytest.mark.parametrize("lengths,H,Hk", [(MANY, 8, 2), ([900, 1300, 0, 20], 32, 4), ([40] * 200, 4, 4)],
+                         ids=["ragged", "long", "short"])
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, False), (5.0, True)])
+def test_prefill_more_work_than_sms(lengths, H, Hk, mask, cap, bias):
+    q, k, v, slopes, prefix = prefill_case(21, lengths, H, Hk, mask, cap, bias)
+    out = run_prefill(q, k, v, lengths, mask, cap, slopes, prefix)
+    ok()
+    want, tol = ref.prefill(q, k, v, SCALE, lengths, mask, cap, slopes, prefix)
+    within(out, want, tol, "out")
+    assert torch.equal(out, run_prefill(q, k, v, lengths, mask, cap, slopes, prefix))
+    ok()
+
+
+def test_prefill_more_work_than_sms_in_a_graph():
+    q, k, v, _, _ = (x if x is None else x.cuda() for x in prefill_case(22, MANY, 8, 2, "causal", 0.0, False))
+    cu, out = cu_of(MANY).cuda(), torch.empty_like(q)
+    want = kda.kda_attn_fwd(q, k, v, SCALE, cu_seqlens=cu).clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            kda.kda_attn_fwd(q, k, v, SCALE, cu_seqlens=cu, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    ok()
+
+
+def test_prefill_malformed_cu_seqlens_with_more_work_than_sms():
+    q, k, v, _, _ = prefill_case(6, [600], 64, 8, "causal", 0.0, False)
+    pad = torch.full((632, 64, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([-5, 900, 30, 2000, 590, 600], dtype=torch.int32).cuda()
+    kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), SCALE, cu_seqlens=cu, out=pad[16:616])
+    torch.cuda.synchronize()
+    assert (pad[:16] == 7).all() and (pad[616:] == 7).all()
+
+
 def test_prefill_malformed_cu_seqlens_stays_in_bounds():
     q, k, v, _, _ = prefill_case(5, [64], 2, 1, "causal", 0.0, False)
     pad = torch.full((96, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
