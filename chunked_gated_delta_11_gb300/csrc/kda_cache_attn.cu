@@ -40,7 +40,7 @@ constexpr int CA_WARPS = 4;
 constexpr int CA_STEP = 32;                          // slots of a warp's stage
 constexpr int CA_STAGE_BYTES = 16 * 512 + 128 + 16;  // 16 pieces per lane, positions, scales
 constexpr int CA_PIECE = 18, CA_ROW = 8 * CA_PIECE;  // floats: a warp's output rows in shared memory
-constexpr int CA_WCHUNK = 512;                       // slots per CTA of the weight sums
+constexpr int ca_wchunk(bool share) { return share ? 128 : 512; }  // slots per CTA of the weight sums
 
 // 8 rows: 3 CTAs per SM, two stages each.  16 and 32 rows (more registers): 2
 // CTAs, three stages.  32 rows keep the queries' operand words in shared memory.
@@ -66,6 +66,7 @@ struct CachePlan {
   int64_t max_len;
   int ctas;        // > 0: that many CTAs share a list of the chunks that exist (plan_kernel)
   int weight_per;  // CTAs of the weight sums per (sequence, KV head)
+  bool share;      // whose warps share the rows of 128 slots, instead of taking 128 slots each
 };
 
 __device__ __forceinline__ void cp16(void* dst, const void* src, bool there) {
@@ -728,26 +729,40 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
   }
 }
 
-// Adds the weights of CA_WCHUNK slots from `first` on; all threads of a CTA of 128.
+// Adds the weights of ca_wchunk(SHARE) slots from `first` on; all threads of a CTA of
+// 128.  Rows in order, 8 of them under way at a time; SHARE: a quarter of every tile's
+// per warp, their loads under way while the denominators are worked out, and the warps'
+// sums in order.
+template <bool SHARE>
 __device__ __forceinline__ void add_weights(const CacheAttnArgs& a, const CachePlan& plan,
                                             const float2* __restrict__ part_ml,
-                                            const float* __restrict__ scores, float* lse, int n,
+                                            const float* __restrict__ scores, float* lse, float (*so)[kDim], int n,
                                             int hk, int len, int first, int* err) {
-  const int l = threadIdx.x & 31;
+  const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
   const unsigned group = a.H / a.c.Hk, rt = 8 * plan.nt;
+  const int most = SHARE ? rt / 4 : 8, mine = SHARE ? w * most : 0;  // the warp's rows of a tile
   int64_t bos;
   int cnt;
   tokens_of(a, plan, n, bos, cnt);
   const int64_t rows = static_cast<int64_t>(cnt) * group;
   const int chunks = chunks_of(plan, len);
   const int64_t slot = first_tile(a, plan, n, bos);
-  const int tok = first + threadIdx.x * 4;         // the thread's 4 slots, of one page
+  const int tok = first + (SHARE ? l : threadIdx.x) * 4;  // the thread's 4 slots, of one page
   const int at = tok < len ? tok : (len - 1) & ~3;  // past the length: reads the last, drops it
   const int pid = tok < len ? page_id(a.c, n, tok >> a.c.lg, err) : -1;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int64_t r0 = 0; r0 < rows; r0 += rt) {
     const int64_t unit = (slot + r0 / rt) * a.c.Hk + hk;
     const int here = rows - r0 < rt ? static_cast<int>(rows - r0) : static_cast<int>(rt);
+    const float* row = scores + unit * rt * plan.max_len + at;
+    float4 x[8];
+    auto load = [&](int r) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = i < most && r + i < here ? *reinterpret_cast<const float4*>(row + (r + i) * plan.max_len)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (SHARE) load(mine);
     __syncthreads();
     {
       // denominators: row threadIdx / 4, its chunks over 4 lanes
@@ -771,20 +786,31 @@ __device__ __forceinline__ void add_weights(const CacheAttnArgs& a, const CacheP
       if ((l & 3) == 0) lse[r] = r >= here ? INFINITY : all == -INFINITY ? 0.f : all + log2f(tot);
     }
     __syncthreads();
-    const float* row = scores + unit * rt * plan.max_len + at;
-    for (int r = 0; r < here; r += 8) {  // 8 rows under way at a time, added in order
-      float4 x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = r + i < here ? *reinterpret_cast<const float4*>(row + (r + i) * plan.max_len) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = mine; r < (SHARE ? mine + 1 : here); r += 8) {
+      if (!SHARE) load(r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = lse[r + i];
+        const float d = i < most ? lse[r + i] : INFINITY;
         sum.x += ex2_approx(x[i].x - d);
         sum.y += ex2_approx(x[i].y - d);
         sum.z += ex2_approx(x[i].z - d);
         sum.w += ex2_approx(x[i].w - d);
       }
+    }
+  }
+  if (SHARE) {
+    __syncthreads();  // (the last chunk's sums have been read)
+    *reinterpret_cast<float4*>(&so[w][l * 4]) = sum;
+    __syncthreads();
+    if (w > 0) return;
+    sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(&so[i][l * 4]);
+      sum.x += x.x;
+      sum.y += x.y;
+      sum.z += x.z;
+      sum.w += x.w;
     }
   }
   if (pid < 0) return;
@@ -800,9 +826,10 @@ __device__ __forceinline__ void add_weights(const CacheAttnArgs& a, const CacheP
 
 // Joins the chunks.  The first CTAs take output rows: 4 each, a warp a row, or
 // (plan.splits > 16) one each, 4 warps over its chunks; always in a fixed order.
-// With `scores` the other CTAs add the weights of 512 slots of a (sequence, KV
-// head) each, the rows in order; a row's denominator they work out again from the
+// With `scores` the other CTAs add the weights of some slots of a (sequence, KV head)
+// each, the rows in a fixed order; a row's denominator they work out again from the
 // chunks' pairs.
+template <bool SHARE>
 __global__ void __launch_bounds__(128)
 join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __restrict__ part_o,
             const float2* __restrict__ part_ml, const float* __restrict__ scores, int* err) {
@@ -898,9 +925,9 @@ join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __r
   const unsigned pair = b / plan.weight_per;
   const int n = pair / static_cast<unsigned>(a.c.Hk), hk = pair - n * a.c.Hk;
   const int len = cached_len(a.c, n, err);
-  for (int64_t first = (b - pair * plan.weight_per) * static_cast<int64_t>(CA_WCHUNK); first < len;
-       first += static_cast<int64_t>(plan.weight_per) * CA_WCHUNK)
-    add_weights(a, plan, part_ml, scores, lse, n, hk, len, static_cast<int>(first), err);
+  const int64_t wide = ca_wchunk(SHARE);
+  for (int64_t first = (b - pair * plan.weight_per) * wide; first < len; first += plan.weight_per * wide)
+    add_weights<SHARE>(a, plan, part_ml, scores, lse, so, n, hk, len, static_cast<int>(first), err);
 }
 
 // Tile heights of 8, 16 and 32 rows by the rows of an average sequence: the cache
@@ -935,7 +962,12 @@ CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   // one's start (256 sequences with a table of their own width: 244 us against 216
   // us), so it is for far more places than that.
   p.ctas = p.splits > 1 && p.tiles * Hk * p.splits > 64 * slots ? static_cast<int>(slots) : 0;
-  const int64_t ranges = (max_len + CA_WCHUNK - 1) / CA_WCHUNK, pairs = static_cast<int64_t>(N) * Hk;
+  // Weight sums: a warp has 128 slots and all rows, unless that leaves SMs idle and there
+  // are rows to share (84 short sequences with 72 rows each: 47 us, shared 32 us; one of
+  // 40,000 slots with 12 rows: 41 us, shared 48 us).
+  const int64_t pairs = static_cast<int64_t>(N) * Hk;
+  p.share = p.nt > 1 && pairs * ((max_len + ca_wchunk(false) - 1) / ca_wchunk(false)) < 2 * 152;
+  const int64_t ranges = (max_len + ca_wchunk(p.share) - 1) / ca_wchunk(p.share);
   const int64_t fill = (32768 + pairs - 1) / pairs;
   p.weight_per = static_cast<int>(ranges < fill ? ranges : fill);
   return p;
@@ -1023,7 +1055,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, in
   const int64_t rows = a.T * a.H, row_ctas = p.splits > 16 ? rows : (rows + 3) / 4;
   const int64_t blocks = row_ctas + weights;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, a, p,
+  return launch_pdl(p.share ? join_kernel<true> : join_kernel<false>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream, a, p,
                     static_cast<unsigned>(row_ctas), static_cast<const float*>(o),
                     static_cast<const float2*>(ml), static_cast<const float*>(scores), err);
 }

@@ -345,6 +345,13 @@ def test_cached_long_sequences(lens, H, Hk, counts):
     check_cached(cache, table, lens, H, [counts] * len(lens), 15, bias=True)
 
 
+@pytest.mark.parametrize("H", [24, 64])
+def test_cached_weights_of_many_slots_and_rows(H):
+    lens = [12000, 9000, 100, 11000]  # enough slots for the weight sums to fill the GPU
+    cache, table = filled(lens, 4, 64, H)
+    check_cached(cache, table, lens, H, [2] * 4, 19)
+
+
 @pytest.mark.parametrize("amp", [0.0, 60.0])
 def test_cached_flat_and_peaked_scores_and_far_scales(amp):
     lens = [900, 64]
