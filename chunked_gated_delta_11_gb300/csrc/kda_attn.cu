@@ -31,6 +31,10 @@
 // products, and no barrier or tensor memory is set up again.  Causal documents of
 // 256 rows: 71 us as a CTA each, 52 us so (8192 rows, 32 heads); of 1024: 96, 84 us.
 //
+// Little work.  With fewer pieces than half the SMs a cluster of CTAs shares each piece's
+// key tiles; the parts are joined through distributed shared memory, every CTA joining
+// some of the channels.
+//
 // Output.  A row's thread holds all of it; written from there, every store of a warp
 // would be 16 bytes of 32 rows (5000 cycles for the 256 rows).  A warp passes half of
 // its channels at a time through 4 KB of its own and stores whole lines (3000).
@@ -63,6 +67,10 @@ constexpr int AT_Q = 0, AT_K = 2 * AT_TILE, AT_V = 4 * AT_TILE, AT_CTL = 6 * AT_
 constexpr int AT_OUT_WARP = 32 * 128;          // 32 rows, 64 channels: staging of a warp's output
 constexpr int AT_OUT = AT_CTL + 512;
 constexpr int AT_SMEM = AT_OUT + 8 * AT_OUT_WARP + 1024;
+// What a CTA does: one piece of work; that and others' (more pieces than SMs); or a share
+// of the key tiles of one, a cluster of CTAs to a piece (few pieces)
+enum { AT_ONE, AT_MORE, AT_SHARE };
+constexpr int AT_MAX_SHARES = 8;
 constexpr float AT_GROW = 16.0f;               // how far a maximum may outgrow the reference
 
 struct AttnMaps {
@@ -232,6 +240,35 @@ struct TileView {
   }
 };
 
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// What the CTA of `rank` has at the place of this CTA's `local`.
+__device__ __forceinline__ uint32_t cluster_place(const void* local, unsigned rank) {
+  uint32_t at;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ float2 cluster_read2(const void* local, unsigned rank) {
+  float2 x;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(cluster_place(local, rank)));
+  return x;
+}
+__device__ __forceinline__ float4 cluster_read4(const void* local, unsigned rank) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(cluster_place(local, rank)));
+  return x;
+}
+
 // Asks for the place of a CTA of this grid that has not started (one lane).  The
 // answer is 16 bytes in ctl->took, counted by ctl->taken.
 __device__ __forceinline__ void ask_place(AttnCtl* ctl) {
@@ -261,9 +298,10 @@ __device__ __forceinline__ bool place_taken(AttnCtl* ctl, uint32_t& place) {
   return yes != 0;
 }
 
-template <bool CAP, bool BIAS, bool MORE>
+template <bool CAP, bool BIAS, int MODE>
 __global__ void __launch_bounds__(AT_THREADS, 1)
-attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, int* err) {
+attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, int shares, int* err) {
+  constexpr bool MORE = MODE == AT_MORE, SHARE = MODE == AT_SHARE;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   AttnCtl* ctl = reinterpret_cast<AttnCtl*>(smem + AT_CTL);
@@ -287,6 +325,24 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     it.prefix = p < 0 ? 0 : (p < it.len ? p : it.len);
     it.slope = BIAS && a.slopes ? __ldg(a.slopes + it.h) * kLog2e : 0.f;
     return it;
+  };
+  const int rank = SHARE ? static_cast<int>(cluster_rank()) : 0;
+  // The key tiles that this CTA takes of an item, last ones first: nj of them, the first
+  // being tile top - 1, and the last n0 and n1 of them for the two query tiles.
+  struct Tiles {
+    int nj, top, n0, n1;
+  };
+  auto tiles_of = [&](const AttnItem& it) -> Tiles {
+    const TileView view{it.len, it.prefix, a.mask};
+    const int n0 = view.tiles(it.i0), n1 = view.tiles(it.i0 + AT_ROWS);
+    const int nj = n0 > n1 ? n0 : n1;
+    if (!SHARE) return {nj, nj, n0, n1};
+    const int from = nj * rank / shares, to = nj * (rank + 1) / shares;
+    auto part = [&](int nt) {
+      const int begin = nj - nt > from ? nj - nt : from;
+      return to > begin ? to - begin : 0;
+    };
+    return {to - from, nj - from, part(n0), part(n1)};
   };
   // The m-th item after the CTA's own, for its readers; false at the end.
   auto next_item = [&](AttnItem& it, int m) -> bool {
@@ -314,7 +370,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     fence_mbar_init();
   }
   if (w == 8) {
-    const AttnItem it = item_at(blockIdx.x);
+    const AttnItem it = item_at(SHARE ? blockIdx.x / static_cast<unsigned>(shares) : blockIdx.x);
     if (l == 0) ctl->first = it;
   }
   if (w == 9) {
@@ -341,10 +397,9 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       for (int m = 0;; ++m) {
         if (l == 0) {
           if (MORE) ask_place(ctl);
-          const TileView view{it.len, it.prefix, a.mask};
-          const int n0 = view.tiles(it.i0), n1 = view.tiles(it.i0 + AT_ROWS);
-          const int nj = n0 > n1 ? n0 : n1, end = first + nj, hk = it.h / (a.H / a.Hk);
-          auto key_row = [&](int g) { return it.bos + static_cast<int64_t>(end - 1 - g) * AT_ROWS; };
+          const Tiles tiles = tiles_of(it);
+          const int nj = tiles.nj, n1 = tiles.n1, end = first + nj, hk = it.h / (a.H / a.Hk);
+          auto key_row = [&](int g) { return it.bos + static_cast<int64_t>(tiles.top - 1 - (g - first)) * AT_ROWS; };
           auto load_k = [&]() -> bool {
             if (ks >= 2 && !wait_for(&ctl->k_empty[ks & 1], ((ks >> 1) - 1) & 1, ctl, err)) return false;
             mbar_arrive_expect_tx(&ctl->k_full[ks & 1], AT_TILE);
@@ -458,9 +513,8 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         int first = 0;             // key tiles of the items before
         int rows0 = 0, rows1 = 0;  // the same of query tiles 0 and 1
         for (int m = 0, items = 0;; ++m) {
-          const TileView view{it.len, it.prefix, a.mask};
-          const int n0 = view.tiles(it.i0), n1 = view.tiles(it.i0 + AT_ROWS);
-          const int nj = n0 > n1 ? n0 : n1;
+          const Tiles tiles = tiles_of(it);
+          const int nj = tiles.nj, n0 = tiles.n0, n1 = tiles.n1;
           // Step j: the weights times key tile nj - 1 - j's values, in stage `stage`, and the
           // next tile's scores (before step 0 those only).  A query tile that sees fewer key
           // tiles joins in at step nj - nt.  False once a wait has run out.
@@ -472,7 +526,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
               if (!wait_for(&ctl->v_full[st], (g >> 1) & 1, ctl, err)) return false;
               if (j == 0) {
                 // the sequence's last keys: zeros in the rows between their end and the last step's
-                const int left = view.len - (nj - 1) * AT_ROWS;
+                const int left = it.len - (tiles.top - 1) * AT_ROWS;
                 steps = left >= AT_ROWS ? AT_ROWS / 16 : (left + 15) / 16;
                 if (left < steps * 16) {
                   for (int r = left; r < steps * 16; ++r)
@@ -524,6 +578,11 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
       }
       __syncwarp();
     }
+    if (SHARE) {
+      __syncwarp();
+      cluster_sync_all();
+      cluster_sync_all();
+    }
   } else {
     regs_take<AT_REGS_SOFTMAX>();
     const int t = w >> 2;
@@ -543,7 +602,13 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     int tiles = 0, items = 0;  // key tiles, and items with any, so far
     for (int m = 0;; ++m) {
       const TileView view{it.len, it.prefix, a.mask};
-      const int i0 = it.i0, nt = view.tiles(i0 + t * AT_ROWS);
+      const int i0 = it.i0, all = view.tiles(i0 + t * AT_ROWS);
+      int nt = all, high = all;  // key tiles, and the one above the first
+      if (SHARE) {
+        const Tiles part = tiles_of(it);
+        nt = t == 0 ? part.n0 : part.n1;
+        high = part.top < all ? part.top : all;
+      }
       const int i = i0 + t * AT_ROWS + (tid & 127);  // row of the sequence
       const int limit = view.limit(i);
       const int tile_lo = view.limit(i0 + t * AT_ROWS);  // least limit of the tile's rows
@@ -554,7 +619,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
         ok = warp_wait(&ctl->s_full[t], (tiles + j) & 1, ctl, err);
         if (!ok) break;
         tc_fence_after();
-        const int j0 = (nt - 1 - j) * AT_ROWS;
+        const int j0 = (high - 1 - j) * AT_ROWS;
         const int lo = i0 + t * AT_ROWS - j0;  // first row less first column
         // Without a cap the row's 128 scores stay in registers.  With one the usual tile
         // takes them 64 at a time in a loop that stays rolled: unrolled, its code
@@ -566,7 +631,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           tmem_wait_ld();
         };
         if (!CAP) load();
-        f2 part[2] = {0ull, 0ull};
+        f2 parts[2] = {0ull, 0ull};
         // weights of a pair of scores, into their sum and a word of P
         auto weigh = [&](f2 x, f2& acc) -> uint32_t {
           float p0, p1;
@@ -602,7 +667,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
                 const f2 u = mul2(xx, xx);
                 f = fma2(u, fma2(u, fma2(u, k3, k2), k1), k0);
               }
-              pk[e >> 1] = weigh(fma2(xx, f, off), part[(e >> 1) & 1]);
+              pk[e >> 1] = weigh(fma2(xx, f, off), parts[(e >> 1) & 1]);
               if (BIAS) off = add2(off, up);
             }
           };
@@ -708,24 +773,97 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           // nothing seen yet: every weight is 0
           const float sub = ref == -INFINITY ? 0.f : ref;
           const f2 off = pair(-sub, -sub);
-          part[0] = part[1] = 0ull;
+          parts[0] = parts[1] = 0ull;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2)
-              pk[e >> 1] = weigh(add2(pair(s[c][e], s[c][e + 1]), off), part[(e >> 1) & 1]);
+              pk[e >> 1] = weigh(add2(pair(s[c][e], s[c][e + 1]), off), parts[(e >> 1) & 1]);
             tmem_st16(S + c * 16, pk);
           }
         }
         float s0, s1;
-        unpair(add2(part[0], part[1]), s0, s1);
+        unpair(add2(parts[0], parts[1]), s0, s1);
         sum += s0 + s1;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&ctl->p_full[t]);
       }
-      if (ok && nt > 0) {
+      if (SHARE) {
+        if (ok && nt > 0) ok = warp_wait(&ctl->o_full[t], 0, ctl, err);
+        tc_fence_after();
+        // Both tiles' products are complete in all of the CTA: the queries' place takes
+        // the rows' references and sums, the keys' and values' their outputs, column
+        // groups of 4 by rows.
+        named_bar(1, 256);
+        const int row = tid & 127;
+        uint8_t* stats = smem + AT_Q + (t * AT_ROWS + row) * 8;
+        uint8_t* mine = smem + AT_K + t * 2 * AT_TILE + row * 16;
+        *reinterpret_cast<float2*>(stats) = make_float2(ok && nt > 0 ? ref : -INFINITY, sum);
+        if (ok && nt > 0) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(O + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(mine + (c * 8 + e) * (AT_ROWS * 16)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        cluster_sync_all();
+        // Every CTA joins a share of the channels, the others' parts in order.
+        float2 ml[AT_MAX_SHARES];
+        float top = -INFINITY, tot = 0.f;
+#pragma unroll
+        for (int p = 0; p < AT_MAX_SHARES; ++p) {
+          ml[p] = make_float2(-INFINITY, 0.f);
+          if (p < shares) ml[p] = cluster_read2(stats, p);
+          top = fmaxf(top, ml[p].x);
+        }
+#pragma unroll
+        for (int p = 0; p < AT_MAX_SHARES; ++p) {
+          ml[p].x = ml[p].x == -INFINITY ? 0.f : ex2_approx(ml[p].x - top);
+          tot = fmaf(ml[p].y, ml[p].x, tot);
+        }
+        const float inv = 1.f / tot;
+        const int rows = view.len - (i - l);
+        uint8_t* out = smem + AT_OUT + w * AT_OUT_WARP;
+        __nv_bfloat16* dst = a.out + ((it.bos + (i - l)) * a.H + it.h) * kDim + (l & 1) * 8;
+        for (int c = rank; c < kDim / 16; c += shares) {  // 16 channels
+          float4 acc[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int p = 0; p < shares; ++p) {
+            float f = 0.f;
+#pragma unroll
+            for (int x = 0; x < AT_MAX_SHARES; ++x) f = x == p ? ml[x].x : f;
+            if (f == 0.f) continue;  // (what a part without a tile left is not its own)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 x = cluster_read4(mine + (c * 4 + e) * (AT_ROWS * 16), p);
+              acc[e].x = fmaf(x.x, f, acc[e].x);
+              acc[e].y = fmaf(x.y, f, acc[e].y);
+              acc[e].z = fmaf(x.z, f, acc[e].z);
+              acc[e].w = fmaf(x.w, f, acc[e].w);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+            *reinterpret_cast<uint4*>(out + l * 32 + (((e >> 1) ^ ((l >> 2) & 1)) << 4)) =
+                make_uint4(pack_bf16(acc[e].x * inv, acc[e].y * inv), pack_bf16(acc[e].z * inv, acc[e].w * inv),
+                           pack_bf16(acc[e + 1].x * inv, acc[e + 1].y * inv), pack_bf16(acc[e + 1].z * inv, acc[e + 1].w * inv));
+          __syncwarp();
+#pragma unroll
+          for (int r = l >> 1; r < 32; r += 16)
+            if (r < rows)
+              *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(r) * a.H * kDim + c * 16) =
+                  *reinterpret_cast<const uint4*>(out + r * 32 + (((l & 1) ^ ((r >> 2) & 1)) << 4));
+          __syncwarp();
+        }
+        cluster_sync_all();  // nobody leaves while its rows are read
+      } else if (ok && nt > 0) {
         ok = warp_wait(&ctl->o_full[t], items & 1, ctl, err);  // the last product
         tc_fence_after();
         if (ok) {
@@ -778,14 +916,37 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
   if (w == 9) tmem_dealloc(tmem, 512);
 }
 
-template <bool CAP, bool BIAS, bool MORE>
-cudaError_t launch_one(const AttnMaps& maps, const AttnArgs& a, int64_t slots, int* err, cudaStream_t stream) {
+template <bool CAP, bool BIAS, int MODE>
+cudaError_t launch_one(const AttnMaps& maps, const AttnArgs& a, int64_t slots, int shares, int* err,
+                       cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto* kernel = attn_kernel<CAP, BIAS, MORE>;
+  auto* kernel = attn_kernel<CAP, BIAS, MODE>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), AT_SMEM, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(slots * a.H)), dim3(AT_THREADS), AT_SMEM, stream,
-                    maps, a, slots, err);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(slots * a.H * shares));
+  cfg.blockDim = dim3(AT_THREADS);
+  cfg.dynamicSmemBytes = AT_SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = shares;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = MODE == AT_SHARE ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, maps, a, slots, shares, err);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const AttnMaps& maps, const AttnArgs& a, int64_t slots, int shares, int* err,
+                        cudaStream_t stream) {
+  // the plain kernel takes its maximum before the scale, which has to be positive for that
+  const bool bias = a.slopes || !(a.scale > 0.f), cap = a.cap > 0.f;
+  auto one = cap ? bias ? launch_one<true, true, MODE> : launch_one<true, false, MODE>
+                 : bias ? launch_one<false, true, MODE> : launch_one<false, false, MODE>;
+  return one(maps, a, slots, shares, err, stream);
 }
 
 }  // namespace
@@ -796,23 +957,23 @@ cudaError_t launch_attn(const AttnArgs& a, int sm_count, int* err, cudaStream_t 
   if (e == cudaSuccess) e = make_tile_map(&maps.k, a.k, a.T, a.Hk, AT_ROWS);
   if (e == cudaSuccess) e = make_tile_map(&maps.v, a.v, a.T, a.Hk, AT_ROWS);
   if (e != cudaSuccess) return e;
-  // the plain kernel takes its maximum before the scale, which has to be positive for that
-  const bool bias = a.slopes || !(a.scale > 0.f), cap = a.cap > 0.f;
   // sequence n owns the slots of 256 rows from floor(bos_n / 256) + n on
   const int64_t slots = a.cu ? a.T / (2 * AT_ROWS) + a.N
                              : (a.T - a.T / a.N) / (2 * AT_ROWS) + a.N - 1 + (a.T / a.N + 2 * AT_ROWS - 1) / (2 * AT_ROWS);
   if (slots * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const int64_t pieces = slots * a.H;
   // A CTA asks for others' work only where some have to wait for a place: asking and its
   // hand-overs cost the smallest calls 0.8 us (64 tokens: 6.9 us against 6.1 us).
-  if (slots * a.H > sm_count)
-    return cap ? bias ? launch_one<true, true, true>(maps, a, slots, err, stream)
-                      : launch_one<true, false, true>(maps, a, slots, err, stream)
-           : bias ? launch_one<false, true, true>(maps, a, slots, err, stream)
-                  : launch_one<false, false, true>(maps, a, slots, err, stream);
-  return cap ? bias ? launch_one<true, true, false>(maps, a, slots, err, stream)
-                    : launch_one<true, false, false>(maps, a, slots, err, stream)
-         : bias ? launch_one<false, true, false>(maps, a, slots, err, stream)
-                : launch_one<false, false, false>(maps, a, slots, err, stream);
+  if (pieces > sm_count) return launch_mode<AT_MORE>(maps, a, slots, 1, err, stream);
+  // Few pieces: a cluster to each, as large as idle SMs allow, where its CTAs have two key
+  // tiles each and that is worth 3 us of joining (4 heads x 2048 tokens: 26.9 us, shared
+  // 16.6 us; 2 x 1024: 15.7 and 12.7 us; 8 x 512: 10.2 and 11.6 us).
+  const int64_t tiles = (a.T / a.N + AT_ROWS - 1) / AT_ROWS;
+  int64_t shares = pieces > 0 ? sm_count / pieces : 1;
+  shares = shares < tiles / 2 ? shares : tiles / 2;
+  shares = tiles < 6 ? 1 : shares < AT_MAX_SHARES ? shares : AT_MAX_SHARES;
+  return shares > 1 ? launch_mode<AT_SHARE>(maps, a, slots, static_cast<int>(shares), err, stream)
+                    : launch_mode<AT_ONE>(maps, a, slots, 1, err, stream);
 }
 
 }  // namespace kda

@@ -183,6 +183,29 @@ def test_prefill_malformed_cu_seqlens_with_more_work_than_sms():
     assert (pad[:16] == 7).all() and (pad[616:] == 7).all()
 
 
+@pytest.mark.parametrize("lengths,H,Hk", [([640], 2, 1), ([1100], 3, 1), ([2200], 2, 2), ([2047, 1, 2500], 1, 1),
+                                          ([0, 1537], 2, 1)])
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix"])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (20.0, True)])
+def test_prefill_few_pieces_shared_by_several_ctas(lengths, H, Hk, mask, cap, bias):
+    q, k, v, slopes, prefix = prefill_case(31, lengths, H, Hk, mask, cap, bias)
+    out = run_prefill(q, k, v, lengths, mask, cap, slopes, prefix)
+    ok()
+    want, tol = ref.prefill(q, k, v, SCALE, lengths, mask, cap, slopes, prefix)
+    within(out, want, tol, "out")
+    assert torch.equal(out, run_prefill(q, k, v, lengths, mask, cap, slopes, prefix))
+    ok()
+
+
+def test_prefill_shared_pieces_of_a_malformed_cu_seqlens():
+    q, k, v, _, _ = prefill_case(32, [2000], 2, 1, "causal", 0.0, False)
+    pad = torch.full((2032, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([-5, 3000, 30], dtype=torch.int32).cuda()
+    kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), SCALE, cu_seqlens=cu, out=pad[16:2016])
+    torch.cuda.synchronize()
+    assert (pad[:16] == 7).all() and (pad[2016:] == 7).all()
+
+
 def test_prefill_malformed_cu_seqlens_stays_in_bounds():
     q, k, v, _, _ = prefill_case(5, [64], 2, 1, "causal", 0.0, False)
     pad = torch.full((96, 2, D), 7.0, dtype=torch.bfloat16, device="cuda")
