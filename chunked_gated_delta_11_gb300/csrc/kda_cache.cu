@@ -18,7 +18,7 @@
 // Both are bound by memory: append reads 2 bytes and writes 1 per element,
 // evict reads one weight per slot and moves 2 x 128 codes per kept slot.
 // Measured (GB300, replayed from a graph): append of 32 ragged prompts (62,700
-// tokens, 8 heads) 84 us = 4.6 TB/s, of 256 single tokens 3.8 us; eviction of 64
+// tokens, 8 heads) 67 us = 5.8 TB/s, of 256 single tokens 3.8 us; eviction of 64
 // ragged sequences to 4096 slots 36 us for the selection and 168 us for the packing,
 // 5.6 TB/s of rows of 128 bytes that lie anywhere; of one sequence 11 us.
 #include "kda_attn.cuh"
@@ -119,106 +119,78 @@ __device__ __forceinline__ bool touched_page(const CacheArgs& c, const int32_t* 
   return p.pid >= 0;
 }
 
-// One CTA per (page that gets rows, KV head).  A row is 16 threads of 8 elements;
-// the new rows stay in registers between the maximum and the codes.
+// A CTA per (page that gets rows, KV head) for its keys and one for its values: what
+// bounds it is the latency of lookups, rows, maximum and codes one after the other, and
+// with one of the two a thread's rows are few enough registers for 6 CTAs per SM (both in
+// one CTA, 4 per SM: 84 us where this takes 67).  A row is 16 threads of 8 elements; the
+// new rows stay in registers between the maximum and the codes.
 template <int PAGE>
 __global__ void __launch_bounds__(256)
 append_kernel(CacheArgs c, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
               const int32_t* __restrict__ positions, const int32_t* __restrict__ cu, int64_t T,
               int* __restrict__ err) {
   constexpr int PASSES = PAGE / 16;
-  __shared__ uint32_t red[2][8];
+  __shared__ uint32_t red[8];
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x, sub = t & 15, row0 = t >> 4, h = blockIdx.y;
+  const bool values = blockIdx.z;
   Touched pg;
   if (!touched_page<PAGE>(c, cu, T, blockIdx.x, err, pg)) return;
   const int lo = pg.lo, hi = pg.hi;
   const int64_t block = static_cast<int64_t>(pg.pid) * c.Hk + h;
+  const __nv_bfloat16* from = (values ? v : k) + (pg.row0 * c.Hk + h) * kDim + sub * 8;
+  float* scale = (values ? c.vs : c.ks) + block;
 
-  uint4 xk[PASSES], xv[PASSES];
-  uint32_t pk = 0u, pv = 0u;  // largest magnitudes, two bf16 at a time as integers
+  uint4 x[PASSES];
+  uint32_t m = 0u;  // largest magnitudes, two bf16 at a time as integers
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int r = p * 16 + row0;
-    xk[p] = xv[p] = make_uint4(0, 0, 0, 0);
-    if (r >= lo && r < hi) {
-      const int64_t at = ((pg.row0 + r - lo) * c.Hk + h) * kDim + sub * 8;
-      xk[p] = *reinterpret_cast<const uint4*>(k + at);
-      xv[p] = *reinterpret_cast<const uint4*>(v + at);
-      pk = larger2(pk, xk[p]);
-      pv = larger2(pv, xv[p]);
-    }
+    x[p] = make_uint4(0, 0, 0, 0);
+    if (r >= lo && r < hi) x[p] = *reinterpret_cast<const uint4*>(from + static_cast<int64_t>(r - lo) * c.Hk * kDim);
   }
-  pk = __reduce_max_sync(0xffffffffu, max(pk & 0xffffu, pk >> 16));
-  pv = __reduce_max_sync(0xffffffffu, max(pv & 0xffffu, pv >> 16));
-  if ((t & 31) == 0) {
-    red[0][t >> 5] = pk;
-    red[1][t >> 5] = pv;
-  }
-  const float oldk = lo > 0 ? c.ks[block] : 0.f, oldv = lo > 0 ? c.vs[block] : 0.f;
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) m = larger2(m, x[p]);
+  m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  if ((t & 31) == 0) red[t >> 5] = m;
+  const float old = lo > 0 ? *scale : 0.f;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    pk = max(pk, red[0][i]);
-    pv = max(pv, red[1][i]);
-  }
-  const bool finite = max(pk, pv) < 0x7f80u;  // the same for the CTA
+  for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+  const bool finite = m < 0x7f80u;  // the same for the CTA
   if (!finite) {
     // infinities or NaN among the rows: the largest finite value, after all
-    float mk = 0.f, mv = 0.f;
+    float most = 0.f;
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      mk = fmaxf(mk, amax8(xk[p]));
-      mv = fmaxf(mv, amax8(xv[p]));
-    }
+    for (int p = 0; p < PASSES; ++p) most = fmaxf(most, amax8(x[p]));
     __syncthreads();
-    const uint32_t bk = __reduce_max_sync(0xffffffffu, __float_as_uint(mk)), bv = __reduce_max_sync(0xffffffffu, __float_as_uint(mv));
-    if ((t & 31) == 0) {
-      red[0][t >> 5] = bk >> 16;
-      red[1][t >> 5] = bv >> 16;
-    }
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    if ((t & 31) == 0) red[t >> 5] = bits >> 16;
     __syncthreads();
-    pk = pv = 0u;
+    m = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      pk = max(pk, red[0][i]);
-      pv = max(pv, red[1][i]);
-    }
+    for (int i = 0; i < 8; ++i) m = max(m, red[i]);
   }
-  const float mk = __uint_as_float(pk << 16), mv = __uint_as_float(pv << 16);
-  const float sk = fmaxf(block_scale(mk), oldk), sv = fmaxf(block_scale(mv), oldv);
-  const float ik = 1.0f / sk, iv = 1.0f / sv;
-  uint8_t* dk = c.k + block * (PAGE * kDim) + sub * 8;
-  uint8_t* dv = c.v + block * (PAGE * kDim) + sub * 8;
+  const float s = fmaxf(block_scale(__uint_as_float(m << 16)), old), inv = 1.0f / s;
+  uint8_t* to = (values ? c.v : c.k) + block * (PAGE * kDim) + sub * 8;
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int r = p * 16 + row0;
     if (r >= lo && r < hi) {
-      *reinterpret_cast<uint2*>(dk + r * kDim) = finite ? encode8<false>(xk[p], ik) : encode8<true>(xk[p], ik);
-      *reinterpret_cast<uint2*>(dv + r * kDim) = finite ? encode8<false>(xv[p], iv) : encode8<true>(xv[p], iv);
-    } else if (r < lo) {
-      if (sk != oldk) {
-        uint2* at = reinterpret_cast<uint2*>(dk + r * kDim);
-        const uint2 x = *at;
-        *at = make_uint2(rescale4(x.x, oldk * ik), rescale4(x.y, oldk * ik));
-      }
-      if (sv != oldv) {
-        uint2* at = reinterpret_cast<uint2*>(dv + r * kDim);
-        const uint2 x = *at;
-        *at = make_uint2(rescale4(x.x, oldv * iv), rescale4(x.y, oldv * iv));
-      }
+      *reinterpret_cast<uint2*>(to + r * kDim) = finite ? encode8<false>(x[p], inv) : encode8<true>(x[p], inv);
+    } else if (r < lo && s != old) {
+      uint2* at = reinterpret_cast<uint2*>(to + r * kDim);
+      const uint2 y = *at;
+      *at = make_uint2(rescale4(y.x, old * inv), rescale4(y.y, old * inv));
     }
   }
-  if (t >= lo && t < hi) {
+  if (!values && t >= lo && t < hi) {
     c.pos[block * PAGE + t] = positions ? __ldg(positions + pg.row0 + t - lo) : static_cast<int32_t>(pg.first + t);
     c.weight[block * PAGE + t] = 0.f;
   }
-  // the old scales were read before the barrier above
-  if (t == 0) {
-    c.ks[block] = sk;
-    c.vs[block] = sv;
-  }
+  // the old scale was read before the barrier above
+  if (t == 0) *scale = s;
 }
 
 // The same for few new rows (serving steps): a warp per (page, KV head), 8 heads
@@ -663,7 +635,7 @@ cudaError_t append_page(const CacheArgs& c, const void* k, const void* v, const 
   if (slots > 0x7fffffffLL) return cudaErrorInvalidValue;
   // a few rows per sequence leave most of a CTA's threads idle: a warp does them
   const bool few = T <= 4 * static_cast<int64_t>(c.N);
-  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(few ? (c.Hk + 7) / 8 : c.Hk));
+  const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(few ? (c.Hk + 7) / 8 : c.Hk), few ? 1 : 2);
   return launch_pdl(few ? append_few_kernel<PAGE> : append_kernel<PAGE>, grid, dim3(256), 0, stream, c,
                     static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), positions, cu,
                     T, err);
