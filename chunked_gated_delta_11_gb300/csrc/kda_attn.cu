@@ -219,7 +219,8 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {
 // maximum error: 2.1e-6, which moves a capped score by 1.5e-4 (in units of log2) at
 // a cap of 50 and so a weight by a twentieth of its bf16 rounding.  Five
 // multiply-adds a score, where an exponential and a reciprocal take 12 cycles of a
-// special-function unit that a tile's weights keep busy already.
+// special-function unit that a tile's weights keep busy already.  For caps up to
+// kCapSmall (a seventh of that rounding); larger ones take kTanhRel, up to kTanhNear.
 constexpr float kTanhMost = 0.7f;
 __device__ constexpr float kTanh[4] = {0.999972696f, -0.332557463f, 0.127291387f, -0.0357217971f};
 
@@ -590,11 +591,14 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
     const uint32_t S = tmem + t * 128 + lane, O = tmem + 256 + t * 128 + lane;
     const float c1 = a.scale * kLog2e;
     const float cap2 = CAP ? a.cap * kLog2e : 0.f, per_cap = CAP ? a.scale / a.cap : 0.f;
-    const float e1 = per_cap * 2.f * kLog2e;
+    const float e1 = CAP ? cap_exponent(a.scale, a.cap) : 0.f;
+    const bool large = CAP && a.cap > kCapSmall;
+    const float tanh_most = large ? kTanhNear : kTanhMost;
     // multipliers of the one-pass scores: s (k0 + k1 s^2 + k2 s^4 + k3 s^6), or s k0
     const float pc2 = per_cap * per_cap;
-    const float w0 = CAP ? kTanh[0] * c1 : c1, w1 = kTanh[1] * c1 * pc2, w2 = kTanh[2] * c1 * pc2 * pc2,
-                w3 = kTanh[3] * c1 * pc2 * pc2 * pc2;
+    const float w0 = CAP ? (large ? kTanhRel[0] : kTanh[0]) * c1 : c1, w1 = (large ? kTanhRel[1] : kTanh[1]) * c1 * pc2,
+                w2 = (large ? kTanhRel[2] : kTanh[2]) * c1 * pc2 * pc2,
+                w3 = (large ? kTanhRel[3] : kTanh[3]) * c1 * pc2 * pc2 * pc2;
     const f2 k0 = pair(w0, w0), k1 = pair(w1, w1), k2 = pair(w2, w2), k3 = pair(w3, w3);
     // a positive scale; with a cap, powers of scale / cap that fp32 holds
     const bool usual = c1 > 0.f && (!CAP || (per_cap > 1e-5f && per_cap < 1e5f));
@@ -696,7 +700,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
           // tanh(y) <= y: c1 is the slope of the capped score at 0 too
           const float bound = most * c1 + base + (BIAS ? fmaxf(step * (AT_ROWS - 1.f), 0.f) : 0.f);
-          done = __all_sync(0xffffffffu, bound <= ref + AT_GROW && (!CAP || most * per_cap <= kTanhMost));
+          done = __all_sync(0xffffffffu, bound <= ref + AT_GROW && (!CAP || most * per_cap <= tanh_most));
           if (CAP && done) {
             tmem_st32(S, first);
             tmem_st32(S + 32, pk);
@@ -712,7 +716,7 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
                 m[(e >> 1) & 1] = fmaxf(fmaxf(m[(e >> 1) & 1], fabsf(__uint_as_float(s[c][e]))), fabsf(__uint_as_float(s[c][e + 1])));
-            small = __all_sync(0xffffffffu, usual && fmaxf(m[0], m[1]) * per_cap <= kTanhMost);
+            small = __all_sync(0xffffffffu, usual && fmaxf(m[0], m[1]) * per_cap <= tanh_most);
           }
           // scores in log2 units, -inf where the row does not see
           if (CAP && small) {
@@ -723,6 +727,13 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
                 const f2 x = pair(s[c][e], s[c][e + 1]), u = mul2(x, x);
                 unpair(mul2(x, fma2(u, fma2(u, fma2(u, k3, k2), k1), k0)), s[c][e], s[c][e + 1]);
               }
+          } else if (CAP && large) {
+            const float one = 1.f / a.cap, far = cap_exponent(1.f, a.cap);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                s[c][e] = __float_as_uint(cap_log2_large(__uint_as_float(s[c][e]) * a.scale, one, far, cap2));
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c)

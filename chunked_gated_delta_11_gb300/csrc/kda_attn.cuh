@@ -49,9 +49,31 @@ struct CacheArgs {
 // cap * tanh(x / cap) * log2 e from one exponential and one reciprocal:
 // tanh(y) = 1 - 2 / (1 + e^(2 y)).  x is scale * q . k; c1 = 2 log2 e / cap, c2 = cap log2 e.
 // The absolute error is a few 2^-24 of cap log2 e (what an exponent can take),
-// which tanh.approx (2^-11 of the result) does not reach.
+// which tanh.approx (2^-11 of the result) does not reach.  For caps up to kCapSmall:
+// there that is 2.2e-5 of a weight at most, a thirtieth of its fp16 rounding.
+constexpr float kCapSmall = 128.0f;
 __device__ __forceinline__ float cap_log2(float x, float c1, float c2) {
   return fmaf(-2.0f * c2, rcp_approx(1.0f + ex2_approx(x * c1)), c2);
+}
+
+// The same to a few 2^-24 of the score itself, for larger caps, where that difference
+// would cancel: tanh(y) = y (t0 + t1 y^2 + t2 y^4 + t3 y^6) for |y| <= 0.35, fitted for
+// the least relative error (3.3e-8; 1.5e-7 with its roundings), and the form above
+// beyond, where it is off by 4.5e-7 of the result at most.  per_cap = 1 / cap.
+constexpr float kTanhNear = 0.35f;
+__device__ constexpr float kTanhRel[4] = {0.99999994f, -0.333324254f, 0.132958218f, -0.0489584431f};
+__device__ __forceinline__ float cap_log2_large(float x, float per_cap, float c1, float c2) {
+  const float y = x * per_cap, u = y * y;
+  const float near = x * kLog2e * fmaf(u, fmaf(u, fmaf(u, kTanhRel[3], kTanhRel[2]), kTanhRel[1]), kTanhRel[0]);
+  const float far = cap_log2(x, c1, c2);
+  return fabsf(y) <= kTanhNear ? near : far;
+}
+
+// c1 of cap_log2 for scores that `scale` is still to be multiplied with; finite for the
+// smallest caps too, so that a score of 0 stays 0.
+__device__ __forceinline__ float cap_exponent(float scale, float cap) {
+  const float c1 = scale * (2.0f * kLog2e / cap);
+  return fminf(fmaxf(c1, -3e38f), 3e38f);
 }
 
 // The cached tokens of sequence n: lens[n], or what its table row can hold (or

@@ -447,7 +447,9 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
 #pragma unroll
       for (int e = 0; e < 2; ++e) qfar[t][e] = POS ? static_cast<float>(qpos[t][e] - qleast) : 0.f;
     if (QSMEM) __syncthreads();
-    const float c1 = CAP ? 2.f * kLog2e / a.cap : 0.f, c2 = CAP ? a.cap * kLog2e : 0.f;
+    const float c1 = CAP ? cap_exponent(1.f, a.cap) : 0.f, c2 = CAP ? a.cap * kLog2e : 0.f;
+    const bool large = CAP && a.cap > kCapSmall;
+    const float per_cap = large ? 1.f / a.cap : 0.f;
 
     float* srow = scores ? scores + unit() * RT * plan.max_len : nullptr;
     int buf = 0;
@@ -542,7 +544,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float& x = s[st][t][2 * r + e];
-              x = CAP ? cap_log2(x * f, c1, c2) + lvs[st] : fmaf(x, f, lvs[st]);
+              x = !CAP ? fmaf(x, f, lvs[st]) : (large ? cap_log2_large(x * f, per_cap, c1, c2) : cap_log2(x * f, c1, c2)) + lvs[st];
             }
           }
       if (bias) {

@@ -1,0 +1,172 @@
+"""The attention operators at the limits of what their contracts allow: caps of any size, keys that a row does not
+see, scales far apart, lengths in place, caches that were evicted from."""
+import itertools
+import math
+
+import pytest
+import torch
+
+import attn_ref as ref
+import chunked_gated_delta_11_gb300 as kda
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+SCALE = D ** -0.5
+SCALE32 = float(torch.tensor(SCALE, dtype=torch.float32))
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    kda.build.build()
+    kda.load()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def randn(g, *shape):
+    return torch.randn(shape, generator=g).to(torch.bfloat16)
+
+
+def cu_of(lengths):
+    return torch.tensor([0] + list(itertools.accumulate(lengths)), dtype=torch.int32)
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def ok():
+    assert kda.kda_device_status() == 0
+
+
+def within(got, want, tol, what):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), f"{what}: non-finite values"
+    over = ((got - want).abs() - tol).max().item()
+    assert over <= 0, f"{what}: {over:.3e} over the tolerance"
+
+
+def to(cache, device):
+    return kda.KvCache(*(t.to(device) for t in cache))
+
+
+# ------------------------------------------------------------------ caps of any size
+# A capped score is off by its fp32 roundings, which are relative to |q||k| and to the score; a cap of at most 128
+# adds up to 2.2e-6 of itself (the fitted tanh of the prefill).  No term grows with a larger cap.
+
+CAPS = [1e-39, 1e-20, 0.5, 50.0, 128.0, 129.0, 1e3, 1e4, 1e5, 1e6, 1e8, 1e30, 3e38]
+
+
+def capped(x, cap):
+    c = float(torch.tensor(cap, dtype=torch.float32))
+    return c * torch.tanh(x / c)
+
+
+def cap_error(cap):
+    return 2.2e-6 * min(cap, 128.0)
+
+
+@pytest.mark.parametrize("cap", CAPS)
+def test_prefill_cap(cap):
+    n, g = 400, gen(1)
+    q, k, v = 4 * randn(g, n, 1, D), randn(g, n, 1, D), randn(g, n, 1, D)
+    out = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), SCALE, cap=cap)
+    ok()
+    qd, kd, vd = (t[:, 0].double() for t in (q, k, v))
+    x = SCALE32 * (qd @ kd.T)
+    d = 160 * ref.F32 * (SCALE32 * (qd.abs() @ kd.abs().T) + x.abs()) + cap_error(cap)
+    seen = torch.ones(n, n, dtype=torch.bool).tril()
+    p = capped(x, cap).masked_fill(~seen, -torch.inf).softmax(1)
+    d = 4 * d.masked_fill(~seen, 0.0).amax(1, keepdim=True)
+    want = p @ vd
+    tol = ref.BF16 * want.abs() * (1 + ref.BF16) + (ref.BF16 + d + 2.0 ** -15) * (p @ vd.abs())
+    within(out[:, 0], want, tol, "out")
+
+
+@pytest.mark.parametrize("H", [1, 12, 24])
+@pytest.mark.parametrize("cap", CAPS)
+def test_cached_cap(cap, H):
+    n, g = 300, gen(2)
+    q = 4 * randn(g, 1, H, D)
+    cache = kda.kda_cache_alloc(5, 1, 64, device="cpu")
+    for t in (cache.k, cache.v):
+        t.copy_(torch.randn(t.shape, generator=g).to(torch.float8_e4m3fn))
+    table = torch.arange(5, dtype=torch.int32)[None]
+    dev = to(cache, "cuda")
+    out = kda.kda_cache_attn(dev, q.cuda(), table.cuda(), ints(n), SCALE, cap=cap, accumulate=True)
+    ok()
+    k, v = (t.double().view(-1, D)[:n] for t in (cache.k, cache.v))
+    x = SCALE32 * (q[0].double() @ k.T)
+    d = 160 * ref.F32 * (SCALE32 * (q[0].double().abs() @ k.abs().T) + x.abs()) + cap_error(cap)
+    p = capped(x, cap).softmax(1)
+    d = 4 * d.amax(1, keepdim=True)
+    want = p @ v
+    tol = ref.BF16 * want.abs() * (1 + ref.BF16) + (ref.F16 + d + 2.0 ** -15) * (p @ v.abs()) \
+        + 4 * 2.0 ** -25 * p.amax(1, keepdim=True) * v.abs().sum(0)
+    within(out[0], want, tol, "out")
+    total = p.sum(0)
+    addtol = ((d + 8 * ref.F32) * p).sum(0) + (H + 4) * ref.F32 * total
+    within(dev.weight.view(-1)[:n], total, addtol, "weight")
+
+
+def one_key(cap, part, n):
+    """A key of capped score L at distance n - 1 against the query's own key of score 0, which a bias brings to 3
+    below it: its weight shows the error of L.  Query's and key's channel 0, the slope, the weight, its score error."""
+    b = 256.0
+    a = float(torch.tensor(part * cap / (SCALE32 * b), dtype=torch.bfloat16))
+    x = torch.tensor(SCALE32 * a * b, dtype=torch.float64)
+    score = float(capped(x, cap))
+    slope = float(torch.tensor((score + 3.0) / (n - 1), dtype=torch.float32))
+    # the keys between have scores of 0 and their own distances
+    gap = torch.arange(n, dtype=torch.float64)
+    s = -slope * gap
+    s[n - 1] += score
+    return a, b, slope, s.softmax(0)[n - 1], 24 * ref.F32 * (abs(float(x)) + abs(score)) + cap_error(cap)
+
+
+@pytest.mark.parametrize("cap", [100.0, 1000.0, 4000.0, 8000.0, 1e5])
+@pytest.mark.parametrize("part", [0.03, 0.1, 0.2, 0.3, 0.36, 0.5, 0.65, 0.9])
+@pytest.mark.parametrize("n", [2, 300])
+def test_prefill_large_scores_under_a_cap(cap, part, n):
+    a, b, slope, weight, d = one_key(cap, part, n)
+    q, k, v = (torch.zeros(n, 1, D, dtype=torch.bfloat16) for _ in range(3))
+    q[:, 0, 0], k[0, 0, 0], v[0] = a, b, 1.0
+    out = kda.kda_attn_fwd(q.cuda(), k.cuda(), v.cuda(), SCALE, cap=cap, slopes=torch.tensor([slope]).cuda())
+    ok()
+    within(out[-1, 0], weight.expand(D), (2.02 * ref.BF16 + 2 * d) * weight, "out")
+
+
+@pytest.mark.parametrize("cap", [100.0, 1000.0, 4000.0, 8000.0, 1e5])
+@pytest.mark.parametrize("part", [0.03, 0.1, 0.2, 0.3, 0.36, 0.5, 0.65, 0.9])
+def test_cached_large_scores_under_a_cap(cap, part):
+    n = 300
+    a, b, slope, weight, d = one_key(cap, part, n)
+    cache = kda.kda_cache_alloc(5, 1, 64, device="cpu")
+    cache.k.view(-1, D)[0, 0] = b
+    cache.pos.view(-1)[:n] = torch.arange(n, dtype=torch.int32)
+    q = torch.zeros(1, 1, D, dtype=torch.bfloat16)
+    q[0, 0, 0] = a
+    dev = to(cache, "cuda")
+    kda.kda_cache_attn(dev, q.cuda(), torch.arange(5, dtype=torch.int32)[None].cuda(), ints(n), SCALE, cap=cap,
+                       slopes=torch.tensor([slope]).cuda(), accumulate=True)
+    ok()
+    within(dev.weight.view(-1)[:1], weight[None], (2 * d + 64 * ref.F32) * weight, "weight")
+
+
+@pytest.mark.parametrize("cap", [1e-39, 1e-37, 1e-20])
+def test_zero_scores_under_a_tiny_cap(cap):
+    n, g = 200, gen(16)
+    zero, v = torch.zeros(n, 1, D, dtype=torch.bfloat16), randn(g, n, 1, D)
+    out = kda.kda_attn_fwd(zero.cuda(), randn(g, n, 1, D).cuda(), v.cuda(), SCALE, mask="full", cap=cap)
+    ok()
+    mean, size = v[:, 0].double().mean(0), v[:, 0].double().abs().mean(0)
+    within(out[:, 0], mean.expand(n, D), ref.BF16 * mean.abs() * (1 + ref.BF16) + (ref.BF16 + 2.0 ** -15) * size, "prefill")
+    cache = kda.kda_cache_alloc(4, 1, 64)
+    table = torch.arange(4, dtype=torch.int32)[None].cuda()
+    kda.kda_cache_append(cache, v.cuda(), v.cuda(), table, ints(0))
+    kda.kda_cache_attn(cache, zero[:1].cuda(), table, ints(n), SCALE, cap=cap, accumulate=True)
+    ok()
+    within(cache.weight.view(-1)[:n], torch.full((n,), 1.0 / n, dtype=torch.float64), 64 * ref.F32 / n, "weight")
