@@ -23,7 +23,8 @@
 //   the exponent, p' = 2^(x + log2 v_scale - m) with m within 2^6 of the running
 //   maximum of x + log2 v_scale, so p' <= 2^6 whatever the scales are and its fp16
 //   rounding (2^-11 of the value at most) is the only one before the output's; the
-//   denominator sums p' / v_scale.
+//   denominator sums p' / v_scale, or (scales far apart, whose p' may leave fp32's range
+//   where their weights do not) 2^(x - m) itself.
 //
 // Measured (GB300, replayed from a graph): one sequence of 131072 slots, 8 KV heads
 // of 4 rows, capped and biased, 56 us = 4.8 TB/s (the cap's instructions and one
@@ -126,6 +127,13 @@ __device__ __forceinline__ float query_factor(float amax) {
   const int f = 14 - e;
   return __uint_as_float(static_cast<uint32_t>((f > 100 ? 100 : f) + 127) << 23);
 }
+
+// A denominator may be as large as 1 / v_scale, so that times 2^d it may count where 2^d
+// is below fp32's range: factors between references are taken as the square of their
+// root, which holds for d down to -252.
+__device__ __forceinline__ float root_factor(float from, float to) { return ex2_approx(0.5f * (from - to)); }
+constexpr float kScaleNormal = 1.17549435e-38f;  // 2^-126: blocks of smaller scales are not seen
+constexpr float kScaleWide = 1.8446744e19f;      // 2^64: value scales that are far apart
 
 // Query tokens of sequence n.
 __device__ __forceinline__ void tokens_of(const CacheAttnArgs& a, const CachePlan& p, int n,
@@ -452,6 +460,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
     const float per_cap = large ? 1.f / a.cap : 0.f;
 
     float* srow = scores ? scores + unit() * RT * plan.max_len : nullptr;
+    float vs_most = 0.f, vs_least = INFINITY;  // v_scale so far
     int buf = 0;
     for (int it = 0; it < steps; ++it) {
       // one group for the keys and one for the values of each stage: 2 STAGES - 1
@@ -514,11 +523,16 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         const float2 sc = *reinterpret_cast<const float2*>(stage + 8320 + st * 8);
-        page_ok[st] = sc.y > 0.f;
+        page_ok[st] = sc.y >= kScaleNormal;
         ksc[st] = sc.x;
         lvs[st] = page_ok[st] ? __log2f(sc.y) : 0.f;
         ivs[st] = page_ok[st] ? ex2_approx(-lvs[st]) : 0.f;  // undoes what the exponent adds
+        vs_most = fmaxf(vs_most, sc.y);
+        vs_least = page_ok[st] ? fminf(vs_least, sc.y) : vs_least;
       }
+      const bool wide = vs_least * kScaleWide < vs_most;  // the same for the warp
+#pragma unroll
+      for (int st = 0; st < 2; ++st) ivs[st] = wide ? 0.f : ivs[st];
       // whole stages of visible slots (almost all) need no selection
       bool whole = t0 + CA_STEP <= we && page_ok[0] && page_ok[1];
       int pl = 0;
@@ -595,7 +609,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
       uint32_t pf[2][NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float mx[2], f[2];
+        float mx[2], f[2], h[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           mx[e] = fmaxf(fmaxf(s[0][t][e], s[0][t][2 + e]), fmaxf(s[1][t][e], s[1][t][2 + e]));
@@ -608,11 +622,11 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
             mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
             const bool grow = mx[e] > m[t][e] + 6.f;
-            f[e] = grow ? ex2_approx(m[t][e] - mx[e]) : 1.f;
+            h[e] = grow ? root_factor(m[t][e], mx[e]) : 1.f;
+            f[e] = h[e] * h[e];
+            sum[t][e] = sum[t][e] * h[e] * h[e];
             if (grow) m[t][e] = mx[e];
           }
-          sum[t][0] *= f[0];
-          sum[t][1] *= f[1];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             o[t][i][0] *= f[0];
@@ -622,6 +636,14 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
           }
         }
         const float ref0 = m[t][0] == -INFINITY ? 0.f : m[t][0], ref1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+        if (wide) {  // the exponentials of the plain scores; p' adds nothing then
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            if (!page_ok[st]) continue;
+            sum[t][0] += ex2_approx(s[st][t][0] - lvs[st] - ref0) + ex2_approx(s[st][t][2] - lvs[st] - ref0);
+            sum[t][1] += ex2_approx(s[st][t][1] - lvs[st] - ref1) + ex2_approx(s[st][t][3] - lvs[st] - ref1);
+          }
+        }
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           const float p0 = ex2_approx(s[st][t][0] - ref0), p1 = ex2_approx(s[st][t][1] - ref1);
@@ -705,11 +727,11 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
 #pragma unroll
       for (int i = 0; i < CA_WARPS; ++i) {
         const float2 ml = sml[i * RT + r];
-        const float f = ex2_approx(ml.x - ref);
+        const float h = root_factor(ml.x, ref), f = h * h;
         const float* at = so + (i * RT + r) * CA_ROW + (l & 3) * (2 * CA_PIECE) + (l >> 2) * 2;
         const float2 x = *reinterpret_cast<const float2*>(at);
         const float2 y = *reinterpret_cast<const float2*>(at + CA_PIECE);
-        tot = fmaf(ml.y, f, tot);
+        tot = fmaf(ml.y * h, h, tot);
         acc.x = fmaf(x.x, f, acc.x);
         acc.y = fmaf(x.y, f, acc.y);
         acc.z = fmaf(y.x, f, acc.z);
@@ -774,13 +796,15 @@ __device__ __forceinline__ void add_weights(const CacheAttnArgs& a, const CacheP
         for (int c0 = l & 3; c0 < chunks; c0 += 4) {
           const float2 ml = part_ml[(unit * plan.splits + c0) * rt + r];
           const float mn = fmaxf(top, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-          tot = tot * ex2_approx(top - ref) + ml.y * ex2_approx(ml.x - ref);
+          const float h0 = root_factor(top, ref), h1 = root_factor(ml.x, ref);
+          tot = tot * h0 * h0 + ml.y * h1 * h1;
           top = mn;
         }
       }
       float all = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, 2));
-      tot *= ex2_approx(top - (all == -INFINITY ? 0.f : all));
+      const float h = root_factor(top, all == -INFINITY ? 0.f : all);
+      tot = tot * h * h;
       tot += __shfl_xor_sync(0xffffffffu, tot, 1);
       tot += __shfl_xor_sync(0xffffffffu, tot, 2);
       // nothing seen: every score of the row is -inf and gives 0 against 0; rows that
@@ -881,17 +905,17 @@ join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __r
       }
       const float mn = fmaxf(fmaxf(fmaxf(top, ml[0].x), ml[1].x), fmaxf(ml[2].x, ml[3].x));
       const float ref = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2_approx(top - ref);
+      const float h = root_factor(top, ref), f = h * h;
       top = mn;
-      tot *= f;
+      tot = tot * h * h;
       acc.x *= f;
       acc.y *= f;
       acc.z *= f;
       acc.w *= f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = ex2_approx(ml[i].x - ref);
-        tot = fmaf(ml[i].y, e, tot);
+        const float r = root_factor(ml[i].x, ref), e = r * r;
+        tot = fmaf(ml[i].y * r, r, tot);
         acc.x = fmaf(x[i].x, e, acc.x);
         acc.y = fmaf(x[i].y, e, acc.y);
         acc.z = fmaf(x[i].z, e, acc.z);
@@ -909,9 +933,9 @@ join_kernel(CacheAttnArgs a, CachePlan plan, unsigned row_ctas, const float* __r
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = ex2_approx(sml[i].x - ref);
+        const float r = root_factor(sml[i].x, ref), e = r * r;
         const float4 x = *reinterpret_cast<const float4*>(&so[i][l * 4]);
-        tot = fmaf(sml[i].y, e, tot);
+        tot = fmaf(sml[i].y * r, r, tot);
         acc.x = fmaf(x.x, e, acc.x);
         acc.y = fmaf(x.y, e, acc.y);
         acc.z = fmaf(x.z, e, acc.z);

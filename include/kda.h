@@ -500,9 +500,11 @@ typedef struct {
  * tokens' own among them.  A query sees the slots whose position is at most its
  * own; with nothing to see (an empty cache) its output is 0.  Slots past
  * lens[n], whatever they hold, reach no result (a NaN code in a slot that only
- * its position hides can spoil queries that share its block).  Scales may be any
- * positive finite numbers; T_total * H is below 2^31.  Sums over splits are added in a fixed order: the same call
- * gives the same bits.
+ * its position hides can spoil queries that share its block).  Key scales may be
+ * any positive finite numbers, value scales any from 2^-100 to 2^120 (kda_cache_append
+ * writes 2^-64 to 2^120), however far apart; a block whose value scale is below 2^-126,
+ * 0 among them, is not seen.  T_total * H is below 2^31.  Sums over splits are
+ * added in a fixed order: the same call gives the same bits.
  * workspace: kda_cache_attn_workspace_size() bytes of device memory, 16-byte
  * aligned, or NULL (= cudaMallocAsync / cudaFreeAsync on the stream). */
 size_t kda_cache_attn_workspace_size(const kda_cache* cache, int64_t T_total, int32_t H, int32_t N,

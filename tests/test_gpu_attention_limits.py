@@ -170,3 +170,46 @@ def test_zero_scores_under_a_tiny_cap(cap):
     kda.kda_cache_attn(cache, zero[:1].cuda(), table, ints(n), SCALE, cap=cap, accumulate=True)
     ok()
     within(cache.weight.view(-1)[:n], torch.full((n,), 1.0 / n, dtype=torch.float64), 64 * ref.F32 / n, "weight")
+
+
+# ------------------------------------------------------------------ scales far apart
+
+@pytest.mark.parametrize("H", [1, 12, 24])
+@pytest.mark.parametrize("small,large", [(None, 70), (None, 110), (-60, 40), (-50, 110), (-60, 30)])
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+def test_cached_blocks_of_scales_far_apart(H, small, large, order):
+    """Blocks of tiny (None: zero) values beside blocks of huge ones: all count in the denominator."""
+    n, page, g = 640, 16, gen(11)
+    blocks = n // page
+    huge = {"up": [j >= blocks // 2 for j in range(blocks)], "down": [j < blocks // 2 for j in range(blocks)],
+            "mixed": [j % 3 == 1 for j in range(blocks)]}[order]
+    k, v = randn(g, n, 1, D), torch.randn((n, 1, D), generator=g)
+    for j, h in enumerate(huge):
+        v[j * page:(j + 1) * page] *= 2.0 ** large if h else 0.0 if small is None else 2.0 ** small
+    cache = kda.kda_cache_alloc(blocks, 1, page)
+    table = torch.arange(blocks, dtype=torch.int32)[None]
+    kda.kda_cache_append(cache, k.cuda(), v.to(torch.bfloat16).cuda(), table.cuda(), ints(0))
+    q = randn(g, 1, H, D)
+    here = to(cache, "cpu")
+    want, tol, add, addtol = ref.cached(here, q, table, [n], SCALE, [1])
+    out = kda.kda_cache_attn(cache, q.cuda(), table.cuda(), ints(n), SCALE, accumulate=True)
+    ok()
+    within(out, want, tol, "out")
+    within(cache.weight, add, addtol + 4 * ref.F32 * add, "weight")
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-40])
+def test_cached_blocks_without_a_normal_scale_are_left_out(scale):
+    n, page, g = 96, 16, gen(12)
+    cache = kda.kda_cache_alloc(6, 1, page)
+    table = torch.arange(6, dtype=torch.int32)[None]
+    kda.kda_cache_append(cache, randn(g, n, 1, D).cuda(), randn(g, n, 1, D).cuda(), table.cuda(), ints(0))
+    cache.v_scale[2] = scale
+    q = randn(g, 1, 4, D)
+    left = to(cache, "cpu")
+    left.pos[2] = n  # after the query
+    want, tol, add, addtol = ref.cached(left, q, table, [n], SCALE, [1])
+    out = kda.kda_cache_attn(cache, q.cuda(), table.cuda(), ints(n), SCALE, accumulate=True)
+    ok()
+    within(out, want, tol, "out")
+    within(cache.weight, add, addtol + 4 * ref.F32 * add, "weight")
