@@ -110,8 +110,9 @@ __device__ __forceinline__ bool touched_page(const CacheArgs& c, const int32_t* 
   const int64_t ahead = s - (bos / PAGE + 2 * static_cast<int64_t>(n));
   const int64_t pj = len / PAGE + ahead;
   p.first = pj * PAGE;
-  // (a malformed cu_seqlens can give a slot before its sequence's first)
-  if (fresh == 0 || ahead < 0 || p.first >= end) return false;
+  // (a malformed cu_seqlens can give a slot before its sequence's first; behind a negative
+  // length, which cached_len reports, there is no place)
+  if (fresh == 0 || ahead < 0 || p.first >= end || __ldg(c.lens + n) < 0) return false;
   p.pid = page_id(c, n, static_cast<int>(pj), err);
   p.lo = static_cast<int>(len > p.first ? len - p.first : 0);
   p.hi = static_cast<int>(end - p.first < PAGE ? end - p.first : PAGE);

@@ -467,7 +467,8 @@ typedef struct {
  * device and are not checked before the launch: an entry outside [0, pages), or
  * a length outside [0, table_width * page_size], makes the kernels skip the page
  * or the surplus, read and write nothing out of range, and latch
- * KDA_ERR_INVALID_ARG for kda_device_status.  No page may stand twice in the
+ * KDA_ERR_INVALID_ARG for kda_device_status.  A negative length counts as an empty
+ * sequence, to which nothing is appended.  No page may stand twice in the
  * tables of one call that writes the cache. */
 
 /* Appends bf16 rows k, v [T_total, Hk, D] of N sequences (cu_seqlens, or equal

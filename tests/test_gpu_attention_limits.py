@@ -213,3 +213,21 @@ def test_cached_blocks_without_a_normal_scale_are_left_out(scale):
     ok()
     within(out, want, tol, "out")
     within(cache.weight, add, addtol + 4 * ref.F32 * add, "weight")
+
+
+# ------------------------------------------------------------------ lengths
+
+@pytest.mark.parametrize("count", [1, 3, 40])
+def test_append_to_a_negative_length_writes_nothing(count):
+    g = gen(8)
+    rows = [0, count, 2 * count]
+    cache = kda.kda_cache_alloc(12, 2, 16)
+    table = torch.arange(12, dtype=torch.int32).view(2, 6).cuda()
+    kda.kda_cache_append(cache, *(randn(g, 40, 2, D).cuda() for _ in range(2)), table, ints(0, 0), positions=ints(*range(40)))
+    was = [t.clone() for t in cache]
+    k, v = (randn(g, 2 * count, 2, D).cuda() for _ in range(2))
+    kda.kda_cache_append(cache, k, v, table, ints(-4, 20), cu_seqlens=ints(*rows))
+    assert kda.kda_device_status() == 1
+    for now, old in zip(cache, was):
+        assert torch.equal(now.view(torch.uint8)[:6], old.view(torch.uint8)[:6])
+    assert not torch.equal(cache.pos[6:], was[4][6:])
