@@ -79,12 +79,14 @@ __device__ __forceinline__ float cap_exponent(float scale, float cap) {
 // The cached tokens of sequence n: lens[n], or what its table row can hold (or
 // 0) and a latched KDA_ERR_INVALID_ARG if it is outside that, so that no later
 // index leaves the tables.
-__device__ __forceinline__ int cached_len(const CacheArgs& c, int n, int* err) {
+__device__ __forceinline__ int checked_len(const CacheArgs& c, int64_t len, int* err) {
   const int64_t most = static_cast<int64_t>(c.width) << c.lg;
-  const int64_t len = __ldg(c.lens + n);
   if (len >= 0 && len <= most) return static_cast<int>(len);
   atomicCAS(err, 0, static_cast<int>(KDA_ERR_INVALID_ARG));
   return static_cast<int>(len < 0 ? 0 : most);
+}
+__device__ __forceinline__ int cached_len(const CacheArgs& c, int n, int* err) {
+  return checked_len(c, __ldg(c.lens + n), err);
 }
 
 // Page id of page j of sequence n, or -1 (and a latched KDA_ERR_INVALID_ARG)

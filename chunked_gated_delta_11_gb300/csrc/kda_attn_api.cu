@@ -245,6 +245,7 @@ extern "C" kda_status kda_cache_evict(const kda_cache* cache, const int32_t* blo
   if ((s = check_table(cache, block_table, table_width, lens, N)) != KDA_OK) return s;
   if (!dst_table || !aligned(dst_table, 4) || dst_width <= 0) return KDA_ERR_INVALID_ARG;
   if (!new_lens || !aligned(new_lens, 4)) return KDA_ERR_INVALID_ARG;
+  if (new_lens != lens && new_lens < lens + N && lens < new_lens + N) return KDA_ERR_INVALID_ARG;
   if (budget <= 0 || recent < 0 || recent > budget) return KDA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t need = kda_cache_evict_workspace_size(cache, N, budget);

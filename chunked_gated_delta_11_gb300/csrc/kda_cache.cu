@@ -317,8 +317,8 @@ __device__ __forceinline__ void pick_digit(uint32_t a, uint32_t b, uint32_t need
 // and counts are summed through distributed shared memory.  What bounds it is the
 // latency of the passes, so few long sequences get the largest cluster.
 __global__ void __launch_bounds__(SEL_THREADS, 2)
-select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restrict__ new_lens,
-              int32_t* __restrict__ kept, int* __restrict__ err) {
+select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restrict__ kept,
+              int* __restrict__ err) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t hist[2][SEL_BINS];  // alternate, so that a pass can be cleared while others read the last
   __shared__ uint32_t coarse[2][SEL_GROUPS];  // sums of 32 bins of each
@@ -333,7 +333,6 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
   const unsigned rank = cluster > 1 ? cluster_rank() : 0u;
   const int n = unit / c.Hk, h = unit - n * c.Hk;
   const int len = cached_len(c, n, err);
-  if (h == 0 && t == 0 && rank == 0) new_lens[n] = len < budget ? len : budget;
   int32_t* list = kept + static_cast<int64_t>(unit) * budget;
   auto row_of = [&](int slot) -> int {
     const int pid = page_id(c, n, slot >> c.lg, err);
@@ -528,7 +527,7 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
 template <int PAGE, int SPLIT>
 __global__ void __launch_bounds__(128, 8)
 pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int budget,
-            const int32_t* __restrict__ kept, int* __restrict__ err) {
+            const int32_t* __restrict__ kept, int32_t* new_lens, int* __restrict__ err) {
   constexpr int LOOKS = (PAGE + 31) / 32;  // rows a lane looks up: lane, lane + 32, ..
   constexpr int GROUPS = PAGE / 4 / SPLIT;  // of 4 rows: the warp's part, + SPLIT, ..
   constexpr int BATCH = GROUPS < 4 ? GROUPS : 4;
@@ -536,7 +535,7 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
   grid_dep_launch();
   const int l = threadIdx.x & 31, unit = blockIdx.x;
   const int n = unit / static_cast<unsigned>(c.Hk), h = unit - n * c.Hk;
-  const int len = cached_len(c, n, err), now = len < budget ? len : budget;
+  const int len = checked_len(c, c.lens[n], err), now = len < budget ? len : budget;
   const int w = threadIdx.x >> 5, part = SPLIT == 1 ? 0 : w;
   const int step = gridDim.y * (4 / SPLIT);
   for (int j = blockIdx.y * (4 / SPLIT) + (SPLIT == 1 ? w : 0); static_cast<int64_t>(j) * PAGE < now; j += step) {
@@ -612,11 +611,14 @@ pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int bud
       c.vs[block] = mv;
     }
   }
+  // new_lens may be lens: here, where every reader comes to the same `now` from either value
+  // (the selection, whose CTAs would not, is over)
+  if (h == 0 && blockIdx.y == 0 && threadIdx.x == 0) new_lens[n] = now;
 }
 
 template <int PAGE>
 cudaError_t launch_pack(const CacheArgs& c, const int32_t* dst, int dst_width, int budget,
-                        const int32_t* kept, int* err, cudaStream_t stream) {
+                        const int32_t* kept, int32_t* new_lens, int* err, cudaStream_t stream) {
   // pages that the kept rows can need, whatever the destination table's width
   const int64_t most = static_cast<int64_t>(c.width) << c.lg;
   const int64_t rows = budget < most ? budget : most;
@@ -626,7 +628,7 @@ cudaError_t launch_pack(const CacheArgs& c, const int32_t* dst, int dst_width, i
   const int64_t y = split ? pages : (pages + 3) / 4;
   return launch_pdl(split ? pack_kernel<PAGE, 4> : pack_kernel<PAGE, 1>,
                     dim3(units, static_cast<unsigned>(y < 65535 ? y : 65535)), dim3(128), 0, stream, c, dst, dst_width,
-                    budget, kept, err);
+                    budget, kept, new_lens, err);
 }
 
 template <int PAGE>
@@ -680,13 +682,13 @@ cudaError_t launch_cache_evict(const CacheArgs& c, const int32_t* dst, int dst_w
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if ((e = cudaLaunchKernelEx(&cfg, select_kernel, c, budget, recent, cluster, new_lens, kept, err)) != cudaSuccess)
+  if ((e = cudaLaunchKernelEx(&cfg, select_kernel, c, budget, recent, cluster, kept, err)) != cudaSuccess)
     return e;
   switch (c.page) {
-    case 16: return launch_pack<16>(c, dst, dst_width, budget, kept, err, stream);
-    case 32: return launch_pack<32>(c, dst, dst_width, budget, kept, err, stream);
-    case 64: return launch_pack<64>(c, dst, dst_width, budget, kept, err, stream);
-    default: return launch_pack<128>(c, dst, dst_width, budget, kept, err, stream);
+    case 16: return launch_pack<16>(c, dst, dst_width, budget, kept, new_lens, err, stream);
+    case 32: return launch_pack<32>(c, dst, dst_width, budget, kept, new_lens, err, stream);
+    case 64: return launch_pack<64>(c, dst, dst_width, budget, kept, new_lens, err, stream);
+    default: return launch_pack<128>(c, dst, dst_width, budget, kept, new_lens, err, stream);
   }
 }
 

@@ -522,8 +522,9 @@ kda_status kda_cache_attn(const kda_cache_attn_options* opts, const kda_cache* c
  * their order.  They are written, with positions and weights, to the pages of
  * dst_table [N, dst_width], none of which may be a page of block_table; their
  * block scale is the largest among the rows' own (codes are rounded again where
- * it differs).  new_lens int32 [N] receives min(lens[n], budget).  A sequence
- * within the budget is copied whole.  The old pages are left as they are.
+ * it differs).  new_lens int32 [N] receives min(lens[n], budget); it may be lens
+ * itself, and must not overlap it otherwise.  A sequence within the budget is
+ * copied whole.  The old pages are left as they are.
  * workspace: kda_cache_evict_workspace_size() bytes, or NULL, as above. */
 size_t kda_cache_evict_workspace_size(const kda_cache* cache, int32_t N, int32_t budget);
 kda_status kda_cache_evict(const kda_cache* cache, const int32_t* block_table, int32_t table_width,

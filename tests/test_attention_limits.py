@@ -1,0 +1,36 @@
+"""Refusals of the softmax-attention entry points at the limits of their contracts (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import chunked_gated_delta_11_gb300 as kda
+from chunked_gated_delta_11_gb300 import attention
+
+FAKE = 1 << 20  # aligned, never dereferenced: validation fails first
+INVALID, WORKSPACE = 1, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kda.build.build()
+    return kda.load()
+
+
+def pool():
+    return attention._Cache(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 8, 64, 2, 128)
+
+
+def evict(lib, lens=FAKE, new_lens=FAKE, budget=100, recent=10, N=4, ws=None, ws_bytes=0):
+    return lib.kda_cache_evict(ctypes.byref(pool()), FAKE, 4, lens, FAKE, 2, budget, recent, N, new_lens, ws, ws_bytes,
+                               None)
+
+
+@pytest.mark.parametrize("shift", [4, 12, -4, -12])
+def test_evict_refuses_new_lengths_that_overlap_the_old_ones(lib, shift):
+    assert evict(lib, new_lens=FAKE + shift) == INVALID
+
+
+@pytest.mark.parametrize("shift", [0, 16, -16])
+def test_evict_takes_lengths_in_place_or_apart(lib, shift):
+    # the next check fails, of a workspace that is too small: nothing was launched
+    assert evict(lib, new_lens=FAKE + shift, ws=FAKE, ws_bytes=16) == WORKSPACE

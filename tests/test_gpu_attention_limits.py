@@ -231,3 +231,34 @@ def test_append_to_a_negative_length_writes_nothing(count):
     for now, old in zip(cache, was):
         assert torch.equal(now.view(torch.uint8)[:6], old.view(torch.uint8)[:6])
     assert not torch.equal(cache.pos[6:], was[4][6:])
+
+
+@pytest.mark.parametrize("lens,budget,recent", [([40_000], 300, 20), ([900, 10, 5000, 300] * 8, 256, 64)])
+def test_evict_lengths_in_place(lens, budget, recent):
+    """new_lens may be the tensor of the lengths."""
+    page, Hk = 64, 4
+    need = [-(-n // page) for n in lens]
+    keep = [-(-min(n, budget) // page) for n in lens]
+    pages = sum(need) + sum(keep)
+    ids = torch.arange(pages, dtype=torch.int32)
+
+    def table_of(counts, first):
+        t = torch.full((len(counts), max(counts)), -1, dtype=torch.int32)
+        for row, m in zip(t, counts):
+            row[:m] = ids[first:first + m]
+            first += m
+        return t.cuda()
+
+    src, dst = table_of(need, 0), table_of(keep, sum(need))
+    made = kda.kda_cache_alloc(pages, Hk, page)
+    made.k.view(torch.uint8).copy_(torch.randint(0, 120, made.k.shape, generator=gen(9), dtype=torch.uint8))
+    made.pos.copy_(torch.arange(made.pos.numel(), dtype=torch.int32).view(made.pos.shape))
+    made.weight.copy_(torch.rand(made.weight.shape, generator=gen(10)))
+    want, got = kda.KvCache(*(t.clone() for t in made)), kda.KvCache(*(t.clone() for t in made))
+    new = kda.kda_cache_evict(want, src, ints(*lens), dst, budget, recent)
+    mine = ints(*lens)
+    assert kda.kda_cache_evict(got, src, mine, dst, budget, recent, new_lens=mine) is not None
+    ok()
+    assert torch.equal(mine, new) and new.tolist() == [min(n, budget) for n in lens]
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
