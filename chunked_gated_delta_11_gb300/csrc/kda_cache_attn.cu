@@ -170,15 +170,6 @@ __device__ __forceinline__ void tile_of(const CacheAttnArgs& a, const CachePlan&
   tile = static_cast<int>(s - first_tile(a, p, n, bos));
 }
 
-// Position of the newest slot, for the slots of KV head hk.
-__device__ __forceinline__ int newest_pos(const CacheAttnArgs& a, int n, int hk, int len, int* err) {
-  if (len == 0) return 0;
-  const int pid = page_id(a.c, n, (len - 1) >> a.c.lg, err);
-  if (pid < 0) return 0;
-  const int64_t b = static_cast<int64_t>(pid) * a.c.Hk + hk;
-  return a.c.pos[b * a.c.page + ((len - 1) & (a.c.page - 1))];
-}
-
 // A warp's view of its stretch [begin, end) of a sequence's slots.
 struct Stretch {
   const CacheArgs& c;
@@ -222,7 +213,7 @@ struct Stretch {
   // take 64 bytes of a row.  Value rows are read by lanes with the rows across the
   // four, so they are copied whole, 8 lanes a row, and their 16-byte pieces stored
   // in the order c ^ (row & 6), where reads of 8 lanes meet no bank conflict.
-  template <bool VALUES, bool POS>
+  template <bool VALUES>
   __device__ __forceinline__ void issue(uint8_t* stage) {
     const int l = threadIdx.x & 31;
     const int r0 = VALUES ? l >> 3 : l >> 2, c0 = VALUES ? l & 7 : l & 3;
@@ -250,7 +241,7 @@ struct Stretch {
     const int half = l >> 4;
     const int64_t mine_row = half ? row[1] : row[0];
     const int mine_left = half ? left[1] : left[0];
-    if (POS) cp4(stage + 8192 + l * 4, c.pos + mine_row + (l & 15), (l & 15) < mine_left);
+    cp4(stage + 8192 + l * 4, c.pos + mine_row + (l & 15), (l & 15) < mine_left);
     if ((l & 15) < 2) cp4(stage + 8320 + half * 8 + (l & 1) * 4, (l & 1 ? c.vs : c.ks) + (mine_row >> c.lg), mine_left > 0);
   }
 };
@@ -306,11 +297,10 @@ plan_kernel(CacheAttnArgs a, CachePlan plan, int32_t* __restrict__ first, int* e
   if (t == 0) first[a.c.N] = static_cast<int32_t>(carry < places ? carry : places);
 }
 
-// POS: query positions matter (a bias, or queries that are not their sequence's
-// newest token).  A CTA takes the chunk that its grid place says, or (LIST, plan.ctas)
+// A CTA takes the chunk that its grid place says, or (LIST, plan.ctas)
 // every so manieth of the list of those that exist: a table much wider than the
 // sequences would otherwise leave most of the grid with nothing to do.
-template <int NT, bool POS, bool CAP, bool LIST>
+template <int NT, bool CAP, bool LIST>
 __global__ void __launch_bounds__(CA_WARPS * 32, ca_ctas(NT))
 cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ list,
                   float* __restrict__ part_o, float2* __restrict__ part_ml,
@@ -365,15 +355,19 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
     const int we = end < wb + quarter ? end : wb + quarter;
     const int steps = we > wb ? (we - wb + CA_STEP - 1) / CA_STEP : 0;
     uint8_t* ring = smem + ca_qbytes(NT) + w * (STAGES * CA_STAGE_BYTES);
+    // Without given positions the queries are the newest tokens.  That slot's page is looked up
+    // beside the first of the chunk's own, its position beside the queries.
+    const bool by_newest = !a.positions && len > 0;
+    const int newest_page = by_newest ? __ldg(a.c.table + static_cast<int64_t>(n) * a.c.width + ((len - 1) >> a.c.lg)) : -1;
     Stretch src(a.c, n, hk, we, err);
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
       if (i < steps) {
         src.locate(wb + i * CA_STEP);
-        src.issue<false, POS>(ring + i * CA_STAGE_BYTES);
+        src.issue<false>(ring + i * CA_STAGE_BYTES);
       }
       cp_commit();
-      if (i < steps) src.issue<true, POS>(ring + i * CA_STAGE_BYTES);
+      if (i < steps) src.issue<true>(ring + i * CA_STAGE_BYTES);
       cp_commit();
     }
 
@@ -383,8 +377,9 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
     float mul[NT][2], slope[NT][2], m[NT][2], sum[NT][2];
     int qpos[NT][2];
     int qleast = 0x7fffffff;  // least position of the tile's queries
-    // without given positions the queries are the newest tokens
-    const int newest = POS && !a.positions ? newest_pos(a, n, hk, len, err) : 0;
+    int newest = 0;  // for a bad page too, which the chunk that has it reports
+    if (newest_page >= 0 && newest_page < a.c.pages)
+      newest = a.c.pos[(static_cast<int64_t>(newest_page) * a.c.Hk + hk) * a.c.page + ((len - 1) & (a.c.page - 1))];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = 8 * t + g;
@@ -428,7 +423,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
         mul[t][e] = __shfl_sync(0xffffffffu, inv, (2 * q + e) * 4) * a.scale * (CAP ? 1.f : kLog2e);
         slope[t][e] = 0.f;
         qpos[t][e] = -1;
-        if (POS && c < rows) {
+        if (c < rows) {
           const unsigned rr = row0 + c, tok = rr / group;
           qpos[t][e] = a.positions ? __ldg(a.positions + bos + tok) : newest - (cnt - 1 - static_cast<int>(tok));
           qleast = qleast < qpos[t][e] ? qleast : qpos[t][e];
@@ -445,15 +440,13 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
-    if (POS) {
-      qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 1));
-      qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 2));
-    }
+    qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 1));
+    qleast = min(qleast, __shfl_xor_sync(0xffffffffu, qleast, 2));
     float qfar[NT][2];  // positions relative to that
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) qfar[t][e] = POS ? static_cast<float>(qpos[t][e] - qleast) : 0.f;
+      for (int e = 0; e < 2; ++e) qfar[t][e] = static_cast<float>(qpos[t][e] - qleast);
     if (QSMEM) __syncthreads();
     const float c1 = CAP ? cap_exponent(1.f, a.cap) : 0.f, c2 = CAP ? a.cap * kLog2e : 0.f;
     const bool large = CAP && a.cap > kCapSmall;
@@ -535,19 +528,16 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
       for (int st = 0; st < 2; ++st) ivs[st] = wide ? 0.f : ivs[st];
       // whole stages of visible slots (almost all) need no selection
       bool whole = t0 + CA_STEP <= we && page_ok[0] && page_ok[1];
-      int pl = 0;
-      if (POS) {
-        pl = *reinterpret_cast<const int*>(stage + 8192 + l * 4);
-        whole = __all_sync(0xffffffffu, whole && pl <= qleast);
-      }
+      const int pl = *reinterpret_cast<const int*>(stage + 8192 + l * 4);
+      whole = __all_sync(0xffffffffu, whole && pl <= qleast);
       // the keys have been read by every lane: refill them while the rest goes on
       __syncwarp();
       if (it + STAGES < steps) {
         src.locate(t0 + STAGES * CA_STEP);
-        src.issue<false, POS>(stage);
+        src.issue<false>(stage);
       }
       cp_commit();
-      const bool bias = POS && a.slopes != nullptr;
+      const bool bias = a.slopes != nullptr;
 #pragma unroll
       for (int st = 0; st < 2; ++st)
 #pragma unroll
@@ -580,13 +570,13 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
         for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int p = POS ? __shfl_sync(0xffffffffu, pl, 16 * st + 8 * r + g) : 0;
+            const int p = __shfl_sync(0xffffffffu, pl, 16 * st + 8 * r + g);
             const bool there = t0 + 16 * st + 8 * r + g < we && page_ok[st];
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int e = 0; e < 2; ++e)
-                if (!there || (POS && p > qpos[t][e])) s[st][t][2 * r + e] = -INFINITY;
+                if (!there || p > qpos[t][e]) s[st][t][2 * r + e] = -INFINITY;
           }
       }
       if (srow) {
@@ -685,7 +675,7 @@ cache_attn_kernel(CacheAttnArgs a, CachePlan plan, const int32_t* __restrict__ l
         }
       }
       __syncwarp();
-      if (it + STAGES < steps) src.issue<true, POS>(stage);
+      if (it + STAGES < steps) src.issue<true>(stage);
       cp_commit();
     }
 
@@ -1020,11 +1010,11 @@ CacheScratch scratch_of(const CachePlan& p, int Hk, bool accumulate) {
   return s;
 }
 
-template <int NT, bool POS, bool CAP, bool LIST>
+template <int NT, bool CAP, bool LIST>
 cudaError_t launch_one(const CacheAttnArgs& a, const CachePlan& p, const int32_t* list, float* o,
                        float2* ml, float* scores, int* err, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  auto* kernel = cache_attn_kernel<NT, POS, CAP, LIST>;
+  auto* kernel = cache_attn_kernel<NT, CAP, LIST>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), ca_smem(NT), done);
   if (e != cudaSuccess) return e;
   const dim3 grid = p.ctas ? dim3(static_cast<unsigned>(p.ctas))
@@ -1033,13 +1023,10 @@ cudaError_t launch_one(const CacheAttnArgs& a, const CachePlan& p, const int32_t
 }
 
 template <int NT>
-cudaError_t launch_variant(bool pos, bool cap, const CacheAttnArgs& a, const CachePlan& p,
-                           const int32_t* list, float* o, float2* ml, float* scores, int* err,
-                           cudaStream_t stream) {
-  auto one = p.ctas ? pos ? cap ? launch_one<NT, true, true, true> : launch_one<NT, true, false, true>
-                          : cap ? launch_one<NT, false, true, true> : launch_one<NT, false, false, true>
-             : pos  ? cap ? launch_one<NT, true, true, false> : launch_one<NT, true, false, false>
-                    : cap ? launch_one<NT, false, true, false> : launch_one<NT, false, false, false>;
+cudaError_t launch_variant(bool cap, const CacheAttnArgs& a, const CachePlan& p, const int32_t* list,
+                           float* o, float2* ml, float* scores, int* err, cudaStream_t stream) {
+  auto one = p.ctas ? cap ? launch_one<NT, true, true> : launch_one<NT, false, true>
+                    : cap ? launch_one<NT, true, false> : launch_one<NT, false, false>;
   return one(a, p, list, o, ml, scores, err, stream);
 }
 
@@ -1070,12 +1057,10 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, in
       if (e != cudaSuccess) return e;
     }
   }
-  // positions matter for the bias, and where a query is not its sequence's newest token
-  const bool pos = a.slopes || a.positions || a.cu || a.T != a.c.N;
   const bool cap = a.cap > 0.f;
-  e = p.nt == 1   ? launch_variant<1>(pos, cap, a, p, list, o, ml, scores, err, stream)
-      : p.nt == 2 ? launch_variant<2>(pos, cap, a, p, list, o, ml, scores, err, stream)
-                  : launch_variant<4>(pos, cap, a, p, list, o, ml, scores, err, stream);
+  e = p.nt == 1   ? launch_variant<1>(cap, a, p, list, o, ml, scores, err, stream)
+      : p.nt == 2 ? launch_variant<2>(cap, a, p, list, o, ml, scores, err, stream)
+                  : launch_variant<4>(cap, a, p, list, o, ml, scores, err, stream);
   if (e != cudaSuccess || !s.total) return e;
   const int64_t weights = a.accumulate ? static_cast<int64_t>(p.weight_per) * a.c.N * a.c.Hk : 0;
   const int64_t rows = a.T * a.H, row_ctas = p.splits > 16 ? rows : (rows + 3) / 4;

@@ -262,3 +262,60 @@ def test_evict_lengths_in_place(lens, budget, recent):
     assert torch.equal(mine, new) and new.tolist() == [min(n, budget) for n in lens]
     for a, b in zip(got, want):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ positions
+
+def test_cached_single_tokens_see_no_later_position():
+    """The newest slot's position is the query's, whatever the other slots hold; the ways to say so agree."""
+    g, n = gen(13), [200, 77]
+    cache = kda.kda_cache_alloc(8, 2, 64)
+    table = torch.arange(8, dtype=torch.int32).view(2, 4)
+    order = torch.cat([torch.randperm(m, generator=g) for m in n]).to(torch.int32)
+    kda.kda_cache_append(cache, randn(g, sum(n), 2, D).cuda(), randn(g, sum(n), 2, D).cuda(), table.cuda(), ints(0, 0),
+                         positions=order.cuda(), cu_seqlens=cu_of(n).cuda())
+    q = randn(g, 2, 8, D)
+    want, tol, add, addtol = ref.cached(to(cache, "cpu"), q, table, n, SCALE, [1, 1])
+    assert (add == 0).sum() > (n[0] + n[1]) // 4
+    call = lambda **kw: kda.kda_cache_attn(cache, q.cuda(), table.cuda(), ints(*n), SCALE, **kw)  # noqa: E731
+    plain = call(accumulate=True)
+    within(plain, want, tol, "out")
+    within(cache.weight, add, addtol + 4 * ref.F32 * add, "weight")
+    for kw in (dict(cu_seqlens=ints(0, 1, 2)), dict(positions=ints(int(order[199]), int(order[276]))),
+               dict(slopes=torch.zeros(8).cuda())):
+        assert torch.equal(call(**kw), plain)
+    ok()
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [1, 4]])
+def test_a_cache_that_was_evicted_from(counts):
+    """After eviction every KV head has slots and positions of its own; new tokens are appended and attended to."""
+    n, page, Hk, H, budget = [500, 333], 64, 2, 8, 130
+    g = gen(14)
+    cache = kda.kda_cache_alloc(32, Hk, page)
+    table = torch.arange(32, dtype=torch.int32).view(2, 16)
+    src, dst = table[:, :8].contiguous(), table[:, 8:].contiguous()
+    rows = lambda m: [randn(g, m, Hk, D).cuda() for _ in range(2)]  # noqa: E731
+    kda.kda_cache_append(cache, *rows(sum(n)), src.cuda(), ints(0, 0), cu_seqlens=cu_of(n).cuda())
+    kda.kda_cache_attn(cache, 4 * randn(g, 2, H, D).cuda(), src.cuda(), ints(*n), SCALE, accumulate=True)
+    lens = kda.kda_cache_evict(cache, src.cuda(), ints(*n), dst.cuda(), budget, 20)
+    positions = [n[s] + i for s, c in enumerate(counts) for i in range(c)]
+    kda.kda_cache_append(cache, *rows(sum(counts)), dst.cuda(), lens, positions=ints(*positions),
+                         cu_seqlens=cu_of(counts).cuda())
+    ok()
+    lens = [m + c for m, c in zip(lens.tolist(), counts)]
+    here = to(cache, "cpu")
+    assert lens == [budget + c for c in counts]
+    assert not torch.equal(here.pos[8, 0], here.pos[8, 1])
+    q = 2 * randn(g, sum(counts), H, D)
+    slopes = 0.05 * torch.rand(H, generator=g)
+    for bias in (None, slopes):
+        for at in (None, torch.tensor(positions, dtype=torch.int32)):
+            was = cache.weight.double().cpu()
+            want, tol, add, addtol = ref.cached(here, q, dst, lens, SCALE, counts, slopes=bias, positions=at)
+            out = kda.kda_cache_attn(cache, q.cuda(), dst.cuda(), ints(*lens), SCALE, accumulate=True,
+                                     slopes=None if bias is None else bias.cuda(),
+                                     positions=None if at is None else at.cuda(), cu_seqlens=cu_of(counts).cuda())
+            ok()
+            within(out, want, tol, "out")
+            within(cache.weight, was + add, addtol + 4 * ref.F32 * (was + add), "weight")
