@@ -72,6 +72,7 @@ constexpr int AT_SMEM = AT_OUT + 8 * AT_OUT_WARP + 1024;
 enum { AT_ONE, AT_MORE, AT_SHARE };
 constexpr int AT_MAX_SHARES = 8;
 constexpr float AT_GROW = 16.0f;               // how far a maximum may outgrow the reference
+constexpr float AT_HEAD = 40.0f;               // and how far above it the reference of a row starts that its first tile hides keys from
 
 struct AttnMaps {
   CUtensorMap q, k, v;
@@ -645,33 +646,55 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
           acc = add2(acc, pair(p0, p1));
           return pack_bf16(p0, p1);
         };
-        // The usual tile: no row's limit in it, a bias linear in the column, scores well
-        // under the cap, none far above the reference.  From products to weights in one
-        // pass, with the largest product found on the way; if that shows that the
-        // reference had to move or the polynomial does not hold, the warp does the tile
-        // again below.
-        bool done = false;
+        // The row's reference becomes `top` where it grows: what it has so far follows.
+        auto move_ref = [&](bool grow, float top) {
+          if (!__any_sync(0xffffffffu, grow)) return;
+          const float now = grow ? top : ref;
+          const float f = grow ? ex2_approx(ref - now) : 1.f;
+          sum *= f;
+          ref = now;
+          if (j == 0) return;
+          // the products of the tiles before are complete (S came after them)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(O + c * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(O + c * 32, o);
+          }
+        };
+        // The usual tile: no row's limit in it, a bias linear in the column.  From products to
+        // weights in one pass, with the largest product found on the way; if that shows that
+        // a row's reference had to move, or that the polynomial does not hold somewhere, the
+        // warp does the tile again.  What a row gets is the same bits either way unless its
+        // own reference moves: the other rows of its warp, which may be another sequence's
+        // or see later keys, do not show in it.
         if (j > 0 && j0 + AT_ROWS <= tile_lo && usual && (!BIAS || lo >= AT_ROWS - 1 || lo + AT_ROWS - 1 <= 0)) {
           const float step = lo >= 0 ? slope : -slope;
           const float base = BIAS ? -step * static_cast<float>(i - j0) : 0.f;
           const f2 up = pair(2.f * step, 2.f * step);
           float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto under_cap = [&](f2 xx) -> f2 {
+            const f2 u = mul2(xx, xx);
+            return fma2(u, fma2(u, fma2(u, k3, k2), k1), k0);
+          };
+          // what the score of column col, and of the next, is off by
+          auto offset = [&](float col, float less) -> f2 {
+            const float off0 = fmaf(step, col, base - less);
+            return pair(off0, off0 + step);
+          };
           // weights of 32 columns from column col on
-          auto columns = [&](const uint32_t (&x)[32], uint32_t* pk, float col) {
-            const float off0 = base - ref + step * col;
-            f2 off = pair(off0, off0 + step);  // what the column's score is off by
+          auto columns = [&](const uint32_t (&x)[32], uint32_t* pk, float col, float less) {
+            f2 off = offset(col, less);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float x0 = __uint_as_float(x[e]), x1 = __uint_as_float(x[e + 1]);
               float& mx = m[(e >> 1) & 3];
               mx = CAP ? fmaxf(fmaxf(mx, fabsf(x0)), fabsf(x1)) : max3(mx, x0, x1);
               const f2 xx = pair(x0, x1);
-              f2 f = k0;
-              if (CAP) {
-                const f2 u = mul2(xx, xx);
-                f = fma2(u, fma2(u, fma2(u, k3, k2), k1), k0);
-              }
-              pk[e >> 1] = weigh(fma2(xx, f, off), parts[(e >> 1) & 1]);
+              pk[e >> 1] = weigh(fma2(xx, CAP ? under_cap(xx) : k0, off), parts[(e >> 1) & 1]);
               if (BIAS) off = add2(off, up);
             }
           };
@@ -686,29 +709,99 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
               tmem_ld32(S + half * 64, s[0]);
               tmem_ld32(S + half * 64 + 32, s[1]);
               tmem_wait_ld();
-              columns(s[0], pk, 64.f * half);
-              columns(s[1], pk + 16, 64.f * half + 32.f);
+              columns(s[0], pk, 64.f * half, ref);
+              columns(s[1], pk + 16, 64.f * half + 32.f, ref);
             }
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t p16[16];
-              columns(s[c], p16, 32.f * c);
+              columns(s[c], p16, 32.f * c, ref);
               tmem_st16(S + c * 16, p16);
             }
           }
           const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
           // tanh(y) <= y: c1 is the slope of the capped score at 0 too
           const float bound = most * c1 + base + (BIAS ? fmaxf(step * (AT_ROWS - 1.f), 0.f) : 0.f);
-          done = __all_sync(0xffffffffu, bound <= ref + AT_GROW && (!CAP || most * per_cap <= tanh_most));
-          if (CAP && done) {
-            tmem_st32(S, first);
-            tmem_st32(S + 32, pk);
+          const bool stays = bound <= ref + AT_GROW && ref > -INFINITY;
+          if (__all_sync(0xffffffffu, stays && (!CAP || most * per_cap <= tanh_most))) {
+            if (CAP) {
+              tmem_st32(S, first);
+              tmem_st32(S + 32, pk);
+            }
+          } else if (!CAP) {
+            float top = most * c1;
+            if (BIAS) {
+              float t[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                f2 off = offset(32.f * c, 0.f);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float x0, x1;
+                  unpair(fma2(pair(s[c][e], s[c][e + 1]), k0, off), x0, x1);
+                  t[(e >> 1) & 1] = max3(t[(e >> 1) & 1], x0, x1);
+                  off = add2(off, up);
+                }
+              }
+              top = fmaxf(t[0], t[1]);
+            }
+            move_ref(!stays && top > ref, top);
+            parts[0] = parts[1] = 0ull;
+            const float less = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t p16[16];
+              columns(s[c], p16, 32.f * c, less);
+              tmem_st16(S + c * 16, p16);
+            }
+          } else {
+            // scores of a pair with their offsets: the polynomial where it holds, else the exact form
+            auto score = [&](const uint32_t& a0, const uint32_t& a1, f2 off) -> f2 {
+              const float x0 = __uint_as_float(a0), x1 = __uint_as_float(a1);
+              const f2 xx = pair(x0, x1);
+              float s0, s1, off0, off1;
+              unpair(fma2(xx, under_cap(xx), off), s0, s1);
+              unpair(off, off0, off1);
+              s0 = fabsf(x0) * per_cap <= tanh_most ? s0 : cap_log2(x0, e1, cap2) + off0;
+              s1 = fabsf(x1) * per_cap <= tanh_most ? s1 : cap_log2(x1, e1, cap2) + off1;
+              return pair(s0, s1);
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(S + c * 32, s[0]);
+              tmem_wait_ld();
+              f2 off = offset(32.f * c, 0.f);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x0, x1;
+                unpair(score(s[0][e], s[0][e + 1], off), x0, x1);
+                top = max3(top, x0, x1);
+                if (BIAS) off = add2(off, up);
+              }
+            }
+            move_ref(!stays && top > ref, top);
+            parts[0] = parts[1] = 0ull;
+            const float less = ref == -INFINITY ? 0.f : ref;
+            // P goes over scores that have been read
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t p16[16];
+              tmem_ld32(S + c * 32, s[0]);
+              tmem_wait_ld();
+              f2 off = offset(32.f * c, less);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                p16[e >> 1] = weigh(score(s[0][e], s[0][e + 1], off), parts[(e >> 1) & 1]);
+                if (BIAS) off = add2(off, up);
+              }
+              tmem_st16(S + c * 16, p16);
+            }
           }
-        }
-        if (!done) {
+        } else {
           if (CAP) load();
-          bool small = false;  // the polynomial holds for the warp's scores
+          // scores in log2 units
           if (CAP) {
             float m[2] = {0.f, 0.f};
 #pragma unroll
@@ -716,30 +809,37 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
                 m[(e >> 1) & 1] = fmaxf(fmaxf(m[(e >> 1) & 1], fabsf(__uint_as_float(s[c][e]))), fabsf(__uint_as_float(s[c][e + 1])));
-            small = __all_sync(0xffffffffu, usual && fmaxf(m[0], m[1]) * per_cap <= tanh_most);
-          }
-          // scores in log2 units, -inf where the row does not see
-          if (CAP && small) {
+            // the polynomial, and the exact form where that does not hold for a score
+            const bool small = __all_sync(0xffffffffu, usual && fmaxf(m[0], m[1]) * per_cap <= tanh_most);
+            if (usual) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const f2 x = pair(s[c][e], s[c][e + 1]), u = mul2(x, x);
-                unpair(mul2(x, fma2(u, fma2(u, fma2(u, k3, k2), k1), k0)), s[c][e], s[c][e + 1]);
+                for (int e = 0; e < 32; e += 2) {
+                  const f2 x = pair(s[c][e], s[c][e + 1]), u = mul2(x, x);
+                  unpair(mul2(x, fma2(u, fma2(u, fma2(u, k3, k2), k1), k0)), s[c][e], s[c][e + 1]);
+                }
+            }
+            if (!small) {
+              const float limit_y = usual ? tanh_most : large ? kTanhNear : -1.f;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t raw[32];
+                tmem_ld32(S + c * 32, raw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  const float x = __uint_as_float(raw[e]), y = x * per_cap;
+                  const float near = usual ? __uint_as_float(s[c][e]) : x * c1 * tanh_ratio(y * y);
+                  s[c][e] = __float_as_uint(fabsf(y) <= limit_y ? near : cap_log2(x, e1, cap2));
+                }
               }
-          } else if (CAP && large) {
-            const float one = 1.f / a.cap, far = cap_exponent(1.f, a.cap);
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[c][e] = __float_as_uint(cap_log2_large(__uint_as_float(s[c][e]) * a.scale, one, far, cap2));
+            }
           } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[c][e] = __float_as_uint(CAP ? cap_log2(__uint_as_float(s[c][e]), e1, cap2) : __uint_as_float(s[c][e]) * c1);
+              for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(__uint_as_float(s[c][e]) * c1);
           }
           if (BIAS) {
 #pragma unroll
@@ -748,43 +848,24 @@ attn_kernel(const __grid_constant__ AttnMaps maps, AttnArgs a, int64_t slots, in
               for (int e = 0; e < 32; ++e)
                 s[c][e] = __float_as_uint(fmaf(-slope, fabsf(static_cast<float>(i - j0 - (c * 32 + e))), __uint_as_float(s[c][e])));
           }
-          float top = row_max(s);
-          if (j0 + AT_ROWS > tile_lo) {
-            const float all = top;
+          // -inf where the row does not see
+          const bool crossed = j0 + AT_ROWS > tile_lo;
+          if (crossed) {
             const int left = limit - j0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (c * 32 + e >= left) s[c][e] = 0xff800000u;
-            top = row_max(s);
-            // A row that sees few keys of its first tile would move its reference again
-            // in the next: the hidden keys' scores say how far it is likely to go.  Up
-            // to 2^60 over the row's maximum costs no accuracy (its weight is then 2^-60).
-            top = top == -INFINITY ? top : fmaxf(top, fminf(all, top + 60.f));
           }
-          const bool grow = top > ref;  // ref = -inf: any finite maximum
-          if (__any_sync(0xffffffffu, grow)) {
-            const float now = grow ? top : ref;
-            const float f = grow ? ex2_approx(ref - now) : 1.f;
-            sum *= f;
-            ref = now;
-            if (j > 0) {  // the products of the tiles before are complete (S came after them)
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(O + c * 32, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st32(O + c * 32, o);
-              }
-            }
-          }
+          // A row that sees few keys of its first tile would move its reference again in the
+          // next: it starts that much higher, which costs no accuracy.
+          float top = row_max(s);
+          if (crossed && ref == -INFINITY) top += AT_HEAD;
+          move_ref(top > ref, top);  // ref = -inf: any finite maximum
           // nothing seen yet: every weight is 0
           const float sub = ref == -INFINITY ? 0.f : ref;
           const f2 off = pair(-sub, -sub);
-          parts[0] = parts[1] = 0ull;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t pk[16];

@@ -62,11 +62,12 @@ __device__ __forceinline__ float cap_log2(float x, float c1, float c2) {
 // beyond, where it is off by 4.5e-7 of the result at most.  per_cap = 1 / cap.
 constexpr float kTanhNear = 0.35f;
 __device__ constexpr float kTanhRel[4] = {0.99999994f, -0.333324254f, 0.132958218f, -0.0489584431f};
+__device__ __forceinline__ float tanh_ratio(float y2) {  // tanh(y) / y
+  return fmaf(y2, fmaf(y2, fmaf(y2, kTanhRel[3], kTanhRel[2]), kTanhRel[1]), kTanhRel[0]);
+}
 __device__ __forceinline__ float cap_log2_large(float x, float per_cap, float c1, float c2) {
-  const float y = x * per_cap, u = y * y;
-  const float near = x * kLog2e * fmaf(u, fmaf(u, fmaf(u, kTanhRel[3], kTanhRel[2]), kTanhRel[1]), kTanhRel[0]);
-  const float far = cap_log2(x, c1, c2);
-  return fabsf(y) <= kTanhNear ? near : far;
+  const float y = x * per_cap;
+  return fabsf(y) <= kTanhNear ? x * kLog2e * tanh_ratio(y * y) : cap_log2(x, c1, c2);
 }
 
 // c1 of cap_log2 for scores that `scale` is still to be multiplied with; finite for the

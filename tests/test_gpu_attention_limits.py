@@ -319,3 +319,73 @@ def test_a_cache_that_was_evicted_from(counts):
             ok()
             within(out, want, tol, "out")
             within(cache.weight, was + add, addtol + 4 * ref.F32 * (was + add), "weight")
+
+
+# ------------------------------------------------------------------ what a row does not see
+
+def prefill_inputs(seed, T, H, Hk):
+    g = gen(seed)
+    return [x.cuda() for x in (3 * randn(g, T, H, D), randn(g, T, Hk, D), randn(g, T, Hk, D))]
+
+
+# one CTA to a piece of work, several pieces to a CTA, several CTAs to a piece
+SHAPES = [([130, 70, 300], 2, 1), ([90, 257, 31, 500] * 12, 8, 2), ([1500, 1000], 1, 1)]
+
+
+@pytest.mark.parametrize("lengths,H,Hk", SHAPES, ids=["one", "more", "share"])
+@pytest.mark.parametrize("mask", ["causal", "full", "prefix"])
+@pytest.mark.parametrize("cap,slope", [(0.0, None), (20.0, None), (0.0, 0.1), (1000.0, 0.1)])
+def test_prefill_other_sequences_change_no_bit(lengths, H, Hk, mask, cap, slope):
+    q, k, v = prefill_inputs(3, sum(lengths), H, Hk)
+    cu = cu_of(lengths)
+    slopes = None if slope is None else torch.full((H,), slope).cuda()
+    prefix = ints(*[n // 3 for n in lengths]) if mask == "prefix" else None
+    call = lambda: kda.kda_attn_fwd(q, k, v, SCALE, mask=mask, cap=cap, slopes=slopes, prefix_lens=prefix,  # noqa: E731
+                                    cu_seqlens=cu.cuda())
+    want = call()
+    odd = torch.zeros(sum(lengths), dtype=torch.bool)
+    for s in range(1, len(lengths), 2):
+        odd[cu[s]:cu[s + 1]] = True
+    odd = odd.cuda()
+    kept = [x.clone() for x in (q, k, v)]
+    for size in (0.0, 1.0, 50.0):
+        for mine in (odd, ~odd):
+            for x, old, new in zip((q, k, v), kept, prefill_inputs(4, sum(lengths), H, Hk)):
+                x.copy_(torch.where(mine[:, None, None], new * size, old))
+            got = call()
+            assert torch.equal(got[~mine], want[~mine]), size
+    ok()
+
+
+@pytest.mark.parametrize("lengths,H,Hk", [([700], 2, 1), ([700, 500] * 15, 8, 2), ([2100], 1, 1)],
+                         ids=["one", "more", "share"])
+@pytest.mark.parametrize("cap,slope", [(0.0, None), (20.0, None), (0.0, 0.1), (1000.0, 0.1)])
+def test_prefill_later_tokens_change_no_bit(lengths, H, Hk, cap, slope):
+    q, k, v = prefill_inputs(5, sum(lengths), H, Hk)
+    cu = cu_of(lengths).cuda()
+    slopes = None if slope is None else torch.full((H,), slope).cuda()
+    call = lambda: kda.kda_attn_fwd(q, k, v, SCALE, cap=cap, slopes=slopes, cu_seqlens=cu)  # noqa: E731
+    want = call()
+    kept = [x.clone() for x in (q, k, v)]
+    last = sum(lengths) - lengths[-1]
+    for size in (0.0, 1.0, 50.0):
+        for at in (1, 37, 128, 300, 450):
+            for x, old, new in zip((q, k, v), kept, prefill_inputs(6, sum(lengths), H, Hk)):
+                x.copy_(old)
+                x[last + at:] = new[last + at:] * size
+            assert torch.equal(call()[:last + at], want[:last + at]), (size, at)
+    ok()
+
+
+@pytest.mark.parametrize("where", [slice(0, 700), slice(700, 1400), slice(1400, 2100), slice(0, 2100), slice(1000, 1001)])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_prefill_nan_keys_and_values_show(where, cap, which):
+    """A visible NaN key or value makes a row NaN, whether one CTA or several take its piece of work."""
+    n = 2100
+    for H in (1, 64):
+        q, k, v = prefill_inputs(7, n, H, 1)
+        (k if which == "k" else v)[where] = float("nan")
+        out = kda.kda_attn_fwd(q, k, v, SCALE, mask="full", cap=cap)
+        ok()
+        assert torch.isnan(out).all(), H
