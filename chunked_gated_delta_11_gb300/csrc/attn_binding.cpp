@@ -110,6 +110,15 @@ int32_t integer(PyObject* o, const char* name) {
   return static_cast<int32_t>(x);
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int x = PyObject_IsTrue(o);
+  if (x < 0) {
+    PyErr_Clear();
+    refuse(PyExc_TypeError, std::string(name) + " must be a truth value");
+  }
+  return x != 0;
+}
+
 int32_t size32(int64_t x, const char* name) {
   if (x > INT32_MAX) refuse(PyExc_ValueError, std::string(name) + " is out of range");
   return static_cast<int32_t>(x);
@@ -259,7 +268,7 @@ PyObject* cache_attn(PyObject* const* a) {
   o.cap = static_cast<float>(number(a[10], "cap"));
   o.slopes = static_cast<const float*>(optional(a[11], "slopes", at::kFloat, {H}, dev));
   o.positions = static_cast<const int32_t*>(optional(a[13], "positions", at::kInt, {T}, dev));
-  o.accumulate = PyObject_IsTrue(a[14]) == 1;
+  o.accumulate = truth(a[14], "accumulate");
   c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   void* op = nullptr;
   at::Tensor out = output(a[15], "out", at::kBFloat16, {T, H, D}, dev, &op);

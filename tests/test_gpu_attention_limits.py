@@ -389,3 +389,20 @@ def test_prefill_nan_keys_and_values_show(where, cap, which):
         out = kda.kda_attn_fwd(q, k, v, SCALE, mask="full", cap=cap)
         ok()
         assert torch.isnan(out).all(), H
+
+
+# ------------------------------------------------------------------ arguments
+
+def small_cache():
+    g = gen(15)
+    cache = kda.kda_cache_alloc(4, 1, 16)
+    table = torch.arange(4, dtype=torch.int32)[None].cuda()
+    kda.kda_cache_append(cache, randn(g, 40, 1, D).cuda(), randn(g, 40, 1, D).cuda(), table, ints(0))
+    return cache, table, randn(g, 1, 4, D).cuda()
+
+
+def test_accumulate_that_is_no_truth_value_is_refused():
+    cache, table, q = small_cache()
+    with pytest.raises(TypeError, match="accumulate"):
+        kda.kda_cache_attn(cache, q, table, ints(40), SCALE, accumulate=torch.zeros(2))
+    ok()
