@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cstring>
 #include <exception>
 #include <initializer_list>
@@ -293,7 +294,8 @@ PyObject* cache_evict(PyObject* const* a) {
   c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
   void* np = nullptr;
   at::Tensor lens = output(a[11], "new_lens", at::kInt, {rows}, dev, &np);
-  const Workspace ws(a[12], kda_cache_evict_workspace_size(&c, N, budget), dev);
+  const int64_t slots = width * c.page_size;  // a budget beyond the table needs no more than one of its slots
+  const Workspace ws(a[12], kda_cache_evict_workspace_size(&c, N, static_cast<int32_t>(std::min<int64_t>(budget, slots))), dev);
   return result(kda_cache_evict(&c, static_cast<const int32_t*>(tp), size32(width, "block_table"),
                                 static_cast<const int32_t*>(lp), static_cast<const int32_t*>(dp),
                                 size32(dst_width, "dst_table"), budget, recent, N, static_cast<int32_t*>(np), ws.at,

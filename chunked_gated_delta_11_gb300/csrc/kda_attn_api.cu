@@ -247,6 +247,10 @@ extern "C" kda_status kda_cache_evict(const kda_cache* cache, const int32_t* blo
   if (!new_lens || !aligned(new_lens, 4)) return KDA_ERR_INVALID_ARG;
   if (new_lens != lens && new_lens < lens + N && lens < new_lens + N) return KDA_ERR_INVALID_ARG;
   if (budget <= 0 || recent < 0 || recent > budget) return KDA_ERR_INVALID_ARG;
+  // a budget beyond the table keeps everything, as one of the table's slots does
+  const int32_t slots = table_width * cache->page_size;
+  budget = budget < slots ? budget : slots;
+  recent = recent < budget ? recent : budget;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t need = kda_cache_evict_workspace_size(cache, N, budget);
   if (workspace && (!aligned(workspace, 16) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;

@@ -525,7 +525,8 @@ kda_status kda_cache_attn(const kda_cache_attn_options* opts, const kda_cache* c
  * it differs).  new_lens int32 [N] receives min(lens[n], budget); it may be lens
  * itself, and must not overlap it otherwise.  A sequence within the budget is
  * copied whole.  The old pages are left as they are.
- * workspace: kda_cache_evict_workspace_size() bytes, or NULL, as above. */
+ * workspace: kda_cache_evict_workspace_size() bytes, of the budget or of the table's
+ * slots if those are fewer, or NULL, as above. */
 size_t kda_cache_evict_workspace_size(const kda_cache* cache, int32_t N, int32_t budget);
 kda_status kda_cache_evict(const kda_cache* cache, const int32_t* block_table, int32_t table_width,
                            const int32_t* lens, const int32_t* dst_table, int32_t dst_width,

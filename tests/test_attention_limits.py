@@ -34,3 +34,11 @@ def test_evict_refuses_new_lengths_that_overlap_the_old_ones(lib, shift):
 def test_evict_takes_lengths_in_place_or_apart(lib, shift):
     # the next check fails, of a workspace that is too small: nothing was launched
     assert evict(lib, new_lens=FAKE + shift, ws=FAKE, ws_bytes=16) == WORKSPACE
+
+
+def test_evict_needs_no_workspace_beyond_the_tables_slots(lib):
+    need = lib.kda_cache_evict_workspace_size(ctypes.byref(pool()), 4, 4 * 64)
+    call = lambda size, ws: evict(lib, budget=2 ** 31 - 1, recent=2 ** 31 - 1, ws=ws, ws_bytes=size)  # noqa: E731
+    assert call(need - 1, FAKE) == WORKSPACE
+    # enough bytes, but too small for another reason: the budget itself is refused
+    assert evict(lib, budget=2 ** 31 - 1, recent=-1, ws=FAKE, ws_bytes=need) == INVALID

@@ -406,3 +406,20 @@ def test_accumulate_that_is_no_truth_value_is_refused():
     with pytest.raises(TypeError, match="accumulate"):
         kda.kda_cache_attn(cache, q, table, ints(40), SCALE, accumulate=torch.zeros(2))
     ok()
+
+
+@pytest.mark.parametrize("recent", [0, 5, 2 ** 31 - 1])
+def test_evict_a_budget_beyond_the_table_copies_everything(recent):
+    cache, table, _ = small_cache()
+    cache.weight.copy_(torch.rand(cache.weight.shape))
+    many = kda.KvCache(*(torch.cat([t.view(torch.uint8)] * 2).view(t.dtype) for t in cache))
+    src = torch.full((64, 4), -1, dtype=torch.int32, device="cuda")
+    src[5] = table[0]
+    lens = torch.zeros(64, dtype=torch.int32, device="cuda")
+    lens[5] = 40
+    new = kda.kda_cache_evict(many, src, lens, torch.where(src >= 0, src + 4, -1), 2 ** 31 - 1, recent)
+    ok()
+    assert torch.equal(new, lens)
+    for t in many:
+        x = t.view(torch.uint8).reshape(8, 16, -1) if t.dim() > 2 else t
+        assert torch.equal(x[4:6], x[:2]) and torch.equal(x[6, :8] if t.dim() > 2 else x[6], x[2, :8] if t.dim() > 2 else x[2])
