@@ -303,6 +303,15 @@ PyObject* cache_evict(PyObject* const* a) {
                 lens);
 }
 
+// torch's own error for device memory that is not to be had, as its allocations in Python give.
+void out_of_memory(const char* text) {
+  PyObject* torch = PyImport_ImportModule("torch");
+  PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+  if (type) PyErr_SetString(type, text);
+  Py_XDECREF(type);
+  Py_XDECREF(torch);
+}
+
 // No C++ exception leaves an entry.
 template <PyObject* (*FN)(PyObject* const*), Py_ssize_t ARGS>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -314,6 +323,10 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return FN(args);
   } catch (const Refused& r) {
     PyErr_SetString(r.type, r.text.c_str());
+  } catch (const c10::OutOfMemoryError& e) {
+    out_of_memory(e.what_without_backtrace());
+  } catch (const c10::Error& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   } catch (...) {

@@ -423,3 +423,12 @@ def test_evict_a_budget_beyond_the_table_copies_everything(recent):
     for t in many:
         x = t.view(torch.uint8).reshape(8, 16, -1) if t.dim() > 2 else t
         assert torch.equal(x[4:6], x[:2]) and torch.equal(x[6, :8] if t.dim() > 2 else x[6], x[2, :8] if t.dim() > 2 else x[2])
+
+
+def test_running_out_of_memory_is_torchs_error():
+    cache, _, q = small_cache()
+    wide = torch.full((1, 1 << 26), -1, dtype=torch.int32, device="cuda")  # 2^30 slots: 550 GB for the splits of 64 heads
+    q = q.repeat(1, 1, 1).expand(256, 4, D).contiguous()
+    with pytest.raises(torch.OutOfMemoryError):
+        kda.kda_cache_attn(cache, q, wide, ints(40), SCALE, accumulate=True)
+    ok()
