@@ -11,12 +11,11 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
-import os
 from typing import NamedTuple
 
 import torch
 
-from .build import BINDING as _BINDING_PATH
+from . import build as _build
 
 MASKS = {"full": 0, "causal": 1, "prefix": 2}
 PAGE_SIZES = (16, 32, 64, 128)
@@ -76,11 +75,12 @@ def load_binding():
     if _binding is None:
         from . import load
         load()  # says so if libkda is not built
-        if not os.path.exists(_BINDING_PATH):
-            raise RuntimeError(f"the attention binding is not built ({_BINDING_PATH} missing); "
-                               "run chunked_gated_delta_11_gb300.build.build()")
-        loader = importlib.machinery.ExtensionFileLoader("attn_binding", _BINDING_PATH)
-        spec = importlib.util.spec_from_file_location("attn_binding", _BINDING_PATH, loader=loader)
+        was, now = _build.binding_built_for(), _build.binding_tag()
+        if was != now:
+            state = f"was built for {was}, this is {now}" if was else f"is not built ({_build.BINDING} missing)"
+            raise RuntimeError(f"the attention binding {state}; run chunked_gated_delta_11_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("attn_binding", _build.BINDING)
+        spec = importlib.util.spec_from_file_location("attn_binding", _build.BINDING, loader=loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         _binding = module

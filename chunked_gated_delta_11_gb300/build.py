@@ -4,14 +4,19 @@ Each .cu under csrc/ compiles to an object in parallel, then nvcc links them
 into ``chunked_gated_delta_11_gb300/_build/libkda.so``.  ``-Xptxas -v``
 register and shared-memory reports go to ``_build/ptxas.log``.  The Python
 extension of the softmax-attention calls, ``_build/attn_binding.so``, is compiled
-beside them with g++ against torch's headers and linked to libkda.
+beside them with g++ against torch's and Python's headers and linked to libkda.
+It belongs to the torch and the Python that it was built with (named in
+``_build/attn_binding.tag``).  Where it cannot be built the rest can: build()
+warns, and the attention calls raise.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +27,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkda.so")
 BINDING = os.path.join(BUILD, "attn_binding.so")
 BINDING_SRC = os.path.join(CSRC, "attn_binding.cpp")
+BINDING_TAG = os.path.join(BUILD, "attn_binding.tag")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
@@ -39,19 +45,37 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _lib_up_to_date() -> bool:
     deps = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                         if f.endswith((".cuh", ".h"))]
-    deps += [os.path.join(INCLUDE, "kda.h"), BINDING_SRC]
-    deps.append(os.path.abspath(__file__))
-    return deps
+    return _newer(LIB, [*deps, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)])
+
+
+def binding_tag() -> str:
+    """What the binding's binary interface depends on."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def binding_built_for() -> str:
+    """The binding_tag() that the binding was built with; "" if it is not there."""
+    if not (os.path.exists(BINDING) and os.path.exists(BINDING_TAG)):
+        return ""
+    with open(BINDING_TAG) as f:
+        return f.read()
+
+
+def _binding_up_to_date() -> bool:
+    return (binding_built_for() == binding_tag()
+            and _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)]))
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _lib_up_to_date() and _binding_up_to_date()
 
 
 def _compile_binding() -> str:
@@ -79,13 +103,34 @@ def _link_binding(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _remove_binding()
     os.replace(tmp, BINDING)
+    with open(BINDING_TAG, "w") as f:
+        f.write(binding_tag())
+
+
+def _remove_binding() -> None:
+    for old in (BINDING_TAG, BINDING):
+        if os.path.exists(old):
+            os.remove(old)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
     os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_compile_binding) if force or not _binding_up_to_date() else None
+        if force or not _lib_up_to_date():
+            _build_lib(verbose)
+        if binding is not None:
+            try:
+                _link_binding(binding.result())
+            except Exception as e:  # the KDA calls do without it
+                _remove_binding()
+                warnings.warn(f"the attention binding was not built: {e}")
+    return LIB
+
+
+def _build_lib(verbose: bool) -> None:
     cc = nvcc()
 
     def compile_one(src):
@@ -97,9 +142,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding)
         results = list(ex.map(compile_one, sources()))
-        binding_obj = binding.result()
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         for obj, log in results:
             f.write(f"== {os.path.basename(obj)}\n{log}\n")
@@ -109,10 +152,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
     if verbose:
         print(open(os.path.join(BUILD, "ptxas.log")).read())
-    return LIB
 
 
 if __name__ == "__main__":

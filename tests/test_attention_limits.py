@@ -42,3 +42,36 @@ def test_evict_needs_no_workspace_beyond_the_tables_slots(lib):
     assert call(need - 1, FAKE) == WORKSPACE
     # enough bytes, but too small for another reason: the budget itself is refused
     assert evict(lib, budget=2 ** 31 - 1, recent=-1, ws=FAKE, ws_bytes=need) == INVALID
+
+
+@pytest.fixture
+def own_binding(lib, tmp_path, monkeypatch):
+    """The binding's files in a folder of the test's, and nothing loaded."""
+    monkeypatch.setattr(kda.build, "BINDING", str(tmp_path / "attn_binding.so"))
+    monkeypatch.setattr(kda.build, "BINDING_TAG", str(tmp_path / "attn_binding.tag"), raising=False)
+    monkeypatch.setattr(attention, "_binding", None)
+    (tmp_path / "libkda.so").symlink_to(kda.build.LIB)
+    return tmp_path
+
+
+def test_the_rest_is_built_where_the_binding_cannot_be(own_binding, monkeypatch):
+    def no_headers():
+        raise RuntimeError("Python.h: no such file")
+
+    monkeypatch.setattr(kda.build, "_compile_binding", no_headers)
+    with pytest.warns(UserWarning, match="Python.h"):
+        assert kda.build.build() == kda.build.LIB
+    kda.load()
+    with pytest.raises(RuntimeError, match="not built"):
+        attention.load_binding()
+
+
+def test_a_binding_of_another_torch_is_not_loaded(own_binding, monkeypatch):
+    (own_binding / "attn_binding.so").write_bytes(b"")
+    (own_binding / "attn_binding.tag").write_text("torch 2.0.0, cpython-38")
+    assert not kda.build.up_to_date()
+    with pytest.raises(RuntimeError, match="built for torch 2.0.0"):
+        attention.load_binding()
+    kda.build.build()
+    assert kda.build.up_to_date()
+    assert hasattr(attention.load_binding(), "attn_fwd")
