@@ -973,11 +973,13 @@ CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   if (chunk < least) chunk = (least + step - 1) / step * step;
   p.chunk = static_cast<int>(chunk);
   p.splits = static_cast<int>((max_len + chunk - 1) / chunk);
-  // A CTA that finds no chunk at its place costs about a microsecond of one of the
-  // `slots`.  The list costs a launch and the overlap of one CTA's end with the next
-  // one's start (256 sequences with a table of their own width: 244 us against 216
-  // us), so it is for far more places than that.
-  p.ctas = p.splits > 1 && p.tiles * Hk * p.splits > 64 * slots ? static_cast<int>(slots) : 0;
+  // A CTA that finds no chunk at its place costs about half a microsecond of one of the
+  // `slots`; the list costs a launch and the overlap of one CTA's end with the next one's
+  // start.  They meet at about 30 rounds of places (8 KV heads of 4 rows, slots in the
+  // sequences and in the table, microseconds without and with the list: 256 x 1024 in 4096, 9
+  // rounds, 95 and 103; 64 x 2000 in 32768, 18 rounds, 59 and 63; 256 x 1024 in 16384, 36
+  // rounds, 108 and 104; in 131072, 72 rounds, 128 and 104; 256 x 100 in 16384, 46 and 33).
+  p.ctas = p.splits > 1 && p.tiles * Hk * p.splits > 32 * slots ? static_cast<int>(slots) : 0;
   // Weight sums: a warp has 128 slots and all rows, unless that leaves SMs idle and there
   // are rows to share (84 short sequences with 72 rows each: 47 us, shared 32 us; one of
   // 40,000 slots with 12 rows: 41 us, shared 48 us).
