@@ -16,6 +16,9 @@
 namespace kda {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// SMs of a GB300.  What a call of the cache is cut into follows from it, and a workspace's
+// size from that, so it is not asked of the device.
+constexpr int kSMs = 152;
 
 // Attention over packed rows.
 struct AttnArgs {
@@ -168,7 +171,6 @@ struct CacheAttnArgs {
   int accumulate;
 };
 size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len, bool accumulate);
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, int* err,
-                              cudaStream_t stream);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int* err, cudaStream_t stream);
 
 }  // namespace kda

@@ -224,7 +224,7 @@ extern "C" kda_status kda_cache_attn(const kda_cache_attn_options* opts, const k
   a.scale = scale;
   a.cap = opts->cap;
   a.accumulate = opts->accumulate != 0;
-  return launch_cache_attn(a, ws.get(), sms, err, st) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+  return launch_cache_attn(a, ws.get(), err, st) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 extern "C" size_t kda_cache_evict_workspace_size(const kda_cache* cache, int32_t N,

@@ -961,7 +961,7 @@ CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   // One sequence: the chunks fill the GPU once, evenly.  More of them are ragged:
   // chunks of at most 2048 slots (or a sixteenth of the longest) keep the last ones
   // short.
-  const int64_t slots = ca_ctas(p.nt) * 152;
+  const int64_t slots = ca_ctas(p.nt) * kSMs;
   const int64_t tiles = (rows + rt - 1) / rt;
   const int64_t units = (tiles > N ? tiles : N) * Hk;
   int64_t chunk = (max_len * units + slots - 1) / slots;
@@ -984,7 +984,7 @@ CachePlan make_plan(int64_t T, int H, int Hk, int N, bool cu, int64_t max_len) {
   // are rows to share (84 short sequences with 72 rows each: 47 us, shared 32 us; one of
   // 40,000 slots with 12 rows: 41 us, shared 48 us).
   const int64_t pairs = static_cast<int64_t>(N) * Hk;
-  p.share = p.nt > 1 && pairs * ((max_len + ca_wchunk(false) - 1) / ca_wchunk(false)) < 2 * 152;
+  p.share = p.nt > 1 && pairs * ((max_len + ca_wchunk(false) - 1) / ca_wchunk(false)) < 2 * kSMs;
   const int64_t ranges = (max_len + ca_wchunk(p.share) - 1) / ca_wchunk(p.share);
   const int64_t fill = (32768 + pairs - 1) / pairs;
   p.weight_per = static_cast<int>(ranges < fill ? ranges : fill);
@@ -1038,9 +1038,7 @@ size_t cache_attn_workspace(int64_t T, int H, int Hk, int N, bool cu, int64_t ma
   return scratch_of(make_plan(T, H, Hk, N, cu, max_len), Hk, accumulate).total;
 }
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int sm_count, int* err,
-                              cudaStream_t stream) {
-  (void)sm_count;
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, void* ws, int* err, cudaStream_t stream) {
   const int64_t max_len = static_cast<int64_t>(a.c.width) << a.c.lg;
   const CachePlan p = make_plan(a.T, a.H, a.c.Hk, a.c.N, a.cu != nullptr, max_len);
   if (p.tiles * a.c.Hk > 0x7fffffffLL / p.splits) return cudaErrorInvalidValue;
