@@ -22,6 +22,8 @@
 // Masks.  Every row sees a prefix of its sequence's keys: all of them, up to
 // itself, or up to max(itself, prefix_len).  Tiles past a query tile's last
 // visible key are skipped, and only tiles that cross a row's limit select.
+// Nothing that a row does not see shows in its bits: its reference comes from visible
+// scores, and what a warp decides for its 32 rows together changes no arithmetic.
 // Rows of V past the sequence's end (another sequence's, whatever they hold)
 // are overwritten with zeros in shared memory before the product.
 //
@@ -29,7 +31,7 @@
 // order of the grid, so long rows first), and its warps go on from one piece to the
 // next by themselves: the next keys and queries are under way during the last
 // products, and no barrier or tensor memory is set up again.  Causal documents of
-// 256 rows: 71 us as a CTA each, 52 us so (8192 rows, 32 heads); of 1024: 96, 84 us.
+// 256 rows: 71 us as a CTA each, 51 us so (8192 rows, 32 heads); of 1024: 96, 88 us.
 //
 // Little work.  With fewer pieces than half the SMs a cluster of CTAs shares each piece's
 // key tiles; the parts are joined through distributed shared memory, every CTA joining
@@ -40,13 +42,14 @@
 // its channels at a time through 4 KB of its own and stores whole lines (3000).
 //
 // Measured (GB300, replayed from a graph, warm): 8192 tokens causal with bias, 64
-// query and 8 KV heads, 700 us = 1.57 PFLOP/s of visible products; the two query
+// query and 8 KV heads, 712 us = 1.54 PFLOP/s of visible products; the two query
 // tiles' chains set it (softmax 1100-1300 cycles a tile, its two products 1024, the
 // hand-overs between them about 600, against 2048 cycles of products for both), and
 // the products' operands take most of what shared memory can deliver.  8 x 1024
-// capped, 32 heads: 100 us; a piece's first tile, with its limits and no reference
-// yet, takes 4800 cycles where a later one takes 1700, its output 3000.  One sequence
-// of 64 tokens: 6.1 us, two launches' worth.
+// capped, 32 heads: 98 us; a piece's first tile, with its limits and no reference
+// yet, took 4800 cycles where a later one takes 1700 (with a second maximum, over hidden
+// scores, that it no longer has), its output 3000.  One sequence of 64 tokens: 6.0 us,
+// two launches' worth.
 #include <type_traits>
 
 #include "kda_attn.cuh"
@@ -217,11 +220,11 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 // tanh(y) = y (c0 + c1 y^2 + c2 y^4 + c3 y^6) for |y| <= 0.7, fitted for the least
-// maximum error: 2.1e-6, which moves a capped score by 1.5e-4 (in units of log2) at
-// a cap of 50 and so a weight by a twentieth of its bf16 rounding.  Five
+// maximum error: 2.1e-6, which moves a capped score by 3.9e-4 (in units of log2) at
+// a cap of 128 and so a weight by a fourteenth of its bf16 rounding.  Five
 // multiply-adds a score, where an exponential and a reciprocal take 12 cycles of a
 // special-function unit that a tile's weights keep busy already.  For caps up to
-// kCapSmall (a seventh of that rounding); larger ones take kTanhRel, up to kTanhNear.
+// kCapSmall; larger ones take kTanhRel, up to kTanhNear.
 constexpr float kTanhMost = 0.7f;
 __device__ constexpr float kTanh[4] = {0.999972696f, -0.332557463f, 0.127291387f, -0.0357217971f};
 

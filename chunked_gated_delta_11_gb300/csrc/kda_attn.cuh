@@ -53,7 +53,7 @@ struct CacheArgs {
 // tanh(y) = 1 - 2 / (1 + e^(2 y)).  x is scale * q . k; c1 = 2 log2 e / cap, c2 = cap log2 e.
 // The absolute error is a few 2^-24 of cap log2 e (what an exponent can take),
 // which tanh.approx (2^-11 of the result) does not reach.  For caps up to kCapSmall:
-// there that is 2.2e-5 of a weight at most, a thirtieth of its fp16 rounding.
+// there that moves a weight by 1.5e-5 at most, a thirtieth of its fp16 rounding.
 constexpr float kCapSmall = 128.0f;
 __device__ __forceinline__ float cap_log2(float x, float c1, float c2) {
   return fmaf(-2.0f * c2, rcp_approx(1.0f + ex2_approx(x * c1)), c2);

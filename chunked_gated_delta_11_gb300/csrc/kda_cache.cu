@@ -19,7 +19,7 @@
 // evict reads one weight per slot and moves 2 x 128 codes per kept slot.
 // Measured (GB300, replayed from a graph): append of 32 ragged prompts (62,700
 // tokens, 8 heads) 67 us = 5.8 TB/s, of 256 single tokens 3.8 us; eviction of 64
-// ragged sequences to 4096 slots 36 us for the selection and 168 us for the packing,
+// ragged sequences to 4096 slots 37 us for the selection and 171 us for the packing,
 // 5.6 TB/s of rows of 128 bytes that lie anywhere; of one sequence 11 us.
 #include "kda_attn.cuh"
 
@@ -523,7 +523,8 @@ select_kernel(CacheArgs c, int budget, int recent, int cluster, int32_t* __restr
 // the page's rows, 8 lanes a row, 4 groups of 4 rows under way at a time.  What
 // bounds it is how many bytes are in flight, so the chain of lookups before the
 // rows (length, kept row) is short and shared by a whole page.  SPLIT = 4: the 4
-// warps share a page, for calls with fewer pages than warps that fit the GPU.
+// warps share a page, for calls with fewer pages than warps that fit the GPU.  64 registers
+// a thread for 32 warps per SM: pages of 64 and 128 spill some (316 and 672 bytes loaded).
 template <int PAGE, int SPLIT>
 __global__ void __launch_bounds__(128, 8)
 pack_kernel(CacheArgs c, const int32_t* __restrict__ dst, int dst_width, int budget,

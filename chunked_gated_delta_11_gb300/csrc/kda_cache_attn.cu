@@ -27,9 +27,9 @@
 //   where their weights do not) 2^(x - m) itself.
 //
 // Measured (GB300, replayed from a graph): one sequence of 131072 slots, 8 KV heads
-// of 4 rows, capped and biased, 56 us = 4.8 TB/s (the cap's instructions and one
-// round of chunks); 256 sequences (498,000 slots) with weights 185 us = 5.5 TB/s and 32 us for the
-// join; one of 4096 slots 7.8 us, three launches' worth.  32 sequences x 4 tokens (32
+// of 4 rows, capped and biased, 57 us = 4.8 TB/s (the cap's instructions and one
+// round of chunks); 256 sequences (498,000 slots) with weights 190 us = 5.4 TB/s and 33 us for the
+// join; one of 4096 slots 8.6 us, two launches' worth.  32 sequences x 4 tokens (32
 // rows per KV head) 132 us = 2.2 TB/s: 8 warps per SM with 255 registers each, which
 // neither the copies nor the products keep busy.
 #include "kda_attn.cuh"
