@@ -18,10 +18,12 @@ import threading
 import torch
 
 from . import attention as _attention
-from .attention import (KvCache, kda_attn_fwd, kda_cache_alloc, kda_cache_append, kda_cache_attn,
-                        kda_cache_evict)
+from . import recurrent as _recurrent
+from .attention import (KvCache, Reservation, kda_attn_fwd, kda_cache_alloc, kda_cache_append,
+                        kda_cache_attn, kda_cache_evict, kda_cache_release, kda_cache_reserve)
 from .build import LIB as _LIB_PATH
 from .build import build as _build
+from .recurrent import kda_conv_fwd, kda_ssm_fwd, kda_ssm_step
 
 __all__ = [
     "KdaError", "load", "kda_workspace_size", "kda_fwd", "kda_chunk_prep",
@@ -31,7 +33,8 @@ __all__ = [
     "kda_fwd_segmented", "kda_segments_auto", "kda_segmented_workspace_size",
     "kda_validate_cu_seqlens", "REC_BYTES", "CHUNK", "HEAD_DIM",
     "KvCache", "kda_attn_fwd", "kda_cache_alloc", "kda_cache_append", "kda_cache_attn",
-    "kda_cache_evict",
+    "kda_cache_evict", "Reservation", "kda_cache_reserve", "kda_cache_release", "kda_conv_fwd",
+    "kda_ssm_fwd", "kda_ssm_step", "kda_ssm_workspace_size",
 ]
 
 CHUNK = 16
@@ -128,6 +131,7 @@ def load(build_if_missing: bool = False):
         lib.kda_selftest_tcgen05.argtypes = [P, P, P, P]
         lib.kda_selftest_tcgen05.restype = ctypes.c_int
         _attention.declare(lib)
+        _recurrent.declare(lib)
         _lib = lib
         return lib
 
@@ -306,6 +310,11 @@ def kda_forward(q, k, v, g_raw, beta_raw, scale, lower_bound, initial_state=None
                             _ptr(final_state), _ptr(workspace), ws_bytes, _stream(stream))
     _check(st, "kda_forward")
     return out, final_state
+
+
+def kda_ssm_workspace_size(T_total: int, H: int, G: int, N: int, P: int, S: int) -> int:
+    """Bytes of workspace that kda_ssm_fwd needs for these sizes on the current device."""
+    return int(load().kda_ssm_workspace_size(int(T_total), int(H), int(G), int(N), int(P), int(S)))
 
 
 def kda_segments_auto(T_total: int, H: int, N: int) -> int:

@@ -1,17 +1,19 @@
 """Softmax attention beside the KDA layers: the binding of kda_attn_fwd,
-kda_cache_append, kda_cache_attn and kda_cache_evict (include/kda.h).
+kda_cache_append, kda_cache_attn, kda_cache_evict, kda_cache_reserve and
+kda_cache_release (include/kda.h).
 
 A hybrid model puts an attention layer after every few KDA layers.  It works on
 the same packed rows ([T_total, H, 128] bf16, cu_seqlens), keeps its keys and
 values in a paged cache of e4m3 codes with one scale per (page, KV head), and
-can drop the cached tokens that got the least attention.
+can drop the cached tokens that got the least attention.  The pages of the cache
+are taken from a pool, and given back, on the device.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.machinery
 import importlib.util
-from typing import NamedTuple
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -29,6 +31,14 @@ class KvCache(NamedTuple):
     v_scale: torch.Tensor  # float32 [pages, Hk]
     pos: torch.Tensor      # int32 [pages, Hk, page_size]
     weight: torch.Tensor   # float32 [pages, Hk, page_size]
+
+
+class Reservation(NamedTuple):
+    """What kda_cache_reserve gives."""
+    lens: torch.Tensor             # int32 [N], with the new rows (the old length where refused)
+    cu_seqlens: torch.Tensor       # int32 [N + 1], packing of the new rows
+    slots: Optional[torch.Tensor]  # int64 [rows], cache slot of every new row, -1 without one
+    free_count: torch.Tensor       # int32 [1], pages left
 
 
 class _AttnOptions(ctypes.Structure):
@@ -64,6 +74,10 @@ def declare(lib):
     lib.kda_cache_evict_workspace_size.restype = sz
     lib.kda_cache_evict.argtypes = [P, P, i32, P, P, i32, i32, i32, i32, P, P, sz, P]
     lib.kda_cache_evict.restype = ctypes.c_int
+    lib.kda_cache_reserve.argtypes = [P, i32, P, P, P, P, i32, i32, i64, i32, P, P, P, P, P]
+    lib.kda_cache_reserve.restype = ctypes.c_int
+    lib.kda_cache_release.argtypes = [P, i32, P, P, P, P, i32, i32, i32, P, P]
+    lib.kda_cache_release.restype = ctypes.c_int
 
 
 _binding = None
@@ -161,3 +175,28 @@ def kda_cache_evict(cache, block_table, lens, dst_table, budget, recent, new_len
     b = _binding or load_binding()
     return _run(stream, "kda_cache_evict", b.cache_evict, *cache, block_table, lens, dst_table,
                 budget, recent, new_lens, workspace)
+
+
+def kda_cache_reserve(block_table, lens, new_rows, free_pages, free_count, page_size, rows=None,
+                      new_lens=None, cu_seqlens=None, slots=None, new_free_count=None, stream=None):
+    """Pages for new_rows int32 [N] more slots of every sequence: taken from the end of
+    the free list (free_pages int32 [pages], a place for every page of the pool; the first
+    free_count int32 [1] are free) and entered in block_table int32 [N, width], in the order
+    of the sequences.  A sequence that the list or its row of the table has no room for
+    gets none.  rows: the new rows of the call's packed tensors, for their slots (None:
+    no slots).  new_lens may be lens, new_free_count free_count; without them the results
+    are new tensors.  Returns a Reservation."""
+    b = _binding or load_binding()
+    return Reservation(*_run(stream, "kda_cache_reserve", b.cache_reserve, block_table, lens, new_rows,
+                             free_pages, free_count, page_size, rows, new_lens, cu_seqlens, slots,
+                             new_free_count))
+
+
+def kda_cache_release(block_table, lens, free_pages, free_count, page_size, keep=None,
+                      new_free_count=None, stream=None):
+    """Gives the pages behind each sequence's first keep int32 [N] slots (None: all of its
+    lens[n] slots' pages) back to the free list, in place; the table stays as it is.
+    Returns the pages free then, int32 [1] (new_free_count, which may be free_count)."""
+    b = _binding or load_binding()
+    return _run(stream, "kda_cache_release", b.cache_release, block_table, lens, free_pages, free_count,
+                page_size, keep, new_free_count)

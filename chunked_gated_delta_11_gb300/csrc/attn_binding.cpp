@@ -1,10 +1,11 @@
-// attn_binding.cpp -- the softmax-attention entry points as a Python extension.
+// attn_binding.cpp -- the softmax-attention, short-convolution and state-space entry
+// points as a Python extension.
 //
 // A serving step makes several of these calls for each token, and checking a
 // dozen tensors and allocating the outputs in Python takes longer than the small
-// calls' kernels do.  Here the tensors are looked at in place.  attention.py
-// documents the functions and names their arguments; everything it passes is
-// checked here before libkda is called.  A function returns what the Python
+// calls' kernels do.  Here the tensors are looked at in place.  attention.py and
+// recurrent.py document the functions and name their arguments; everything they pass
+// is checked here before libkda is called.  A function returns what the Python
 // function returns, or libkda's status as an int if that is not KDA_OK.
 #include <Python.h>
 
@@ -201,6 +202,68 @@ PyObject* result(kda_status st, const at::Tensor& t) {
   return st == KDA_OK ? THPVariable_Wrap(t) : PyLong_FromLong(st);
 }
 
+// A tuple of tensors (None for one that is not there).
+PyObject* result(kda_status st, std::initializer_list<at::Tensor> all) {
+  if (st != KDA_OK) return PyLong_FromLong(st);
+  PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(all.size()));
+  if (!r) return nullptr;
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : all) {
+    PyObject* o = t.defined() ? THPVariable_Wrap(t) : (Py_INCREF(Py_None), Py_None);
+    if (!o) {
+      Py_DECREF(r);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(r, i++, o);
+  }
+  return r;
+}
+
+// Checks rows that may be cut out of wider ones (dimensions but the first contiguous, rows
+// a multiple of `unit` elements apart); returns their address and the elements between
+// two of them (0: one after the other).
+void* strided(PyObject* o, const char* name, std::initializer_list<int64_t> shape, int64_t unit, int64_t device,
+              int64_t& stride) {
+  const at::Tensor& t = tensor(o, name);
+  stride = 0;
+  if (t.dim() < 2 || t.scalar_type() != at::kBFloat16 || !t.is_cuda() || t.get_device() != device ||
+      !t.sizes().equals(c10::IntArrayRef(shape.begin(), shape.size())) || t.is_contiguous())
+    return address(t, name, at::kBFloat16, shape, device);
+  int64_t row = 1;
+  for (int64_t d = t.dim() - 1; d > 0; --d) {
+    if (t.size(d) != 1 && t.stride(d) != row)
+      refuse(PyExc_ValueError, std::string(name) + " must be contiguous but for its first dimension");
+    row *= t.size(d);
+  }
+  if (t.stride(0) < row || t.stride(0) % unit != 0)
+    refuse(PyExc_ValueError, std::string(name) + " has rows " + std::to_string(t.stride(0)) + " elements apart: at least " +
+                                 std::to_string(row) + " and a multiple of " + std::to_string(unit) + " are needed");
+  stride = t.stride(0);
+  return t.data_ptr();
+}
+
+// The initial state (or None) and the final one: the caller's, a new one of the same type (fp32
+// without any), or none.
+struct States {
+  const void* init = nullptr;
+  void* fin = nullptr;
+  at::Tensor keep;
+  at::ScalarType type = at::kFloat;
+  // `only`: the one type that states have, or Undefined for fp32 or bf16
+  States(PyObject* i, PyObject* f, PyObject* want, at::ScalarType only, std::initializer_list<int64_t> shape, int64_t device) {
+    if (only != at::ScalarType::Undefined) {
+      type = only;
+    } else if (i != Py_None || f != Py_None) {
+      const char* name = i != Py_None ? "initial_state" : "final_state";
+      type = tensor(i != Py_None ? i : f, name).scalar_type();
+      if (type != at::kFloat && type != at::kBFloat16)
+        refuse(PyExc_TypeError, std::string(name) + " must be torch.float32 or torch.bfloat16, got " + name_of(type));
+    }
+    init = optional(i, "initial_state", type, shape, device);
+    if (f != Py_None || truth(want, "output_final_state")) keep = output(f, "final_state", type, shape, device, &fin);
+  }
+};
+
 // q, k, v, scale, mask, cap, slopes, prefix_lens, cu_seqlens, N, out
 PyObject* attn_fwd(PyObject* const* a) {
   const at::Tensor& q = sized(a[0], "q", 3, "[T_total, heads, 128]");
@@ -303,6 +366,108 @@ PyObject* cache_evict(PyObject* const* a) {
                 lens);
 }
 
+// x, weight, bias, initial_state, cu_seqlens, N, silu, out, final_state, output_final_state
+PyObject* conv_fwd(PyObject* const* a) {
+  const at::Tensor& x = sized(a[0], "x", 2, "[T_total, C]");
+  const at::Tensor& w = sized(a[1], "weight", 2, "[C, W]");
+  const int64_t T = x.size(0), C = x.size(1), W = w.size(1), dev = x.get_device();
+  kda_conv_options o{};
+  void* xp = strided(a[0], "x", {T, C}, 8, dev, o.x_stride);
+  void* wp = address(w, "weight", at::kBFloat16, {C, W}, dev);
+  void* bp = optional(a[2], "bias", at::kBFloat16, {C}, dev);
+  int32_t N = 0;
+  const int32_t* cu = sequences(a[4], a[5], dev, N);
+  o.silu = truth(a[6], "silu");
+  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  void* op = nullptr;
+  at::Tensor out = output(a[7], "out", at::kBFloat16, {T, C}, dev, &op);
+  const States s(a[3], a[8], a[9], at::kBFloat16, {N, W - 1, C}, dev);
+  return result(kda_conv_fwd(&o, xp, wp, bp, s.init, cu, T, size32(C, "x"), size32(W, "weight"), N, op, s.fin,
+                             stream_of(dev)),
+                {out, s.keep});
+}
+
+// x, dt, A, B, C, skip, dt_bias, initial_state, cu_seqlens, N, out, final_state, output_final_state, workspace
+template <bool STEP>
+PyObject* ssm(PyObject* const* a) {
+  const at::Tensor& x = sized(a[0], "x", 3, "[T_total, heads, channels]");
+  const at::Tensor& b = sized(a[3], "B", 3, "[T_total, groups, state]");
+  const int64_t T = x.size(0), H = x.size(1), P = x.size(2), G = b.size(1), S = b.size(2), dev = x.get_device();
+  kda_ssm_options o{};
+  void* xp = strided(a[0], "x", {T, H, P}, 8, dev, o.x_stride);
+  void* dp = strided(a[1], "dt", {T, H}, 1, dev, o.dt_stride);
+  const float* ap = static_cast<const float*>(address(a[2], "A", at::kFloat, {H}, dev));
+  void* bp = strided(a[3], "B", {T, G, S}, 8, dev, o.b_stride);
+  void* cp = strided(a[4], "C", {T, G, S}, 8, dev, o.c_stride);
+  o.skip = static_cast<const float*>(optional(a[5], "skip", at::kFloat, {H}, dev));
+  o.dt_bias = static_cast<const float*>(optional(a[6], "dt_bias", at::kFloat, {H}, dev));
+  int32_t N = 0;
+  const int32_t* cu = sequences(a[8], a[9], dev, N);
+  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  void* op = nullptr;
+  at::Tensor out = output(a[10], "out", at::kBFloat16, {T, H, P}, dev, &op);
+  const States s(a[7], a[11], a[12], at::ScalarType::Undefined, {N, H, P, S}, dev);
+  o.state_dtype = s.type == at::kBFloat16 ? KDA_STATE_BF16 : KDA_STATE_F32;
+  const int32_t h = size32(H, "x"), g = size32(G, "B"), p = size32(P, "x"), n = size32(S, "B");
+  if constexpr (STEP)
+    return result(kda_ssm_step(&o, xp, dp, ap, bp, cp, s.init, cu, T, h, g, N, p, n, op, s.fin, stream_of(dev)),
+                  {out, s.keep});
+  const Workspace ws(a[13], kda_ssm_workspace_size(T, h, g, N, p, n), dev);
+  return result(kda_ssm_fwd(&o, xp, dp, ap, bp, cp, s.init, cu, T, h, g, N, p, n, op, s.fin, ws.at, ws.bytes,
+                            stream_of(dev)),
+                {out, s.keep});
+}
+
+// block_table, lens, new_rows, free_pages, free_count, page_size, rows, new_lens, cu_seqlens, slots, new_free_count
+PyObject* cache_reserve(PyObject* const* a) {
+  const at::Tensor& table = sized(a[0], "block_table", 2, "[N, width]");
+  const at::Tensor& list = sized(a[3], "free_pages", 1, "[pages]");
+  const int64_t N = table.size(0), width = table.size(1), pages = list.size(0), dev = table.get_device();
+  void* tp = address(table, "block_table", at::kInt, {N, width}, dev);
+  void* lp = address(a[1], "lens", at::kInt, {N}, dev);
+  void* np = address(a[2], "new_rows", at::kInt, {N}, dev);
+  void* fp = address(list, "free_pages", at::kInt, {pages}, dev);
+  void* cp = address(a[4], "free_count", at::kInt, {1}, dev);
+  const int32_t page = integer(a[5], "page_size");
+  const bool known = a[6] != Py_None;
+  const int64_t T = known ? integer(a[6], "rows") : INT32_MAX;
+  if (T < 0) refuse(PyExc_ValueError, "rows is out of range");
+  if (!known && a[9] != Py_None) refuse(PyExc_ValueError, "slots needs rows");
+  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  void *lens = nullptr, *cu = nullptr, *slots = nullptr, *left = nullptr;
+  const at::Tensor new_lens = output(a[7], "new_lens", at::kInt, {N}, dev, &lens);
+  const at::Tensor sums = output(a[8], "cu_seqlens", at::kInt, {N + 1}, dev, &cu);
+  const at::Tensor places = known ? output(a[9], "slots", at::kLong, {T}, dev, &slots) : at::Tensor();
+  const at::Tensor count = output(a[10], "new_free_count", at::kInt, {1}, dev, &left);
+  return result(kda_cache_reserve(static_cast<int32_t*>(tp), size32(width, "block_table"), static_cast<const int32_t*>(lp),
+                                  static_cast<const int32_t*>(np), static_cast<const int32_t*>(fp),
+                                  static_cast<const int32_t*>(cp), size32(pages, "free_pages"), page, T,
+                                  size32(N, "block_table"), static_cast<int32_t*>(lens), static_cast<int32_t*>(cu),
+                                  static_cast<int64_t*>(slots), static_cast<int32_t*>(left), stream_of(dev)),
+                {new_lens, sums, places, count});
+}
+
+// block_table, lens, free_pages, free_count, page_size, keep, new_free_count
+PyObject* cache_release(PyObject* const* a) {
+  const at::Tensor& table = sized(a[0], "block_table", 2, "[N, width]");
+  const at::Tensor& list = sized(a[2], "free_pages", 1, "[pages]");
+  const int64_t N = table.size(0), width = table.size(1), pages = list.size(0), dev = table.get_device();
+  void* tp = address(table, "block_table", at::kInt, {N, width}, dev);
+  void* lp = address(a[1], "lens", at::kInt, {N}, dev);
+  void* fp = address(list, "free_pages", at::kInt, {pages}, dev);
+  void* cp = address(a[3], "free_count", at::kInt, {1}, dev);
+  const int32_t page = integer(a[4], "page_size");
+  void* kp = optional(a[5], "keep", at::kInt, {N}, dev);
+  c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(dev));
+  void* left = nullptr;
+  const at::Tensor count = output(a[6], "new_free_count", at::kInt, {1}, dev, &left);
+  return result(kda_cache_release(static_cast<const int32_t*>(tp), size32(width, "block_table"),
+                                  static_cast<const int32_t*>(lp), static_cast<const int32_t*>(kp),
+                                  static_cast<int32_t*>(fp), static_cast<const int32_t*>(cp), size32(pages, "free_pages"),
+                                  page, size32(N, "block_table"), static_cast<int32_t*>(left), stream_of(dev)),
+                count);
+}
+
 // torch's own error for device memory that is not to be had, as its allocations in Python give.
 void out_of_memory(const char* text) {
   PyObject* torch = PyImport_ImportModule("torch");
@@ -342,6 +507,9 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<attn_fwd, 11>("attn_fwd"), method<cache_append, 12>("cache_append"),
                          method<cache_attn, 17>("cache_attn"), method<cache_evict, 13>("cache_evict"),
+                         method<conv_fwd, 10>("conv_fwd"), method<ssm<false>, 14>("ssm_fwd"),
+                         method<ssm<true>, 14>("ssm_step"), method<cache_reserve, 11>("cache_reserve"),
+                         method<cache_release, 7>("cache_release"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "attn_binding", "Softmax attention of libkda on torch tensors.", -1,
                           methods, nullptr, nullptr, nullptr, nullptr};

@@ -533,6 +533,101 @@ kda_status kda_cache_evict(const kda_cache* cache, const int32_t* block_table, i
                            int32_t budget, int32_t recent, int32_t N, int32_t* new_lens,
                            void* workspace, size_t workspace_bytes, void* stream);
 
+/* Pages of sequences, taken from a pool and given back on the device.  The free list
+ * free_pages int32 [pages] has a place for every page of the pool; its first *free_count
+ * entries are the pages in no table.  page_size is the cache's (16, 32, 64 or 128), N at most
+ * 16384.  All values live on the device: a count of free pages outside [0, pages], a length
+ * outside [0, table_width * page_size], a negative number of new rows, more of them than
+ * T_total, a page id outside [0, pages), or more released pages than the list has room
+ * for, latch KDA_ERR_INVALID_ARG, and nothing is read or written out of range.
+ *
+ * kda_cache_reserve: room for new_rows[n] more slots of every sequence, before the calls that
+ * write and read them.  In the order of the sequences, each takes the pages that its new
+ * slots need beyond those its lens[n] slots have, from the end of the free list (the last
+ * entry first), into its next entries of block_table.  A sequence whose pages, with those of
+ * the sequences before it, are more than the list has, or whose slots are more than its
+ * row of the table holds, gets none and keeps its length; one that needs no page is never
+ * refused for want of pages.  Writes
+ *   new_lens int32 [N]        lens[n] + new_rows[n], or lens[n] where refused; may be lens
+ *   cu_seqlens int32 [N + 1]  sums of new_rows, refused or not: the packing of the new rows
+ *   slots int64 [T_total]     page * page_size + place of every new row, -1 for the rows of
+ *                             refused sequences and behind the last one; NULL: not wanted
+ *   new_free_count int32 [1]  pages left; may be free_count
+ * T_total: the new rows that the call's packed tensors have (2^31 - 1 with slots == NULL
+ * where that is not known); a sequence with rows beyond it is refused, and cu_seqlens stays
+ * within it.  Rows of a sequence that was refused must not be appended (its table has no
+ * pages for them).
+ *
+ * kda_cache_release: the pages behind each sequence's first keep[n] slots (keep == NULL: all
+ * pages) go to the end of the free list, in the order of the tables.  A page belongs to the
+ * sequence if its lens[n] slots need it; block_table and lens are left as they are.
+ * new_free_count as above.  An id outside the pool becomes -1 in the list. */
+kda_status kda_cache_reserve(int32_t* block_table, int32_t table_width, const int32_t* lens,
+                             const int32_t* new_rows, const int32_t* free_pages,
+                             const int32_t* free_count, int32_t pages, int32_t page_size,
+                             int64_t T_total, int32_t N, int32_t* new_lens, int32_t* cu_seqlens,
+                             int64_t* slots, int32_t* new_free_count, void* stream);
+kda_status kda_cache_release(const int32_t* block_table, int32_t table_width, const int32_t* lens,
+                             const int32_t* keep, int32_t* free_pages, const int32_t* free_count,
+                             int32_t pages, int32_t page_size, int32_t N, int32_t* new_free_count,
+                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * Other recurrent layers of a hybrid model: the short causal convolution that
+ * stands before a recurrence (KDA's q, k and v, a state-space layer's x, B and C),
+ * and the selective state-space recurrence.  No counterpart on the pages.  Rows
+ * are packed as in kda_fwd (cu_seqlens, or N equal sequences); inputs may be cut
+ * out of wider rows (a stride in elements between rows, 0 = C or the row's own
+ * length, a multiple of 8 but for dt).  Rows behind the last sequence are not
+ * written.  Pointers 16-byte aligned, dt 2, fp32 and int32 arrays 4.  out must not
+ * overlap an input or a state; initial_state and final_state are the same buffer
+ * or lie apart.  Calls are asynchronous on `stream` and keep nothing between calls.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int64_t x_stride; /* elements between rows of x; 0 = C */
+  int32_t silu;     /* != 0: out = y sigmoid(y), else out = y */
+} kda_conv_options;
+
+/* y[t, c] = bias[c] + sum_{j < W} weight[c, j] x[t - W + 1 + j, c] inside each sequence, W = 2, 3
+ * or 4.  x, out bf16 [T_total, C] (C a multiple of 8), weight bf16 [C, W], bias bf16 [C]
+ * or NULL; initial_state bf16 [N, W - 1, C] or NULL (= zeros): the rows before each
+ * sequence, oldest first; final_state the same of the rows at its end (its own last rows,
+ * or those and the newest of the initial state if it is shorter), or NULL.  Sums are fp32.
+ * For any number of rows a sequence, single tokens among them. */
+kda_status kda_conv_fwd(const kda_conv_options* opts, const void* x, const void* weight,
+                        const void* bias, const void* initial_state, const int32_t* cu_seqlens,
+                        int64_t T_total, int32_t C, int32_t W, int32_t N, void* out,
+                        void* final_state, void* stream);
+
+typedef struct {
+  int64_t x_stride, dt_stride, b_stride, c_stride; /* elements between tokens; 0 = contiguous */
+  const float* skip;    /* fp32 [H] or NULL (= 0) */
+  const float* dt_bias; /* fp32 [H] or NULL (= 0) */
+  int32_t state_dtype;  /* KDA_STATE_*, of both states */
+} kda_ssm_options;
+
+/* Per sequence and head, with a state M [P, S] that starts at initial_state[n][h] or 0, for
+ * each token in order:
+ *     d = softplus(dt + dt_bias[h])
+ *     M = exp(A[h] d) M + d x B^T
+ *     y = M C + skip[h] x
+ * x, out bf16 [T_total, H, P], dt bf16 [T_total, H], B, C bf16 [T_total, G, S] (head h has those
+ * of group h / (H / G)), A fp32 [H], not positive; states [N, H, P, S], fp32 or bf16.  P and S
+ * are 64 or 128, N * H below 2^23.
+ * kda_ssm_step: token by token with the state in registers, in fp32 throughout; for one or a
+ *   few tokens a sequence, where moving the state is what counts.
+ * kda_ssm_fwd: the same result for prompts. */
+kda_status kda_ssm_step(const kda_ssm_options* opts, const void* x, const void* dt, const float* A,
+                        const void* B, const void* C, const void* initial_state,
+                        const int32_t* cu_seqlens, int64_t T_total, int32_t H, int32_t G, int32_t N,
+                        int32_t P, int32_t S, void* out, void* final_state, void* stream);
+size_t kda_ssm_workspace_size(int64_t T_total, int32_t H, int32_t G, int32_t N, int32_t P, int32_t S);
+kda_status kda_ssm_fwd(const kda_ssm_options* opts, const void* x, const void* dt, const float* A,
+                       const void* B, const void* C, const void* initial_state,
+                       const int32_t* cu_seqlens, int64_t T_total, int32_t H, int32_t G, int32_t N,
+                       int32_t P, int32_t S, void* out, void* final_state, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
