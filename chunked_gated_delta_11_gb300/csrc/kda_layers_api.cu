@@ -162,8 +162,15 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_options* opts, const void* x, co
                                   const int32_t* cu_seqlens, int64_t T_total, int32_t H, int32_t G,
                                   int32_t N, int32_t P, int32_t S, void* out, void* final_state,
                                   void* workspace, size_t workspace_bytes, void* stream) {
+  SsmArgs a;
+  kda_status s = check_ssm(opts, x, dt, A, B, C, initial_state, cu_seqlens, T_total, H, G, N, P, S, out, final_state, a);
+  if (s != KDA_OK) return s;
+  if (T_total >= (static_cast<int64_t>(1) << 31) - 128) return KDA_ERR_INVALID_ARG;
   (void)workspace, (void)workspace_bytes;
-  return kda_ssm_step(opts, x, dt, A, B, C, initial_state, cu_seqlens, T_total, H, G, N, P, S, out, final_state, stream);
+  int sms = 0, *err = nullptr;
+  if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;
+  return launch_ssm_fwd(a, P, S, sms, nullptr, err, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
+                                                                                                  : KDA_ERR_LAUNCH;
 }
 
 namespace {

@@ -1,0 +1,805 @@
+// kda_ssm.cu -- the state-space recurrence over prompts (kda_ssm_fwd) on tcgen05.
+//
+// A chunk of 128 tokens at a time.  With d the step sizes and l_i the sum of A d up to
+// token i of the chunk (log of the decay since its start), Q its last token:
+//
+//   Y_i = e^{l_i} M C_i + sum_{j <= i} e^{l_i - l_j} d_j (C_i . B_j) x_j + skip x_i
+//   M'  = e^{l_Q} M + sum_j (e^{l_Q - l_j} d_j x_j) B_j^T
+//
+// A CTA has 128 channels of one sequence (or of a piece of one): two heads of 64 that share
+// B and C, or one of 128.  20 warps:
+//   warps 0-3    weights: S = C B^T (one thread a row) times e^{l_i - l_j} d_j, per head, in bf16
+//                over S in tensor memory
+//   warps 4-7    the state, a thread a channel: M in tensor memory (fp32), its bf16 copy for
+//                the products with C in shared memory, its decay
+//   warps 8-11   the weighted rows x' = e^{l_Q - l_j} d_j x_j, transposed (a thread a channel)
+//                into tensor memory, as the left operand of M' += x'^T B
+//   warps 12-15  outputs: e^{l_i} M C_i in tensor memory, then the finished rows
+//   warp 16      TMA;  warp 17  the products;  warps 18, 19  step sizes and decays
+// Tensor memory: S and P | Y | M | x' (four places of 64 tokens), 128 columns each.
+//
+// Roundings.  x' enters the product with B as the sum of `terms` bf16 numbers: three hold
+// all 24 bits, so that a state in fp32 is one.  P and the copy of M that the outputs see are
+// rounded to bf16 once (2^-9 of the value at most, as the output).
+#include <type_traits>
+
+#include "kda_attn.cuh"
+#include "kda_layers.cuh"
+#include "kda_tc.cuh"
+#include "kda_tma.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int SS_TOK = 128;              // tokens of a chunk, channels of a CTA
+constexpr int SS_BOX = SS_TOK * 128;     // bytes of 64 elements of 128 rows
+constexpr int SS_THREADS = 640;
+// five warpgroups of 96 registers a thread at launch: 144 + 88 + 2 x 96 + 56 = 5 x 96
+constexpr int SS_REGS_WEIGHTS = 144, SS_REGS_STATE = 88, SS_REGS_ISSUE = 56;
+constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384;  // columns
+
+// Steps and decays of a chunk's tokens for one head, in units of log2.
+struct SsmPrep {
+  float l[SS_TOK];   // sum of A d up to the token
+  float d[SS_TOK];   // step size; 0 behind the sequence's end
+  float w[SS_TOK];   // e^{l_Q - l_j} d_j
+  float e[SS_TOK];   // e^{l_i}
+  float cf[192];     // e^{l_b - l_j} d_j, b the last token before rows 32, 64, 96 (32, 64, 96 of them)
+  float keep, pad[3];  // e^{l_Q}
+};
+
+struct SsmItem {
+  int64_t tok;   // first token
+  int len;       // tokens; < 0: nothing to do
+  int n, k;      // sequence, piece
+  int last;      // its last piece
+};
+
+struct SsmCtl {
+  uint64_t x_full[2], x_empty[2], b_full[2], b_empty[2], c_full, c_empty, prep_full[2], prep_empty[2];
+  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[4], xp_empty[4], zeroed, drained;
+  SsmItem item;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(SsmCtl) <= 512, "control block");
+
+struct SsmMaps {
+  CUtensorMap x, b, c;
+};
+
+template <int S>
+struct SsmSmem {
+  static constexpr int SB = S / 64;
+  static constexpr int X = 0, B = 4 * SS_BOX, C = B + 2 * SB * SS_BOX, H = C + SB * SS_BOX;
+  static constexpr int OUT = H + SB * SS_BOX, PREP = OUT + 4 * 4096;
+  static constexpr int CTL = PREP + 4 * static_cast<int>(sizeof(SsmPrep));
+  static constexpr int BYTES = CTL + 512 + 1024;
+};
+static_assert(SsmSmem<128>::BYTES <= 227 * 1024, "shared memory");
+
+// A piece's state from zero and its decay, as kept between the two kernels of a split
+// pass: [slot][unit][S / 4][128 channels] float4, then [slot][unit][2].
+struct SsmParts {
+  float* m;
+  float* keep;
+  const void* init;  // initial states, where the pass does not write
+};
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One arrival a warp, after all its lanes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// PRE: only the state that each piece but a sequence's last adds, walking from its last
+// chunk to its first: with weights that reach to the piece's end, the products of all
+// chunks add up in tensor memory.
+template <int P, int S, bool PRE>
+__global__ void __launch_bounds__(SS_THREADS, 1)
+ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, int terms, int* err) {
+  using L = SsmSmem<S>;
+  constexpr int HU = SS_TOK / P;  // heads of a unit
+  constexpr int SB = L::SB;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  SsmCtl* ctl = reinterpret_cast<SsmCtl*>(smem + L::CTL);
+  SsmPrep* prep = reinterpret_cast<SsmPrep*>(smem + L::PREP);  // [stage][head]
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
+  const int unit = blockIdx.x % units;
+  const int64_t slot = blockIdx.x / units;
+  const int per_group = a.H / a.G, upg = (per_group + HU - 1) / HU;
+  const int g = unit / upg, hu = (unit % upg) * HU, h0 = g * per_group + hu;
+  const int nh = per_group - hu < HU ? per_group - hu : HU;  // heads that exist
+
+  if (tid == 0) {
+    constexpr int users = PRE ? 4 : 16;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->x_full[i], 1);
+      mbar_init(&ctl->x_empty[i], PRE ? 4 : 5);
+      mbar_init(&ctl->b_full[i], 1);
+      mbar_init(&ctl->b_empty[i], 1);
+      mbar_init(&ctl->prep_full[i], HU);
+      mbar_init(&ctl->prep_empty[i], users);
+    }
+    mbar_init(&ctl->c_full, 1);
+    mbar_init(&ctl->c_empty, 1);
+    mbar_init(&ctl->s_full, 1);
+    mbar_init(&ctl->p_full, 4);
+    mbar_init(&ctl->yoff_full, 1);
+    mbar_init(&ctl->y_scaled, 4);
+    mbar_init(&ctl->y_full, 1);
+    mbar_init(&ctl->y_empty, 4);
+    mbar_init(&ctl->m_full, 1);
+    mbar_init(&ctl->h_full, 4);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ctl->xp_full[i], 4);
+      mbar_init(&ctl->xp_empty[i], 1);
+    }
+    mbar_init(&ctl->zeroed, 4);
+    mbar_init(&ctl->drained, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (w == 16) {
+    // Sequence n owns the slots from floor(bos_n / piece) + n on, one for each of its pieces.
+    const int n = seq_of_slot(a.cu, a.T, a.N, static_cast<int>(piece), 1, slot);
+    int64_t bos, eos;
+    seq_bounds(a.cu, a.T, a.N, n, bos, eos);
+    const int64_t k = slot - (bos / piece + n), first = k * piece;
+    const bool there = k >= 0 && (k == 0 || first < eos - bos);  // (a malformed cu_seqlens can give less)
+    const int64_t left = eos - bos - first;
+    SsmItem it;
+    it.tok = bos + first;
+    it.len = there ? static_cast<int>(left < piece ? left : piece) : -1;
+    it.n = n;
+    it.k = static_cast<int>(k);
+    it.last = left <= piece;
+    if (PRE && it.last) it.len = -1;
+    if (l == 0) ctl->item = it;
+  }
+  if (w == 17) {
+    tmem_alloc(&ctl->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const SsmItem it = ctl->item;
+  const int nc = it.len > 0 ? (it.len + SS_TOK - 1) / SS_TOK : 0;
+  const int64_t part = slot * units + unit;
+  // the c-th chunk that is worked on, and its tokens
+  auto chunk = [&](int c) { return PRE ? nc - 1 - c : c; };
+  auto tokens = [&](int c) {
+    const int left = it.len - chunk(c) * SS_TOK;
+    return left < SS_TOK ? left : SS_TOK;
+  };
+
+  if (w >= 16) {
+    regs_give<SS_REGS_ISSUE>();
+    if (w == 16) {
+      if (l == 0) {
+        bool ok = true;
+        int c = 0, cs = 0;
+        for (; ok && c < nc; ++c) {
+          const int st = c & 1, row = static_cast<int>(it.tok + chunk(c) * SS_TOK);
+          if (c >= 2) ok = wait_for(&ctl->x_empty[st], ((c >> 1) - 1) & 1, ctl, err);
+          if (!ok) break;
+          const int boxes = P == 64 ? nh : 2;
+          mbar_arrive_expect_tx(&ctl->x_full[st], boxes * SS_BOX);
+          for (int b = 0; b < boxes; ++b)
+            tma_box2(smem + L::X + (2 * st + b) * SS_BOX, &maps.x, h0 * P + b * 64, row, &ctl->x_full[st]);
+          if (c >= 2) ok = wait_for(&ctl->b_empty[st], ((c >> 1) - 1) & 1, ctl, err);
+          if (!ok) {
+            mbar_wait(&ctl->x_full[st], (c >> 1) & 1);
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl->b_full[st], SB * SS_BOX);
+          for (int b = 0; b < SB; ++b)
+            tma_box2(smem + L::B + (SB * st + b) * SS_BOX, &maps.b, g * S + b * 64, row, &ctl->b_full[st]);
+          if (!PRE) {
+            if (c >= 1) ok = wait_for(&ctl->c_empty, (c - 1) & 1, ctl, err);
+            if (!ok) {
+              mbar_wait(&ctl->x_full[st], (c >> 1) & 1);
+              mbar_wait(&ctl->b_full[st], (c >> 1) & 1);
+              break;
+            }
+            mbar_arrive_expect_tx(&ctl->c_full, SB * SS_BOX);
+            for (int b = 0; b < SB; ++b)
+              tma_box2(smem + L::C + b * SS_BOX, &maps.c, g * S + b * 64, row, &ctl->c_full);
+            ++cs;
+          }
+        }
+        // copies that may be in flight after a wait that ran out land first
+        if (*reinterpret_cast<volatile int*>(&ctl->abort) || !ok) {
+          for (int i = c > 2 ? c - 2 : 0; i < c; ++i) {
+            mbar_wait(&ctl->x_full[i & 1], (i >> 1) & 1);
+            mbar_wait(&ctl->b_full[i & 1], (i >> 1) & 1);
+          }
+          if (cs > 0) mbar_wait(&ctl->c_full, (cs - 1) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (w == 17) {
+      if (elect_one()) {
+        const uint32_t sb = smem_u32(smem);
+        constexpr uint32_t id_s = make_idesc(1, SS_TOK, SS_TOK);
+        constexpr uint32_t id_m = make_idesc(1, SS_TOK, S) | (1u << 16);  // B is MN-major
+        constexpr uint32_t id_y = make_idesc(1, SS_TOK, P) | (1u << 16);
+        const uint64_t rows_desc = make_sdesc(sb, 16, 1024, 2), cols_desc = make_sdesc(sb, SS_BOX, 1024, 2);
+        const uint32_t hi = static_cast<uint32_t>(rows_desc >> 32);  // the same for both
+        const uint32_t rows_lo = static_cast<uint32_t>(rows_desc), cols_lo = static_cast<uint32_t>(cols_desc);
+        constexpr uint32_t BX = SS_BOX >> 4, C0 = L::C >> 4, H0 = L::H >> 4;
+        // products over S channels of C with rows of B or of the state's copy
+        auto over_state = [&](uint32_t d, auto b_at, uint32_t b_lo) {
+          constexpr uint32_t b0 = b_at.value;
+          mma_ss_step<C0, b0>(d, rows_lo, b_lo, hi, id_s, 0);
+          mma_ss_step<C0 + 2, b0 + 2>(d, rows_lo, b_lo, hi, id_s, 1);
+          mma_ss_step<C0 + 4, b0 + 4>(d, rows_lo, b_lo, hi, id_s, 1);
+          mma_ss_step<C0 + 6, b0 + 6>(d, rows_lo, b_lo, hi, id_s, 1);
+          if constexpr (SB == 2) {
+            mma_ss_step<C0 + BX, b0 + BX>(d, rows_lo, b_lo, hi, id_s, 1);
+            mma_ss_step<C0 + BX + 2, b0 + BX + 2>(d, rows_lo, b_lo, hi, id_s, 1);
+            mma_ss_step<C0 + BX + 4, b0 + BX + 4>(d, rows_lo, b_lo, hi, id_s, 1);
+            mma_ss_step<C0 + BX + 6, b0 + BX + 6>(d, rows_lo, b_lo, hi, id_s, 1);
+          }
+        };
+        int i = 0;  // places of x' used so far
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+          const uint32_t st = c & 1;
+          const int len = tokens(c);
+          const uint32_t b_stage = (L::B >> 4) + st * SB * BX, x_stage = (L::X >> 4) + st * 2 * BX;
+          ok = wait_for(&ctl->b_full[st], (c >> 1) & 1, ctl, err);
+          if (!ok) break;
+          if (!PRE) {
+            ok = wait_for(&ctl->c_full, c & 1, ctl, err);
+            if (!ok) break;
+            // the tensor core runs these in order: S may follow into the columns P was read from
+            over_state(tmem + SS_SP, std::integral_constant<uint32_t, 0>{}, rows_lo + b_stage);
+            tc_commit(&ctl->s_full);
+            ok = wait_for(&ctl->h_full, c & 1, ctl, err) && (c == 0 || wait_for(&ctl->y_empty, (c - 1) & 1, ctl, err));
+            if (!ok) break;
+            tc_fence_after();
+            over_state(tmem + SS_Y, std::integral_constant<uint32_t, H0>{}, rows_lo);
+            tc_commit(&ctl->yoff_full);
+            tc_commit(&ctl->c_empty);
+          }
+          for (int half = 0; half < (len > 64 ? 2 : 1); ++half) {
+            const uint32_t b_lo = cols_lo + b_stage + half * 512;
+            for (int t = 0; t < terms; ++t, ++i) {
+              ok = wait_for(&ctl->xp_full[i & 3], (i >> 2) & 1, ctl, err);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t x = tmem + SS_XP + (i & 3) * 32;
+              mma_ts_step<0, 0>(tmem + SS_M, x, b_lo, hi, id_m, !PRE || i > 0);
+              mma_ts_step<8, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+              mma_ts_step<16, 256>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+              mma_ts_step<24, 384>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+              tc_commit(&ctl->xp_empty[i & 3]);
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
+          tc_commit(&ctl->b_empty[st]);
+          if (!PRE || c + 1 == nc) tc_commit(&ctl->m_full);
+          if (!PRE) {
+            ok = wait_for(&ctl->p_full, c & 1, ctl, err) && wait_for(&ctl->y_scaled, c & 1, ctl, err);
+            if (!ok) break;
+            tc_fence_after();
+            const int steps = (len + 15) / 16;
+#pragma unroll
+            for (int hh = 0; hh < HU; ++hh) {
+              if (hh >= nh) break;
+              const uint32_t d = tmem + SS_Y + hh * 64, p = tmem + SS_SP + hh * 64, x_lo = cols_lo + x_stage + hh * BX;
+              mma_ts_step<0, 0>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 1) mma_ts_step<8, 128>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 2) mma_ts_step<16, 256>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 3) mma_ts_step<24, 384>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 4) mma_ts_step<32, 512>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 5) mma_ts_step<40, 640>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 6) mma_ts_step<48, 768>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 7) mma_ts_step<56, 896>(d, p, x_lo, hi, id_y, 1);
+            }
+            tc_commit(&ctl->y_full);
+            tc_commit(&ctl->x_empty[st]);
+          }
+        }
+        // nothing may be running in tensor memory when it is freed
+        tc_commit(&ctl->drained);
+        mbar_wait(&ctl->drained, 0);
+      }
+      __syncwarp();
+    } else {
+      // Step sizes and decays of one head, four tokens to a lane.
+      const int hh = w - 18;
+      if (hh < HU) {
+        const bool there = hh < nh;
+        const int h = h0 + (there ? hh : 0);
+        const float rate = nc > 0 ? __ldg(a.A + h) * kLog2e : 0.f, bias = nc > 0 && a.dt_bias ? __ldg(a.dt_bias + h) : 0.f;
+        float tail = 0.f;  // of the chunks behind (PRE)
+        for (int c = 0; c < nc; ++c) {
+          const int st = c & 1, len = tokens(c);
+          const __nv_bfloat16* dt = a.dt + (it.tok + chunk(c) * SS_TOK) * a.dt_stride + h;
+          float d[4], s[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = 4 * l + e;
+            const bool in = there && t < len;
+            const float raw = in ? __bfloat162float(dt[t * a.dt_stride]) : 0.f;
+            d[e] = in ? softplus(raw + bias) : 0.f;
+            s[e] = in ? rate * d[e] : 0.f;
+          }
+          // sums up to a token from the chunk's start, and behind it to the chunk's end
+          float pre[4], suf[4];
+          pre[0] = s[0];
+          suf[3] = 0.f;
+#pragma unroll
+          for (int e = 1; e < 4; ++e) {
+            pre[e] = pre[e - 1] + s[e];
+            suf[3 - e] = suf[4 - e] + s[4 - e];
+          }
+          const float mine = pre[3];
+          float before = mine, behind = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, before, o), y = __shfl_down_sync(0xffffffffu, behind, o);
+            if (l >= o) before += x;
+            if (l + o < 32) behind += y;
+          }
+          const float all = __shfl_sync(0xffffffffu, behind, 0);
+          const float lo = __shfl_up_sync(0xffffffffu, before, 1), hi = __shfl_down_sync(0xffffffffu, behind, 1);
+          const float start = l == 0 ? 0.f : lo, end = l == 31 ? 0.f : hi;
+          const float edge[3] = {__shfl_sync(0xffffffffu, before, 7), __shfl_sync(0xffffffffu, before, 15),
+                                 __shfl_sync(0xffffffffu, before, 23)};
+          if (c >= 2 && !warp_wait(&ctl->prep_empty[st], ((c >> 1) - 1) & 1, ctl, err)) break;
+          SsmPrep& o = prep[st * 2 + hh];
+          float ll[4], ww[4], ee[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ll[e] = start + pre[e];
+            ww[e] = exp2f(suf[e] + end + tail) * d[e];
+            ee[e] = ex2_approx(ll[e]);
+          }
+          *reinterpret_cast<float4*>(o.w + 4 * l) = make_float4(ww[0], ww[1], ww[2], ww[3]);
+          if (!PRE) {
+            *reinterpret_cast<float4*>(o.l + 4 * l) = make_float4(ll[0], ll[1], ll[2], ll[3]);
+            *reinterpret_cast<float4*>(o.d + 4 * l) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4*>(o.e + 4 * l) = make_float4(ee[0], ee[1], ee[2], ee[3]);
+#pragma unroll
+            for (int b = 1; b < 4; ++b)
+              if (l < 8 * b) {
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = ex2_approx(edge[b - 1] - ll[e]) * d[e];
+                *reinterpret_cast<float4*>(o.cf + 16 * b * (b - 1) + 4 * l) = make_float4(f[0], f[1], f[2], f[3]);
+              }
+          }
+          if (PRE) tail += all;
+          if (l == 0) o.keep = exp2f(PRE ? tail : all);
+          warp_arrive(&ctl->prep_full[st]);
+        }
+        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = exp2f(tail);
+      }
+      __syncwarp();
+    }
+  } else if (w < 4) {
+    regs_take<SS_REGS_WEIGHTS>();
+    const uint32_t SP = tmem + SS_SP + (static_cast<uint32_t>(w * 32) << 16);
+    const int i = w * 32 + l;
+    for (int c = 0; !PRE && c < nc; ++c) {
+      const int st = c & 1;
+      if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
+      if (!warp_wait(&ctl->s_full, c & 1, ctl, err)) break;
+      tc_fence_after();
+      const SsmPrep* pr = prep + st * 2;
+      float li[HU];
+      f2 ri[HU];
+#pragma unroll
+      for (int hh = 0; hh < HU; ++hh) {
+        li[hh] = pr[hh].l[i];
+        const float r = w > 0 ? ex2_approx(li[hh] - pr[hh].l[w * 32 - 1]) : 0.f;
+        ri[hh] = pair(r, r);
+      }
+      uint32_t held[HU > 1 ? 64 : 1];  // the second head's weights: S is still to be read where they go
+#pragma unroll
+      for (int jb = 0; jb < 4; ++jb) {
+        uint32_t p[HU][16];
+        if (jb > w) {
+#pragma unroll
+          for (int hh = 0; hh < HU; ++hh)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) p[hh][e] = 0u;
+        } else {
+          uint32_t s[32];
+          tmem_ld32(SP + jb * 32, s);
+          tmem_wait_ld();
+#pragma unroll
+          for (int hh = 0; hh < HU; ++hh) {
+            if (jb < w) {
+              const float4* cf = reinterpret_cast<const float4*>(pr[hh].cf + 16 * w * (w - 1) + jb * 32);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float4 f = cf[q];
+                float x0, x1, x2, x3;
+                unpair(mul2(pair(s[4 * q], s[4 * q + 1]), mul2(pair(f.x, f.y), ri[hh])), x0, x1);
+                unpair(mul2(pair(s[4 * q + 2], s[4 * q + 3]), mul2(pair(f.z, f.w), ri[hh])), x2, x3);
+                p[hh][2 * q] = pack_bf16(x0, x1);
+                p[hh][2 * q + 1] = pack_bf16(x2, x3);
+              }
+            } else {
+              const float4* lj = reinterpret_cast<const float4*>(pr[hh].l + jb * 32);
+              const float4* dj = reinterpret_cast<const float4*>(pr[hh].d + jb * 32);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float4 f = lj[q], d = dj[q];
+                const float fl[4] = {f.x, f.y, f.z, f.w}, fd[4] = {d.x, d.y, d.z, d.w};
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  x[e] = 4 * q + e <= l ? __uint_as_float(s[4 * q + e]) * (ex2_approx(li[hh] - fl[e]) * fd[e]) : 0.f;
+                p[hh][2 * q] = pack_bf16(x[0], x[1]);
+                p[hh][2 * q + 1] = pack_bf16(x[2], x[3]);
+              }
+            }
+          }
+        }
+        tmem_st16(SP + jb * 16, p[0]);
+        if (HU > 1) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) held[jb * 16 + e] = p[HU - 1][e];
+        }
+      }
+      if constexpr (HU > 1) {
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p[e] = held[jb * 16 + e];
+          tmem_st16(SP + 64 + jb * 16, p);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&ctl->p_full);
+      warp_arrive(&ctl->prep_empty[st]);
+    }
+  } else if (w < 8) {
+    regs_give<SS_REGS_STATE>();
+    const int r = tid & 127, hh = r / P;  // channel of the unit, its head
+    const bool there = hh < nh;
+    const uint32_t M = tmem + SS_M + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    const int64_t row = ((static_cast<int64_t>(it.n) * a.H + h0 + hh) * P + r % P) * S;  // of the states
+    bool ok = true;
+    if (!PRE && it.len >= 0) {
+      // the state that the piece starts from
+#pragma unroll 1
+      for (int cb = 0; cb < S / 32; ++cb) {
+        float m[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) m[e] = 0.f;
+        if (parts.init && there) {
+          if (a.bf16_state) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(parts.init) + row + cb * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint4 x = src[q];
+              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                m[8 * q + 2 * e] = __uint_as_float(u[e] << 16);
+                m[8 * q + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+              }
+            }
+          } else {
+            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(parts.init) + row + cb * 32);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 x = src[q];
+              m[4 * q] = x.x;
+              m[4 * q + 1] = x.y;
+              m[4 * q + 2] = x.z;
+              m[4 * q + 3] = x.w;
+            }
+          }
+        }
+        for (int j = 0; j < it.k; ++j) {
+          const int64_t p = (slot - it.k + j) * units + unit;
+          const float keep = there ? parts.keep[p * 2 + hh] : 0.f;
+          const float4* src = reinterpret_cast<const float4*>(parts.m) + (p * (S / 4) + cb * 8) * SS_TOK + r;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 x = src[q * SS_TOK];
+            m[4 * q] = fmaf(m[4 * q], keep, x.x);
+            m[4 * q + 1] = fmaf(m[4 * q + 1], keep, x.y);
+            m[4 * q + 2] = fmaf(m[4 * q + 2], keep, x.z);
+            m[4 * q + 3] = fmaf(m[4 * q + 3], keep, x.w);
+          }
+        }
+        uint32_t u[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(m[e]);
+        tmem_st32(M + cb * 32, u);
+      }
+      tmem_wait_st();
+      for (int c = 0; c < nc; ++c) {
+        const int st = c & 1;
+        ok = (c == 0 || warp_wait(&ctl->m_full, (c - 1) & 1, ctl, err)) && warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err);
+        if (!ok) break;
+        tc_fence_after();
+        const float keep = prep[st * 2 + hh].keep;
+#pragma unroll
+        for (int cb = 0; cb < S / 32; ++cb) {
+          uint32_t m[32];
+          tmem_ld32(M + cb * 32, m);
+          tmem_wait_ld();
+          uint8_t* dst = smem + L::H + (cb >> 1) * SS_BOX + r * 128;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[e] = pack_bf16(__uint_as_float(m[8 * q + 2 * e]), __uint_as_float(m[8 * q + 2 * e + 1]));
+            *reinterpret_cast<uint4*>(dst + ((((cb & 1) * 4 + q) ^ (r & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) m[e] = __float_as_uint(__uint_as_float(m[e]) * keep);
+          tmem_st32(M + cb * 32, m);
+        }
+        tmem_wait_st();
+        fence_async();
+        tc_fence_before();
+        warp_arrive(&ctl->h_full);
+        warp_arrive(&ctl->prep_empty[st]);
+      }
+    }
+    // the state at the end
+    if (ok && nc > 0) ok = warp_wait(&ctl->m_full, PRE ? 0 : (nc - 1) & 1, ctl, err);
+    if (ok && (PRE ? nc > 0 : it.len >= 0 && it.last && a.fin != nullptr)) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int cb = 0; cb < S / 32; ++cb) {
+        uint32_t m[32];
+        tmem_ld32(M + cb * 32, m);
+        tmem_wait_ld();
+        if (PRE) {
+          float4* dst = reinterpret_cast<float4*>(parts.m) + (part * (S / 4) + cb * 8) * SS_TOK + r;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[q * SS_TOK] = make_float4(__uint_as_float(m[4 * q]), __uint_as_float(m[4 * q + 1]),
+                                          __uint_as_float(m[4 * q + 2]), __uint_as_float(m[4 * q + 3]));
+        } else if (there && a.bf16_state) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.fin) + row + cb * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              p[e] = pack_bf16(__uint_as_float(m[8 * q + 2 * e]), __uint_as_float(m[8 * q + 2 * e + 1]));
+            dst[q] = make_uint4(p[0], p[1], p[2], p[3]);
+          }
+        } else if (there) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(a.fin) + row + cb * 32);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[q] = make_uint4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
+        }
+      }
+    }
+  } else if (w < 12) {
+    const int r = tid & 127, hh = r / P;
+    const uint32_t XP = tmem + SS_XP + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    int i = 0;  // places of x' used so far
+    for (int c = 0; c < nc; ++c) {
+      const int st = c & 1, len = tokens(c);
+      if (!warp_wait(&ctl->x_full[st], (c >> 1) & 1, ctl, err)) break;
+      uint8_t* x = smem + L::X + 2 * st * SS_BOX;
+      if (len < SS_TOK) {
+        // rows behind the sequence's end (another's, whatever they hold) take no part in a product
+        if (!warp_wait(&ctl->b_full[st], (c >> 1) & 1, ctl, err)) break;
+        if (r >= len) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<uint4*>(x + (e >> 3) * SS_BOX + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          uint8_t* b = smem + L::B + SB * st * SS_BOX;
+#pragma unroll
+          for (int e = 0; e < 8 * SB; ++e)
+            *reinterpret_cast<uint4*>(b + (e >> 3) * SS_BOX + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async();
+        warp_arrive(&ctl->zeroed);  // one chunk of a piece at most
+        if (!warp_wait(&ctl->zeroed, 0, ctl, err)) break;
+      }
+      if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
+      const float* weight = prep[st * 2 + hh].w;
+      const uint8_t* mine = x + (r >> 6) * SS_BOX + (r & 7) * 2;
+      const int piece16 = (r & 63) >> 3;
+      bool ok = true;
+      for (int half = 0; half < (len > 64 ? 2 : 1); ++half) {
+        for (int t = 0; ok && t < terms; ++t)
+          if (i + t >= 4) ok = warp_wait(&ctl->xp_empty[(i + t) & 3], (((i + t) >> 2) - 1) & 1, ctl, err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int sub = 0; sub < 2; ++sub) {
+          const int t0 = half * 64 + sub * 32;
+          const uint8_t* from = mine + t0 * 128;
+          const float4* wt = reinterpret_cast<const float4*>(weight + t0);
+          float v[32];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = wt[q];
+            const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = 4 * q + e;
+              const uint32_t raw = *reinterpret_cast<const uint16_t*>(from + t * 128 + ((piece16 ^ (t & 7)) << 4));
+              v[t] = __uint_as_float(raw << 16) * ff[e];
+            }
+          }
+          for (int t = 0; t < terms; ++t) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              p[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+              v[2 * e] -= __uint_as_float(p[e] << 16);
+              v[2 * e + 1] -= __uint_as_float(p[e] & 0xffff0000u);
+            }
+            tmem_st16(XP + ((i + t) & 3) * 32 + sub * 16, p);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        for (int t = 0; t < terms; ++t) warp_arrive(&ctl->xp_full[(i + t) & 3]);
+        i += terms;
+      }
+      if (!ok) break;
+      warp_arrive(&ctl->prep_empty[st]);
+      if (PRE) warp_arrive(&ctl->x_empty[st]);
+    }
+  } else {
+    const int i = tid & 127;
+    const uint32_t Y = tmem + SS_Y + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    uint8_t* stage = smem + L::OUT + (w & 3) * 4096;
+    for (int c = 0; !PRE && c < nc; ++c) {
+      const int st = c & 1, len = tokens(c);
+      if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
+      if (!warp_wait(&ctl->yoff_full, c & 1, ctl, err)) break;
+      tc_fence_after();
+      float e[HU];
+#pragma unroll
+      for (int hh = 0; hh < HU; ++hh) e[hh] = prep[st * 2 + hh].e[i];
+#pragma unroll
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t y[32];
+        tmem_ld32(Y + cb * 32, y);
+        tmem_wait_ld();
+        const float f = e[cb * HU / 4];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+        tmem_st32(Y + cb * 32, y);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(&ctl->y_scaled);
+      warp_arrive(&ctl->prep_empty[st]);
+      if (!warp_wait(&ctl->y_full, c & 1, ctl, err)) break;
+      tc_fence_after();
+      const uint8_t* x = smem + L::X + 2 * st * SS_BOX + i * 128;
+      const int rows = len - (i - l);  // of the warp's 32, those there
+      __nv_bfloat16* dst = a.out + ((it.tok + c * SS_TOK + (i - l)) * a.H + h0) * P;
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int h = h0 + (HU > 1 ? (half < nh ? half : 0) : 0);
+        const float skip = a.skip ? __ldg(a.skip + h) : 0.f;
+        uint32_t y[64];
+        {
+          uint32_t y0[32], y1[32];
+          tmem_ld32(Y + half * 64, y0);
+          tmem_ld32(Y + half * 64 + 32, y1);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            y[k] = y0[k];
+            y[32 + k] = y1[k];
+          }
+        }
+        if (half == 1) {
+          tc_fence_before();
+          warp_arrive(&ctl->y_empty);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[8 * q + k]);
+          if (a.skip) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x + half * SS_BOX + ((q ^ (i & 7)) << 4));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = fmaf(skip, __uint_as_float(u[k] << 16), f[2 * k]);
+              f[2 * k + 1] = fmaf(skip, __uint_as_float(u[k] & 0xffff0000u), f[2 * k + 1]);
+            }
+          }
+          *reinterpret_cast<uint4*>(stage + l * 128 + ((q ^ (l & 7)) << 4)) =
+              make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        }
+        __syncwarp();
+        if (HU == 1 || half < nh) {
+#pragma unroll
+          for (int q = l >> 3; q < 32; q += 4)
+            if (q < rows)
+              *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(q) * a.H * P + half * 64 + (l & 7) * 8) =
+                  *reinterpret_cast<const uint4*>(stage + q * 128 + (((l & 7) ^ (q & 7)) << 4));
+        }
+        __syncwarp();
+      }
+      warp_arrive(&ctl->x_empty[st]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (w == 17) tmem_dealloc(tmem, 512);
+}
+
+int units_of(const SsmArgs& a, int P) {
+  const int per_group = a.H / a.G, heads = SS_TOK / P;
+  return a.G * ((per_group + heads - 1) / heads);
+}
+
+// How a call is cut: pieces of `piece` tokens (beyond T: sequences stay whole).
+struct Plan {
+  int64_t piece, slots;
+};
+
+Plan plan_of(const SsmArgs& a, int P, int sm_count) {
+  (void)sm_count, (void)P;
+  const int64_t whole = (a.T / SS_TOK + 1) * SS_TOK;  // (T is below 2^31 - 128)
+  return {whole, a.N};
+}
+
+template <int P, int S, bool PRE>
+cudaError_t launch_one(const SsmMaps& maps, const SsmArgs& a, const SsmParts& parts, const Plan& plan, int units, int* err,
+                       cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  auto* kernel = ssm_kernel<P, S, PRE>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), SsmSmem<S>::BYTES, done);
+  if (e != cudaSuccess) return e;
+  // a state in fp32 takes all bits of its addends, one in bf16 two roundings' worth, and one
+  // that only the outputs see one
+  const int terms = !a.fin ? 1 : a.bf16_state ? 2 : 3;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(plan.slots * units)), dim3(SS_THREADS), SsmSmem<S>::BYTES, stream, maps,
+                    a, parts, plan.piece, units, terms, err);
+}
+
+template <int P, int S>
+cudaError_t launch(const SsmArgs& a, const Plan& plan, void* ws, int* err, cudaStream_t stream) {
+  SsmMaps maps{};
+  const int units = units_of(a, P);
+  if (a.T > 0) {
+    cudaError_t e = make_matrix_map(&maps.x, a.x, a.T, static_cast<int64_t>(a.H) * P, a.x_stride, SS_TOK);
+    if (e == cudaSuccess) e = make_matrix_map(&maps.b, a.B, a.T, static_cast<int64_t>(a.G) * S, a.b_stride, SS_TOK);
+    if (e == cudaSuccess) e = make_matrix_map(&maps.c, a.C, a.T, static_cast<int64_t>(a.G) * S, a.c_stride, SS_TOK);
+    if (e != cudaSuccess) return e;
+  }
+  (void)ws;
+  SsmParts parts{nullptr, nullptr, a.init};
+  return launch_one<P, S, false>(maps, a, parts, plan, units, err, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, int P, int S, int sm_count, void* ws, int* err, cudaStream_t stream) {
+  const Plan plan = plan_of(a, P, sm_count);
+  if (P == 64) return S == 64 ? launch<64, 64>(a, plan, ws, err, stream) : launch<64, 128>(a, plan, ws, err, stream);
+  return S == 64 ? launch<128, 64>(a, plan, ws, err, stream) : launch<128, 128>(a, plan, ws, err, stream);
+}
+
+}  // namespace kda

@@ -66,6 +66,23 @@ cudaError_t make_tile_map(CUtensorMap* map, const void* base, int64_t T_total, i
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Tiles of 64 elements x `rows` rows of a bf16 matrix whose rows are `stride` elements
+// apart (kda_ssm.cu), 128-byte swizzled.
+cudaError_t make_matrix_map(CUtensorMap* map, const void* base, int64_t T_total, int64_t cols, int64_t stride, int rows) {
+  if (T_total < 1 || T_total >= (static_cast<int64_t>(1) << 31) || cols < 64 || cols >= (static_cast<int64_t>(1) << 31))
+    return cudaErrorInvalidValue;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(T_total)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_raw_maps(RawMaps* maps, const void* q, const void* k, const void* v,
                           const void* g, int64_t T_total, int H, bool gate_scalar) {
   std::memset(maps, 0, sizeof(RawMaps));

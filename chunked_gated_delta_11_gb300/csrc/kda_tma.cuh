@@ -64,4 +64,15 @@ cudaError_t make_raw_maps(RawMaps* maps, const void* q, const void* k, const voi
 // swizzled.  The x coordinates used with it are 0 and 64 channels.
 cudaError_t make_tile_map(CUtensorMap* map, const void* base, int64_t T_total, int H, int rows);
 
+// The same boxes of a matrix [T_total, cols] whose rows are `stride` elements apart
+// (a multiple of 8).  The x coordinates used with it are multiples of 64.
+cudaError_t make_matrix_map(CUtensorMap* map, const void* base, int64_t T_total, int64_t cols, int64_t stride, int rows);
+__device__ __forceinline__ void tma_box2(void* dst, const CUtensorMap* map, int x, int t, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(t), "r"(smem_u32(bar))
+      : "memory");
+}
+
 }  // namespace kda
