@@ -42,7 +42,7 @@ constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384;  // columns
 // Steps and decays of a chunk's tokens for one head, in units of log2.
 struct SsmPrep {
   float l[SS_TOK];   // sum of A d up to the token
-  float d[SS_TOK];   // step size; 0 behind the sequence's end
+  float r[SS_TOK];   // l_j - log2 d_j: e^{l_i - l_j} d_j = e^{l_i - r_j}; +inf behind the sequence's end
   float w[SS_TOK];   // e^{l_Q - l_j} d_j
   float e[SS_TOK];   // e^{l_i}
   float cf[192];     // e^{l_b - l_j} d_j, b the last token before rows 32, 64, 96 (32, 64, 96 of them)
@@ -66,14 +66,14 @@ struct SsmCtl {
 static_assert(sizeof(SsmCtl) <= 512, "control block");
 
 struct SsmMaps {
-  CUtensorMap x, b, c;
+  CUtensorMap x, b, c, out;
 };
 
 template <int S>
 struct SsmSmem {
   static constexpr int SB = S / 64;
   static constexpr int X = 0, B = 4 * SS_BOX, C = B + 2 * SB * SS_BOX, H = C + SB * SS_BOX;
-  static constexpr int OUT = H + SB * SS_BOX, PREP = OUT + 4 * 4096;
+  static constexpr int PREP = H + SB * SS_BOX;
   static constexpr int CTL = PREP + 4 * static_cast<int>(sizeof(SsmPrep));
   static constexpr int BYTES = CTL + 512 + 1024;
 };
@@ -88,6 +88,36 @@ struct SsmParts {
 };
 
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Four 8 x 8 matrices of bf16, each transposed; a lane's address is a row's.
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+
+// 16 lanes x 32 columns in the layout that transposed matrices have: r[2 j] and r[2 j + 1] are column
+// 4 j + l % 4 of lanes l / 4 and l / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 32 rows of 64 channels from shared memory, and the wait until they have been read.
+__device__ __forceinline__ void tma_store_box(const CUtensorMap* map, int x, int t, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(t), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_stores_read() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
 
 // One arrival a warp, after all its lanes.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -324,16 +354,25 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         const int h = h0 + (there ? hh : 0);
         const float rate = nc > 0 ? __ldg(a.A + h) * kLog2e : 0.f, bias = nc > 0 && a.dt_bias ? __ldg(a.dt_bias + h) : 0.f;
         float tail = 0.f;  // of the chunks behind (PRE)
+        // raw step sizes are loaded a chunk ahead
+        __nv_bfloat16 raw[4], next[4];
+        auto load = [&](int c, __nv_bfloat16 (&to)[4]) {
+          const __nv_bfloat16* dt = a.dt + (it.tok + chunk(c) * SS_TOK) * a.dt_stride + h;
+          const int len = tokens(c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to[e] = there && 4 * l + e < len ? dt[(4 * l + e) * a.dt_stride] : __nv_bfloat16{};
+        };
+        if (nc > 0) load(0, next);
         for (int c = 0; c < nc; ++c) {
           const int st = c & 1, len = tokens(c);
-          const __nv_bfloat16* dt = a.dt + (it.tok + chunk(c) * SS_TOK) * a.dt_stride + h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) raw[e] = next[e];
+          if (c + 1 < nc) load(c + 1, next);
           float d[4], s[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int t = 4 * l + e;
-            const bool in = there && t < len;
-            const float raw = in ? __bfloat162float(dt[t * a.dt_stride]) : 0.f;
-            d[e] = in ? softplus(raw + bias) : 0.f;
+            const bool in = there && 4 * l + e < len;
+            d[e] = in ? softplus(__bfloat162float(raw[e]) + bias) : 0.f;
             s[e] = in ? rate * d[e] : 0.f;
           }
           // sums up to a token from the chunk's start, and behind it to the chunk's end
@@ -370,7 +409,8 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           *reinterpret_cast<float4*>(o.w + 4 * l) = make_float4(ww[0], ww[1], ww[2], ww[3]);
           if (!PRE) {
             *reinterpret_cast<float4*>(o.l + 4 * l) = make_float4(ll[0], ll[1], ll[2], ll[3]);
-            *reinterpret_cast<float4*>(o.d + 4 * l) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4*>(o.r + 4 * l) =
+                make_float4(ll[0] - __log2f(d[0]), ll[1] - __log2f(d[1]), ll[2] - __log2f(d[2]), ll[3] - __log2f(d[3]));
             *reinterpret_cast<float4*>(o.e + 4 * l) = make_float4(ee[0], ee[1], ee[2], ee[3]);
 #pragma unroll
             for (int b = 1; b < 4; ++b)
@@ -407,63 +447,77 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         const float r = w > 0 ? ex2_approx(li[hh] - pr[hh].l[w * 32 - 1]) : 0.f;
         ri[hh] = pair(r, r);
       }
-      uint32_t held[HU > 1 ? 64 : 1];  // the second head's weights: S is still to be read where they go
+      // Blocks of 32 columns before the row's own: e^{l_i - l_b} (e^{l_b - l_j} d_j), two factors
+      // that stay below 1.  The second head's weights are held back where S is still to be read.
+      uint32_t held[HU > 1 ? 48 : 1];
 #pragma unroll
-      for (int jb = 0; jb < 4; ++jb) {
-        uint32_t p[HU][16];
-        if (jb > w) {
-#pragma unroll
-          for (int hh = 0; hh < HU; ++hh)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) p[hh][e] = 0u;
-        } else {
+      for (int jb = 0; jb < 3; ++jb) {
+        if (jb < w) {
           uint32_t s[32];
           tmem_ld32(SP + jb * 32, s);
           tmem_wait_ld();
 #pragma unroll
           for (int hh = 0; hh < HU; ++hh) {
-            if (jb < w) {
-              const float4* cf = reinterpret_cast<const float4*>(pr[hh].cf + 16 * w * (w - 1) + jb * 32);
+            const float4* cf = reinterpret_cast<const float4*>(pr[hh].cf + 16 * w * (w - 1) + jb * 32);
+            uint32_t p[16];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 f = cf[q];
-                float x0, x1, x2, x3;
-                unpair(mul2(pair(s[4 * q], s[4 * q + 1]), mul2(pair(f.x, f.y), ri[hh])), x0, x1);
-                unpair(mul2(pair(s[4 * q + 2], s[4 * q + 3]), mul2(pair(f.z, f.w), ri[hh])), x2, x3);
-                p[hh][2 * q] = pack_bf16(x0, x1);
-                p[hh][2 * q + 1] = pack_bf16(x2, x3);
-              }
+            for (int q = 0; q < 8; ++q) {
+              const float4 f = cf[q];
+              float x0, x1, x2, x3;
+              unpair(mul2(pair(s[4 * q], s[4 * q + 1]), mul2(pair(f.x, f.y), ri[hh])), x0, x1);
+              unpair(mul2(pair(s[4 * q + 2], s[4 * q + 3]), mul2(pair(f.z, f.w), ri[hh])), x2, x3);
+              p[2 * q] = pack_bf16(x0, x1);
+              p[2 * q + 1] = pack_bf16(x2, x3);
+            }
+            if (hh == 0) {
+              tmem_st16(SP + jb * 16, p);
             } else {
-              const float4* lj = reinterpret_cast<const float4*>(pr[hh].l + jb * 32);
-              const float4* dj = reinterpret_cast<const float4*>(pr[hh].d + jb * 32);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float4 f = lj[q], d = dj[q];
-                const float fl[4] = {f.x, f.y, f.z, f.w}, fd[4] = {d.x, d.y, d.z, d.w};
-                float x[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  x[e] = 4 * q + e <= l ? __uint_as_float(s[4 * q + e]) * (ex2_approx(li[hh] - fl[e]) * fd[e]) : 0.f;
-                p[hh][2 * q] = pack_bf16(x[0], x[1]);
-                p[hh][2 * q + 1] = pack_bf16(x[2], x[3]);
-              }
+              for (int e = 0; e < 16; ++e) held[jb * 16 + e] = p[e];
             }
           }
         }
-        tmem_st16(SP + jb * 16, p[0]);
-        if (HU > 1) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) held[jb * 16 + e] = p[HU - 1][e];
-        }
       }
-      if constexpr (HU > 1) {
+      {
+        // the row's own block, the last one of S that it needs
+        uint32_t s[32];
+        tmem_ld32(SP + w * 32, s);
+        tmem_wait_ld();
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
+        for (int hh = 0; hh < HU; ++hh) {
+          const float4* rj = reinterpret_cast<const float4*>(pr[hh].r + w * 32);
           uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) p[e] = held[jb * 16 + e];
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = rj[q];
+            const float fr[4] = {f.x, f.y, f.z, f.w};
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y = __uint_as_float(s[4 * q + e]) * ex2_approx(li[hh] - fr[e]);
+              x[e] = 4 * q + e <= l ? y : 0.f;
+            }
+            p[2 * q] = pack_bf16(x[0], x[1]);
+            p[2 * q + 1] = pack_bf16(x[2], x[3]);
+          }
+          tmem_st16(SP + hh * 64 + w * 16, p);
+        }
+      }
+#pragma unroll
+      for (int jb = 0; jb < 3; ++jb)
+        if (HU > 1 && jb < w) {
+          uint32_t p[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) p[e] = held[(jb * 16 + e) % (HU > 1 ? 48 : 1)];
           tmem_st16(SP + 64 + jb * 16, p);
         }
+      if (w < 3) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = 0u;
+        for (int jb = w + 1; jb < 4; ++jb)
+#pragma unroll
+          for (int hh = 0; hh < HU; ++hh) tmem_st16(SP + hh * 64 + jb * 16, p);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -534,7 +588,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         if (!ok) break;
         tc_fence_after();
         const float keep = prep[st * 2 + hh].keep;
-#pragma unroll
+#pragma unroll 1
         for (int cb = 0; cb < S / 32; ++cb) {
           uint32_t m[32];
           tmem_ld32(M + cb * 32, m);
@@ -594,6 +648,13 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   } else if (w < 12) {
     const int r = tid & 127, hh = r / P;
     const uint32_t XP = tmem + SS_XP + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    // where a lane's row of an 8 x 8 matrix lies, for the warp's first and second 16 channels
+    uint32_t at[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int channel = (w & 3) * 32 + q * 16 + ((l >> 3) & 1) * 8, token = (l >> 4) * 8 + (l & 7);
+      at[q] = (channel >> 6) * SS_BOX + token * 128 + ((((channel & 63) >> 3) ^ (l & 7)) << 4);
+    }
     int i = 0;  // places of x' used so far
     for (int c = 0; c < nc; ++c) {
       const int st = c & 1, len = tokens(c);
@@ -616,47 +677,50 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         if (!warp_wait(&ctl->zeroed, 0, ctl, err)) break;
       }
       if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
-      const float* weight = prep[st * 2 + hh].w;
-      const uint8_t* mine = x + (r >> 6) * SS_BOX + (r & 7) * 2;
-      const int piece16 = (r & 63) >> 3;
+      const float* weight = prep[st * 2 + hh].w + 2 * (l & 3);
+      const uint32_t from = smem_u32(x);
       bool ok = true;
-      for (int half = 0; half < (len > 64 ? 2 : 1); ++half) {
-        for (int t = 0; ok && t < terms; ++t)
-          if (i + t >= 4) ok = warp_wait(&ctl->xp_empty[(i + t) & 3], (((i + t) >> 2) - 1) & 1, ctl, err);
-        if (!ok) break;
-        tc_fence_after();
 #pragma unroll 1
-        for (int sub = 0; sub < 2; ++sub) {
-          const int t0 = half * 64 + sub * 32;
-          const uint8_t* from = mine + t0 * 128;
-          const float4* wt = reinterpret_cast<const float4*>(weight + t0);
-          float v[32];
+      for (int half = 0; half < (len > 64 ? 2 : 1); ++half) {
+        // Transposed on the way into registers: of 16 channels at a time, a lane has tokens 8 j + 2
+        // (l % 4) and the next of channels l / 4 and l / 4 + 8.
+        f2 v[2][16];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 f = wt[q];
-            const float ff[4] = {f.x, f.y, f.z, f.w};
+        for (int j = 0; j < 8; j += 2) {
+          const float2 w0 = *reinterpret_cast<const float2*>(weight + half * 64 + 8 * j);
+          const float2 w1 = *reinterpret_cast<const float2*>(weight + half * 64 + 8 * j + 8);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int t = 4 * q + e;
-              const uint32_t raw = *reinterpret_cast<const uint16_t*>(from + t * 128 + ((piece16 ^ (t & 7)) << 4));
-              v[t] = __uint_as_float(raw << 16) * ff[e];
-            }
+          for (int q = 0; q < 2; ++q) {
+            uint32_t raw[4];
+            ldmatrix_t(raw, from + (half * 64 + 8 * j) * 128 + at[q]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[q][2 * j + e] = mul2(pair(raw[e] << 16, raw[e] & 0xffff0000u), e < 2 ? pair(w0.x, w0.y) : pair(w1.x, w1.y));
           }
-          for (int t = 0; t < terms; ++t) {
+        }
+        // one bf16 addend after the other, each of what the ones before leave
+        const f2 minus = pair(-1.f, -1.f);
+#pragma unroll 1
+        for (int t = 0; t < terms; ++t, ++i) {
+          if (i >= 4 && !(ok = warp_wait(&ctl->xp_empty[i & 3], ((i >> 2) - 1) & 1, ctl, err))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
             uint32_t p[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              p[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-              v[2 * e] -= __uint_as_float(p[e] << 16);
-              v[2 * e + 1] -= __uint_as_float(p[e] & 0xffff0000u);
+              float x0, x1;
+              unpair(v[q][e], x0, x1);
+              p[e] = pack_bf16(x0, x1);
+              v[q][e] = fma2(pair(p[e] << 16, p[e] & 0xffff0000u), minus, v[q][e]);
             }
-            tmem_st16(XP + ((i + t) & 3) * 32 + sub * 16, p);
+            tmem_st_16x128(XP + (static_cast<uint32_t>(q * 16) << 16) + (i & 3) * 32, p);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          warp_arrive(&ctl->xp_full[i & 3]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        for (int t = 0; t < terms; ++t) warp_arrive(&ctl->xp_full[(i + t) & 3]);
-        i += terms;
+        if (!ok) break;
       }
       if (!ok) break;
       warp_arrive(&ctl->prep_empty[st]);
@@ -665,23 +729,46 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   } else {
     const int i = tid & 127;
     const uint32_t Y = tmem + SS_Y + (static_cast<uint32_t>((w & 3) * 32) << 16);
-    uint8_t* stage = smem + L::OUT + (w & 3) * 4096;
+    f2 skip[HU];
+#pragma unroll
+    for (int hh = 0; hh < HU; ++hh) {
+      const float s = !PRE && a.skip && hh < nh ? __ldg(a.skip + h0 + hh) : 0.f;
+      skip[hh] = pair(s, s);
+    }
     for (int c = 0; !PRE && c < nc; ++c) {
       const int st = c & 1, len = tokens(c);
       if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
+      if (!warp_wait(&ctl->x_full[st], (c >> 1) & 1, ctl, err)) break;
       if (!warp_wait(&ctl->yoff_full, c & 1, ctl, err)) break;
       tc_fence_after();
-      float e[HU];
+      // what the tokens of the chunk add comes on top of e^{l_i} M C_i + skip x_i
+      uint8_t* x = smem + L::X + 2 * st * SS_BOX + i * 128;
+      f2 e[HU];
 #pragma unroll
-      for (int hh = 0; hh < HU; ++hh) e[hh] = prep[st * 2 + hh].e[i];
-#pragma unroll
+      for (int hh = 0; hh < HU; ++hh) {
+        const float f = prep[st * 2 + hh].e[i];
+        e[hh] = pair(f, f);
+      }
+#pragma unroll 1
       for (int cb = 0; cb < 4; ++cb) {
         uint32_t y[32];
         tmem_ld32(Y + cb * 32, y);
         tmem_wait_ld();
-        const float f = e[cb * HU / 4];
+        const f2 f = HU > 1 && cb >= 2 ? e[HU - 1] : e[0], s = HU > 1 && cb >= 2 ? skip[HU - 1] : skip[0];
+        if (a.skip) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+          for (int q = 0; q < 4; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4*>(x + (cb >> 1) * SS_BOX + ((((cb & 1) * 4 + q) ^ (i & 7)) << 4));
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              unpair(fma2(pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]), f, mul2(pair(u[k] << 16, u[k] & 0xffff0000u), s)),
+                     y[8 * q + 2 * k], y[8 * q + 2 * k + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) unpair(mul2(pair(y[k], y[k + 1]), f), y[k], y[k + 1]);
+        }
         tmem_st32(Y + cb * 32, y);
       }
       tmem_wait_st();
@@ -690,55 +777,43 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       warp_arrive(&ctl->prep_empty[st]);
       if (!warp_wait(&ctl->y_full, c & 1, ctl, err)) break;
       tc_fence_after();
-      const uint8_t* x = smem + L::X + 2 * st * SS_BOX + i * 128;
+      uint32_t p[64];
+#pragma unroll
+      for (int cb = 0; cb < 4; ++cb) {
+        uint32_t y[32];
+        tmem_ld32(Y + cb * 32, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) p[cb * 16 + k] = pack_bf16(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+      }
+      tc_fence_before();
+      warp_arrive(&ctl->y_empty);
+      // The rows take the place of x's, which no product reads any more, and leave from there: 32
+      // at a time by TMA, or those of them that are the sequence's own.
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        *reinterpret_cast<uint4*>(x + (q >> 3) * SS_BOX + (((q & 7) ^ (i & 7)) << 4)) =
+            make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
       const int rows = len - (i - l);  // of the warp's 32, those there
-      __nv_bfloat16* dst = a.out + ((it.tok + c * SS_TOK + (i - l)) * a.H + h0) * P;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const int h = h0 + (HU > 1 ? (half < nh ? half : 0) : 0);
-        const float skip = a.skip ? __ldg(a.skip + h) : 0.f;
-        uint32_t y[64];
-        {
-          uint32_t y0[32], y1[32];
-          tmem_ld32(Y + half * 64, y0);
-          tmem_ld32(Y + half * 64 + 32, y1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            y[k] = y0[k];
-            y[32 + k] = y1[k];
-          }
-        }
-        if (half == 1) {
-          tc_fence_before();
-          warp_arrive(&ctl->y_empty);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          float f[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(y[8 * q + k]);
-          if (a.skip) {
-            const uint4 v = *reinterpret_cast<const uint4*>(x + half * SS_BOX + ((q ^ (i & 7)) << 4));
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              f[2 * k] = fmaf(skip, __uint_as_float(u[k] << 16), f[2 * k]);
-              f[2 * k + 1] = fmaf(skip, __uint_as_float(u[k] & 0xffff0000u), f[2 * k + 1]);
-            }
-          }
-          *reinterpret_cast<uint4*>(stage + l * 128 + ((q ^ (l & 7)) << 4)) =
-              make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        }
+      const int64_t tok = it.tok + c * SS_TOK + (i - l);
+      const int boxes = HU > 1 ? nh : 2;
+      const uint8_t* first = smem + L::X + 2 * st * SS_BOX + (i - l) * 128;
+      if (rows >= 32) {
+        fence_async();
         __syncwarp();
-        if (HU == 1 || half < nh) {
-#pragma unroll
-          for (int q = l >> 3; q < 32; q += 4)
-            if (q < rows)
-              *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(q) * a.H * P + half * 64 + (l & 7) * 8) =
-                  *reinterpret_cast<const uint4*>(stage + q * 128 + (((l & 7) ^ (q & 7)) << 4));
+        if (l == 0) {
+          for (int b = 0; b < boxes; ++b)
+            tma_store_box(&maps.out, h0 * P + b * 64, static_cast<int>(tok), first + b * SS_BOX);
+          tma_stores_read();
         }
+      } else {
         __syncwarp();
+        __nv_bfloat16* dst = a.out + (tok * a.H + h0) * P + (l & 7) * 8;
+        for (int b = 0; b < boxes; ++b)
+          for (int q = l >> 3; q < rows; q += 4)
+            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(q) * a.H * P + b * 64) =
+                *reinterpret_cast<const uint4*>(first + b * SS_BOX + q * 128 + (((l & 7) ^ (q & 7)) << 4));
+        fence_async();  // before x's next rows
       }
       warp_arrive(&ctl->x_empty[st]);
     }
@@ -787,6 +862,7 @@ cudaError_t launch(const SsmArgs& a, const Plan& plan, void* ws, int* err, cudaS
     cudaError_t e = make_matrix_map(&maps.x, a.x, a.T, static_cast<int64_t>(a.H) * P, a.x_stride, SS_TOK);
     if (e == cudaSuccess) e = make_matrix_map(&maps.b, a.B, a.T, static_cast<int64_t>(a.G) * S, a.b_stride, SS_TOK);
     if (e == cudaSuccess) e = make_matrix_map(&maps.c, a.C, a.T, static_cast<int64_t>(a.G) * S, a.c_stride, SS_TOK);
+    if (e == cudaSuccess) e = make_matrix_map(&maps.out, a.out, a.T, static_cast<int64_t>(a.H) * P, static_cast<int64_t>(a.H) * P, 32);
     if (e != cudaSuccess) return e;
   }
   (void)ws;
