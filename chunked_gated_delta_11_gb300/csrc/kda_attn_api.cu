@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "kda_attn.cuh"
+#include "kda_workspace.cuh"
 
 namespace kda {
 
@@ -81,35 +82,6 @@ size_t cached_need(const kda_cache* c, int64_t T, int H, int N, int64_t max_len,
   const size_t b = T % N == 0 ? cache_attn_workspace(T, H, c->Hk, N, false, max_len, accumulate) : 0;
   return a > b ? a : b;
 }
-
-// A workspace of the caller's, or one allocated on the stream for this call.
-class Workspace {
- public:
-  Workspace(void* given, size_t bytes, size_t need, cudaStream_t stream) : stream_(stream) {
-    if (need == 0) return;
-    if (given) {
-      ok_ = aligned(given, 16) && bytes >= need;
-      ptr_ = given;
-    } else if (cudaMallocAsync(&ptr_, need, stream) == cudaSuccess) {
-      own_ = true;
-    } else {
-      cudaGetLastError();
-      ok_ = false;
-    }
-  }
-  ~Workspace() {
-    if (own_) cudaFreeAsync(ptr_, stream_);
-  }
-  Workspace(const Workspace&) = delete;
-  Workspace& operator=(const Workspace&) = delete;
-  bool ok() const { return ok_; }
-  void* get() const { return ptr_; }
-
- private:
-  cudaStream_t stream_;
-  void* ptr_ = nullptr;
-  bool own_ = false, ok_ = true;
-};
 
 }  // namespace
 }  // namespace kda

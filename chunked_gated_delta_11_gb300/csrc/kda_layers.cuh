@@ -41,7 +41,8 @@ struct SsmArgs {
   int bf16_state;
 };
 cudaError_t launch_ssm_step(const SsmArgs& a, int P, int S, cudaStream_t stream);
-cudaError_t launch_ssm_fwd(const SsmArgs& a, int P, int S, int sm_count, void* ws, int* err, cudaStream_t stream);
+size_t ssm_workspace(int64_t T, int H, int G, int N, int P, int S);
+cudaError_t launch_ssm_fwd(const SsmArgs& a, int P, int S, void* ws, int* err, cudaStream_t stream);
 
 // log(1 + e^v), the step size of a token
 __device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }

@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "kda_layers.cuh"
+#include "kda_workspace.cuh"
 
 namespace kda {
 
@@ -40,18 +41,24 @@ bool good_states(const void* init, const void* fin, int64_t bytes) {
   return aligned(init, 16) && aligned(fin, 16) && (init == fin || !overlap(init, bytes, fin, bytes));
 }
 
-}  // namespace
+constexpr int64_t kSsmMaxT = (static_cast<int64_t>(1) << 31) - 128;  // a chunk's end is an int32 too
+
+kda_status check_ssm_sizes(int64_t T, int32_t H, int32_t G, int32_t N, int32_t P, int32_t S) {
+  if ((P != 64 && P != 128) || (S != 64 && S != 128)) return KDA_ERR_UNSUPPORTED;
+  if (H <= 0 || G <= 0 || H % G != 0 || H > 65535) return KDA_ERR_INVALID_ARG;
+  if (T < 0 || T >= (static_cast<int64_t>(1) << 31) || N <= 0) return KDA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(N) * H > 0x7fffffLL) return KDA_ERR_INVALID_ARG;
+  if (T > kMaxElems / (static_cast<int64_t>(H) * P)) return KDA_ERR_INVALID_ARG;
+  return KDA_OK;
+}
 
 kda_status check_ssm(const kda_ssm_options* o, const void* x, const void* dt, const float* A, const void* B,
                      const void* C, const void* init, const int32_t* cu, int64_t T, int32_t H, int32_t G, int32_t N,
                      int32_t P, int32_t S, void* out, void* fin, SsmArgs& a) {
   if (!o) return KDA_ERR_INVALID_ARG;
-  if ((P != 64 && P != 128) || (S != 64 && S != 128)) return KDA_ERR_UNSUPPORTED;
-  if (H <= 0 || G <= 0 || H % G != 0 || H > 65535) return KDA_ERR_INVALID_ARG;
-  kda_status s = check_packing(T, N, cu);
+  kda_status s = check_ssm_sizes(T, H, G, N, P, S);
+  if (s == KDA_OK) s = check_packing(T, N, cu);
   if (s != KDA_OK) return s;
-  if (static_cast<int64_t>(N) * H > 0x7fffffLL) return KDA_ERR_INVALID_ARG;
-  if (T > kMaxElems / (static_cast<int64_t>(H) * P)) return KDA_ERR_INVALID_ARG;
   if (o->state_dtype != KDA_STATE_F32 && o->state_dtype != KDA_STATE_BF16) return KDA_ERR_INVALID_ARG;
   a = SsmArgs{};
   a.x_stride = o->x_stride;
@@ -94,6 +101,7 @@ kda_status check_ssm(const kda_ssm_options* o, const void* x, const void* dt, co
   return KDA_OK;
 }
 
+}  // namespace
 }  // namespace kda
 
 using namespace kda;
@@ -153,8 +161,8 @@ extern "C" kda_status kda_ssm_step(const kda_ssm_options* opts, const void* x, c
 }
 
 extern "C" size_t kda_ssm_workspace_size(int64_t T_total, int32_t H, int32_t G, int32_t N, int32_t P, int32_t S) {
-  (void)T_total, (void)H, (void)G, (void)N, (void)P, (void)S;
-  return 0;
+  if (check_ssm_sizes(T_total, H, G, N, P, S) != KDA_OK || T_total >= kSsmMaxT) return 0;
+  return ssm_workspace(T_total, H, G, N, P, S);
 }
 
 extern "C" kda_status kda_ssm_fwd(const kda_ssm_options* opts, const void* x, const void* dt, const float* A,
@@ -165,12 +173,15 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_options* opts, const void* x, co
   SsmArgs a;
   kda_status s = check_ssm(opts, x, dt, A, B, C, initial_state, cu_seqlens, T_total, H, G, N, P, S, out, final_state, a);
   if (s != KDA_OK) return s;
-  if (T_total >= (static_cast<int64_t>(1) << 31) - 128) return KDA_ERR_INVALID_ARG;
-  (void)workspace, (void)workspace_bytes;
+  if (T_total >= kSsmMaxT) return KDA_ERR_INVALID_ARG;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t need = ssm_workspace(T_total, H, G, N, P, S);
+  if (workspace && (!aligned(workspace, 16) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   int sms = 0, *err = nullptr;
   if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;
-  return launch_ssm_fwd(a, P, S, sms, nullptr, err, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
-                                                                                                  : KDA_ERR_LAUNCH;
+  Workspace ws(workspace, workspace_bytes, need, st);
+  if (!ws.ok()) return KDA_ERR_WORKSPACE;
+  return launch_ssm_fwd(a, P, S, ws.get(), err, st) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 namespace {

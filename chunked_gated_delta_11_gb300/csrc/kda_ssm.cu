@@ -130,7 +130,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 // chunks add up in tensor memory.
 template <int P, int S, bool PRE>
 __global__ void __launch_bounds__(SS_THREADS, 1)
-ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, int terms, int* err) {
+ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, int terms, bool ranked, int* err) {
   using L = SsmSmem<S>;
   constexpr int HU = SS_TOK / P;  // heads of a unit
   constexpr int SB = L::SB;
@@ -176,12 +176,14 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     ctl->abort = 0;
     fence_mbar_init();
   }
+  // Sequence n owns the slots from floor(bos_n / piece) + n on, one for each of its pieces; whole
+  // ones come in the order of their lengths, the longest first.
+  const int whole = ranked ? seq_by_rank(a.cu, a.N, static_cast<int>(slot), reinterpret_cast<int*>(smem)) : 0;
   if (w == 16) {
-    // Sequence n owns the slots from floor(bos_n / piece) + n on, one for each of its pieces.
-    const int n = seq_of_slot(a.cu, a.T, a.N, static_cast<int>(piece), 1, slot);
+    const int n = ranked ? whole : seq_of_slot(a.cu, a.T, a.N, static_cast<int>(piece), 1, slot);
     int64_t bos, eos;
     seq_bounds(a.cu, a.T, a.N, n, bos, eos);
-    const int64_t k = slot - (bos / piece + n), first = k * piece;
+    const int64_t k = ranked ? 0 : slot - (bos / piece + n), first = k * piece;
     const bool there = k >= 0 && (k == 0 || first < eos - bos);  // (a malformed cu_seqlens can give less)
     const int64_t left = eos - bos - first;
     SsmItem it;
@@ -824,24 +826,54 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   if (w == 17) tmem_dealloc(tmem, 512);
 }
 
-int units_of(const SsmArgs& a, int P) {
-  const int per_group = a.H / a.G, heads = SS_TOK / P;
-  return a.G * ((per_group + heads - 1) / heads);
+int units_of(int H, int G, int P) {
+  const int per_group = H / G, heads = SS_TOK / P;
+  return G * ((per_group + heads - 1) / heads);
 }
 
 // How a call is cut: pieces of `piece` tokens (beyond T: sequences stay whole).
 struct Plan {
   int64_t piece, slots;
+  int units;
+  bool split;
+  size_t part_bytes, keep_bytes, state_bytes;  // of the workspace
+  size_t bytes() const { return split ? part_bytes + keep_bytes + state_bytes : 0; }
 };
 
-Plan plan_of(const SsmArgs& a, int P, int sm_count) {
-  (void)sm_count, (void)P;
-  const int64_t whole = (a.T / SS_TOK + 1) * SS_TOK;  // (T is below 2^31 - 128)
-  return {whole, a.N};
+// Sequences are cut where whole ones would leave SMs without work.  A piece's state from
+// zero takes about half of what the piece itself does, and each kernel a few chunks' time to
+// start and to end; the number of pieces is the one of least time under that count.
+Plan plan_of(int64_t T, int H, int G, int N, int P, int S) {
+  Plan p{};
+  p.units = units_of(H, G, P);
+  p.piece = (T / SS_TOK + 1) * SS_TOK;  // (T is below 2^31 - 128)
+  p.slots = N;
+  const int64_t ctas = static_cast<int64_t>(N) * p.units, chunks = (T / N + SS_TOK - 1) / SS_TOK;
+  if (ctas >= kSMs || chunks < 4) return p;
+  constexpr int64_t kEnds = 4;  // chunks' time, twice that of a kernel's start and end
+  int64_t best = 2 * chunks, k_best = 1;
+  for (int64_t k = 2; k <= 32 && 2 * k <= chunks; ++k) {
+    const int64_t each = (chunks + k - 1) / k;
+    const int64_t main = (ctas * k + kSMs - 1) / kSMs * (2 * each + kEnds);
+    const int64_t pre = (ctas * (k - 1) + kSMs - 1) / kSMs * (each + kEnds);
+    if (main + pre - kEnds < best) {
+      best = main + pre - kEnds;
+      k_best = k;
+    }
+  }
+  if (k_best == 1) return p;
+  p.split = true;
+  p.piece = (chunks + k_best - 1) / k_best * SS_TOK;
+  p.slots = T / p.piece + N;
+  const auto round = [](size_t b) { return (b + 255) & ~static_cast<size_t>(255); };
+  p.part_bytes = round(static_cast<size_t>(p.slots) * p.units * SS_TOK * S * 4);
+  p.keep_bytes = round(static_cast<size_t>(p.slots) * p.units * 8);
+  p.state_bytes = round(static_cast<size_t>(N) * H * P * S * 4);
+  return p;
 }
 
 template <int P, int S, bool PRE>
-cudaError_t launch_one(const SsmMaps& maps, const SsmArgs& a, const SsmParts& parts, const Plan& plan, int units, int* err,
+cudaError_t launch_one(const SsmMaps& maps, const SsmArgs& a, const SsmParts& parts, const Plan& plan, int* err,
                        cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
   auto* kernel = ssm_kernel<P, S, PRE>;
@@ -850,30 +882,48 @@ cudaError_t launch_one(const SsmMaps& maps, const SsmArgs& a, const SsmParts& pa
   // a state in fp32 takes all bits of its addends, one in bf16 two roundings' worth, and one
   // that only the outputs see one
   const int terms = !a.fin ? 1 : a.bf16_state ? 2 : 3;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(plan.slots * units)), dim3(SS_THREADS), SsmSmem<S>::BYTES, stream, maps,
-                    a, parts, plan.piece, units, terms, err);
+  const bool ranked = !plan.split && a.cu && a.N > 1 && a.N <= kOrderMaxN;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(plan.slots * plan.units)), dim3(SS_THREADS), SsmSmem<S>::BYTES, stream,
+                    maps, a, parts, plan.piece, plan.units, terms, ranked, err);
 }
 
 template <int P, int S>
 cudaError_t launch(const SsmArgs& a, const Plan& plan, void* ws, int* err, cudaStream_t stream) {
   SsmMaps maps{};
-  const int units = units_of(a, P);
   if (a.T > 0) {
-    cudaError_t e = make_matrix_map(&maps.x, a.x, a.T, static_cast<int64_t>(a.H) * P, a.x_stride, SS_TOK);
-    if (e == cudaSuccess) e = make_matrix_map(&maps.b, a.B, a.T, static_cast<int64_t>(a.G) * S, a.b_stride, SS_TOK);
-    if (e == cudaSuccess) e = make_matrix_map(&maps.c, a.C, a.T, static_cast<int64_t>(a.G) * S, a.c_stride, SS_TOK);
-    if (e == cudaSuccess) e = make_matrix_map(&maps.out, a.out, a.T, static_cast<int64_t>(a.H) * P, static_cast<int64_t>(a.H) * P, 32);
+    const int64_t row = static_cast<int64_t>(a.H) * P, wide = static_cast<int64_t>(a.G) * S;
+    cudaError_t e = make_matrix_map(&maps.x, a.x, a.T, row, a.x_stride, SS_TOK);
+    if (e == cudaSuccess) e = make_matrix_map(&maps.b, a.B, a.T, wide, a.b_stride, SS_TOK);
+    if (e == cudaSuccess) e = make_matrix_map(&maps.c, a.C, a.T, wide, a.c_stride, SS_TOK);
+    if (e == cudaSuccess) e = make_matrix_map(&maps.out, a.out, a.T, row, row, 32);
     if (e != cudaSuccess) return e;
   }
-  (void)ws;
   SsmParts parts{nullptr, nullptr, a.init};
-  return launch_one<P, S, false>(maps, a, parts, plan, units, err, stream);
+  if (plan.split) {
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    parts.m = reinterpret_cast<float*>(at);
+    parts.keep = reinterpret_cast<float*>(at + plan.part_bytes);
+    if (a.init && a.init == a.fin) {
+      // every piece reads the initial state, and the last may write it before the others have
+      void* copy = at + plan.part_bytes + plan.keep_bytes;
+      const size_t bytes = static_cast<size_t>(a.N) * a.H * P * S * (a.bf16_state ? 2 : 4);
+      const cudaError_t e = cudaMemcpyAsync(copy, a.init, bytes, cudaMemcpyDeviceToDevice, stream);
+      if (e != cudaSuccess) return e;
+      parts.init = copy;
+    }
+    const cudaError_t e = launch_one<P, S, true>(maps, a, parts, plan, err, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_one<P, S, false>(maps, a, parts, plan, err, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_ssm_fwd(const SsmArgs& a, int P, int S, int sm_count, void* ws, int* err, cudaStream_t stream) {
-  const Plan plan = plan_of(a, P, sm_count);
+size_t ssm_workspace(int64_t T, int H, int G, int N, int P, int S) { return plan_of(T, H, G, N, P, S).bytes(); }
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, int P, int S, void* ws, int* err, cudaStream_t stream) {
+  const Plan plan = plan_of(a.T, a.H, a.G, a.N, P, S);
+  if (plan.slots * plan.units > 0x7fffffffLL) return cudaErrorInvalidValue;
   if (P == 64) return S == 64 ? launch<64, 64>(a, plan, ws, err, stream) : launch<64, 128>(a, plan, ws, err, stream);
   return S == 64 ? launch<128, 64>(a, plan, ws, err, stream) : launch<128, 128>(a, plan, ws, err, stream);
 }
