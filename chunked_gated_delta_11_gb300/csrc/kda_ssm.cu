@@ -7,16 +7,18 @@
 //   M'  = e^{l_Q} M + sum_j (e^{l_Q - l_j} d_j x_j) B_j^T
 //
 // A CTA has 128 channels of one sequence (or of a piece of one): two heads of 64 that share
-// B and C, or one of 128.  20 warps:
+// B and C, or one of 128.  24 warps:
 //   warps 0-3    weights: S = C B^T (one thread a row) times e^{l_i - l_j} d_j, per head, in bf16
 //                over S in tensor memory
 //   warps 4-7    the state, a thread a channel: M in tensor memory (fp32), its bf16 copy for
 //                the products with C in shared memory, its decay
-//   warps 8-11   the weighted rows x' = e^{l_Q - l_j} d_j x_j, transposed (a thread a channel)
-//                into tensor memory, as the left operand of M' += x'^T B
-//   warps 12-15  outputs: e^{l_i} M C_i in tensor memory, then the finished rows
-//   warp 16      TMA;  warp 17  the products;  warps 18, 19  step sizes and decays
-// Tensor memory: S and P | Y | M | x' (four places of 64 tokens), 128 columns each.
+//   warps 8-15   the weighted rows x' = e^{l_Q - l_j} d_j x_j, transposed into tensor memory, as
+//                the left operand of M' += x'^T B: groups of 32 tokens, each four warps' every other
+//   warps 16-19  outputs: e^{l_i} M C_i + skip x_i in tensor memory, then the finished rows
+//   warp 20      TMA;  warp 21  the products;  warps 22, 23  step sizes and decays
+// Tensor memory: S and P | Y | M, 128 columns each, x' (two places of a group), 96, and the rest of P,
+// 32.  The loops are kept short (rolled, and one copy of what two products share): unrolled,
+// the roles' code outgrew the instruction caches (37 % of fetches missed, 9300 cycles a chunk).
 //
 // Roundings.  x' enters the product with B as the sum of `terms` bf16 numbers: three hold
 // all 24 bits, so that a state in fp32 is one.  P and the copy of M that the outputs see are
@@ -34,10 +36,12 @@ namespace {
 
 constexpr int SS_TOK = 128;              // tokens of a chunk, channels of a CTA
 constexpr int SS_BOX = SS_TOK * 128;     // bytes of 64 elements of 128 rows
-constexpr int SS_THREADS = 640;
-// five warpgroups of 96 registers a thread at launch: 144 + 88 + 2 x 96 + 56 = 5 x 96
-constexpr int SS_REGS_WEIGHTS = 144, SS_REGS_STATE = 88, SS_REGS_ISSUE = 56;
-constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384;  // columns
+constexpr int SS_THREADS = 768;
+// six warpgroups of 80 registers a thread at launch: 128 + 80 + 2 x 64 + 88 + 56 = 6 x 80
+constexpr int SS_REGS_WEIGHTS = 128, SS_REGS_ROWS = 64, SS_REGS_OUT = 88, SS_REGS_ISSUE = 56;
+constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384, SS_P1 = 480;  // columns
+constexpr int SS_GROUP = 32;             // tokens of a place of x'
+constexpr int SS_TERMS = 3;              // addends of x' at most, 16 columns each
 
 // Steps and decays of a chunk's tokens for one head, in units of log2.
 struct SsmPrep {
@@ -58,7 +62,7 @@ struct SsmItem {
 
 struct SsmCtl {
   uint64_t x_full[2], x_empty[2], b_full[2], b_empty[2], c_full, c_empty, prep_full[2], prep_empty[2];
-  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[4], xp_empty[4], zeroed, drained;
+  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[2], xp_empty[2], zeroed, drained;
   SsmItem item;
   uint32_t tmem;
   int abort;
@@ -97,15 +101,12 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t at) {
                : "memory");
 }
 
-// 16 lanes x 32 columns in the layout that transposed matrices have: r[2 j] and r[2 j + 1] are column
+// 16 lanes x 16 columns in the layout that transposed matrices have: r[2 j] and r[2 j + 1] are column
 // 4 j + l % 4 of lanes l / 4 and l / 4 + 8.
-__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // 32 rows of 64 channels from shared memory, and the wait until they have been read.
@@ -118,6 +119,22 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* map, int x, int
 __device__ __forceinline__ void tma_stores_read() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
+
+// Columns of the weights of 32 keys, block jb of head hh.  They go where S has been read, block
+// after block (its columns 32 jb..): the first head's to 16 jb, the second's last two
+// blocks to 64 and 80; its first two to columns of their own.
+__device__ __forceinline__ uint32_t weights_at(int hh, int jb) {
+  return hh == 0 ? SS_SP + 16 * jb : jb < 2 ? SS_P1 + 16 * jb : SS_SP + 32 + 16 * jb;
+}
+
+// v - h for a bf16 h.
+__device__ __forceinline__ float minus_bf16(float v, uint16_t h) {
+  float r;
+  asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(r) : "h"(h), "h"(static_cast<uint16_t>(0xbf80)), "f"(v));
+  return r;
+}
+
+__device__ __noinline__ float step_size(float v) { return softplus(v); }
 
 // One arrival a warp, after all its lanes.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -148,10 +165,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   const int nh = per_group - hu < HU ? per_group - hu : HU;  // heads that exist
 
   if (tid == 0) {
-    constexpr int users = PRE ? 4 : 16;
+    constexpr int users = PRE ? 8 : 20;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->x_full[i], 1);
-      mbar_init(&ctl->x_empty[i], PRE ? 4 : 5);
+      mbar_init(&ctl->x_empty[i], PRE ? 8 : 5);
       mbar_init(&ctl->b_full[i], 1);
       mbar_init(&ctl->b_empty[i], 1);
       mbar_init(&ctl->prep_full[i], HU);
@@ -167,7 +184,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     mbar_init(&ctl->y_empty, 4);
     mbar_init(&ctl->m_full, 1);
     mbar_init(&ctl->h_full, 4);
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->xp_full[i], 4);
       mbar_init(&ctl->xp_empty[i], 1);
     }
@@ -179,7 +196,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   // Sequence n owns the slots from floor(bos_n / piece) + n on, one for each of its pieces; whole
   // ones come in the order of their lengths, the longest first.
   const int whole = ranked ? seq_by_rank(a.cu, a.N, static_cast<int>(slot), reinterpret_cast<int*>(smem)) : 0;
-  if (w == 16) {
+  if (w == 20) {
     const int n = ranked ? whole : seq_of_slot(a.cu, a.T, a.N, static_cast<int>(piece), 1, slot);
     int64_t bos, eos;
     seq_bounds(a.cu, a.T, a.N, n, bos, eos);
@@ -195,7 +212,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     if (PRE && it.last) it.len = -1;
     if (l == 0) ctl->item = it;
   }
-  if (w == 17) {
+  if (w == 21) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
@@ -213,9 +230,9 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     return left < SS_TOK ? left : SS_TOK;
   };
 
-  if (w >= 16) {
+  if (w >= 20) {
     regs_give<SS_REGS_ISSUE>();
-    if (w == 16) {
+    if (w == 20) {
       if (l == 0) {
         bool ok = true;
         int c = 0, cs = 0;
@@ -258,7 +275,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         }
       }
       __syncwarp();
-    } else if (w == 17) {
+    } else if (w == 21) {
       if (elect_one()) {
         const uint32_t sb = smem_u32(smem);
         constexpr uint32_t id_s = make_idesc(1, SS_TOK, SS_TOK);
@@ -267,22 +284,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         const uint64_t rows_desc = make_sdesc(sb, 16, 1024, 2), cols_desc = make_sdesc(sb, SS_BOX, 1024, 2);
         const uint32_t hi = static_cast<uint32_t>(rows_desc >> 32);  // the same for both
         const uint32_t rows_lo = static_cast<uint32_t>(rows_desc), cols_lo = static_cast<uint32_t>(cols_desc);
-        constexpr uint32_t BX = SS_BOX >> 4, C0 = L::C >> 4, H0 = L::H >> 4;
-        // products over S channels of C with rows of B or of the state's copy
-        auto over_state = [&](uint32_t d, auto b_at, uint32_t b_lo) {
-          constexpr uint32_t b0 = b_at.value;
-          mma_ss_step<C0, b0>(d, rows_lo, b_lo, hi, id_s, 0);
-          mma_ss_step<C0 + 2, b0 + 2>(d, rows_lo, b_lo, hi, id_s, 1);
-          mma_ss_step<C0 + 4, b0 + 4>(d, rows_lo, b_lo, hi, id_s, 1);
-          mma_ss_step<C0 + 6, b0 + 6>(d, rows_lo, b_lo, hi, id_s, 1);
-          if constexpr (SB == 2) {
-            mma_ss_step<C0 + BX, b0 + BX>(d, rows_lo, b_lo, hi, id_s, 1);
-            mma_ss_step<C0 + BX + 2, b0 + BX + 2>(d, rows_lo, b_lo, hi, id_s, 1);
-            mma_ss_step<C0 + BX + 4, b0 + BX + 4>(d, rows_lo, b_lo, hi, id_s, 1);
-            mma_ss_step<C0 + BX + 6, b0 + BX + 6>(d, rows_lo, b_lo, hi, id_s, 1);
-          }
-        };
-        int i = 0;  // places of x' used so far
+        constexpr uint32_t BX = SS_BOX >> 4, C0 = L::C >> 4;
         bool ok = true;
         for (int c = 0; c < nc; ++c) {
           const uint32_t st = c & 1;
@@ -291,32 +293,49 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           ok = wait_for(&ctl->b_full[st], (c >> 1) & 1, ctl, err);
           if (!ok) break;
           if (!PRE) {
-            ok = wait_for(&ctl->c_full, c & 1, ctl, err);
-            if (!ok) break;
-            // the tensor core runs these in order: S may follow into the columns P was read from
-            over_state(tmem + SS_SP, std::integral_constant<uint32_t, 0>{}, rows_lo + b_stage);
-            tc_commit(&ctl->s_full);
-            ok = wait_for(&ctl->h_full, c & 1, ctl, err) && (c == 0 || wait_for(&ctl->y_empty, (c - 1) & 1, ctl, err));
-            if (!ok) break;
-            tc_fence_after();
-            over_state(tmem + SS_Y, std::integral_constant<uint32_t, H0>{}, rows_lo);
-            tc_commit(&ctl->yoff_full);
-            tc_commit(&ctl->c_empty);
-          }
-          for (int half = 0; half < (len > 64 ? 2 : 1); ++half) {
-            const uint32_t b_lo = cols_lo + b_stage + half * 512;
-            for (int t = 0; t < terms; ++t, ++i) {
-              ok = wait_for(&ctl->xp_full[i & 3], (i >> 2) & 1, ctl, err);
+            // C with the rows of B, then with those of the state's copy.  The tensor core runs what
+            // one lane issues in order: S may follow into the columns P was read from.
+#pragma unroll 1
+            for (int of_m = 0; of_m < 2; ++of_m) {
+              ok = wait_for(of_m ? &ctl->h_full : &ctl->c_full, c & 1, ctl, err);
+              if (ok && of_m && c > 0) ok = wait_for(&ctl->y_empty, (c - 1) & 1, ctl, err);
               if (!ok) break;
               tc_fence_after();
-              const uint32_t x = tmem + SS_XP + (i & 3) * 32;
-              mma_ts_step<0, 0>(tmem + SS_M, x, b_lo, hi, id_m, !PRE || i > 0);
-              mma_ts_step<8, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-              mma_ts_step<16, 256>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-              mma_ts_step<24, 384>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-              tc_commit(&ctl->xp_empty[i & 3]);
+              const uint32_t d = tmem + (of_m ? SS_Y : SS_SP), b_lo = rows_lo + (of_m ? L::H >> 4 : b_stage);
+              mma_ss_step<C0, 0>(d, rows_lo, b_lo, hi, id_s, 0);
+              mma_ss_step<C0 + 2, 2>(d, rows_lo, b_lo, hi, id_s, 1);
+              mma_ss_step<C0 + 4, 4>(d, rows_lo, b_lo, hi, id_s, 1);
+              mma_ss_step<C0 + 6, 6>(d, rows_lo, b_lo, hi, id_s, 1);
+              if constexpr (SB == 2) {
+                mma_ss_step<C0 + BX, BX>(d, rows_lo, b_lo, hi, id_s, 1);
+                mma_ss_step<C0 + BX + 2, BX + 2>(d, rows_lo, b_lo, hi, id_s, 1);
+                mma_ss_step<C0 + BX + 4, BX + 4>(d, rows_lo, b_lo, hi, id_s, 1);
+                mma_ss_step<C0 + BX + 6, BX + 6>(d, rows_lo, b_lo, hi, id_s, 1);
+              }
+              tc_commit(of_m ? &ctl->yoff_full : &ctl->s_full);
             }
             if (!ok) break;
+            tc_commit(&ctl->c_empty);
+          }
+          const int groups = (len + SS_GROUP - 1) / SS_GROUP;
+          for (int q = 0; q < groups; ++q) {
+            // a whole chunk uses each place twice
+            ok = wait_for(&ctl->xp_full[q & 1], (q >> 1) & 1, ctl, err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t x = tmem + SS_XP + (q & 1) * 48, b_lo = cols_lo + b_stage + q * 256;
+            const uint32_t add = !PRE || c > 0 || q > 0;
+            mma_ts_step<0, 0>(tmem + SS_M, x, b_lo, hi, id_m, add);
+            mma_ts_step<8, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            if (terms > 1) {
+              mma_ts_step<16, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+              mma_ts_step<24, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            }
+            if (terms > 2) {
+              mma_ts_step<32, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+              mma_ts_step<40, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            }
+            tc_commit(&ctl->xp_empty[q & 1]);
           }
           if (!ok) break;
           tc_commit(&ctl->b_empty[st]);
@@ -326,18 +345,18 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             if (!ok) break;
             tc_fence_after();
             const int steps = (len + 15) / 16;
-#pragma unroll
-            for (int hh = 0; hh < HU; ++hh) {
-              if (hh >= nh) break;
-              const uint32_t d = tmem + SS_Y + hh * 64, p = tmem + SS_SP + hh * 64, x_lo = cols_lo + x_stage + hh * BX;
+#pragma unroll 1
+            for (int hh = 0; hh < nh; ++hh) {
+              const uint32_t d = tmem + SS_Y + hh * 64, p = tmem + weights_at(hh, 0), p2 = tmem + weights_at(hh, 2);
+              const uint32_t x_lo = cols_lo + x_stage + hh * BX;
               mma_ts_step<0, 0>(d, p, x_lo, hi, id_y, 1);
               if (steps > 1) mma_ts_step<8, 128>(d, p, x_lo, hi, id_y, 1);
               if (steps > 2) mma_ts_step<16, 256>(d, p, x_lo, hi, id_y, 1);
               if (steps > 3) mma_ts_step<24, 384>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 4) mma_ts_step<32, 512>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 5) mma_ts_step<40, 640>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 6) mma_ts_step<48, 768>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 7) mma_ts_step<56, 896>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 4) mma_ts_step<0, 512>(d, p2, x_lo, hi, id_y, 1);
+              if (steps > 5) mma_ts_step<8, 640>(d, p2, x_lo, hi, id_y, 1);
+              if (steps > 6) mma_ts_step<16, 768>(d, p2, x_lo, hi, id_y, 1);
+              if (steps > 7) mma_ts_step<24, 896>(d, p2, x_lo, hi, id_y, 1);
             }
             tc_commit(&ctl->y_full);
             tc_commit(&ctl->x_empty[st]);
@@ -350,7 +369,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       __syncwarp();
     } else {
       // Step sizes and decays of one head, four tokens to a lane.
-      const int hh = w - 18;
+      const int hh = w - 22;
       if (hh < HU) {
         const bool there = hh < nh;
         const int h = h0 + (there ? hh : 0);
@@ -374,7 +393,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool in = there && 4 * l + e < len;
-            d[e] = in ? softplus(__bfloat162float(raw[e]) + bias) : 0.f;
+            d[e] = in ? step_size(__bfloat162float(raw[e]) + bias) : 0.f;
             s[e] = in ? rate * d[e] : 0.f;
           }
           // sums up to a token from the chunk's start, and behind it to the chunk's end
@@ -405,7 +424,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             ll[e] = start + pre[e];
-            ww[e] = exp2f(suf[e] + end + tail) * d[e];
+            ww[e] = ex2_approx(suf[e] + end + tail) * d[e];
             ee[e] = ex2_approx(ll[e]);
           }
           *reinterpret_cast<float4*>(o.w + 4 * l) = make_float4(ww[0], ww[1], ww[2], ww[3]);
@@ -424,10 +443,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
               }
           }
           if (PRE) tail += all;
-          if (l == 0) o.keep = exp2f(PRE ? tail : all);
+          if (l == 0) o.keep = ex2_approx(PRE ? tail : all);
           warp_arrive(&ctl->prep_full[st]);
         }
-        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = exp2f(tail);
+        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = ex2_approx(tail);
       }
       __syncwarp();
     }
@@ -441,85 +460,68 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (!warp_wait(&ctl->s_full, c & 1, ctl, err)) break;
       tc_fence_after();
       const SsmPrep* pr = prep + st * 2;
-      float li[HU];
+      uint32_t s[32];
+      // Blocks of 32 columns before the row's own: e^{l_i - l_b} (e^{l_b - l_j} d_j), two factors
+      // that stay below 1.
       f2 ri[HU];
 #pragma unroll
       for (int hh = 0; hh < HU; ++hh) {
-        li[hh] = pr[hh].l[i];
-        const float r = w > 0 ? ex2_approx(li[hh] - pr[hh].l[w * 32 - 1]) : 0.f;
+        const float r = w > 0 ? ex2_approx(pr[hh].l[i] - pr[hh].l[w * 32 - 1]) : 0.f;
         ri[hh] = pair(r, r);
       }
-      // Blocks of 32 columns before the row's own: e^{l_i - l_b} (e^{l_b - l_j} d_j), two factors
-      // that stay below 1.  The second head's weights are held back where S is still to be read.
-      uint32_t held[HU > 1 ? 48 : 1];
-#pragma unroll
-      for (int jb = 0; jb < 3; ++jb) {
-        if (jb < w) {
-          uint32_t s[32];
-          tmem_ld32(SP + jb * 32, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int hh = 0; hh < HU; ++hh) {
-            const float4* cf = reinterpret_cast<const float4*>(pr[hh].cf + 16 * w * (w - 1) + jb * 32);
-            uint32_t p[16];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 f = cf[q];
-              float x0, x1, x2, x3;
-              unpair(mul2(pair(s[4 * q], s[4 * q + 1]), mul2(pair(f.x, f.y), ri[hh])), x0, x1);
-              unpair(mul2(pair(s[4 * q + 2], s[4 * q + 3]), mul2(pair(f.z, f.w), ri[hh])), x2, x3);
-              p[2 * q] = pack_bf16(x0, x1);
-              p[2 * q + 1] = pack_bf16(x2, x3);
-            }
-            if (hh == 0) {
-              tmem_st16(SP + jb * 16, p);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) held[jb * 16 + e] = p[e];
-            }
-          }
-        }
-      }
-      {
-        // the row's own block, the last one of S that it needs
-        uint32_t s[32];
-        tmem_ld32(SP + w * 32, s);
+#pragma unroll 1
+      for (int jb = 0; jb < w; ++jb) {
+        tmem_ld32(SP + jb * 32, s);
         tmem_wait_ld();
 #pragma unroll
         for (int hh = 0; hh < HU; ++hh) {
-          const float4* rj = reinterpret_cast<const float4*>(pr[hh].r + w * 32);
+          const float4* cf = reinterpret_cast<const float4*>(pr[hh].cf + 16 * w * (w - 1) + jb * 32);
           uint32_t p[16];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const float4 f = rj[q];
-            const float fr[4] = {f.x, f.y, f.z, f.w};
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float y = __uint_as_float(s[4 * q + e]) * ex2_approx(li[hh] - fr[e]);
-              x[e] = 4 * q + e <= l ? y : 0.f;
-            }
-            p[2 * q] = pack_bf16(x[0], x[1]);
-            p[2 * q + 1] = pack_bf16(x[2], x[3]);
+            const float4 f = cf[q];
+            float x0, x1, x2, x3;
+            unpair(mul2(pair(s[4 * q], s[4 * q + 1]), mul2(pair(f.x, f.y), ri[hh])), x0, x1);
+            unpair(mul2(pair(s[4 * q + 2], s[4 * q + 3]), mul2(pair(f.z, f.w), ri[hh])), x2, x3);
+            p[2 * q] = pack_bf16(x0, x1);
+            p[2 * q + 1] = pack_bf16(x2, x3);
           }
-          tmem_st16(SP + hh * 64 + w * 16, p);
+          tmem_st16(SP + weights_at(hh, jb), p);
         }
       }
-#pragma unroll
-      for (int jb = 0; jb < 3; ++jb)
-        if (HU > 1 && jb < w) {
-          uint32_t p[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) p[e] = held[(jb * 16 + e) % (HU > 1 ? 48 : 1)];
-          tmem_st16(SP + 64 + jb * 16, p);
-        }
-      if (w < 3) {
+      // its own block, the last one of S that it needs
+      tmem_ld32(SP + w * 32, s);
+      tmem_wait_ld();
+#pragma unroll 1
+      for (int hh = 0; hh < HU; ++hh) {
+        const float li = pr[hh].l[i];
+        const float4* rj = reinterpret_cast<const float4*>(pr[hh].r + w * 32);
         uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = 0u;
-        for (int jb = w + 1; jb < 4; ++jb)
+        for (int q = 0; q < 8; ++q) {
+          const float4 f = rj[q];
+          const float fr[4] = {f.x, f.y, f.z, f.w};
+          float x[4];
 #pragma unroll
-          for (int hh = 0; hh < HU; ++hh) tmem_st16(SP + hh * 64 + jb * 16, p);
+          for (int e = 0; e < 4; ++e) {
+            const float y = __uint_as_float(s[4 * q + e]) * ex2_approx(li - fr[e]);
+            x[e] = 4 * q + e <= l ? y : 0.f;
+          }
+          p[2 * q] = pack_bf16(x[0], x[1]);
+          p[2 * q + 1] = pack_bf16(x[2], x[3]);
+        }
+        tmem_st16(SP + weights_at(hh, w), p);
+      }
+      // and none behind it
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = 0u;
+#pragma unroll 1
+      for (int jb = w + 1; jb < 4; ++jb) {
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[e] = s[e];
+#pragma unroll
+        for (int hh = 0; hh < HU; ++hh) tmem_st16(SP + weights_at(hh, jb), p);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -527,7 +529,6 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       warp_arrive(&ctl->prep_empty[st]);
     }
   } else if (w < 8) {
-    regs_give<SS_REGS_STATE>();
     const int r = tid & 127, hh = r / P;  // channel of the unit, its head
     const bool there = hh < nh;
     const uint32_t M = tmem + SS_M + (static_cast<uint32_t>((w & 3) * 32) << 16);
@@ -605,7 +606,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             *reinterpret_cast<uint4*>(dst + ((((cb & 1) * 4 + q) ^ (r & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) m[e] = __float_as_uint(__uint_as_float(m[e]) * keep);
+          for (int e = 0; e < 32; e += 2) unpair(mul2(pair(m[e], m[e + 1]), pair(keep, keep)), m[e], m[e + 1]);
           tmem_st32(M + cb * 32, m);
         }
         tmem_wait_st();
@@ -647,88 +648,95 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         }
       }
     }
-  } else if (w < 12) {
+  } else if (w < 16) {
+    regs_give<SS_REGS_ROWS>();
+    const int place = (w - 8) >> 2, wq = w & 3;
     const int r = tid & 127, hh = r / P;
-    const uint32_t XP = tmem + SS_XP + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    const uint32_t XP = tmem + SS_XP + place * 48 + (static_cast<uint32_t>(wq * 32) << 16);
     // where a lane's row of an 8 x 8 matrix lies, for the warp's first and second 16 channels
     uint32_t at[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int channel = (w & 3) * 32 + q * 16 + ((l >> 3) & 1) * 8, token = (l >> 4) * 8 + (l & 7);
+      const int channel = wq * 32 + q * 16 + ((l >> 3) & 1) * 8, token = (l >> 4) * 8 + (l & 7);
       at[q] = (channel >> 6) * SS_BOX + token * 128 + ((((channel & 63) >> 3) ^ (l & 7)) << 4);
     }
-    int i = 0;  // places of x' used so far
+    int used = 0;  // groups so far
     for (int c = 0; c < nc; ++c) {
       const int st = c & 1, len = tokens(c);
       if (!warp_wait(&ctl->x_full[st], (c >> 1) & 1, ctl, err)) break;
       uint8_t* x = smem + L::X + 2 * st * SS_BOX;
       if (len < SS_TOK) {
         // rows behind the sequence's end (another's, whatever they hold) take no part in a product
-        if (!warp_wait(&ctl->b_full[st], (c >> 1) & 1, ctl, err)) break;
-        if (r >= len) {
+        if (place == 0) {
+          if (!warp_wait(&ctl->b_full[st], (c >> 1) & 1, ctl, err)) break;
+          if (r >= len) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            *reinterpret_cast<uint4*>(x + (e >> 3) * SS_BOX + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-          uint8_t* b = smem + L::B + SB * st * SS_BOX;
+            for (int e = 0; e < 16; ++e)
+              *reinterpret_cast<uint4*>(x + (e >> 3) * SS_BOX + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            uint8_t* b = smem + L::B + SB * st * SS_BOX;
 #pragma unroll
-          for (int e = 0; e < 8 * SB; ++e)
-            *reinterpret_cast<uint4*>(b + (e >> 3) * SS_BOX + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8 * SB; ++e)
+              *reinterpret_cast<uint4*>(b + (e >> 3) * SS_BOX + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
+          warp_arrive(&ctl->zeroed);  // one chunk of a piece at most
         }
-        fence_async();
-        warp_arrive(&ctl->zeroed);  // one chunk of a piece at most
         if (!warp_wait(&ctl->zeroed, 0, ctl, err)) break;
       }
       if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
       const float* weight = prep[st * 2 + hh].w + 2 * (l & 3);
       const uint32_t from = smem_u32(x);
+      const int groups = (len + SS_GROUP - 1) / SS_GROUP;
       bool ok = true;
 #pragma unroll 1
-      for (int half = 0; half < (len > 64 ? 2 : 1); ++half) {
+      for (int q = place; q < groups; q += 2, ++used) {
         // Transposed on the way into registers: of 16 channels at a time, a lane has tokens 8 j + 2
         // (l % 4) and the next of channels l / 4 and l / 4 + 8.
-        f2 v[2][16];
+        uint32_t raw[4][4];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float2 w0 = *reinterpret_cast<const float2*>(weight + half * 64 + 8 * j);
-          const float2 w1 = *reinterpret_cast<const float2*>(weight + half * 64 + 8 * j + 8);
+        for (int k = 0; k < 4; ++k) ldmatrix_t(raw[k], from + (q * SS_GROUP + (k >> 1) * 16) * 128 + at[k & 1]);
+        float v[2][16];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t raw[4];
-            ldmatrix_t(raw, from + (half * 64 + 8 * j) * 128 + at[q]);
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(weight + q * SS_GROUP + 8 * j);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[q][2 * j + e] = mul2(pair(raw[e] << 16, raw[e] & 0xffff0000u), e < 2 ? pair(w0.x, w0.y) : pair(w1.x, w1.y));
-          }
-        }
-        // one bf16 addend after the other, each of what the ones before leave
-        const f2 minus = pair(-1.f, -1.f);
-#pragma unroll 1
-        for (int t = 0; t < terms; ++t, ++i) {
-          if (i >= 4 && !(ok = warp_wait(&ctl->xp_empty[i & 3], ((i >> 2) - 1) & 1, ctl, err))) break;
-          tc_fence_after();
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x0, x1;
-              unpair(v[q][e], x0, x1);
-              p[e] = pack_bf16(x0, x1);
-              v[q][e] = fma2(pair(p[e] << 16, p[e] & 0xffff0000u), minus, v[q][e]);
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t u = raw[2 * (j >> 1) + k][2 * (j & 1) + e];
+              unpair(mul2(pair(u << 16, u & 0xffff0000u), pair(f.x, f.y)), v[k][4 * j + 2 * e], v[k][4 * j + 2 * e + 1]);
             }
-            tmem_st_16x128(XP + (static_cast<uint32_t>(q * 16) << 16) + (i & 3) * 32, p);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          warp_arrive(&ctl->xp_full[i & 3]);
         }
-        if (!ok) break;
+        if (used > 0 && !(ok = warp_wait(&ctl->xp_empty[place], (used - 1) & 1, ctl, err))) break;
+        tc_fence_after();
+        // one bf16 addend after the other, each of what the ones before leave: three hold all 24 bits
+#pragma unroll
+        for (int t = 0; t < SS_TERMS; ++t) {
+          if (t >= terms) break;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              p[e] = pack_bf16(v[k][2 * e], v[k][2 * e + 1]);
+              if (t + 1 < SS_TERMS) {
+                v[k][2 * e] = minus_bf16(v[k][2 * e], static_cast<uint16_t>(p[e]));
+                v[k][2 * e + 1] = minus_bf16(v[k][2 * e + 1], static_cast<uint16_t>(p[e] >> 16));
+              }
+            }
+            tmem_st_16x128(XP + t * 16 + (static_cast<uint32_t>(k * 16) << 16), p);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(&ctl->xp_full[place]);
       }
       if (!ok) break;
       warp_arrive(&ctl->prep_empty[st]);
       if (PRE) warp_arrive(&ctl->x_empty[st]);
     }
   } else {
+    regs_take<SS_REGS_OUT>();
     const int i = tid & 127;
     const uint32_t Y = tmem + SS_Y + (static_cast<uint32_t>((w & 3) * 32) << 16);
     f2 skip[HU];
@@ -779,23 +787,27 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       warp_arrive(&ctl->prep_empty[st]);
       if (!warp_wait(&ctl->y_full, c & 1, ctl, err)) break;
       tc_fence_after();
-      uint32_t p[64];
-#pragma unroll
+      // The rows take the place of x's, which no product reads any more, and leave from there: 32
+      // at a time by TMA, or those of them that are the sequence's own.
+#pragma unroll 1
       for (int cb = 0; cb < 4; ++cb) {
         uint32_t y[32];
         tmem_ld32(Y + cb * 32, y);
         tmem_wait_ld();
+        if (cb == 3) {
+          tc_fence_before();
+          warp_arrive(&ctl->y_empty);
+        }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) p[cb * 16 + k] = pack_bf16(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1]));
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            p[k] = pack_bf16(__uint_as_float(y[8 * q + 2 * k]), __uint_as_float(y[8 * q + 2 * k + 1]));
+          *reinterpret_cast<uint4*>(x + (cb >> 1) * SS_BOX + ((((cb & 1) * 4 + q) ^ (i & 7)) << 4)) =
+              make_uint4(p[0], p[1], p[2], p[3]);
+        }
       }
-      tc_fence_before();
-      warp_arrive(&ctl->y_empty);
-      // The rows take the place of x's, which no product reads any more, and leave from there: 32
-      // at a time by TMA, or those of them that are the sequence's own.
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        *reinterpret_cast<uint4*>(x + (q >> 3) * SS_BOX + (((q & 7) ^ (i & 7)) << 4)) =
-            make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
       const int rows = len - (i - l);  // of the warp's 32, those there
       const int64_t tok = it.tok + c * SS_TOK + (i - l);
       const int boxes = HU > 1 ? nh : 2;
@@ -823,7 +835,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (w == 17) tmem_dealloc(tmem, 512);
+  if (w == 21) tmem_dealloc(tmem, 512);
 }
 
 int units_of(int H, int G, int P) {
