@@ -116,6 +116,11 @@ __device__ __forceinline__ void tma_store_box(const CUtensorMap* map, int x, int
                "r"(x), "r"(t), "r"(smem_u32(src))
                : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_box(const CUtensorMap* map, int x, int t) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(t)
+               : "memory");
+}
 __device__ __forceinline__ void tma_stores_read() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
@@ -238,20 +243,25 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         int c = 0, cs = 0;
         for (; ok && c < nc; ++c) {
           const int st = c & 1, row = static_cast<int>(it.tok + chunk(c) * SS_TOK);
-          if (c >= 2) ok = wait_for(&ctl->x_empty[st], ((c >> 1) - 1) & 1, ctl, err);
-          if (!ok) break;
           const int boxes = P == 64 ? nh : 2;
-          mbar_arrive_expect_tx(&ctl->x_full[st], boxes * SS_BOX);
-          for (int b = 0; b < boxes; ++b)
-            tma_box2(smem + L::X + (2 * st + b) * SS_BOX, &maps.x, h0 * P + b * 64, row, &ctl->x_full[st]);
+          // in the order in which their places become free
           if (c >= 2) ok = wait_for(&ctl->b_empty[st], ((c >> 1) - 1) & 1, ctl, err);
-          if (!ok) {
-            mbar_wait(&ctl->x_full[st], (c >> 1) & 1);
-            break;
-          }
+          if (!ok) break;
           mbar_arrive_expect_tx(&ctl->b_full[st], SB * SS_BOX);
           for (int b = 0; b < SB; ++b)
             tma_box2(smem + L::B + (SB * st + b) * SS_BOX, &maps.b, g * S + b * 64, row, &ctl->b_full[st]);
+          if (c + 1 < nc) {  // the next rows come to L2 meanwhile
+            const int next = static_cast<int>(it.tok + chunk(c + 1) * SS_TOK);
+            for (int b = 0; b < boxes; ++b) tma_prefetch_box(&maps.x, h0 * P + b * 64, next);
+          }
+          if (c >= 2) ok = wait_for(&ctl->x_empty[st], ((c >> 1) - 1) & 1, ctl, err);
+          if (!ok) {
+            mbar_wait(&ctl->b_full[st], (c >> 1) & 1);
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl->x_full[st], boxes * SS_BOX);
+          for (int b = 0; b < boxes; ++b)
+            tma_box2(smem + L::X + (2 * st + b) * SS_BOX, &maps.x, h0 * P + b * 64, row, &ctl->x_full[st]);
           if (!PRE) {
             if (c >= 1) ok = wait_for(&ctl->c_empty, (c - 1) & 1, ctl, err);
             if (!ok) {
