@@ -109,6 +109,16 @@ __device__ __forceinline__ void tmem_st_16x128(uint32_t taddr, const uint32_t (&
                : "memory");
 }
 
+// 16 lanes x 32 columns of 32 bits: r[4 j] and r[4 j + 1] are columns 8 j + 2 (l % 4) and the next of lane l / 4,
+// r[4 j + 2] and r[4 j + 3] those of lane l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // 32 rows of 64 channels from shared memory, and the wait until they have been read.
 __device__ __forceinline__ void tma_store_box(const CUtensorMap* map, int x, int t, const void* src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
@@ -470,68 +480,80 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (!warp_wait(&ctl->s_full, c & 1, ctl, err)) break;
       tc_fence_after();
       const SsmPrep* pr = prep + st * 2;
-      uint32_t s[32];
+      // A lane has columns 8 j + 2 (l % 4) and the next of rows l / 4, + 8, + 16 and + 24: two factors of
+      // 8 columns to load, not eight.
+      uint32_t s[2][16];
+      auto load = [&](int jb) {
+        tmem_ld_16x256(SP + jb * 32, s[0]);
+        tmem_ld_16x256(SP + jb * 32 + (16u << 16), s[1]);
+        tmem_wait_ld();
+      };
+      const int row = w * 32 + (l >> 2), col = 2 * (l & 3);
       // Blocks of 32 columns before the row's own: e^{l_i - l_b} (e^{l_b - l_j} d_j), two factors
       // that stay below 1.
-      f2 ri[HU];
+      float ri[HU][4];
 #pragma unroll
-      for (int hh = 0; hh < HU; ++hh) {
-        const float r = w > 0 ? ex2_approx(pr[hh].l[i] - pr[hh].l[w * 32 - 1]) : 0.f;
-        ri[hh] = pair(r, r);
-      }
+      for (int hh = 0; hh < HU; ++hh)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ri[hh][k] = w > 0 ? ex2_approx(pr[hh].l[row + 8 * k] - pr[hh].l[w * 32 - 1]) : 0.f;
 #pragma unroll 1
       for (int jb = 0; jb < w; ++jb) {
-        tmem_ld32(SP + jb * 32, s);
-        tmem_wait_ld();
+        load(jb);
 #pragma unroll
         for (int hh = 0; hh < HU; ++hh) {
-          const float4* cf = reinterpret_cast<const float4*>(pr[hh].cf + 16 * w * (w - 1) + jb * 32);
-          uint32_t p[16];
+          const float* cf = pr[hh].cf + 16 * w * (w - 1) + jb * 32 + col;
+          uint32_t p[2][8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 f = cf[q];
-            float x0, x1, x2, x3;
-            unpair(mul2(pair(s[4 * q], s[4 * q + 1]), mul2(pair(f.x, f.y), ri[hh])), x0, x1);
-            unpair(mul2(pair(s[4 * q + 2], s[4 * q + 3]), mul2(pair(f.z, f.w), ri[hh])), x2, x3);
-            p[2 * q] = pack_bf16(x0, x1);
-            p[2 * q + 1] = pack_bf16(x2, x3);
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = *reinterpret_cast<const float2*>(cf + 8 * j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x0, x1;
+              unpair(mul2(pair(s[k >> 1][4 * j + 2 * (k & 1)], s[k >> 1][4 * j + 2 * (k & 1) + 1]),
+                          mul2(pair(f.x, f.y), pair(ri[hh][k], ri[hh][k]))),
+                     x0, x1);
+              p[k >> 1][2 * j + (k & 1)] = pack_bf16(x0, x1);
+            }
           }
-          tmem_st16(SP + weights_at(hh, jb), p);
+          tmem_st_16x128(SP + weights_at(hh, jb), p[0]);
+          tmem_st_16x128(SP + weights_at(hh, jb) + (16u << 16), p[1]);
         }
       }
       // its own block, the last one of S that it needs
-      tmem_ld32(SP + w * 32, s);
-      tmem_wait_ld();
+      load(w);
+      const int ahead = (l >> 2) - col;  // the lane's first row less its first column
 #pragma unroll 1
       for (int hh = 0; hh < HU; ++hh) {
-        const float li = pr[hh].l[i];
-        const float4* rj = reinterpret_cast<const float4*>(pr[hh].r + w * 32);
-        uint32_t p[16];
+        float li[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 f = rj[q];
-          const float fr[4] = {f.x, f.y, f.z, f.w};
-          float x[4];
+        for (int k = 0; k < 4; ++k) li[k] = pr[hh].l[row + 8 * k];
+        const float* rj = pr[hh].r + w * 32 + col;
+        uint32_t p[2][8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float y = __uint_as_float(s[4 * q + e]) * ex2_approx(li - fr[e]);
-            x[e] = 4 * q + e <= l ? y : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = *reinterpret_cast<const float2*>(rj + 8 * j);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t word = 0u;
+            if (j <= k) {  // (others are behind the diagonal in every lane)
+              const float x0 = __uint_as_float(s[k >> 1][4 * j + 2 * (k & 1)]) * ex2_approx(li[k] - f.x);
+              const float x1 = __uint_as_float(s[k >> 1][4 * j + 2 * (k & 1) + 1]) * ex2_approx(li[k] - f.y);
+              word = pack_bf16(8 * (j - k) <= ahead ? x0 : 0.f, 8 * (j - k) + 1 <= ahead ? x1 : 0.f);
+            }
+            p[k >> 1][2 * j + (k & 1)] = word;
           }
-          p[2 * q] = pack_bf16(x[0], x[1]);
-          p[2 * q + 1] = pack_bf16(x[2], x[3]);
         }
-        tmem_st16(SP + weights_at(hh, w), p);
+        tmem_st_16x128(SP + weights_at(hh, w), p[0]);
+        tmem_st_16x128(SP + weights_at(hh, w) + (16u << 16), p[1]);
       }
       // and none behind it
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = 0u;
 #pragma unroll 1
       for (int jb = w + 1; jb < 4; ++jb) {
-        uint32_t p[16];
+        uint32_t none[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) p[e] = s[e];
+        for (int e = 0; e < 16; ++e) none[e] = 0u;
 #pragma unroll
-        for (int hh = 0; hh < HU; ++hh) tmem_st16(SP + weights_at(hh, jb), p);
+        for (int hh = 0; hh < HU; ++hh) tmem_st16(SP + weights_at(hh, jb), none);
       }
       tmem_wait_st();
       tc_fence_before();
