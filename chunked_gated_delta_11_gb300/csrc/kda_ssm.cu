@@ -62,7 +62,7 @@ struct SsmItem {
 
 struct SsmCtl {
   uint64_t x_full[2], x_empty[2], b_full[2], b_empty[2], c_full, c_empty, prep_full[2], prep_empty[2];
-  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[2], xp_empty[2], zeroed, drained;
+  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[2], xp_empty[2], zeroed, start_full, start_read, drained;
   SsmItem item;
   uint32_t tmem;
   int abort;
@@ -70,7 +70,7 @@ struct SsmCtl {
 static_assert(sizeof(SsmCtl) <= 512, "control block");
 
 struct SsmMaps {
-  CUtensorMap x, b, c, out;
+  CUtensorMap x, b, c, out, init, fin;
 };
 
 template <int S>
@@ -80,6 +80,13 @@ struct SsmSmem {
   static constexpr int PREP = H + SB * SS_BOX;
   static constexpr int CTL = PREP + 4 * static_cast<int>(sizeof(SsmPrep));
   static constexpr int BYTES = CTL + 512 + 1024;
+  // A state on its way in or out, 32 rows of 128 bytes at a time: in, over the second places of B and
+  // x, which the second chunk's rows wait for; out, over both places of B.
+  static constexpr int STATE_BOX = 32 * 128;
+  static __device__ __forceinline__ int state_in(int box) {
+    return box < SB * 4 ? B + SB * SS_BOX + box * STATE_BOX : X + 2 * SS_BOX + (box - SB * 4) * STATE_BOX;
+  }
+  static __device__ __forceinline__ int state_out(int box) { return B + box * STATE_BOX; }
 };
 static_assert(SsmSmem<128>::BYTES <= 227 * 1024, "shared memory");
 
@@ -204,6 +211,8 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       mbar_init(&ctl->xp_empty[i], 1);
     }
     mbar_init(&ctl->zeroed, 4);
+    mbar_init(&ctl->start_full, 1);
+    mbar_init(&ctl->start_read, 4);
     mbar_init(&ctl->drained, 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -227,6 +236,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     if (PRE && it.last) it.len = -1;
     if (l == 0) ctl->item = it;
   }
+  if (w == 22 && l < 6) {
+    const CUtensorMap* map = &maps.x + l;
+    if (l < 2 || (!PRE && (l < 4 || (l == 4 ? parts.init : a.fin)))) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+  }
   if (w == 21) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
@@ -238,6 +251,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   const SsmItem it = ctl->item;
   const int nc = it.len > 0 ? (it.len + SS_TOK - 1) / SS_TOK : 0;
   const int64_t part = slot * units + unit;
+  // the state that the piece starts from: bytes of a value and of a channel's row, first row
+  const int state_size = a.bf16_state ? 2 : 4, state_row = S * state_size;
+  const int64_t state_first = (static_cast<int64_t>(it.n) * a.H + h0) * P;
+  const bool start = !PRE && parts.init != nullptr && it.len >= 0;
   // the c-th chunk that is worked on, and its tokens
   auto chunk = [&](int c) { return PRE ? nc - 1 - c : c; };
   auto tokens = [&](int c) {
@@ -251,11 +268,19 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (l == 0) {
         bool ok = true;
         int c = 0, cs = 0;
+        if (start) {
+          const int rows = nh * P / 32, boxes = rows * (state_row / 128);
+          mbar_arrive_expect_tx(&ctl->start_full, boxes * L::STATE_BOX);
+          for (int b = 0; b < boxes; ++b)
+            tma_box2(smem + L::state_in(b), &maps.init, b / rows * (128 / state_size),
+                     static_cast<int>(state_first) + b % rows * 32, &ctl->start_full);
+        }
         for (; ok && c < nc; ++c) {
           const int st = c & 1, row = static_cast<int>(it.tok + chunk(c) * SS_TOK);
           const int boxes = P == 64 ? nh : 2;
           // in the order in which their places become free
           if (c >= 2) ok = wait_for(&ctl->b_empty[st], ((c >> 1) - 1) & 1, ctl, err);
+          if (c == 1 && start) ok = wait_for(&ctl->start_read, 0, ctl, err);
           if (!ok) break;
           mbar_arrive_expect_tx(&ctl->b_full[st], SB * SS_BOX);
           for (int b = 0; b < SB; ++b)
@@ -286,6 +311,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           }
         }
         // copies that may be in flight after a wait that ran out land first
+        if (start) mbar_wait(&ctl->start_full, 0);
         if (*reinterpret_cast<volatile int*>(&ctl->abort) || !ok) {
           for (int i = c > 2 ? c - 2 : 0; i < c; ++i) {
             mbar_wait(&ctl->x_full[i & 1], (i >> 1) & 1);
@@ -393,7 +419,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (hh < HU) {
         const bool there = hh < nh;
         const int h = h0 + (there ? hh : 0);
-        const float rate = nc > 0 ? __ldg(a.A + h) * kLog2e : 0.f, bias = nc > 0 && a.dt_bias ? __ldg(a.dt_bias + h) : 0.f;
+        const float rate = __ldg(a.A + h) * kLog2e, bias = a.dt_bias ? __ldg(a.dt_bias + h) : 0.f;
         float tail = 0.f;  // of the chunks behind (PRE)
         // raw step sizes are loaded a chunk ahead
         __nv_bfloat16 raw[4], next[4];
@@ -564,21 +590,24 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     const int r = tid & 127, hh = r / P;  // channel of the unit, its head
     const bool there = hh < nh;
     const uint32_t M = tmem + SS_M + (static_cast<uint32_t>((w & 3) * 32) << 16);
-    const int64_t row = ((static_cast<int64_t>(it.n) * a.H + h0 + hh) * P + r % P) * S;  // of the states
     bool ok = true;
     if (!PRE && it.len >= 0) {
-      // the state that the piece starts from
+      if (start) ok = warp_wait(&ctl->start_full, 0, ctl, err);
+      // column `at` (in 16 bytes) of the channel's row
+      auto piece16 = [&](int at) -> uint4 {
+        return *reinterpret_cast<const uint4*>(smem + L::state_in((at >> 3) * (nh * P / 32) + (r >> 5)) + l * 128 +
+                                               (((at & 7) ^ (l & 7)) << 4));
+      };
 #pragma unroll 1
       for (int cb = 0; cb < S / 32; ++cb) {
         float m[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) m[e] = 0.f;
-        if (parts.init && there) {
+        if (start && ok && there) {
           if (a.bf16_state) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(parts.init) + row + cb * 32);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint4 x = src[q];
+              const uint4 x = piece16(cb * 4 + q);
               const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -587,14 +616,13 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
               }
             }
           } else {
-            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(parts.init) + row + cb * 32);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const float4 x = src[q];
-              m[4 * q] = x.x;
-              m[4 * q + 1] = x.y;
-              m[4 * q + 2] = x.z;
-              m[4 * q + 3] = x.w;
+              const uint4 x = piece16(cb * 8 + q);
+              m[4 * q] = __uint_as_float(x.x);
+              m[4 * q + 1] = __uint_as_float(x.y);
+              m[4 * q + 2] = __uint_as_float(x.z);
+              m[4 * q + 3] = __uint_as_float(x.w);
             }
           }
         }
@@ -617,7 +645,8 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         tmem_st32(M + cb * 32, u);
       }
       tmem_wait_st();
-      for (int c = 0; c < nc; ++c) {
+      warp_arrive(&ctl->start_read);
+      for (int c = 0; ok && c < nc; ++c) {
         const int st = c & 1;
         ok = (c == 0 || warp_wait(&ctl->m_full, (c - 1) & 1, ctl, err)) && warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err);
         if (!ok) break;
@@ -650,6 +679,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     }
     // the state at the end
     if (ok && nc > 0) ok = warp_wait(&ctl->m_full, PRE ? 0 : (nc - 1) & 1, ctl, err);
+    if (ok && nc == 0 && start) ok = warp_wait(&ctl->start_read, 0, ctl, err);  // (it goes out over where it came in)
     if (ok && (PRE ? nc > 0 : it.len >= 0 && it.last && a.fin != nullptr)) {
       tc_fence_after();
 #pragma unroll 1
@@ -663,21 +693,37 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           for (int q = 0; q < 8; ++q)
             dst[q * SS_TOK] = make_float4(__uint_as_float(m[4 * q]), __uint_as_float(m[4 * q + 1]),
                                           __uint_as_float(m[4 * q + 2]), __uint_as_float(m[4 * q + 3]));
-        } else if (there && a.bf16_state) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.fin) + row + cb * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[e] = pack_bf16(__uint_as_float(m[8 * q + 2 * e]), __uint_as_float(m[8 * q + 2 * e + 1]));
-            dst[q] = make_uint4(p[0], p[1], p[2], p[3]);
-          }
         } else if (there) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<float*>(a.fin) + row + cb * 32);
+          // out through shared memory, by TMA
+          auto piece16 = [&](int at) -> uint4* {
+            return reinterpret_cast<uint4*>(smem + L::state_out((at >> 3) * (nh * P / 32) + (r >> 5)) + l * 128 +
+                                            (((at & 7) ^ (l & 7)) << 4));
+          };
+          if (a.bf16_state) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[q] = make_uint4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t p[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                p[e] = pack_bf16(__uint_as_float(m[8 * q + 2 * e]), __uint_as_float(m[8 * q + 2 * e + 1]));
+              *piece16(cb * 4 + q) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) *piece16(cb * 8 + q) = make_uint4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
+          }
         }
+      }
+      if (!PRE && there) {
+        fence_async();
+        __syncwarp();
+        if (l == 0) {
+          for (int b = 0; b < state_row / 128; ++b)
+            tma_store_box(&maps.fin, b * (128 / state_size), static_cast<int>(state_first) + r,
+                          smem + L::state_out(b * (nh * P / 32) + (r >> 5)));
+          tma_stores_read();
+        }
+        __syncwarp();
       }
     }
   } else if (w < 16) {
@@ -943,6 +989,9 @@ cudaError_t launch(const SsmArgs& a, const Plan& plan, void* ws, int* err, cudaS
     if (e != cudaSuccess) return e;
   }
   SsmParts parts{nullptr, nullptr, a.init};
+  const auto state_map = [&](CUtensorMap* map, const void* at) {
+    return at ? make_state_map(map, at, static_cast<int64_t>(a.N) * a.H * P, S, a.bf16_state) : cudaSuccess;
+  };
   if (plan.split) {
     uint8_t* at = static_cast<uint8_t*>(ws);
     parts.m = reinterpret_cast<float*>(at);
@@ -958,6 +1007,9 @@ cudaError_t launch(const SsmArgs& a, const Plan& plan, void* ws, int* err, cudaS
     const cudaError_t e = launch_one<P, S, true>(maps, a, parts, plan, err, stream);
     if (e != cudaSuccess) return e;
   }
+  cudaError_t e = state_map(&maps.init, parts.init);
+  if (e == cudaSuccess) e = state_map(&maps.fin, a.fin);
+  if (e != cudaSuccess) return e;
   return launch_one<P, S, false>(maps, a, parts, plan, err, stream);
 }
 

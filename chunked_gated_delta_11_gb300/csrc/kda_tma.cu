@@ -83,6 +83,22 @@ cudaError_t make_matrix_map(CUtensorMap* map, const void* base, int64_t T_total,
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// 128 bytes of 32 rows of a state's matrix [rows, cols], fp32 or bf16 (kda_ssm.cu), 128-byte swizzled.
+cudaError_t make_state_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, bool bf16) {
+  if (rows < 1 || rows >= (static_cast<int64_t>(1) << 31)) return cudaErrorInvalidValue;
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t make_raw_maps(RawMaps* maps, const void* q, const void* k, const void* v,
                           const void* g, int64_t T_total, int H, bool gate_scalar) {
   std::memset(maps, 0, sizeof(RawMaps));

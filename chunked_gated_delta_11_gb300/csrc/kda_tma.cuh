@@ -67,6 +67,8 @@ cudaError_t make_tile_map(CUtensorMap* map, const void* base, int64_t T_total, i
 // The same boxes of a matrix [T_total, cols] whose rows are `stride` elements apart
 // (a multiple of 8).  The x coordinates used with it are multiples of 64.
 cudaError_t make_matrix_map(CUtensorMap* map, const void* base, int64_t T_total, int64_t cols, int64_t stride, int rows);
+// Boxes of 128 bytes of 32 rows of a matrix [rows, cols] of fp32 or bf16.
+cudaError_t make_state_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, bool bf16);
 __device__ __forceinline__ void tma_box2(void* dst, const CUtensorMap* map, int x, int t, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
