@@ -7,15 +7,16 @@
 //   M'  = e^{l_Q} M + sum_j (e^{l_Q - l_j} d_j x_j) B_j^T
 //
 // A CTA has 128 channels of one sequence (or of a piece of one): two heads of 64 that share
-// B and C, or one of 128.  24 warps:
+// B and C, or one of 128.  28 warps:
 //   warps 0-3    weights: S = C B^T (one thread a row) times e^{l_i - l_j} d_j, per head, in bf16
 //                over S in tensor memory
 //   warps 4-7    the state, a thread a channel: M in tensor memory (fp32), its bf16 copy for
 //                the products with C in shared memory, its decay
 //   warps 8-15   the weighted rows x' = e^{l_Q - l_j} d_j x_j, transposed into tensor memory, as
 //                the left operand of M' += x'^T B: groups of 32 tokens, each four warps' every other
-//   warps 16-19  outputs: e^{l_i} M C_i + skip x_i in tensor memory, then the finished rows
-//   warp 20      TMA;  warp 21  the products;  warps 22, 23  step sizes and decays
+//   warps 16-23  outputs: e^{l_i} M C_i + skip x_i in tensor memory, then the finished rows, four
+//                warps 64 channels
+//   warp 24      TMA;  warp 25  the products;  warps 26, 27  step sizes and decays
 // Tensor memory: S and P | Y | M, 128 columns each, x' (two places of a group), 96, and the rest of P,
 // 32.  The loops are kept short (rolled, and one copy of what two products share): unrolled,
 // the roles' code outgrew the instruction caches (37 % of fetches missed, 9300 cycles a chunk).
@@ -36,9 +37,9 @@ namespace {
 
 constexpr int SS_TOK = 128;              // tokens of a chunk, channels of a CTA
 constexpr int SS_BOX = SS_TOK * 128;     // bytes of 64 elements of 128 rows
-constexpr int SS_THREADS = 768;
-// six warpgroups of 80 registers a thread at launch: 128 + 80 + 2 x 64 + 88 + 56 = 6 x 80
-constexpr int SS_REGS_WEIGHTS = 128, SS_REGS_ROWS = 64, SS_REGS_OUT = 88, SS_REGS_ISSUE = 56;
+constexpr int SS_THREADS = 896;
+// seven warpgroups of 72 registers a thread at launch: 104 + 72 + 2 x 64 + 2 x 72 + 56 = 7 x 72
+constexpr int SS_REGS_WEIGHTS = 104, SS_REGS_ROWS = 64, SS_REGS_ISSUE = 56;
 constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384, SS_P1 = 480;  // columns
 constexpr int SS_GROUP = 32;             // tokens of a place of x'
 constexpr int SS_TERMS = 3;              // addends of x' at most, 16 columns each
@@ -187,10 +188,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   const int nh = per_group - hu < HU ? per_group - hu : HU;  // heads that exist
 
   if (tid == 0) {
-    constexpr int users = PRE ? 8 : 20;
+    constexpr int users = PRE ? 8 : 24;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->x_full[i], 1);
-      mbar_init(&ctl->x_empty[i], PRE ? 8 : 5);
+      mbar_init(&ctl->x_empty[i], PRE ? 8 : 9);
       mbar_init(&ctl->b_full[i], 1);
       mbar_init(&ctl->b_empty[i], 1);
       mbar_init(&ctl->prep_full[i], HU);
@@ -201,9 +202,9 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     mbar_init(&ctl->s_full, 1);
     mbar_init(&ctl->p_full, 4);
     mbar_init(&ctl->yoff_full, 1);
-    mbar_init(&ctl->y_scaled, 4);
+    mbar_init(&ctl->y_scaled, 8);
     mbar_init(&ctl->y_full, 1);
-    mbar_init(&ctl->y_empty, 4);
+    mbar_init(&ctl->y_empty, 8);
     mbar_init(&ctl->m_full, 1);
     mbar_init(&ctl->h_full, 4);
     for (int i = 0; i < 2; ++i) {
@@ -220,7 +221,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   // Sequence n owns the slots from floor(bos_n / piece) + n on, one for each of its pieces; whole
   // ones come in the order of their lengths, the longest first.
   const int whole = ranked ? seq_by_rank(a.cu, a.N, static_cast<int>(slot), reinterpret_cast<int*>(smem)) : 0;
-  if (w == 20) {
+  if (w == 24) {
     const int n = ranked ? whole : seq_of_slot(a.cu, a.T, a.N, static_cast<int>(piece), 1, slot);
     int64_t bos, eos;
     seq_bounds(a.cu, a.T, a.N, n, bos, eos);
@@ -236,11 +237,11 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     if (PRE && it.last) it.len = -1;
     if (l == 0) ctl->item = it;
   }
-  if (w == 22 && l < 6) {
+  if (w == 26 && l < 6) {
     const CUtensorMap* map = &maps.x + l;
     if (l < 2 || (!PRE && (l < 4 || (l == 4 ? parts.init : a.fin)))) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
-  if (w == 21) {
+  if (w == 25) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
@@ -262,9 +263,9 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     return left < SS_TOK ? left : SS_TOK;
   };
 
-  if (w >= 20) {
+  if (w >= 24) {
     regs_give<SS_REGS_ISSUE>();
-    if (w == 20) {
+    if (w == 24) {
       if (l == 0) {
         bool ok = true;
         int c = 0, cs = 0;
@@ -321,7 +322,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         }
       }
       __syncwarp();
-    } else if (w == 21) {
+    } else if (w == 25) {
       if (elect_one()) {
         const uint32_t sb = smem_u32(smem);
         constexpr uint32_t id_s = make_idesc(1, SS_TOK, SS_TOK);
@@ -415,7 +416,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       __syncwarp();
     } else {
       // Step sizes and decays of one head, four tokens to a lane.
-      const int hh = w - 22;
+      const int hh = w - 26;
       if (hh < HU) {
         const bool there = hh < nh;
         const int h = h0 + (there ? hh : 0);
@@ -814,15 +815,12 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (PRE) warp_arrive(&ctl->x_empty[st]);
     }
   } else {
-    regs_take<SS_REGS_OUT>();
-    const int i = tid & 127;
-    const uint32_t Y = tmem + SS_Y + (static_cast<uint32_t>((w & 3) * 32) << 16);
-    f2 skip[HU];
-#pragma unroll
-    for (int hh = 0; hh < HU; ++hh) {
-      const float s = !PRE && a.skip && hh < nh ? __ldg(a.skip + h0 + hh) : 0.f;
-      skip[hh] = pair(s, s);
-    }
+    const int i = tid & 127, side = (w - 16) >> 2;  // row; 64 channels
+    const int hh = side * 64 / P;                   // their head
+    const bool there = hh < nh;
+    const uint32_t Y = tmem + SS_Y + side * 64 + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    const float sk = !PRE && a.skip && there ? __ldg(a.skip + h0 + hh) : 0.f;
+    const f2 skip = pair(sk, sk);
     for (int c = 0; !PRE && c < nc; ++c) {
       const int st = c & 1, len = tokens(c);
       if (!warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err)) break;
@@ -830,27 +828,23 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (!warp_wait(&ctl->yoff_full, c & 1, ctl, err)) break;
       tc_fence_after();
       // what the tokens of the chunk add comes on top of e^{l_i} M C_i + skip x_i
-      uint8_t* x = smem + L::X + 2 * st * SS_BOX + i * 128;
-      f2 e[HU];
-#pragma unroll
-      for (int hh = 0; hh < HU; ++hh) {
-        const float f = prep[st * 2 + hh].e[i];
-        e[hh] = pair(f, f);
-      }
+      uint8_t* x = smem + L::X + (2 * st + side) * SS_BOX;
+      uint8_t* row = x + i * 128;
+      const float ei = prep[st * 2 + hh].e[i];
+      const f2 f = pair(ei, ei);
 #pragma unroll 1
-      for (int cb = 0; cb < 4; ++cb) {
+      for (int cb = 0; cb < 2; ++cb) {
         uint32_t y[32];
         tmem_ld32(Y + cb * 32, y);
         tmem_wait_ld();
-        const f2 f = HU > 1 && cb >= 2 ? e[HU - 1] : e[0], s = HU > 1 && cb >= 2 ? skip[HU - 1] : skip[0];
         if (a.skip) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4*>(x + (cb >> 1) * SS_BOX + ((((cb & 1) * 4 + q) ^ (i & 7)) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (((cb * 4 + q) ^ (i & 7)) << 4));
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              unpair(fma2(pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]), f, mul2(pair(u[k] << 16, u[k] & 0xffff0000u), s)),
+              unpair(fma2(pair(y[8 * q + 2 * k], y[8 * q + 2 * k + 1]), f, mul2(pair(u[k] << 16, u[k] & 0xffff0000u), skip)),
                      y[8 * q + 2 * k], y[8 * q + 2 * k + 1]);
           }
         } else {
@@ -868,11 +862,11 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       // The rows take the place of x's, which no product reads any more, and leave from there: 32
       // at a time by TMA, or those of them that are the sequence's own.
 #pragma unroll 1
-      for (int cb = 0; cb < 4; ++cb) {
+      for (int cb = 0; cb < 2; ++cb) {
         uint32_t y[32];
         tmem_ld32(Y + cb * 32, y);
         tmem_wait_ld();
-        if (cb == 3) {
+        if (cb == 1) {
           tc_fence_before();
           warp_arrive(&ctl->y_empty);
         }
@@ -882,30 +876,24 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             p[k] = pack_bf16(__uint_as_float(y[8 * q + 2 * k]), __uint_as_float(y[8 * q + 2 * k + 1]));
-          *reinterpret_cast<uint4*>(x + (cb >> 1) * SS_BOX + ((((cb & 1) * 4 + q) ^ (i & 7)) << 4)) =
-              make_uint4(p[0], p[1], p[2], p[3]);
+          *reinterpret_cast<uint4*>(row + (((cb * 4 + q) ^ (i & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
         }
       }
       const int rows = len - (i - l);  // of the warp's 32, those there
       const int64_t tok = it.tok + c * SS_TOK + (i - l);
-      const int boxes = HU > 1 ? nh : 2;
-      const uint8_t* first = smem + L::X + 2 * st * SS_BOX + (i - l) * 128;
-      if (rows >= 32) {
-        fence_async();
-        __syncwarp();
+      const uint8_t* first = x + (i - l) * 128;
+      fence_async();
+      __syncwarp();
+      if (there && rows >= 32) {
         if (l == 0) {
-          for (int b = 0; b < boxes; ++b)
-            tma_store_box(&maps.out, h0 * P + b * 64, static_cast<int>(tok), first + b * SS_BOX);
+          tma_store_box(&maps.out, h0 * P + side * 64, static_cast<int>(tok), first);
           tma_stores_read();
         }
-      } else {
-        __syncwarp();
-        __nv_bfloat16* dst = a.out + (tok * a.H + h0) * P + (l & 7) * 8;
-        for (int b = 0; b < boxes; ++b)
-          for (int q = l >> 3; q < rows; q += 4)
-            *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(q) * a.H * P + b * 64) =
-                *reinterpret_cast<const uint4*>(first + b * SS_BOX + q * 128 + (((l & 7) ^ (q & 7)) << 4));
-        fence_async();  // before x's next rows
+      } else if (there) {
+        __nv_bfloat16* dst = a.out + (tok * a.H + h0) * P + side * 64 + (l & 7) * 8;
+        for (int q = l >> 3; q < rows; q += 4)
+          *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(q) * a.H * P) =
+              *reinterpret_cast<const uint4*>(first + q * 128 + (((l & 7) ^ (q & 7)) << 4));
       }
       warp_arrive(&ctl->x_empty[st]);
     }
@@ -913,7 +901,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (w == 21) tmem_dealloc(tmem, 512);
+  if (w == 25) tmem_dealloc(tmem, 512);
 }
 
 int units_of(int H, int G, int P) {
