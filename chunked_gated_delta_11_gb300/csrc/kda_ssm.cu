@@ -63,7 +63,7 @@ struct SsmItem {
 
 struct SsmCtl {
   uint64_t x_full[2], x_empty[2], b_full[2], b_empty[2], c_full, c_empty, prep_full[2], prep_empty[2];
-  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[2], xp_empty[2], zeroed, start_full, start_read, drained;
+  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[4], xp_empty[4], zeroed, start_full, start_read, drained;
   SsmItem item;
   uint32_t tmem;
   int abort;
@@ -167,13 +167,16 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 
 // PRE: only the state that each piece but a sequence's last adds, walking from its last
 // chunk to its first: with weights that reach to the piece's end, the products of all
-// chunks add up in tensor memory.
+// chunks add up in tensor memory.  The output warps join in with x' there, each four with a
+// group and a place of its own (8192 tokens, 64 heads, four pieces: 45 us with two places).
 template <int P, int S, bool PRE>
 __global__ void __launch_bounds__(SS_THREADS, 1)
 ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, int terms, bool ranked, int* err) {
   using L = SsmSmem<S>;
   constexpr int HU = SS_TOK / P;  // heads of a unit
   constexpr int SB = L::SB;
+  constexpr int SIDES = PRE ? 4 : 2;                // warpgroups of x', and its places
+  constexpr uint32_t XP0 = PRE ? SS_SP : SS_XP;     // their columns
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   SsmCtl* ctl = reinterpret_cast<SsmCtl*>(smem + L::CTL);
@@ -188,10 +191,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   const int nh = per_group - hu < HU ? per_group - hu : HU;  // heads that exist
 
   if (tid == 0) {
-    constexpr int users = PRE ? 8 : 24;
+    constexpr int users = PRE ? 16 : 24;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->x_full[i], 1);
-      mbar_init(&ctl->x_empty[i], PRE ? 8 : 9);
+      mbar_init(&ctl->x_empty[i], PRE ? 16 : 9);
       mbar_init(&ctl->b_full[i], 1);
       mbar_init(&ctl->b_empty[i], 1);
       mbar_init(&ctl->prep_full[i], HU);
@@ -207,7 +210,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     mbar_init(&ctl->y_empty, 8);
     mbar_init(&ctl->m_full, 1);
     mbar_init(&ctl->h_full, 4);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < SIDES; ++i) {
       mbar_init(&ctl->xp_full[i], 4);
       mbar_init(&ctl->xp_empty[i], 1);
     }
@@ -366,11 +369,11 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           }
           const int groups = (len + SS_GROUP - 1) / SS_GROUP;
           for (int q = 0; q < groups; ++q) {
-            // a whole chunk uses each place twice
-            ok = wait_for(&ctl->xp_full[q & 1], (q >> 1) & 1, ctl, err);
+            const int place = q % SIDES;  // a whole chunk uses each 4 / SIDES times
+            ok = wait_for(&ctl->xp_full[place], (PRE ? c : q >> 1) & 1, ctl, err);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t x = tmem + SS_XP + (q & 1) * 48, b_lo = cols_lo + b_stage + q * 256;
+            const uint32_t x = tmem + XP0 + place * 48, b_lo = cols_lo + b_stage + q * 256;
             const uint32_t add = !PRE || c > 0 || q > 0;
             mma_ts_step<0, 0>(tmem + SS_M, x, b_lo, hi, id_m, add);
             mma_ts_step<8, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
@@ -382,7 +385,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
               mma_ts_step<32, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
               mma_ts_step<40, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
             }
-            tc_commit(&ctl->xp_empty[q & 1]);
+            tc_commit(&ctl->xp_empty[place]);
           }
           if (!ok) break;
           tc_commit(&ctl->b_empty[st]);
@@ -727,11 +730,11 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         __syncwarp();
       }
     }
-  } else if (w < 16) {
+  } else if (w < 8 + 4 * SIDES) {
     regs_give<SS_REGS_ROWS>();
     const int place = (w - 8) >> 2, wq = w & 3;
     const int r = tid & 127, hh = r / P;
-    const uint32_t XP = tmem + SS_XP + place * 48 + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t XP = tmem + XP0 + place * 48 + (static_cast<uint32_t>(wq * 32) << 16);
     // where a lane's row of an 8 x 8 matrix lies, for the warp's first and second 16 channels
     uint32_t at[2];
 #pragma unroll
@@ -768,7 +771,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       const int groups = (len + SS_GROUP - 1) / SS_GROUP;
       bool ok = true;
 #pragma unroll 1
-      for (int q = place; q < groups; q += 2, ++used) {
+      for (int q = place; q < groups; q += SIDES, ++used) {
         // Transposed on the way into registers: of 16 channels at a time, a lane has tokens 8 j + 2
         // (l % 4) and the next of channels l / 4 and l / 4 + 8.
         uint32_t raw[4][4];
