@@ -5,93 +5,93 @@
 // where the W - 1 rows before a sequence's first come from its state, and its last W - 1
 // rows are the next state.  Products and sums are fp32, the output is rounded once.
 //
-// A thread has 8 channels (one 16-byte access a row) and walks down a strip of rows with
-// the last W - 1 of them in registers, so that a row is read once but for the W - 1 before
-// a strip.  A sequence's first W - 1 rows and its two states are a block's of their own
-// (a head block): it reads the old state before it writes the new one, so that the two may
-// be the same buffer, and a step of one token a sequence is such blocks alone.
+// A thread has 4 channels (8 bytes a row, whole lines a warp) and walks down a strip of rows
+// with the last W - 1 of them in registers, 8 rows under way at a time, so that a row is
+// read once but for the W - 1 before a strip.  (With 8 channels a thread the weights and the
+// rows took 166 registers, and too few rows were under way: 209 us for the rows below.)  A
+// sequence's first W - 1 rows and its two states are a block's of their own (a head block):
+// it reads the old state before it writes the new one, so that the two may be the same
+// buffer, and a step of one token a sequence is such blocks alone.
 #include "kda_attn.cuh"
 #include "kda_layers.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 
 namespace {
 
 constexpr int CV_THREADS = 128;
-constexpr int CV_CHANNELS = CV_THREADS * 8;
-constexpr int CV_AHEAD = 8;  // rows under way in a thread
+constexpr int CV_VEC = 4;                        // channels of a thread
+constexpr int CV_CHANNELS = CV_THREADS * CV_VEC;
+constexpr int CV_AHEAD = 8;                      // rows under way in a thread
 
-__device__ __forceinline__ void widen(const uint4& r, float (&f)[8]) {
-  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
+// Four channels of a row, in pairs.
+struct Row {
+  f2 lo, hi;
+};
+__device__ __forceinline__ Row widen(uint2 r) {
+  return {pair(r.x << 16, r.x & 0xffff0000u), pair(r.y << 16, r.y & 0xffff0000u)};
 }
 
-// The taps and the bias of a thread's 8 channels.
+__device__ __forceinline__ uint2 row_of(const __nv_bfloat16* base, int64_t stride, int64_t row, int c) {
+  return __ldg(reinterpret_cast<const uint2*>(base + row * stride + c));
+}
+
+__device__ __forceinline__ uint32_t silu_pair(f2 y, bool silu) {
+  float a, b;
+  unpair(y, a, b);
+  if (silu) {
+    a *= sigmoid_fast(a);
+    b *= sigmoid_fast(b);
+  }
+  return pack_bf16(a, b);
+}
+
+// The taps and the bias of a thread's channels.
 template <int W>
 struct Taps {
-  float w[8][W], b[8];
+  Row w[W], b;
   __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+    float f[CV_VEC][W];
 #pragma unroll
-    for (int k = 0; k < W; ++k) {  // 8 W values, 16 bytes at a time
-      float f[8];
-      widen(__ldg(reinterpret_cast<const uint4*>(a.w + static_cast<int64_t>(c) * W) + k), f);
+    for (int k = 0; k < W; ++k) {  // 4 W values, 8 bytes at a time
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(a.w + static_cast<int64_t>(c) * W) + k);
+      const uint32_t x[2] = {u.x, u.y};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[(8 * k + e) / W][(8 * k + e) % W] = f[e];
+      for (int e = 0; e < 4; ++e)
+        f[(4 * k + e) / W][(4 * k + e) % W] = __uint_as_float(e & 1 ? x[e >> 1] & 0xffff0000u : x[e >> 1] << 16);
     }
-    if (a.bias) {
-      widen(__ldg(reinterpret_cast<const uint4*>(a.bias + c)), b);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = 0.f;
-    }
+    for (int j = 0; j < W; ++j) w[j] = {pair(f[0][j], f[1][j]), pair(f[2][j], f[3][j])};
+    b = a.bias ? widen(__ldg(reinterpret_cast<const uint2*>(a.bias + c))) : Row{0ull, 0ull};
   }
   // rows: the W rows that end with the output's own
-  __device__ __forceinline__ uint4 output(const uint4 (&rows)[W], bool silu) const {
-    float y[8];
+  __device__ __forceinline__ uint2 output(const Row (&rows)[W], bool silu) const {
+    Row y = b;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = b[e];
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-      float f[8];
-      widen(rows[j], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = fmaf(w[e][j], f[e], y[e]);
-    }
-    if (silu) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= sigmoid_fast(y[e]);
-    }
-    return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    for (int j = 0; j < W; ++j) y = {fma2(w[j].lo, rows[j].lo, y.lo), fma2(w[j].hi, rows[j].hi, y.hi)};
+    return make_uint2(silu_pair(y.lo, silu), silu_pair(y.hi, silu));
   }
 };
-
-// Rows of a thread's channels, from the input or a state.
-__device__ __forceinline__ uint4 row_of(const __nv_bfloat16* base, int64_t stride, int64_t row, int c) {
-  return __ldg(reinterpret_cast<const uint4*>(base + row * stride + c));
-}
 
 template <int W>
 __global__ void __launch_bounds__(CV_THREADS)
 conv_kernel(ConvArgs a, int heads, int strip) {
   grid_dep_wait();
   grid_dep_launch();
-  const int c = (blockIdx.y * CV_THREADS + threadIdx.x) * 8;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int c = (blockIdx.y * CV_THREADS + threadIdx.x) * CV_VEC;
   if (static_cast<int>(blockIdx.x) < heads) {
     const int n = blockIdx.x;
     int64_t bos, eos;
     seq_bounds(a.cu, a.T, a.N, n, bos, eos);
     if (c >= a.C) return;
     const int64_t len = eos - bos, at = static_cast<int64_t>(n) * (W - 1);
-    uint4 rows[2 * (W - 1)];  // the old state, then the first rows
+    const uint2 zero = make_uint2(0, 0);
+    uint2 rows[2 * (W - 1)];  // the old state, then the first rows
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
       // not the read-only path: the state may be written further down
-      rows[r] = a.init ? *reinterpret_cast<const uint4*>(a.init + (at + r) * a.C + c) : zero;
+      rows[r] = a.init ? *reinterpret_cast<const uint2*>(a.init + (at + r) * a.C + c) : zero;
       rows[W - 1 + r] = r < len ? row_of(a.x, a.x_stride, bos + r, c) : zero;
     }
     Taps<W> taps;
@@ -99,7 +99,7 @@ conv_kernel(ConvArgs a, int heads, int strip) {
     if (a.fin) {
 #pragma unroll
       for (int r = 0; r < W - 1; ++r) {
-        uint4 last = zero;
+        uint2 last = zero;
         if (len >= W - 1) {
           last = row_of(a.x, a.x_stride, eos - (W - 1) + r, c);
         } else {
@@ -107,15 +107,15 @@ conv_kernel(ConvArgs a, int heads, int strip) {
           for (int k = 0; k < 2 * (W - 1); ++k)
             if (k == len + r) last = rows[k];
         }
-        *reinterpret_cast<uint4*>(a.fin + (at + r) * a.C + c) = last;
+        *reinterpret_cast<uint2*>(a.fin + (at + r) * a.C + c) = last;
       }
     }
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) {
-      uint4 in[W];
+      Row in[W];
 #pragma unroll
-      for (int j = 0; j < W; ++j) in[j] = rows[r + j];
-      if (r < len) *reinterpret_cast<uint4*>(a.out + (bos + r) * a.C + c) = taps.output(in, a.silu);
+      for (int j = 0; j < W; ++j) in[j] = widen(rows[r + j]);
+      if (r < len) *reinterpret_cast<uint2*>(a.out + (bos + r) * a.C + c) = taps.output(in, a.silu);
     }
     return;
   }
@@ -140,22 +140,28 @@ conv_kernel(ConvArgs a, int heads, int strip) {
     }
     if (!loaded) taps.load(a, c);
     loaded = true;
-    uint4 rows[W - 1 + CV_AHEAD];
+    Row in[W];  // the rows before, then the current one
 #pragma unroll
-    for (int r = 0; r < W - 1; ++r) rows[r] = row_of(a.x, a.x_stride, t - (W - 1) + r, c);
-    for (; t < end; t += CV_AHEAD) {
-#pragma unroll
-      for (int r = 0; r < CV_AHEAD; ++r)
-        if (t + r < end) rows[W - 1 + r] = row_of(a.x, a.x_stride, t + r, c);
+    for (int r = 0; r < W - 1; ++r) in[r] = widen(row_of(a.x, a.x_stride, t - (W - 1) + r, c));
+    const __nv_bfloat16* x = a.x + t * a.x_stride + c;
+    __nv_bfloat16* out = a.out + t * a.C + c;
+    for (int left = static_cast<int>(end - t); left > 0; left -= CV_AHEAD) {
+      uint2 raw[CV_AHEAD];
 #pragma unroll
       for (int r = 0; r < CV_AHEAD; ++r) {
-        uint4 in[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j) in[j] = rows[r + j];
-        if (t + r < end) *reinterpret_cast<uint4*>(a.out + (t + r) * a.C + c) = taps.output(in, a.silu);
+        raw[r] = make_uint2(0, 0);
+        if (r < left) raw[r] = __ldg(reinterpret_cast<const uint2*>(x + r * a.x_stride));
       }
 #pragma unroll
-      for (int r = 0; r < W - 1; ++r) rows[r] = rows[CV_AHEAD + r];
+      for (int r = 0; r < CV_AHEAD; ++r) {
+        in[W - 1] = widen(raw[r]);
+        const uint2 y = taps.output(in, a.silu);
+        if (r < left) *reinterpret_cast<uint2*>(out + static_cast<int64_t>(r) * a.C) = y;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) in[j] = in[j + 1];
+      }
+      x += CV_AHEAD * a.x_stride;
+      out += static_cast<int64_t>(CV_AHEAD) * a.C;
     }
     t = end;
   }

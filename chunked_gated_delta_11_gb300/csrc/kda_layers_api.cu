@@ -116,7 +116,7 @@ extern "C" kda_status kda_conv_fwd(const kda_conv_options* opts, const void* x, 
   kda_status s = check_packing(T_total, N, cu_seqlens);
   if (s != KDA_OK) return s;
   if (T_total > kMaxElems / C || N > kMaxElems / C) return KDA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(C) > 65535LL * 1024) return KDA_ERR_INVALID_ARG;  // blocks of 1024 channels
+  if (static_cast<int64_t>(C) > 65535LL * 512) return KDA_ERR_INVALID_ARG;  // blocks of 512 channels
   if (static_cast<int64_t>(N) + T_total / 8 + 1 > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
   int64_t stride = opts->x_stride;
   if (!good_stride(stride, C, 8)) return KDA_ERR_INVALID_ARG;
