@@ -75,7 +75,7 @@ struct Taps {
 };
 
 template <int W>
-__global__ void __launch_bounds__(CV_THREADS)
+__global__ void __launch_bounds__(CV_THREADS, 8)
 conv_kernel(ConvArgs a, int heads, int strip) {
   grid_dep_wait();
   grid_dep_launch();
@@ -170,8 +170,8 @@ conv_kernel(ConvArgs a, int heads, int strip) {
 template <int W>
 cudaError_t launch(const ConvArgs& a, int sm_count, cudaStream_t stream) {
   const int64_t blocks_c = (a.C + CV_CHANNELS - 1) / CV_CHANNELS;
-  // strips of 32 rows (3 rows read twice in 32), or of 8 where that leaves the SMs idle
-  const int strip = (a.T + 31) / 32 * blocks_c >= 4 * sm_count ? 32 : 8;
+  // strips of 64 rows (3 rows read twice in 64), or of 8 where that leaves the SMs idle
+  const int strip = (a.T + 63) / 64 * blocks_c >= 4 * sm_count ? 64 : 8;
   const int64_t blocks = a.N + (a.T + strip - 1) / strip;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   return launch_pdl(conv_kernel<W>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(blocks_c)),

@@ -2,12 +2,13 @@
 // (kda_cache_reserve, kda_cache_release).
 //
 // Both are prefix sums over the sequences and a scatter: sequence n's pages lie in the
-// free list behind those of the sequences before it.  Every CTA of a small cluster takes
-// the sums over all sequences into its own shared memory (a few thousand lengths, from
-// L2), then the CTAs share the rows (reserve) or the pages (release) and find the
-// sequence of each by a binary search in shared memory; lengths and the count of free
-// pages may be updated in place, so they are written after a cluster barrier.  No sum
-// depends on the order in which anything runs.  Launch latency bounds both.
+// free list behind those of the sequences before it.  Every CTA takes the
+// sums over all sequences into its own shared memory (a few thousand lengths, from L2),
+// then the CTAs share the rows (reserve) or the pages (release) and find the sequence of
+// each by a binary search in shared memory.  Where lengths or the count of free pages are
+// updated in place, which others still read, the CTAs are one cluster and write them after
+// its barrier.  No sum depends on the order in which anything runs.  Launch latency bounds
+// both; 256 rows take less than the 9 us in which the host makes the call and its results.
 #include "kda_layers.cuh"
 
 namespace kda {
@@ -15,7 +16,8 @@ namespace kda {
 namespace {
 
 constexpr int PG_THREADS = 1024;
-constexpr int PG_CTAS = 8;
+constexpr int PG_CTAS = 8;               // of a cluster
+constexpr int PG_ROWS = 4 * PG_THREADS;  // rows of a CTA at a time
 
 struct Sums {
   long long x, y;
@@ -56,11 +58,6 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total)
   return v;
 }
 
-__device__ __forceinline__ unsigned cta_rank() {
-  unsigned r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
@@ -108,15 +105,16 @@ __device__ __forceinline__ long long pages_of(const PagesArgs& a, long long slot
 // Pages for the new rows of every sequence, in the order of the sequences: off[n] is the
 // number of pages taken before sequence n, or -1 if its rows get none.
 __global__ void __launch_bounds__(PG_THREADS)
-reserve_kernel(PagesArgs a, int* err) {
+reserve_kernel(PagesArgs a, bool in_place, int* err) {
   extern __shared__ int pages_smem[];
   __shared__ Sums warp_sums[32];
   __shared__ int taken;
-  int* cu = pages_smem;           // [N + 1]
-  int* off = pages_smem + a.N + 1;  // [N]
+  int* cu = pages_smem;                  // [N + 1]
+  int* off = pages_smem + a.N + 1;       // [N]
+  int* lens = pages_smem + 2 * a.N + 1;  // [N]
   grid_dep_wait();
   grid_dep_launch();
-  const unsigned rank = cta_rank(), ctas = gridDim.x;
+  const unsigned rank = blockIdx.x, ctas = gridDim.x;
   const int free_pages = free_count_of(a, err);
   if (threadIdx.x == 0) taken = 0;
   __syncthreads();
@@ -125,11 +123,12 @@ reserve_kernel(PagesArgs a, int* err) {
     const int n = n0 + threadIdx.x;
     Sums mine{0, 0};
     bool fits = true;
+    int len = 0;
     if (n < a.N) {
       const Span s = span_of(a, n, err);
       fits = s.fits;
-      const long long add = a.other[n];
-      mine.x = add < 0 ? 0 : add;
+      len = static_cast<int>(s.first);
+      mine.x = s.upto - s.first;
       mine.y = s.fits ? pages_of(a, s.upto) - pages_of(a, s.first) : 0;
     }
     Sums total;
@@ -142,6 +141,7 @@ reserve_kernel(PagesArgs a, int* err) {
       }
       const bool granted = fits && (mine.y == 0 || pages <= free_pages);
       cu[n + 1] = clamp32(rows, a.T);
+      lens[n] = len;
       off[n] = granted ? static_cast<int>(mine.y == 0 ? 0 : pages - mine.y) : -1;
       if (granted && mine.y > 0) atomicMax(&taken, static_cast<int>(pages));
     }
@@ -166,7 +166,7 @@ reserve_kernel(PagesArgs a, int* err) {
       if (t >= total) continue;
       while (t >= cu[n + 1]) ++n;  // t < cu[N]
       if (off[n] < 0) continue;
-      const long long len = a.lens[n], p = len + (t - cu[n]);
+      const long long len = lens[n], p = len + (t - cu[n]);
       const long long j = p >> a.lg, had = pages_of(a, len);
       int id;
       if (j >= had) {
@@ -186,10 +186,9 @@ reserve_kernel(PagesArgs a, int* err) {
       }
     }
   }
-  // every CTA has read the lengths and the count
-  cluster_barrier();
+  if (in_place) cluster_barrier();  // every CTA has read the lengths and the count
   for (int n = rank * PG_THREADS + threadIdx.x; n < a.N; n += ctas * PG_THREADS) {
-    const int len = a.lens[n];
+    const int len = lens[n];
     a.new_lens[n] = off[n] < 0 ? len : len + (cu[n + 1] - cu[n]);
     a.cu[n + 1] = cu[n + 1];
   }
@@ -201,14 +200,14 @@ reserve_kernel(PagesArgs a, int* err) {
 
 // Pages behind the slots that sequences keep, to the end of the free list.
 __global__ void __launch_bounds__(PG_THREADS)
-release_kernel(PagesArgs a, int* err) {
+release_kernel(PagesArgs a, bool in_place, int* err) {
   extern __shared__ int pages_smem[];
   __shared__ Sums warp_sums[32];
   int* from = pages_smem;             // [N + 1]: pages before sequence n's
   int* first = pages_smem + a.N + 1;  // [N]: its first page that goes
   grid_dep_wait();
   grid_dep_launch();
-  const unsigned rank = cta_rank(), ctas = gridDim.x;
+  const unsigned rank = blockIdx.x, ctas = gridDim.x;
   const int count = free_count_of(a, err);
   const int room = a.pages - count;
   long long before = 0;
@@ -240,20 +239,24 @@ release_kernel(PagesArgs a, int* err) {
     if (!there) bad(err);
     a.free_pages[count + i] = there ? id : -1;
   }
-  cluster_barrier();
+  if (in_place) cluster_barrier();
   if (rank == 0 && threadIdx.x == 0) *a.new_free_count = count + pages;
 }
 
 std::atomic<uint64_t> g_reserve_set{0}, g_release_set{0};
 
-cudaError_t launch(void (*kernel)(PagesArgs, int*), const PagesArgs& a, int ctas, int* err, cudaStream_t stream,
-                   std::atomic<uint64_t>& set) {
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), (2 * kPagesMaxN + 1) * 4, set);
+// Over `work` rows or pages at most, with `arrays` arrays of N in shared memory.
+cudaError_t launch(void (*kernel)(PagesArgs, bool, int*), const PagesArgs& a, int64_t work, int arrays, bool in_place,
+                   int* err, cudaStream_t stream, std::atomic<uint64_t>& set) {
+  const cudaError_t e =
+      ensure_smem_limit(reinterpret_cast<const void*>(kernel), (arrays * kPagesMaxN + 1) * 4, set);
   if (e != cudaSuccess) return e;
+  const int64_t most = in_place ? PG_CTAS : 128, want = (work + PG_ROWS - 1) / PG_ROWS;
+  const int ctas = want <= 1 ? 1 : in_place ? PG_CTAS : static_cast<int>(want < most ? want : most);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(PG_THREADS);
-  cfg.dynamicSmemBytes = static_cast<size_t>(2 * a.N + 1) * 4;
+  cfg.dynamicSmemBytes = static_cast<size_t>(arrays * a.N + 1) * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -263,19 +266,22 @@ cudaError_t launch(void (*kernel)(PagesArgs, int*), const PagesArgs& a, int ctas
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, err);
+  cfg.numAttrs = in_place ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, in_place, err);
 }
 
 }  // namespace
 
 cudaError_t launch_reserve(const PagesArgs& a, int* err, cudaStream_t stream) {
-  return launch(reserve_kernel, a, a.T > 4 * PG_THREADS ? PG_CTAS : 1, err, stream, g_reserve_set);
+  const bool in_place = a.new_lens == a.lens || a.new_free_count == a.free_count;
+  // without slots the rows may not be known: no more than the tables hold
+  const int64_t most = (static_cast<int64_t>(a.N) * a.width) << a.lg;
+  return launch(reserve_kernel, a, a.slots || a.T < most ? a.T : most, 3, in_place, err, stream, g_reserve_set);
 }
 
 cudaError_t launch_release(const PagesArgs& a, int* err, cudaStream_t stream) {
-  const long long most = static_cast<long long>(a.N) * a.width;
-  return launch(release_kernel, a, most > 4 * PG_THREADS ? PG_CTAS : 1, err, stream, g_release_set);
+  return launch(release_kernel, a, static_cast<int64_t>(a.N) * a.width, 2, a.new_free_count == a.free_count, err,
+                stream, g_release_set);
 }
 
 }  // namespace kda
