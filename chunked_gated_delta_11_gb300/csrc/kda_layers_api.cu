@@ -192,9 +192,9 @@ kda_status check_pages(const int32_t* table, int32_t width, const int32_t* lens,
                        const int32_t* new_free_count) {
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return KDA_ERR_UNSUPPORTED;
   if (N > kPagesMaxN) return KDA_ERR_UNSUPPORTED;
-  if (width <= 0 || N <= 0 || pages <= 0) return KDA_ERR_INVALID_ARG;
+  if (width <= 0 || N <= 0 || pages < 0) return KDA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(width) * page_size > 0x7fffff00LL) return KDA_ERR_INVALID_ARG;
-  if (!table || !lens || !free_pages || !free_count || !new_free_count) return KDA_ERR_INVALID_ARG;
+  if (!table || !lens || (pages > 0 && !free_pages) || !free_count || !new_free_count) return KDA_ERR_INVALID_ARG;
   if (!aligned(table, 4) || !aligned(lens, 4) || !aligned(free_pages, 4) || !aligned(free_count, 4) ||
       !aligned(new_free_count, 4))
     return KDA_ERR_INVALID_ARG;
