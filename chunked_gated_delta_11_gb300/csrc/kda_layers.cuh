@@ -44,8 +44,8 @@ cudaError_t launch_ssm_step(const SsmArgs& a, int P, int S, cudaStream_t stream)
 size_t ssm_workspace(int64_t T, int H, int G, int N, int P, int S);
 cudaError_t launch_ssm_fwd(const SsmArgs& a, int P, int S, void* ws, int* err, cudaStream_t stream);
 
-// log(1 + e^v), the step size of a token
-__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+// log(1 + e^v), the step size of a token; no branch, so that several are under way at once
+__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v))); }
 
 // Pages of a cache: what sequences take and give back.
 struct PagesArgs {

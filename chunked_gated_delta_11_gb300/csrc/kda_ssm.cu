@@ -157,8 +157,6 @@ __device__ __forceinline__ float minus_bf16(float v, uint16_t h) {
   return r;
 }
 
-__device__ __noinline__ float step_size(float v) { return softplus(v); }
-
 // One arrival a warp, after all its lanes.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -443,7 +441,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool in = there && 4 * l + e < len;
-            d[e] = in ? step_size(__bfloat162float(raw[e]) + bias) : 0.f;
+            d[e] = in ? softplus(__bfloat162float(raw[e]) + bias) : 0.f;
             s[e] = in ? rate * d[e] : 0.f;
           }
           // sums up to a token from the chunk's start, and behind it to the chunk's end
