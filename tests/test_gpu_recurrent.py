@@ -422,3 +422,14 @@ def test_refusals():
     with pytest.raises(TypeError, match="bfloat16"):
         kda.kda_conv_fwd(rows, w, initial_state=torch.zeros(1, 3, 24, device="cuda"))
     ok()
+
+
+def test_the_layer_serves_a_prompt_and_its_continuation():
+    """The example's path: prompts, then tokens one at a time, against one pass over all of them."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import state_space_layer
+    report = state_space_layer.main(["--tokens", "300", "--steps", "5", "--heads", "6"])
+    # the outputs of both are rounded to bf16 at the end and a few times on the way
+    assert report["outputs_differ"] < 1e-2 and report["states_differ"] < 1e-4
