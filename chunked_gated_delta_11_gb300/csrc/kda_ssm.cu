@@ -23,7 +23,16 @@
 //
 // Roundings.  x' enters the product with B as the sum of `terms` bf16 numbers: three hold
 // all 24 bits, so that a state in fp32 is one.  P and the copy of M that the outputs see are
-// rounded to bf16 once (2^-9 of the value at most, as the output).
+// rounded to bf16 once (2^-8 of the value at most, as the output).
+//
+// Measured (GB300; heads of 64, states of 128 in fp32): 16 ragged prompts, 33,600 tokens, 64 heads,
+// 235 us, about 6300 cycles a chunk.  The products themselves are 3100 of them; one lane
+// issues them in order, at 75 to 100 cycles each, because their operands take most of what
+// shared memory delivers beside what the roles read and write there (5300 of 128 bytes a
+// chunk), and the order S, M C, M' += .., P x waits for each role once.  Tried and slower:
+// two lanes that issue the outputs' and the state's products side by side (291 us), rolled
+// issue loops (247 to 260), 16-token places of x' (266), half of x' before M C (244); no
+// faster: eight warps for the weights or for the state.
 #include <type_traits>
 
 #include "kda_attn.cuh"
@@ -920,8 +929,12 @@ struct Plan {
 };
 
 // Sequences are cut where whole ones would leave SMs without work.  A piece's state from
-// zero takes about half of what the piece itself does, and each kernel a few chunks' time to
-// start and to end; the number of pieces is the one of least time under that count.
+// zero takes about half of what the piece itself does, each kernel a few chunks' time to
+// start and to end, and each piece before one half a chunk's (its state is read); the number
+// of pieces is the one of least time under that count.  Whole and cut, in us (heads of 64,
+// states of 128): 8192 tokens, 64 heads 191 and 100 (4 pieces; 5 take a second round: 134);
+// 16384 tokens, 8 heads 364 and 74 (16); 2048 tokens, 16 heads 52 and 35 (8); 1024 tokens, 64
+// heads 30 and 31 (4); four sequences of 2048 tokens, 64 heads 62 and 99 (2, not taken).
 Plan plan_of(int64_t T, int H, int G, int N, int P, int S) {
   Plan p{};
   p.units = units_of(H, G, P);
@@ -929,11 +942,11 @@ Plan plan_of(int64_t T, int H, int G, int N, int P, int S) {
   p.slots = N;
   const int64_t ctas = static_cast<int64_t>(N) * p.units, chunks = (T / N + SS_TOK - 1) / SS_TOK;
   if (ctas >= kSMs || chunks < 4) return p;
-  constexpr int64_t kEnds = 4;  // chunks' time, twice that of a kernel's start and end
+  constexpr int64_t kEnds = 4;  // of half a chunk's time
   int64_t best = 2 * chunks, k_best = 1;
   for (int64_t k = 2; k <= 32 && 2 * k <= chunks; ++k) {
     const int64_t each = (chunks + k - 1) / k;
-    const int64_t main = (ctas * k + kSMs - 1) / kSMs * (2 * each + kEnds);
+    const int64_t main = (ctas * k + kSMs - 1) / kSMs * (2 * each + kEnds) + k;
     const int64_t pre = (ctas * (k - 1) + kSMs - 1) / kSMs * (each + kEnds);
     if (main + pre - kEnds < best) {
       best = main + pre - kEnds;
