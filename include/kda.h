@@ -616,7 +616,17 @@ typedef struct {
  * are 64 or 128, N * H below 2^23.
  * kda_ssm_step: token by token with the state in registers, in fp32 throughout; for one or a
  *   few tokens a sequence, where moving the state is what counts.
- * kda_ssm_fwd: the same result for prompts. */
+ * kda_ssm_fwd: the same result for prompts, in chunks of 128 tokens.  Sums are fp32; the
+ *   weights between a chunk's tokens and the copy of the state that its outputs read are
+ *   rounded to bf16; what a token adds to the state keeps all bits of fp32 where the final
+ *   state is fp32 (16 where it is bf16, 8 where final_state is NULL).  Rows of other
+ *   sequences, whatever they hold, reach no result; inside a sequence a non-finite row of x, B,
+ *   C or dt can also spoil the outputs of the 127 tokens before it (they share its tile).
+ *   T_total is below 2^31 - 128.  Few sequences are cut into pieces that run at once and are
+ *   joined through their states, which takes a workspace: kda_ssm_workspace_size() bytes of
+ *   device memory (0 where none is cut), 16-byte aligned, or NULL (= cudaMallocAsync /
+ *   cudaFreeAsync on the stream).  The same call gives the same bits.
+ * Both: a wait that runs out on the device is reported by kda_device_status. */
 kda_status kda_ssm_step(const kda_ssm_options* opts, const void* x, const void* dt, const float* A,
                         const void* B, const void* C, const void* initial_state,
                         const int32_t* cu_seqlens, int64_t T_total, int32_t H, int32_t G, int32_t N,
