@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(CV_THREADS, 8)
 conv_kernel(ConvArgs a, int heads, int strip) {
   grid_dep_wait();
   grid_dep_launch();
-  const int c = (blockIdx.y * CV_THREADS + threadIdx.x) * CV_VEC;
+  int c = (blockIdx.y * CV_THREADS + threadIdx.x) * CV_VEC;
   if (static_cast<int>(blockIdx.x) < heads) {
     const int n = blockIdx.x;
     int64_t bos, eos;
@@ -125,11 +125,18 @@ conv_kernel(ConvArgs a, int heads, int strip) {
   int n = seq_of_slot(a.cu, a.T, a.N, 1, 0, t0);
   int64_t bos, eos;
   seq_bounds(a.cu, a.T, a.N, n, bos, eos);
-  if (c >= a.C) return;
+  // (threads behind the last channel write its values once more: whole warps look for sequences)
+  c = c < a.C ? c : a.C - CV_VEC;
   Taps<W> taps;
   bool loaded = false;
   for (int64_t t = t0; t < t1;) {
-    while (t >= eos && n + 1 < a.N) seq_bounds(a.cu, a.T, a.N, ++n, bos, eos);
+    if (t >= eos && n + 1 < a.N) seq_bounds(a.cu, a.T, a.N, ++n, bos, eos);
+    if (t >= eos && n + 1 < a.N) {  // empty ones between
+      const int at = seq_of_slot(a.cu, a.T, a.N, 1, 0, t);
+      n = at > n ? at : n + 1;
+      seq_bounds(a.cu, a.T, a.N, n, bos, eos);
+      if (t >= eos && n + 1 < a.N) continue;  // (a malformed cu_seqlens)
+    }
     if (t >= eos) return;  // rows behind the last sequence stay as they are
     // this sequence's rows of the strip, but for its first W - 1
     const int64_t end = eos < t1 ? eos : t1;

@@ -24,6 +24,8 @@
 // Roundings.  x' enters the product with B as the sum of `terms` bf16 numbers: three hold
 // all 24 bits, so that a state in fp32 is one.  P and the copy of M that the outputs see are
 // rounded to bf16 once (2^-8 of the value at most, as the output).
+// A state in fp32 is off by 1.4e-7 to 6e-7 of its norm, and by up to 1.9e-6 in a head that hardly
+// decays (A d = 0.002): a bias toward zero, from the 24 products that a chunk adds to it there.
 //
 // Measured (GB300; heads of 64, states of 128 in fp32): 16 ragged prompts, 33,600 tokens, 64 heads,
 // 235 us, about 6300 cycles a chunk.  The products themselves are 3100 of them; one lane
@@ -53,12 +55,13 @@ constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384, SS_P1 = 480; 
 constexpr int SS_GROUP = 32;             // tokens of a place of x'
 constexpr int SS_TERMS = 3;              // addends of x' at most, 16 columns each
 
-// Steps and decays of a chunk's tokens for one head, in units of log2.
+// Steps and decays of a chunk's tokens for one head, in units of log2.  All are sums of A d over the
+// tokens in question, and not differences of longer sums, but for those inside 32 tokens.
 struct SsmPrep {
-  float l[SS_TOK];   // sum of A d up to the token
+  float l[SS_TOK];   // sum of A d up to the token in its block of 32
   float r[SS_TOK];   // l_j - log2 d_j: e^{l_i - l_j} d_j = e^{l_i - r_j}; +inf behind the sequence's end
   float w[SS_TOK];   // e^{l_Q - l_j} d_j
-  float e[SS_TOK];   // e^{l_i}
+  float e[SS_TOK];   // e^{l_i}, l_i from the chunk's start
   float cf[192];     // e^{l_b - l_j} d_j, b the last token before rows 32, 64, 96 (32, 64, 96 of them)
   float keep, pad[3];  // e^{l_Q}
 };
@@ -453,7 +456,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             d[e] = in ? softplus(__bfloat162float(raw[e]) + bias) : 0.f;
             s[e] = in ? rate * d[e] : 0.f;
           }
-          // sums up to a token from the chunk's start, and behind it to the chunk's end
+          // sums up to a token from its block's start, and behind it to the block's end
           float pre[4], suf[4];
           pre[0] = s[0];
           suf[3] = 0.f;
@@ -462,27 +465,33 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             pre[e] = pre[e - 1] + s[e];
             suf[3 - e] = suf[4 - e] + s[4 - e];
           }
-          const float mine = pre[3];
-          float before = mine, behind = mine;
+          const int seat = l & 7;  // eight lanes a block
+          float upto = pre[3], from = pre[3];
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const float x = __shfl_up_sync(0xffffffffu, before, o), y = __shfl_down_sync(0xffffffffu, behind, o);
-            if (l >= o) before += x;
-            if (l + o < 32) behind += y;
+          for (int o = 1; o < 8; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, upto, o), y = __shfl_down_sync(0xffffffffu, from, o);
+            if (seat >= o) upto += x;
+            if (seat + o < 8) from += y;
           }
-          const float all = __shfl_sync(0xffffffffu, behind, 0);
-          const float lo = __shfl_up_sync(0xffffffffu, before, 1), hi = __shfl_down_sync(0xffffffffu, behind, 1);
-          const float start = l == 0 ? 0.f : lo, end = l == 31 ? 0.f : hi;
-          const float edge[3] = {__shfl_sync(0xffffffffu, before, 7), __shfl_sync(0xffffffffu, before, 15),
-                                 __shfl_sync(0xffffffffu, before, 23)};
+          float block[4];  // sums of whole blocks
+#pragma unroll
+          for (int b = 0; b < 4; ++b) block[b] = __shfl_sync(0xffffffffu, from, 8 * b);
+          const float lo = __shfl_up_sync(0xffffffffu, upto, 1), hi = __shfl_down_sync(0xffffffffu, from, 1);
+          const float before = seat == 0 ? 0.f : lo, behind = seat == 7 ? 0.f : hi;
+          const int mine = l >> 3;
+          float first = 0.f, last = tail;  // blocks before and behind the lane's
+#pragma unroll
+          for (int b = 0; b < 3; ++b) first += b < mine ? block[b] : 0.f;
+#pragma unroll
+          for (int b = 3; b > 0; --b) last += b > mine ? block[b] : 0.f;
           if (c >= 2 && !warp_wait(&ctl->prep_empty[st], ((c >> 1) - 1) & 1, ctl, err)) break;
           SsmPrep& o = prep[st * 2 + hh];
           float ll[4], ww[4], ee[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            ll[e] = start + pre[e];
-            ww[e] = ex2_approx(suf[e] + end + tail) * d[e];
-            ee[e] = ex2_approx(ll[e]);
+            ll[e] = before + pre[e];
+            ww[e] = ex2_approx(suf[e] + behind + last) * d[e];
+            ee[e] = ex2_approx(first + ll[e]);
           }
           *reinterpret_cast<float4*>(o.w + 4 * l) = make_float4(ww[0], ww[1], ww[2], ww[3]);
           if (!PRE) {
@@ -490,20 +499,25 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             *reinterpret_cast<float4*>(o.r + 4 * l) =
                 make_float4(ll[0] - __log2f(d[0]), ll[1] - __log2f(d[1]), ll[2] - __log2f(d[2]), ll[3] - __log2f(d[3]));
             *reinterpret_cast<float4*>(o.e + 4 * l) = make_float4(ee[0], ee[1], ee[2], ee[3]);
+            float between = 0.f;  // blocks between the lane's and block b
 #pragma unroll
-            for (int b = 1; b < 4; ++b)
-              if (l < 8 * b) {
+            for (int b = 1; b < 4; ++b) {
+              if (b - 1 > mine) between += block[b - 1];
+              if (b > mine) {
                 float f[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = ex2_approx(edge[b - 1] - ll[e]) * d[e];
+                for (int e = 0; e < 4; ++e) f[e] = ex2_approx(suf[e] + behind + between) * d[e];
                 *reinterpret_cast<float4*>(o.cf + 16 * b * (b - 1) + 4 * l) = make_float4(f[0], f[1], f[2], f[3]);
               }
+            }
           }
+          const float all = (block[0] + block[1]) + (block[2] + block[3]);
           if (PRE) tail += all;
-          if (l == 0) o.keep = ex2_approx(PRE ? tail : all);
+          // 2^all to half a step where it is near 1 and counts in many chunks
+          if (l == 0) o.keep = 1.f + expm1f(all * 0.693147181f);
           warp_arrive(&ctl->prep_full[st]);
         }
-        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = ex2_approx(tail);
+        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = 1.f + expm1f(tail * 0.693147181f);
       }
       __syncwarp();
     }
@@ -532,7 +546,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
 #pragma unroll
       for (int hh = 0; hh < HU; ++hh)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) ri[hh][k] = w > 0 ? ex2_approx(pr[hh].l[row + 8 * k] - pr[hh].l[w * 32 - 1]) : 0.f;
+        for (int k = 0; k < 4; ++k) ri[hh][k] = ex2_approx(pr[hh].l[row + 8 * k]);
 #pragma unroll 1
       for (int jb = 0; jb < w; ++jb) {
         load(jb);

@@ -81,6 +81,12 @@ def test_conv_long_rows_and_many_sequences():
     check_conv(conv_case(4, [1] * 300, 520, 4, True, True), [1] * 300, cu=False)
 
 
+@pytest.mark.parametrize("C", [24, 520])
+def test_conv_runs_of_empty_sequences(C):
+    lengths = [0] * 700 + [5] + [0] * 2000 + [40, 0, 1] + [0] * 90 + [2] + [0] * 33 + [66] + [0] * 500
+    check_conv(conv_case(10, lengths, C, 4, True, True), lengths)
+
+
 def test_conv_wide_rows_go_by_the_longer_strips():
     check_conv(conv_case(5, [4000, 100], 8 * 640, 4, False, True), [4000, 100])
 
