@@ -14,6 +14,7 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 constexpr int64_t kMaxElems = static_cast<int64_t>(1) << 40;
+constexpr int64_t kMaxSpan = static_cast<int64_t>(1) << 60;  // elements between a tensor's ends
 
 kda_status check_packing(int64_t T, int32_t N, const int32_t* cu) {
   if (T < 0 || T >= (static_cast<int64_t>(1) << 31) || N <= 0) return KDA_ERR_INVALID_ARG;
@@ -21,10 +22,10 @@ kda_status check_packing(int64_t T, int32_t N, const int32_t* cu) {
   return aligned(cu, 4) ? KDA_OK : KDA_ERR_INVALID_ARG;
 }
 
-// Rows of `row` elements, `stride` apart (0: one after the other).
-bool good_stride(int64_t& stride, int64_t row, int64_t unit) {
+// T rows of `row` elements, `stride` apart (0: one after the other).
+bool good_stride(int64_t& stride, int64_t T, int64_t row, int64_t unit) {
   if (stride == 0) stride = row;
-  return stride >= row && stride <= kMaxElems && stride % unit == 0;
+  return stride >= row && stride <= kMaxElems && T <= kMaxSpan / stride && stride % unit == 0;
 }
 
 // Bytes [p, p + bytes) and [q, q + more) have some in common.
@@ -66,8 +67,8 @@ kda_status check_ssm(const kda_ssm_options* o, const void* x, const void* dt, co
   a.b_stride = o->b_stride;
   a.c_stride = o->c_stride;
   const int64_t row = static_cast<int64_t>(H) * P, wide = static_cast<int64_t>(G) * S;
-  if (!good_stride(a.x_stride, row, 8) || !good_stride(a.dt_stride, H, 1) || !good_stride(a.b_stride, wide, 8) ||
-      !good_stride(a.c_stride, wide, 8))
+  if (!good_stride(a.x_stride, T, row, 8) || !good_stride(a.dt_stride, T, H, 1) ||
+      !good_stride(a.b_stride, T, wide, 8) || !good_stride(a.c_stride, T, wide, 8))
     return KDA_ERR_INVALID_ARG;
   if (!A || !aligned(A, 4) || !aligned(o->skip, 4) || !aligned(o->dt_bias, 4)) return KDA_ERR_INVALID_ARG;
   const int64_t state = static_cast<int64_t>(N) * H * P * S * (o->state_dtype == KDA_STATE_BF16 ? 2 : 4);
@@ -77,9 +78,13 @@ kda_status check_ssm(const kda_ssm_options* o, const void* x, const void* dt, co
     if (!aligned(x, 16) || !aligned(dt, 2) || !aligned(B, 16) || !aligned(C, 16) || !aligned(out, 16))
       return KDA_ERR_INVALID_ARG;
     const int64_t bytes = T * row * 2;
-    if (overlap(out, bytes, x, span(T, a.x_stride, row)) || overlap(out, bytes, dt, span(T, a.dt_stride, H)) ||
-        overlap(out, bytes, B, span(T, a.b_stride, wide)) || overlap(out, bytes, C, span(T, a.c_stride, wide)) ||
-        overlap(out, bytes, init, state) || overlap(out, bytes, fin, state))
+    const int64_t x_bytes = span(T, a.x_stride, row), dt_bytes = span(T, a.dt_stride, H);
+    const int64_t b_bytes = span(T, a.b_stride, wide), c_bytes = span(T, a.c_stride, wide);
+    if (overlap(out, bytes, x, x_bytes) || overlap(out, bytes, dt, dt_bytes) || overlap(out, bytes, B, b_bytes) ||
+        overlap(out, bytes, C, c_bytes) || overlap(out, bytes, init, state) || overlap(out, bytes, fin, state))
+      return KDA_ERR_INVALID_ARG;
+    if (overlap(fin, state, x, x_bytes) || overlap(fin, state, dt, dt_bytes) || overlap(fin, state, B, b_bytes) ||
+        overlap(fin, state, C, c_bytes))
       return KDA_ERR_INVALID_ARG;
   }
   a.x = static_cast<const __nv_bfloat16*>(x);
@@ -119,7 +124,7 @@ extern "C" kda_status kda_conv_fwd(const kda_conv_options* opts, const void* x, 
   if (static_cast<int64_t>(C) > 65535LL * 512) return KDA_ERR_INVALID_ARG;  // blocks of 512 channels
   if (static_cast<int64_t>(N) + T_total / 8 + 1 > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
   int64_t stride = opts->x_stride;
-  if (!good_stride(stride, C, 8)) return KDA_ERR_INVALID_ARG;
+  if (!good_stride(stride, T_total, C, 8)) return KDA_ERR_INVALID_ARG;
   if (!weight || !aligned(weight, 16) || !aligned(bias, 16)) return KDA_ERR_INVALID_ARG;
   const int64_t state = static_cast<int64_t>(N) * (W - 1) * C * 2, bytes = T_total * C * 2;
   if (!good_states(initial_state, final_state, state)) return KDA_ERR_INVALID_ARG;

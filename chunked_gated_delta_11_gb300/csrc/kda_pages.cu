@@ -232,8 +232,9 @@ release_kernel(PagesArgs a, bool in_place, int* err) {
   __syncthreads();
   if (before > room) bad(err);  // more than the pool has
   const int pages = from[a.N];
-  for (int i = rank * PG_THREADS + threadIdx.x; i < pages; i += ctas * PG_THREADS) {
-    const int n = last_at(from, a.N, i);
+  // (64 bits: the step behind the last page of the largest pool passes 32)
+  for (long long i = rank * PG_THREADS + threadIdx.x; i < pages; i += ctas * PG_THREADS) {
+    const int n = last_at(from, a.N, static_cast<int>(i));
     const int id = a.table[static_cast<long long>(n) * a.width + first[n] + (i - from[n])];
     const bool there = id >= 0 && id < a.pages;
     if (!there) bad(err);

@@ -89,6 +89,21 @@ def test_ssm_workspace(lib):
     assert size(-1, 4, 2, 1, 64, 128) == 0 and size(64, 4, 3, 1, 64, 128) == 0 and size(64, 4, 2, 1, 80, 128) == 0
 
 
+@pytest.mark.parametrize("entry,ws", [("kda_ssm_step", ()), ("kda_ssm_fwd", (None, 0))])
+@pytest.mark.parametrize("kw", [
+    dict(x=FAKE * 2, fin=FAKE * 2), dict(dt=FAKE * 2, fin=FAKE * 2), dict(B=FAKE * 2, fin=FAKE * 2),
+    dict(C=FAKE * 2, fin=FAKE * 2 - 65536 * 2 + 16),      # its last 16 bytes
+    # rows whose offsets would pass 64 bits
+    *(dict(T=1 << 30, out=1 << 45, strides=tuple(i == k and 1 << 40 for k in range(4))) for i in range(4)),
+])
+def test_ssm_rejects_states_over_inputs_and_endless_rows(lib, entry, ws, kw):
+    assert ssm(lib, entry=entry, ws=ws, **kw) == INVALID
+
+
+def test_conv_rejects_endless_rows(lib):
+    assert conv(lib, T=1 << 30, stride=1 << 40, out=1 << 45) == INVALID
+
+
 def reserve(lib, *, table=FAKE, width=8, lens=FAKE + (1 << 20), new=FAKE + (2 << 20), free=FAKE + (3 << 20),
             count=FAKE + (4 << 20), pages=64, page=64, T=128, N=4, new_lens=FAR, cu=FAR + (1 << 20), slots=FAR + (2 << 20),
             left=FAR + (3 << 20)):
