@@ -28,7 +28,7 @@
 // decays (A d = 0.002): a bias toward zero, from the 24 products that a chunk adds to it there.
 //
 // Measured (GB300; heads of 64, states of 128 in fp32): 16 ragged prompts, 33,600 tokens, 64 heads,
-// 235 us, about 6300 cycles a chunk.  The products themselves are 3100 of them; one lane
+// 239 us, about 6300 cycles a chunk (235 before decays were summed in blocks of 32).  The products themselves are 3100 of them; one lane
 // issues them in order, at 75 to 100 cycles each, because their operands take most of what
 // shared memory delivers beside what the roles read and write there (5300 of 128 bytes a
 // chunk), and the order S, M C, M' += .., P x waits for each role once.  Tried and slower:
