@@ -169,6 +169,10 @@ __device__ __forceinline__ float minus_bf16(float v, uint16_t h) {
   return r;
 }
 
+// 2^s, s <= 0, to half a step where it is near 1 and counts in many chunks, and to two steps of
+// itself where it is not (1 + expm1 would leave nothing of 2^-24 there).
+__device__ __forceinline__ float decay_of(float s) { return s > -0.5f ? 1.f + expm1f(s * 0.693147181f) : exp2f(s); }
+
 // One arrival a warp, after all its lanes.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -513,11 +517,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           }
           const float all = (block[0] + block[1]) + (block[2] + block[3]);
           if (PRE) tail += all;
-          // 2^all to half a step where it is near 1 and counts in many chunks
-          if (l == 0) o.keep = 1.f + expm1f(all * 0.693147181f);
+          if (l == 0) o.keep = decay_of(all);
           warp_arrive(&ctl->prep_full[st]);
         }
-        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = 1.f + expm1f(tail * 0.693147181f);
+        if (PRE && l == 0 && nc > 0) parts.keep[part * 2 + hh] = decay_of(tail);
       }
       __syncwarp();
     }
