@@ -54,12 +54,15 @@ constexpr int SS_REGS_WEIGHTS = 104, SS_REGS_ROWS = 64, SS_REGS_ISSUE = 56;
 constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384, SS_P1 = 480;  // columns
 constexpr int SS_GROUP = 32;             // tokens of a place of x'
 constexpr int SS_TERMS = 3;              // addends of x' at most, 16 columns each
+constexpr float SS_LEAST = -128.f;       // log2 of the strongest decay that a token counts for
 
 // Steps and decays of a chunk's tokens for one head, in units of log2.  All are sums of A d over the
-// tokens in question, and not differences of longer sums, but for those inside 32 tokens.
+// tokens in question, and not differences of longer sums, but for those inside 32 tokens.  So
+// that such a difference keeps its bits, a token counts for SS_LEAST at most: less than the least
+// float is left of anything behind it either way.
 struct SsmPrep {
   float l[SS_TOK];   // sum of A d up to the token in its block of 32
-  float r[SS_TOK];   // l_j - log2 d_j: e^{l_i - l_j} d_j = e^{l_i - r_j}; +inf behind the sequence's end
+  float d[SS_TOK];   // step size; 0 behind the sequence's end
   float w[SS_TOK];   // e^{l_Q - l_j} d_j
   float e[SS_TOK];   // e^{l_i}, l_i from the chunk's start
   float cf[192];     // e^{l_b - l_j} d_j, b the last token before rows 32, 64, 96 (32, 64, 96 of them)
@@ -459,6 +462,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             const bool in = there && 4 * l + e < len;
             d[e] = in ? softplus(__bfloat162float(raw[e]) + bias) : 0.f;
             s[e] = in ? rate * d[e] : 0.f;
+            if (s[e] < SS_LEAST) s[e] = SS_LEAST;  // (a NaN stays one)
           }
           // sums up to a token from its block's start, and behind it to the block's end
           float pre[4], suf[4];
@@ -500,8 +504,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           *reinterpret_cast<float4*>(o.w + 4 * l) = make_float4(ww[0], ww[1], ww[2], ww[3]);
           if (!PRE) {
             *reinterpret_cast<float4*>(o.l + 4 * l) = make_float4(ll[0], ll[1], ll[2], ll[3]);
-            *reinterpret_cast<float4*>(o.r + 4 * l) =
-                make_float4(ll[0] - __log2f(d[0]), ll[1] - __log2f(d[1]), ll[2] - __log2f(d[2]), ll[3] - __log2f(d[3]));
+            *reinterpret_cast<float4*>(o.d + 4 * l) = make_float4(d[0], d[1], d[2], d[3]);
             *reinterpret_cast<float4*>(o.e + 4 * l) = make_float4(ee[0], ee[1], ee[2], ee[3]);
             float between = 0.f;  // blocks between the lane's and block b
 #pragma unroll
@@ -581,17 +584,18 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         float li[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) li[k] = pr[hh].l[row + 8 * k];
-        const float* rj = pr[hh].r + w * 32 + col;
+        const float *lj = pr[hh].l + w * 32 + col, *dj = pr[hh].d + w * 32 + col;
         uint32_t p[2][8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = *reinterpret_cast<const float2*>(rj + 8 * j);
+          const float2 f = *reinterpret_cast<const float2*>(lj + 8 * j), d = *reinterpret_cast<const float2*>(dj + 8 * j);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t word = 0u;
             if (j <= k) {  // (others are behind the diagonal in every lane)
-              const float x0 = __uint_as_float(s[k >> 1][4 * j + 2 * (k & 1)]) * ex2_approx(li[k] - f.x);
-              const float x1 = __uint_as_float(s[k >> 1][4 * j + 2 * (k & 1) + 1]) * ex2_approx(li[k] - f.y);
+              // (d is a factor and not part of the exponent: a token's own weight is d whatever l is)
+              const float x0 = __uint_as_float(s[k >> 1][4 * j + 2 * (k & 1)]) * (ex2_approx(li[k] - f.x) * d.x);
+              const float x1 = __uint_as_float(s[k >> 1][4 * j + 2 * (k & 1) + 1]) * (ex2_approx(li[k] - f.y) * d.y);
               word = pack_bf16(8 * (j - k) <= ahead ? x0 : 0.f, 8 * (j - k) + 1 <= ahead ? x1 : 0.f);
             }
             p[k >> 1][2 * j + (k & 1)] = word;
