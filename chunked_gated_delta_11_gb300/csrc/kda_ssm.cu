@@ -21,9 +21,10 @@
 // 32.  The loops are kept short (rolled, and one copy of what two products share): unrolled,
 // the roles' code outgrew the instruction caches (37 % of fetches missed, 9300 cycles a chunk).
 //
-// Roundings.  x' enters the product with B as the sum of `terms` bf16 numbers: three hold
-// all 24 bits, so that a state in fp32 is one.  P and the copy of M that the outputs see are
-// rounded to bf16 once (2^-8 of the value at most, as the output).
+// Roundings.  x' enters the product with B as the sum of three bf16 numbers, which hold all 24
+// bits, so that a state in fp32 is one.  (Fewer where the caller takes the state in bf16 or not at all
+// gained 3 %, but the outputs of a call then depended on that.)  P and the copy of M that the outputs
+// see are rounded to bf16 once (2^-8 of the value at most, as the output).
 // A state in fp32 is off by 1.4e-7 to 6e-7 of its norm, and by up to 1.9e-6 in a head that hardly
 // decays (A d = 0.002): a bias toward zero, from the 24 products that a chunk adds to it there.
 //
@@ -53,7 +54,7 @@ constexpr int SS_THREADS = 896;
 constexpr int SS_REGS_WEIGHTS = 104, SS_REGS_ROWS = 64, SS_REGS_ISSUE = 56;
 constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384, SS_P1 = 480;  // columns
 constexpr int SS_GROUP = 32;             // tokens of a place of x'
-constexpr int SS_TERMS = 3;              // addends of x' at most, 16 columns each
+constexpr int SS_TERMS = 3;              // addends of x', 16 columns each
 constexpr float SS_LEAST = -128.f;       // log2 of the strongest decay that a token counts for
 
 // Steps and decays of a chunk's tokens for one head, in units of log2.  All are sums of A d over the
@@ -188,7 +189,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 // group and a place of its own (8192 tokens, 64 heads, four pieces: 45 us with two places).
 template <int P, int S, bool PRE>
 __global__ void __launch_bounds__(SS_THREADS, 1)
-ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, int terms, bool ranked, int* err) {
+ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, bool ranked, int* err) {
   using L = SsmSmem<S>;
   constexpr int HU = SS_TOK / P;  // heads of a unit
   constexpr int SB = L::SB;
@@ -394,14 +395,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             const uint32_t add = !PRE || c > 0 || q > 0;
             mma_ts_step<0, 0>(tmem + SS_M, x, b_lo, hi, id_m, add);
             mma_ts_step<8, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            if (terms > 1) {
-              mma_ts_step<16, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-              mma_ts_step<24, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            }
-            if (terms > 2) {
-              mma_ts_step<32, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-              mma_ts_step<40, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            }
+            mma_ts_step<16, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            mma_ts_step<24, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            mma_ts_step<32, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            mma_ts_step<40, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
             tc_commit(&ctl->xp_empty[place]);
           }
           if (!ok) break;
@@ -822,7 +819,6 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         // one bf16 addend after the other, each of what the ones before leave: three hold all 24 bits
 #pragma unroll
         for (int t = 0; t < SS_TERMS; ++t) {
-          if (t >= terms) break;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint32_t p[8];
@@ -992,12 +988,9 @@ cudaError_t launch_one(const SsmMaps& maps, const SsmArgs& a, const SsmParts& pa
   auto* kernel = ssm_kernel<P, S, PRE>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kernel), SsmSmem<S>::BYTES, done);
   if (e != cudaSuccess) return e;
-  // a state in fp32 takes all bits of its addends, one in bf16 two roundings' worth, and one
-  // that only the outputs see one
-  const int terms = !a.fin ? 1 : a.bf16_state ? 2 : 3;
   const bool ranked = !plan.split && a.cu && a.N > 1 && a.N <= kOrderMaxN;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(plan.slots * plan.units)), dim3(SS_THREADS), SsmSmem<S>::BYTES, stream,
-                    maps, a, parts, plan.piece, plan.units, terms, ranked, err);
+                    maps, a, parts, plan.piece, plan.units, ranked, err);
 }
 
 template <int P, int S>

@@ -619,9 +619,8 @@ typedef struct {
  *   few tokens a sequence, where moving the state is what counts.
  * kda_ssm_fwd: the same result for prompts, in chunks of 128 tokens.  Sums are fp32; the
  *   weights between a chunk's tokens and the copy of the state that its outputs read are
- *   rounded to bf16; what a token adds to the state keeps all bits of fp32 where the final
- *   state is fp32 (16 where it is bf16, 8 where final_state is NULL).  Rows of other
- *   sequences, whatever they hold, reach no result; inside a sequence a non-finite row of x, B,
+ *   rounded to bf16; what a token adds to the state keeps all bits of fp32, whichever state
+ *   the caller takes.  Rows of other sequences, whatever they hold, reach no result; inside a sequence a non-finite row of x, B,
  *   C or dt can also spoil the outputs of the 127 tokens before it (they share its tile).
  *   T_total is below 2^31 - 128.  Few sequences are cut into pieces that run at once and are
  *   joined through their states, which takes a workspace: kda_ssm_workspace_size() bytes of
