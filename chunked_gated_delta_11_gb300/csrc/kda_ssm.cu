@@ -10,23 +10,28 @@
 // B and C, or one of 128.  28 warps:
 //   warps 0-3    weights: S = C B^T (one thread a row) times e^{l_i - l_j} d_j, per head, in bf16
 //                over S in tensor memory
-//   warps 4-7    the state, a thread a channel: M in tensor memory (fp32), its bf16 copy for
-//                the products with C in shared memory, its decay
+//   warps 4-7    the state, a thread a channel: M' from M and the chunk's sum
 //   warps 8-15   the weighted rows x' = e^{l_Q - l_j} d_j x_j, transposed into tensor memory, as
 //                the left operand of M' += x'^T B: groups of 32 tokens, each four warps' every other
 //   warps 16-23  outputs: e^{l_i} M C_i + skip x_i in tensor memory, then the finished rows, four
 //                warps 64 channels
 //   warp 24      TMA;  warp 25  the products;  warps 26, 27  step sizes and decays
-// Tensor memory: S and P | Y | M, 128 columns each, x' (two places of a group), 96, and the rest of P,
-// 32.  The loops are kept short (rolled, and one copy of what two products share): unrolled,
+// Tensor memory: S and P | Y | a chunk's sum x'^T B, 128 columns each, x' (two places of a group), 96,
+// and 32 columns of M.
+// M is fp32: 64 columns in the state warps' registers, the others (of 128) in tensor and shared memory.
+// A chunk's products add up from zero, and their sum comes to M in one rounded fma.  An accumulator
+// is cut off, not rounded, at each of a chunk's 24 products: added to M itself they drew it toward
+// zero, by 4.2e-5 over 8192 tokens without decay and 2.1e-4 over 32,768.  As it is, M is off by 5e-7
+// of its norm however long the sequence.
+// (M as bf16 upper halves, which the copy is anyway, and lower ones beside them: 250 us for the 16
+// prompts below instead of 195, and the same with the output warps taking half of the columns.)
+// The loops are kept short (rolled, and one copy of what two products share): unrolled,
 // the roles' code outgrew the instruction caches (37 % of fetches missed, 9300 cycles a chunk).
 //
 // Roundings.  x' enters the product with B as the sum of three bf16 numbers, which hold all 24
 // bits, so that a state in fp32 is one.  (Fewer where the caller takes the state in bf16 or not at all
 // gained 3 %, but the outputs of a call then depended on that.)  P and the copy of M that the outputs
 // see are rounded to bf16 once (2^-8 of the value at most, as the output).
-// A state in fp32 is off by 1.4e-7 to 6e-7 of its norm, and by up to 1.9e-6 in a head that hardly
-// decays (A d = 0.002): a bias toward zero, from the 24 products that a chunk adds to it there.
 //
 // Measured (GB300; heads of 64, states of 128 in fp32): 16 ragged prompts, 33,600 tokens, 64 heads,
 // 239 us, about 6300 cycles a chunk (235 before decays were summed in blocks of 32).  The products themselves are 3100 of them; one lane
@@ -50,9 +55,10 @@ namespace {
 constexpr int SS_TOK = 128;              // tokens of a chunk, channels of a CTA
 constexpr int SS_BOX = SS_TOK * 128;     // bytes of 64 elements of 128 rows
 constexpr int SS_THREADS = 896;
-// seven warpgroups of 72 registers a thread at launch: 104 + 72 + 2 x 64 + 2 x 72 + 56 = 7 x 72
-constexpr int SS_REGS_WEIGHTS = 104, SS_REGS_ROWS = 64, SS_REGS_ISSUE = 56;
-constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_M = 256, SS_XP = 384, SS_P1 = 480;  // columns
+// seven warpgroups of 72 registers a thread at launch: 88 + 112 + 2 x 64 + 2 x 64 + 48 = 7 x 72
+// (PRE: 72 + 112 + 4 x 64 + 56)
+constexpr int SS_REGS_WEIGHTS = 88, SS_REGS_STATE = 112, SS_REGS_ROWS = 64, SS_REGS_OUT = 64, SS_REGS_ISSUE = 48;
+constexpr uint32_t SS_SP = 0, SS_Y = 128, SS_D = 256, SS_XP = 384, SS_M = 480;  // columns
 constexpr int SS_GROUP = 32;             // tokens of a place of x'
 constexpr int SS_TERMS = 3;              // addends of x', 16 columns each
 constexpr float SS_LEAST = -128.f;       // log2 of the strongest decay that a token counts for
@@ -78,7 +84,9 @@ struct SsmItem {
 
 struct SsmCtl {
   uint64_t x_full[2], x_empty[2], b_full[2], b_empty[2], c_full, c_empty, prep_full[2], prep_empty[2];
-  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, m_full, h_full, xp_full[4], xp_empty[4], zeroed, start_full, start_read, drained;
+  uint64_t s_full, p_full, yoff_full, y_scaled, y_full, y_empty, xp_full[4], xp_empty[4], zeroed, start_full, start_read, drained;
+  // a chunk's sum is there; M's copy for the next chunk is there and the sum has been read (PRE: two sums in turn)
+  uint64_t d_full[2], h_full[2];
   SsmItem item;
   uint32_t tmem;
   int abort;
@@ -93,7 +101,10 @@ template <int S>
 struct SsmSmem {
   static constexpr int SB = S / 64;
   static constexpr int X = 0, B = 4 * SS_BOX, C = B + 2 * SB * SS_BOX, H = C + SB * SS_BOX;
-  static constexpr int PREP = H + SB * SS_BOX;
+  static constexpr int M = H + SB * SS_BOX;  // M's last 32 columns of 128, 128 bytes a channel
+  static constexpr int PREP = M + (SB - 1) * SS_BOX;
+  // PRE: the state so far, fp32, over C and H
+  static constexpr int SUM = C;
   static constexpr int CTL = PREP + 4 * static_cast<int>(sizeof(SsmPrep));
   static constexpr int BYTES = CTL + 512 + 1024;
   // A state on its way in or out, 32 rows of 128 bytes at a time: in, over the second places of B and
@@ -158,12 +169,8 @@ __device__ __forceinline__ void tma_stores_read() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Columns of the weights of 32 keys, block jb of head hh.  They go where S has been read, block
-// after block (its columns 32 jb..): the first head's to 16 jb, the second's last two
-// blocks to 64 and 80; its first two to columns of their own.
-__device__ __forceinline__ uint32_t weights_at(int hh, int jb) {
-  return hh == 0 ? SS_SP + 16 * jb : jb < 2 ? SS_P1 + 16 * jb : SS_SP + 32 + 16 * jb;
-}
+// Columns of the weights of 32 keys, block jb of head hh: where the block of S was that they come from.
+__device__ __forceinline__ uint32_t weights_at(int hh, int jb) { return SS_SP + 32 * jb + 16 * hh; }
 
 // v - h for a bf16 h.
 __device__ __forceinline__ float minus_bf16(float v, uint16_t h) {
@@ -183,9 +190,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 }
 
 // PRE: only the state that each piece but a sequence's last adds, walking from its last
-// chunk to its first: with weights that reach to the piece's end, the products of all
-// chunks add up in tensor memory.  The output warps join in with x' there, each four with a
-// group and a place of its own (8192 tokens, 64 heads, four pieces: 45 us with two places).
+// chunk to its first, with weights that reach to the piece's end: the chunks' sums, two in turn
+// in tensor memory, add up in shared memory.  The output warps join in with x' there, each four with
+// a group and a place of its own (8192 tokens, 64 heads, four pieces: 45 us with two places).
 template <int P, int S, bool PRE>
 __global__ void __launch_bounds__(SS_THREADS, 1)
 ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int64_t piece, int units, bool ranked, int* err) {
@@ -225,8 +232,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
     mbar_init(&ctl->y_scaled, 8);
     mbar_init(&ctl->y_full, 1);
     mbar_init(&ctl->y_empty, 8);
-    mbar_init(&ctl->m_full, 1);
-    mbar_init(&ctl->h_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->d_full[i], 1);
+      mbar_init(&ctl->h_full[i], 4);
+    }
     for (int i = 0; i < SIDES; ++i) {
       mbar_init(&ctl->xp_full[i], 4);
       mbar_init(&ctl->xp_empty[i], 1);
@@ -284,7 +293,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   };
 
   if (w >= 24) {
-    regs_give<SS_REGS_ISSUE>();
+    regs_give<PRE ? 56 : SS_REGS_ISSUE>();
     if (w == 24) {
       if (l == 0) {
         bool ok = true;
@@ -364,7 +373,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             // one lane issues in order: S may follow into the columns P was read from.
 #pragma unroll 1
             for (int of_m = 0; of_m < 2; ++of_m) {
-              ok = wait_for(of_m ? &ctl->h_full : &ctl->c_full, c & 1, ctl, err);
+              ok = wait_for(of_m ? &ctl->h_full[0] : &ctl->c_full, c & 1, ctl, err);
               if (ok && of_m && c > 0) ok = wait_for(&ctl->y_empty, (c - 1) & 1, ctl, err);
               if (!ok) break;
               tc_fence_after();
@@ -384,6 +393,10 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             if (!ok) break;
             tc_commit(&ctl->c_empty);
           }
+          // the chunk's sum: into what the state warps have read (before M's copy was there, or two chunks ago)
+          const uint32_t sum = tmem + SS_D + (PRE ? st * 128 : 0);
+          if (PRE && c >= 2) ok = wait_for(&ctl->h_full[st], ((c >> 1) - 1) & 1, ctl, err);
+          if (!ok) break;
           const int groups = (len + SS_GROUP - 1) / SS_GROUP;
           for (int q = 0; q < groups; ++q) {
             const int place = q % SIDES;  // a whole chunk uses each 4 / SIDES times
@@ -391,18 +404,17 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             if (!ok) break;
             tc_fence_after();
             const uint32_t x = tmem + XP0 + place * 48, b_lo = cols_lo + b_stage + q * 256;
-            const uint32_t add = !PRE || c > 0 || q > 0;
-            mma_ts_step<0, 0>(tmem + SS_M, x, b_lo, hi, id_m, add);
-            mma_ts_step<8, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            mma_ts_step<16, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            mma_ts_step<24, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            mma_ts_step<32, 0>(tmem + SS_M, x, b_lo, hi, id_m, 1);
-            mma_ts_step<40, 128>(tmem + SS_M, x, b_lo, hi, id_m, 1);
+            mma_ts_step<0, 0>(sum, x, b_lo, hi, id_m, q > 0);
+            mma_ts_step<8, 128>(sum, x, b_lo, hi, id_m, 1);
+            mma_ts_step<16, 0>(sum, x, b_lo, hi, id_m, 1);
+            mma_ts_step<24, 128>(sum, x, b_lo, hi, id_m, 1);
+            mma_ts_step<32, 0>(sum, x, b_lo, hi, id_m, 1);
+            mma_ts_step<40, 128>(sum, x, b_lo, hi, id_m, 1);
             tc_commit(&ctl->xp_empty[place]);
           }
           if (!ok) break;
           tc_commit(&ctl->b_empty[st]);
-          if (!PRE || c + 1 == nc) tc_commit(&ctl->m_full);
+          tc_commit(&ctl->d_full[PRE ? st : 0]);
           if (!PRE) {
             ok = wait_for(&ctl->p_full, c & 1, ctl, err) && wait_for(&ctl->y_scaled, c & 1, ctl, err);
             if (!ok) break;
@@ -410,16 +422,16 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
             const int steps = (len + 15) / 16;
 #pragma unroll 1
             for (int hh = 0; hh < nh; ++hh) {
-              const uint32_t d = tmem + SS_Y + hh * 64, p = tmem + weights_at(hh, 0), p2 = tmem + weights_at(hh, 2);
+              const uint32_t d = tmem + SS_Y + hh * 64, p = tmem + weights_at(hh, 0);
               const uint32_t x_lo = cols_lo + x_stage + hh * BX;
               mma_ts_step<0, 0>(d, p, x_lo, hi, id_y, 1);
               if (steps > 1) mma_ts_step<8, 128>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 2) mma_ts_step<16, 256>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 3) mma_ts_step<24, 384>(d, p, x_lo, hi, id_y, 1);
-              if (steps > 4) mma_ts_step<0, 512>(d, p2, x_lo, hi, id_y, 1);
-              if (steps > 5) mma_ts_step<8, 640>(d, p2, x_lo, hi, id_y, 1);
-              if (steps > 6) mma_ts_step<16, 768>(d, p2, x_lo, hi, id_y, 1);
-              if (steps > 7) mma_ts_step<24, 896>(d, p2, x_lo, hi, id_y, 1);
+              if (steps > 2) mma_ts_step<32, 256>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 3) mma_ts_step<40, 384>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 4) mma_ts_step<64, 512>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 5) mma_ts_step<72, 640>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 6) mma_ts_step<96, 768>(d, p, x_lo, hi, id_y, 1);
+              if (steps > 7) mma_ts_step<104, 896>(d, p, x_lo, hi, id_y, 1);
             }
             tc_commit(&ctl->y_full);
             tc_commit(&ctl->x_empty[st]);
@@ -524,7 +536,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       __syncwarp();
     }
   } else if (w < 4) {
-    regs_take<SS_REGS_WEIGHTS>();
+    if (!PRE) regs_take<SS_REGS_WEIGHTS>();
     const uint32_t SP = tmem + SS_SP + (static_cast<uint32_t>(w * 32) << 16);
     const int i = w * 32 + l;
     for (int c = 0; !PRE && c < nc; ++c) {
@@ -617,13 +629,43 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       warp_arrive(&ctl->prep_empty[st]);
     }
   } else if (w < 8) {
+    regs_take<SS_REGS_STATE>();
     const int r = tid & 127, hh = r / P;  // channel of the unit, its head
     const bool there = hh < nh;
-    const uint32_t M = tmem + SS_M + (static_cast<uint32_t>((w & 3) * 32) << 16);
+    const uint32_t lanes = static_cast<uint32_t>((w & 3) * 32) << 16;
+    const uint32_t D = tmem + SS_D + lanes, M = tmem + SS_M + lanes;
     bool ok = true;
-    if (!PRE && it.len >= 0) {
+    if (PRE) {
+      float4* sum = reinterpret_cast<float4*>(smem + L::SUM) + r;
+      float4* dst = reinterpret_cast<float4*>(parts.m) + part * (S / 4) * SS_TOK + r;
+      for (int c = 0; ok && c < nc; ++c) {
+        ok = warp_wait(&ctl->d_full[c & 1], (c >> 1) & 1, ctl, err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int cb = 0; cb < S / 32; ++cb) {
+          uint32_t d[32];
+          tmem_ld32(D + (c & 1) * 128 + cb * 32, d);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            float4 v = make_float4(__uint_as_float(d[4 * q]), __uint_as_float(d[4 * q + 1]), __uint_as_float(d[4 * q + 2]),
+                                   __uint_as_float(d[4 * q + 3]));
+            const int at = (cb * 8 + q) * SS_TOK;
+            if (c > 0) {
+              const float4 u = sum[at];
+              v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            if (c + 1 < nc) sum[at] = v;
+            else dst[at] = v;
+          }
+        }
+        tc_fence_before();
+        warp_arrive(&ctl->h_full[c & 1]);
+      }
+    } else if (it.len >= 0) {
       if (start) ok = warp_wait(&ctl->start_full, 0, ctl, err);
-      // column `at` (in 16 bytes) of the channel's row
+      // column `at` (in 16 bytes) of the channel's row of the state that comes in
       auto piece16 = [&](int at) -> uint4 {
         return *reinterpret_cast<const uint4*>(smem + L::state_in((at >> 3) * (nh * P / 32) + (r >> 5)) + l * 128 +
                                                (((at & 7) ^ (l & 7)) << 4));
@@ -672,79 +714,119 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         uint32_t u[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(m[e]);
-        tmem_st32(M + cb * 32, u);
+        tmem_st32(D + cb * 32, u);
       }
       tmem_wait_st();
       warp_arrive(&ctl->start_read);
-      for (int c = 0; ok && c < nc; ++c) {
-        const int st = c & 1;
-        ok = (c == 0 || warp_wait(&ctl->m_full, (c - 1) & 1, ctl, err)) && warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err);
-        if (!ok) break;
-        tc_fence_after();
-        const float keep = prep[st * 2 + hh].keep;
-#pragma unroll 1
-        for (int cb = 0; cb < S / 32; ++cb) {
-          uint32_t m[32];
-          tmem_ld32(M + cb * 32, m);
+      // Sixteen columns of M each: h < 4 in registers, 4 and 5 in tensor memory, 6 and 7 in shared memory.
+      uint32_t m[64];
+      auto held = [&](int h, int q) { return reinterpret_cast<uint4*>(smem + L::M + r * 128 + (((4 * (h & 1) + q) ^ (r & 7)) << 4)); };
+      auto fetch = [&](int h, uint32_t (&v)[16]) {
+        if (h < 4) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = m[(16 * h + e) & 63];
+        } else if (h < 6) {
+          tmem_ld16(M + 16 * (h - 4), v);
           tmem_wait_ld();
-          uint8_t* dst = smem + L::H + (cb >> 1) * SS_BOX + r * 128;
+        } else {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
+            const uint4 x = *held(h, q);
+            v[4 * q] = x.x;
+            v[4 * q + 1] = x.y;
+            v[4 * q + 2] = x.z;
+            v[4 * q + 3] = x.w;
+          }
+        }
+      };
+      auto store = [&](int h, const uint32_t (&v)[16]) {
+        if (h < 4) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) m[(16 * h + e) & 63] = v[e];
+        } else if (h < 6) {
+          tmem_st16(M + 16 * (h - 4), v);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) *held(h, q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+      };
+      {
+        uint32_t none[16];  // -0: what is added to it stays
+#pragma unroll
+        for (int e = 0; e < 16; ++e) none[e] = 0x80000000u;
+#pragma unroll
+        for (int h = 0; h < S / 16; ++h) store(h, none);
+        tmem_wait_st();
+      }
+      // M becomes keep M + the sum in tensor memory: the state that the piece starts from, then chunk after
+      // chunk; the last one's M is the state at the end.
+      const bool wanted = it.last && a.fin != nullptr;
+      for (int c = -1; ok && c < nc; ++c) {
+        const int st = c & 1;
+        float keep = 1.f;
+        if (c >= 0) {
+          if (c + 1 == nc && !wanted) break;
+          ok = warp_wait(&ctl->prep_full[st], (c >> 1) & 1, ctl, err) && warp_wait(&ctl->d_full[0], c & 1, ctl, err);
+          if (!ok) break;
+          tc_fence_after();
+          keep = prep[st * 2 + hh].keep;
+        }
+        const f2 keeps = pair(keep, keep);
+        uint32_t d[2][16];
+        tmem_ld16(D, d[0]);
+#pragma unroll
+        for (int h = 0; h < S / 16; ++h) {
+          uint32_t v[16];
+          fetch(h, v);
+          tmem_wait_ld();
+          if (h + 1 < S / 16) tmem_ld16(D + 16 * (h + 1), d[(h + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            unpair(fma2(pair(v[e], v[e + 1]), keeps, pair(d[h & 1][e], d[h & 1][e + 1])), v[e], v[e + 1]);
+          store(h, v);
+          uint8_t* dst = smem + L::H + (h >> 2) * SS_BOX + r * 128;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
             uint32_t p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              p[e] = pack_bf16(__uint_as_float(m[8 * q + 2 * e]), __uint_as_float(m[8 * q + 2 * e + 1]));
-            *reinterpret_cast<uint4*>(dst + ((((cb & 1) * 4 + q) ^ (r & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
+              p[e] = pack_bf16(__uint_as_float(v[8 * q + 2 * e]), __uint_as_float(v[8 * q + 2 * e + 1]));
+            *reinterpret_cast<uint4*>(dst + ((((h & 3) * 2 + q) ^ (r & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
           }
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) unpair(mul2(pair(m[e], m[e + 1]), pair(keep, keep)), m[e], m[e + 1]);
-          tmem_st32(M + cb * 32, m);
         }
         tmem_wait_st();
-        fence_async();
-        tc_fence_before();
-        warp_arrive(&ctl->h_full);
-        warp_arrive(&ctl->prep_empty[st]);
+        if (c + 1 < nc) {
+          fence_async();
+          tc_fence_before();
+          warp_arrive(&ctl->h_full[0]);
+          if (c >= 0) warp_arrive(&ctl->prep_empty[st]);
+        }
       }
-    }
-    // the state at the end
-    if (ok && nc > 0) ok = warp_wait(&ctl->m_full, PRE ? 0 : (nc - 1) & 1, ctl, err);
-    if (ok && nc == 0 && start) ok = warp_wait(&ctl->start_read, 0, ctl, err);  // (it goes out over where it came in)
-    if (ok && (PRE ? nc > 0 : it.len >= 0 && it.last && a.fin != nullptr)) {
-      tc_fence_after();
-#pragma unroll 1
-      for (int cb = 0; cb < S / 32; ++cb) {
-        uint32_t m[32];
-        tmem_ld32(M + cb * 32, m);
-        tmem_wait_ld();
-        if (PRE) {
-          float4* dst = reinterpret_cast<float4*>(parts.m) + (part * (S / 4) + cb * 8) * SS_TOK + r;
+      if (ok && nc == 0 && start) ok = warp_wait(&ctl->start_read, 0, ctl, err);  // (it goes out over where it came in)
+      if (ok && wanted && there) {
+        // out through shared memory, by TMA
+        auto out16 = [&](int at) -> uint4* {
+          return reinterpret_cast<uint4*>(smem + L::state_out((at >> 3) * (nh * P / 32) + (r >> 5)) + l * 128 +
+                                          (((at & 7) ^ (l & 7)) << 4));
+        };
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[q * SS_TOK] = make_float4(__uint_as_float(m[4 * q]), __uint_as_float(m[4 * q + 1]),
-                                          __uint_as_float(m[4 * q + 2]), __uint_as_float(m[4 * q + 3]));
-        } else if (there) {
-          // out through shared memory, by TMA
-          auto piece16 = [&](int at) -> uint4* {
-            return reinterpret_cast<uint4*>(smem + L::state_out((at >> 3) * (nh * P / 32) + (r >> 5)) + l * 128 +
-                                            (((at & 7) ^ (l & 7)) << 4));
-          };
+        for (int h = 0; h < S / 16; ++h) {
+          uint32_t v[16];
+          fetch(h, v);
           if (a.bf16_state) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t p[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                p[e] = pack_bf16(__uint_as_float(m[8 * q + 2 * e]), __uint_as_float(m[8 * q + 2 * e + 1]));
-              *piece16(cb * 4 + q) = make_uint4(p[0], p[1], p[2], p[3]);
+                p[e] = pack_bf16(__uint_as_float(v[8 * q + 2 * e]), __uint_as_float(v[8 * q + 2 * e + 1]));
+              *out16(2 * h + q) = make_uint4(p[0], p[1], p[2], p[3]);
             }
           } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) *piece16(cb * 8 + q) = make_uint4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
+            for (int q = 0; q < 4; ++q) *out16(4 * h + q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
           }
         }
-      }
-      if (!PRE && there) {
         fence_async();
         __syncwarp();
         if (l == 0) {
@@ -818,7 +900,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
         if (used > 0 && !(ok = warp_wait(&ctl->xp_empty[place], (used - 1) & 1, ctl, err))) break;
         tc_fence_after();
         // One bf16 addend after the other, each of what the ones before leave: three hold all 24 bits.
-        // (Rolled: unrolled, 16 prompts took 200 us instead of 190.)
+        // (Rolled: unrolled, 16 prompts took 200 us instead of 185.)
 #pragma unroll 1
         for (int t = 0; t < SS_TERMS; ++t) {
 #pragma unroll
@@ -842,6 +924,7 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
       if (PRE) warp_arrive(&ctl->x_empty[st]);
     }
   } else {
+    regs_give<SS_REGS_OUT>();
     const int i = tid & 127, side = (w - 16) >> 2;  // row; 64 channels
     const int hh = side * 64 / P;                   // their head
     const bool there = hh < nh;
