@@ -369,12 +369,13 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           ok = wait_for(&ctl->b_full[st], (c >> 1) & 1, ctl, err);
           if (!ok) break;
           if (!PRE) {
-            // C with the rows of B, then with those of the state's copy.  The tensor core runs what
-            // one lane issues in order: S may follow into the columns P was read from.
+            // C with the rows of B, then with those of the state's copy.  S goes into the columns that the
+            // products of the chunk before read P from, and waits until they have ended: products of another
+            // shape and accumulator are not ordered by being issued first.
 #pragma unroll 1
             for (int of_m = 0; of_m < 2; ++of_m) {
               ok = wait_for(of_m ? &ctl->h_full[0] : &ctl->c_full, c & 1, ctl, err);
-              if (ok && of_m && c > 0) ok = wait_for(&ctl->y_empty, (c - 1) & 1, ctl, err);
+              if (ok && c > 0) ok = wait_for(of_m ? &ctl->y_empty : &ctl->y_full, (c - 1) & 1, ctl, err);
               if (!ok) break;
               tc_fence_after();
               const uint32_t d = tmem + (of_m ? SS_Y : SS_SP), b_lo = rows_lo + (of_m ? L::H >> 4 : b_stage);

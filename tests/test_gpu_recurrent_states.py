@@ -123,3 +123,22 @@ def test_the_error_of_a_state_does_not_grow_with_its_length(T, H, P, S, A, whole
     # no bias: the cuts of a chunk's own sum (24 halves of a step of half of it), the weights' functions
     bias = (err.sum() / want.sum()).item()
     assert abs(bias) <= 12 * 2.0 ** -24 + 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("lengths,H,G,P,S", [([2048] * 8, 64, 8, 64, 128), ([1500, 700, 2000, 128] * 3, 32, 1, 128, 64),
+                                             ([8192], 64, 8, 64, 128)])
+def test_the_same_bits_every_time(lengths, H, G, P, S):
+    """Every SM at work for many chunks, other work between the calls."""
+    case = [dev(t) for t in ssm_case(73, lengths, H, G, P, S, rate=0.2)]
+    cu = cu_of(lengths).cuda()
+    call = lambda: kda.kda_ssm_fwd(*case[:-1], initial_state=case[-1], cu_seqlens=cu)  # noqa: E731
+    out, fin = call()
+    want, state = kda.kda_ssm_step(*case[:-1], initial_state=case[-1], cu_seqlens=cu)
+    for got, ref_, tol in ((out, want, 1e-2), (fin, state, 1e-5)):
+        assert (got.double() - ref_.double()).norm() <= tol * ref_.double().norm()
+    for k in range(12):
+        if k % 3 == 2:
+            torch.empty(40 << 20, device="cuda").normal_()
+        again, fin2 = call()
+        assert torch.equal(again, out) and torch.equal(fin2, fin)
+    assert kda.kda_device_status() == 0
