@@ -481,6 +481,8 @@ static __device__ __noinline__ int seq_by_rank(const int32_t* __restrict__ cu, i
   }
   __syncthreads();
   const int n = *pick;
+  // TMA may write `scratch` next: these accesses come first for it too
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
   return n;
 }
