@@ -268,7 +268,9 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
   }
   if (w == 26 && l < 6) {
     const CUtensorMap* map = &maps.x + l;
-    if (l < 2 || (!PRE && (l < 4 || (l == 4 ? parts.init : a.fin)))) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+    // (without rows there are no maps of rows, without states none of states)
+    const bool used = l < 4 ? a.T > 0 && (l < 2 || !PRE) : !PRE && (l == 4 ? parts.init : a.fin) != nullptr;
+    if (used) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
   if (w == 25) {
     tmem_alloc(&ctl->tmem, 512);

@@ -142,3 +142,14 @@ def test_the_same_bits_every_time(lengths, H, G, P, S):
         again, fin2 = call()
         assert torch.equal(again, out) and torch.equal(fin2, fin)
     assert kda.kda_device_status() == 0
+
+
+@pytest.mark.parametrize("entry", ["kda_ssm_fwd", "kda_ssm_step"])
+@pytest.mark.parametrize("state", ["fp32", "bf16", None])
+def test_a_call_without_rows(entry, state):
+    case = ssm_case(74, [0, 0, 0], 3, 1, 64, 128, state)
+    out, fin = run_ssm(entry, case, [0, 0, 0])
+    assert out.shape == (0, 3, 64)
+    assert torch.equal(fin.cpu(), case[-1] if state else torch.zeros(3, 3, 64, 128))
+    out, fin = run_ssm(entry, case, [0, 0, 0], output_final_state=False)
+    assert out.numel() == 0 and fin is None
