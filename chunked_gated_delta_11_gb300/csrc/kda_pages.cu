@@ -171,6 +171,7 @@ reserve_kernel(PagesArgs a, bool in_place, int* err) {
       int id;
       if (j >= had) {
         id = a.free_pages[free_pages - 1 - (off[n] + (j - had))];
+        if (id < 0 || id >= a.pages) id = -1;
         if ((p & (page - 1)) == 0) a.table[static_cast<long long>(n) * a.width + j] = id;
       } else {
         id = a.table[static_cast<long long>(n) * a.width + j];

@@ -553,6 +553,7 @@ kda_status kda_cache_evict(const kda_cache* cache, const int32_t* block_table, i
  *   slots int64 [T_total]     page * page_size + place of every new row, -1 for the rows of
  *                             refused sequences and behind the last one; NULL: not wanted
  *   new_free_count int32 [1]  pages left; may be free_count
+ * An id outside the pool becomes -1 in the table.
  * T_total: the new rows that the call's packed tensors have (2^31 - 1 with slots == NULL
  * where that is not known); a sequence with rows beyond it is refused, and cu_seqlens stays
  * within it.  Rows of a sequence that was refused must not be appended (its table has no
