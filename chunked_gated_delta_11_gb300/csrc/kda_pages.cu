@@ -164,7 +164,7 @@ reserve_kernel(PagesArgs a, bool in_place, int* err) {
       const long long t = t0 + e;
       slot[e] = -1;
       if (t >= total) continue;
-      while (t >= cu[n + 1]) ++n;  // t < cu[N]
+      if (t >= cu[n + 1] && t >= cu[++n + 1]) n = last_at(cu, a.N, static_cast<int>(t));  // (t < cu[N]; empty ones between)
       if (off[n] < 0) continue;
       const long long len = lens[n], p = len + (t - cu[n]);
       const long long j = p >> a.lg, had = pages_of(a, len);

@@ -30,3 +30,12 @@ def test_an_id_outside_the_pool_does_not_reach_the_table(bad):
     # its rows have no slots: sequence 1's from position 48 on
     slots = r.slots.tolist()
     assert all((s == -1) == (10 + 18 <= i < 30) for i, s in enumerate(slots))
+
+
+@pytest.mark.parametrize("new", [[1] + [0] * 16382 + [1], [2 * (i % 997 == 5) + (i % 1009 == 7) for i in range(16384)],
+                                 [0] * 3000 + [5] + [0] * 40 + [1, 0, 0, 1] + [0] * 500])
+def test_rows_among_long_runs_of_sequences_without_any(new):
+    lens = [(7 * i) % 40 for i in range(len(new))]
+    need = sum(-(-(a + b) // 16) + (a // -16) for a, b in zip(lens, new))
+    table, free, count, pages = pool(11, lens, 16, 4, need)
+    check_reserve(table, lens, new, free, count, 16, pages, rows=sum(new) + 1)
