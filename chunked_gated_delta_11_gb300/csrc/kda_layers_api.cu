@@ -35,6 +35,17 @@ bool overlap(const void* p, int64_t bytes, const void* q, int64_t more) {
   return a < b + static_cast<uintptr_t>(more) && b < a + static_cast<uintptr_t>(bytes);
 }
 
+// Written arrays lie apart from the others (and from one another), but for those pairs that may be one.
+struct Range {
+  const void* at;
+  int64_t bytes;
+};
+bool apart(const Range& w, const Range* others, int n) {
+  for (int i = 0; i < n; ++i)
+    if (overlap(w.at, w.bytes, others[i].at, others[i].bytes)) return false;
+  return true;
+}
+
 int64_t span(int64_t T, int64_t stride, int64_t row) { return T > 0 ? ((T - 1) * stride + row) * 2 : 0; }
 
 // A state that is updated in place, or two that lie apart.
@@ -55,7 +66,7 @@ kda_status check_ssm_sizes(int64_t T, int32_t H, int32_t G, int32_t N, int32_t P
 
 kda_status check_ssm(const kda_ssm_options* o, const void* x, const void* dt, const float* A, const void* B,
                      const void* C, const void* init, const int32_t* cu, int64_t T, int32_t H, int32_t G, int32_t N,
-                     int32_t P, int32_t S, void* out, void* fin, SsmArgs& a) {
+                     int32_t P, int32_t S, void* out, void* fin, const void* ws, int64_t need, SsmArgs& a) {
   if (!o) return KDA_ERR_INVALID_ARG;
   kda_status s = check_ssm_sizes(T, H, G, N, P, S);
   if (s == KDA_OK) s = check_packing(T, N, cu);
@@ -77,16 +88,12 @@ kda_status check_ssm(const kda_ssm_options* o, const void* x, const void* dt, co
     if (!x || !dt || !B || !C || !out) return KDA_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(dt, 2) || !aligned(B, 16) || !aligned(C, 16) || !aligned(out, 16))
       return KDA_ERR_INVALID_ARG;
-    const int64_t bytes = T * row * 2;
-    const int64_t x_bytes = span(T, a.x_stride, row), dt_bytes = span(T, a.dt_stride, H);
-    const int64_t b_bytes = span(T, a.b_stride, wide), c_bytes = span(T, a.c_stride, wide);
-    if (overlap(out, bytes, x, x_bytes) || overlap(out, bytes, dt, dt_bytes) || overlap(out, bytes, B, b_bytes) ||
-        overlap(out, bytes, C, c_bytes) || overlap(out, bytes, init, state) || overlap(out, bytes, fin, state))
-      return KDA_ERR_INVALID_ARG;
-    if (overlap(fin, state, x, x_bytes) || overlap(fin, state, dt, dt_bytes) || overlap(fin, state, B, b_bytes) ||
-        overlap(fin, state, C, c_bytes))
-      return KDA_ERR_INVALID_ARG;
   }
+  // inputs, then the initial state and what is written (also the workspace: need == 0 where there is none)
+  const Range all[] = {{x, span(T, a.x_stride, row)}, {dt, span(T, a.dt_stride, H)}, {B, span(T, a.b_stride, wide)},
+                       {C, span(T, a.c_stride, wide)}, {A, H * 4LL}, {o->skip, H * 4LL}, {o->dt_bias, H * 4LL},
+                       {cu, (N + 1LL) * 4}, {init, state}, {fin, state}, {out, T * row * 2}};
+  if (!apart(all[9], all, 8) || !apart(all[10], all, 10) || !apart({ws, need}, all, 11)) return KDA_ERR_INVALID_ARG;
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.dt = static_cast<const __nv_bfloat16*>(dt);
   a.B = static_cast<const __nv_bfloat16*>(B);
@@ -128,13 +135,10 @@ extern "C" kda_status kda_conv_fwd(const kda_conv_options* opts, const void* x, 
   if (!weight || !aligned(weight, 16) || !aligned(bias, 16)) return KDA_ERR_INVALID_ARG;
   const int64_t state = static_cast<int64_t>(N) * (W - 1) * C * 2, bytes = T_total * C * 2;
   if (!good_states(initial_state, final_state, state)) return KDA_ERR_INVALID_ARG;
-  if (T_total > 0) {
-    if (!x || !out || !aligned(x, 16) || !aligned(out, 16)) return KDA_ERR_INVALID_ARG;
-    const int64_t rows = span(T_total, stride, C);
-    if (overlap(out, bytes, x, rows) || overlap(out, bytes, initial_state, state) ||
-        overlap(out, bytes, final_state, state) || overlap(final_state, state, x, rows))
-      return KDA_ERR_INVALID_ARG;
-  }
+  if (T_total > 0 && (!x || !out || !aligned(x, 16) || !aligned(out, 16))) return KDA_ERR_INVALID_ARG;
+  const Range all[] = {{x, span(T_total, stride, C)}, {weight, C * 2LL * W}, {bias, C * 2LL}, {cu_seqlens, (N + 1LL) * 4},
+                       {initial_state, state}, {final_state, state}, {out, bytes}};
+  if (!apart(all[5], all, 4) || !apart(all[6], all, 6)) return KDA_ERR_INVALID_ARG;
   int sms = 0, *err = nullptr;
   if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;
   ConvArgs a{};
@@ -160,7 +164,7 @@ extern "C" kda_status kda_ssm_step(const kda_ssm_options* opts, const void* x, c
                                    int32_t S, void* out, void* final_state, void* stream) {
   SsmArgs a;
   const kda_status s = check_ssm(opts, x, dt, A, B, C, initial_state, cu_seqlens, T_total, H, G, N, P, S, out,
-                                 final_state, a);
+                                 final_state, nullptr, 0, a);
   if (s != KDA_OK) return s;
   return launch_ssm_step(a, P, S, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
@@ -176,12 +180,13 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_options* opts, const void* x, co
                                   int32_t N, int32_t P, int32_t S, void* out, void* final_state,
                                   void* workspace, size_t workspace_bytes, void* stream) {
   SsmArgs a;
-  kda_status s = check_ssm(opts, x, dt, A, B, C, initial_state, cu_seqlens, T_total, H, G, N, P, S, out, final_state, a);
+  const size_t need = kda_ssm_workspace_size(T_total, H, G, N, P, S);
+  if (workspace && (!aligned(workspace, 16) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  kda_status s = check_ssm(opts, x, dt, A, B, C, initial_state, cu_seqlens, T_total, H, G, N, P, S, out, final_state,
+                           workspace, static_cast<int64_t>(need), a);
   if (s != KDA_OK) return s;
   if (T_total >= kSsmMaxT) return KDA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t need = ssm_workspace(T_total, H, G, N, P, S);
-  if (workspace && (!aligned(workspace, 16) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   int sms = 0, *err = nullptr;
   if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;
   Workspace ws(workspace, workspace_bytes, need, st);
@@ -207,17 +212,6 @@ kda_status check_pages(const int32_t* table, int32_t width, const int32_t* lens,
 }
 
 int log2_of(int32_t page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7; }
-
-// Written arrays lie apart from the others (and from one another), but for those pairs that may be one.
-struct Range {
-  const void* at;
-  int64_t bytes;
-};
-bool apart(const Range& w, const Range* others, int n) {
-  for (int i = 0; i < n; ++i)
-    if (overlap(w.at, w.bytes, others[i].at, others[i].bytes)) return false;
-  return true;
-}
 
 }  // namespace
 

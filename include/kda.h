@@ -581,8 +581,8 @@ kda_status kda_cache_release(const int32_t* block_table, int32_t table_width, co
  * out of wider rows (a stride in elements between rows, 0 = C or the row's own
  * length, a multiple of 8 but for dt).  Rows behind the last sequence are not
  * written.  Pointers 16-byte aligned, dt 2, fp32 and int32 arrays 4.  out must not
- * overlap an input or a state, nor final_state an input of rows; initial_state and
- * final_state are the same buffer or lie apart.  Calls are asynchronous on `stream`
+ * overlap an input or a state, nor final_state an input, nor a workspace any of them;
+ * initial_state and final_state are the same buffer or lie apart.  Calls are asynchronous on `stream`
  * and keep nothing between calls.
  * ------------------------------------------------------------------------ */
 typedef struct {
