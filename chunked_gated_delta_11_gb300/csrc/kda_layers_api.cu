@@ -53,6 +53,7 @@ bool good_states(const void* init, const void* fin, int64_t bytes) {
   return aligned(init, 16) && aligned(fin, 16) && (init == fin || !overlap(init, bytes, fin, bytes));
 }
 
+constexpr int64_t kMaxMapStride = static_cast<int64_t>(1) << 39;  // elements of 2 bytes between a tensor map's rows
 constexpr int64_t kSsmMaxT = (static_cast<int64_t>(1) << 31) - 128;  // a chunk's end is an int32 too
 
 kda_status check_ssm_sizes(int64_t T, int32_t H, int32_t G, int32_t N, int32_t P, int32_t S) {
@@ -186,6 +187,7 @@ extern "C" kda_status kda_ssm_fwd(const kda_ssm_options* opts, const void* x, co
                            workspace, static_cast<int64_t>(need), a);
   if (s != KDA_OK) return s;
   if (T_total >= kSsmMaxT) return KDA_ERR_INVALID_ARG;
+  if (a.x_stride >= kMaxMapStride || a.b_stride >= kMaxMapStride || a.c_stride >= kMaxMapStride) return KDA_ERR_INVALID_ARG;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   int sms = 0, *err = nullptr;
   if ((s = device_info_for_attn(&sms, &err)) != KDA_OK) return s;

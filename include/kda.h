@@ -623,7 +623,7 @@ typedef struct {
  *   rounded to bf16; what a token adds to the state keeps all bits of fp32, whichever state
  *   the caller takes.  Rows of other sequences, whatever they hold, reach no result; inside a sequence a non-finite row of x, B,
  *   C or dt can also spoil the outputs of the 127 tokens before it (they share its tile).
- *   T_total is below 2^31 - 128.  Few sequences are cut into pieces that run at once and are
+ *   T_total is below 2^31 - 128, strides of x, B and C below 2^39.  Few sequences are cut into pieces that run at once and are
  *   joined through their states, which takes a workspace: kda_ssm_workspace_size() bytes of
  *   device memory (0 where none is cut), 16-byte aligned, or NULL (= cudaMallocAsync /
  *   cudaFreeAsync on the stream).  The same call gives the same bits.

@@ -38,3 +38,10 @@ def test_ssm_rejects_a_workspace_over_the_rest(lib, name):  # noqa: F811
     # one that is too small or skewed is refused as that
     assert ssm(lib, entry="kda_ssm_fwd", T=8192, ws=(HERE, need - 1), **{**far, name: HERE}) == WORKSPACE
     assert ssm(lib, entry="kda_ssm_fwd", T=8192, ws=(HERE + 8, need), **far) == WORKSPACE
+
+
+@pytest.mark.parametrize("which", [0, 2, 3])
+def test_ssm_fwd_rejects_strides_that_no_tensor_map_holds(lib, which):  # noqa: F811
+    strides = tuple(i == which and 1 << 39 for i in range(4))
+    kw = dict(T=2, strides=strides, out=1 << 50, fin=1 << 52)
+    assert ssm(lib, entry="kda_ssm_fwd", ws=(None, 0), **kw) == INVALID
