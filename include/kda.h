@@ -618,15 +618,18 @@ typedef struct {
  * are 64 or 128, N * H below 2^23.
  * kda_ssm_step: token by token with the state in registers, in fp32 throughout; for one or a
  *   few tokens a sequence, where moving the state is what counts.
- * kda_ssm_fwd: the same result for prompts, in chunks of 128 tokens.  Sums are fp32; the
- *   weights between a chunk's tokens and the copy of the state that its outputs read are
- *   rounded to bf16; what a token adds to the state keeps all bits of fp32, whichever state
- *   the caller takes.  Rows of other sequences, whatever they hold, reach no result; inside a sequence a non-finite row of x, B,
- *   C or dt can also spoil the outputs of the 127 tokens before it (they share its tile).
- *   T_total is below 2^31 - 128, strides of x, B and C below 2^39.  Few sequences are cut into pieces that run at once and are
- *   joined through their states, which takes a workspace: kda_ssm_workspace_size() bytes of
- *   device memory (0 where none is cut), 16-byte aligned, or NULL (= cudaMallocAsync /
- *   cudaFreeAsync on the stream).  The same call gives the same bits.
+ * kda_ssm_fwd: the same result for prompts, in chunks of 128 tokens.  Sums and states are fp32, and what
+ *   a token adds to the state keeps all bits of fp32, whichever state the caller takes; an fp32
+ *   state is off by about 5e-7 of its norm at any length.  The weights between a chunk's tokens and
+ *   the copy of the state that its outputs read are rounded to bf16 once, for the tensor cores;
+ *   beside the rounding of the outputs themselves that adds 5 to 25 % to their error (kda_ssm_step
+ *   has neither, for any number of tokens).  Rows of other sequences, whatever they hold, reach
+ *   no result; a non-finite value of x can also spoil its own channel in the up to 127 tokens of its
+ *   sequence before it (they share a tile), one of dt, B or C nothing before it.
+ *   T_total is below 2^31 - 128, strides of x, B and C below 2^39.  Few sequences are cut into
+ *   pieces that run at once and are joined through their states, which takes a workspace:
+ *   kda_ssm_workspace_size() bytes of device memory (0 where none is cut), 16-byte aligned, or
+ *   NULL (= cudaMallocAsync / cudaFreeAsync on the stream).  The same call gives the same bits.
  * Both: a wait that runs out on the device is reported by kda_device_status. */
 kda_status kda_ssm_step(const kda_ssm_options* opts, const void* x, const void* dt, const float* A,
                         const void* B, const void* C, const void* initial_state,

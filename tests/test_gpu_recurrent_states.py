@@ -153,3 +153,28 @@ def test_a_call_without_rows(entry, state):
     assert torch.equal(fin.cpu(), case[-1] if state else torch.zeros(3, 3, 64, 128))
     out, fin = run_ssm(entry, case, [0, 0, 0], output_final_state=False)
     assert out.numel() == 0 and fin is None
+
+
+@pytest.mark.parametrize("entry", ["kda_ssm_fwd", "kda_ssm_step"])
+@pytest.mark.parametrize("at", [200, 255, 256, 300])
+def test_what_a_token_that_is_not_finite_reaches(entry, at):
+    """Nothing before it but, in the chunks' form and through x alone, its own channel in its chunk."""
+    lengths, H, P = [450], 3, 64
+    case = ssm_case(75, lengths, H, 1, P, 128, rate=0.5)
+    out, _ = run_ssm(entry, case, lengths)
+    for which in (1, 3, 4):                       # dt, B, C
+        spoilt = [t if t is None else t.clone() for t in case]
+        spoilt[which][at] = float("nan")
+        got, fin = run_ssm(entry, spoilt, lengths)
+        assert torch.equal(got[:at], out[:at])
+        assert torch.isnan(got[at]).all()
+        assert torch.isnan(fin).all() == (which != 4) and (which != 4 or torch.equal(got[at + 1:], out[at + 1:]))
+    spoilt = [t if t is None else t.clone() for t in case]
+    spoilt[0][at, 1, 7] = float("inf")
+    got, fin = run_ssm(entry, spoilt, lengths)
+    chunk = at // ref.CHUNK * ref.CHUNK
+    first = chunk if entry == "kda_ssm_fwd" else at
+    mine = torch.zeros_like(out, dtype=torch.bool)
+    mine[first:, 1, 7] = True
+    assert torch.equal(got[~mine], out[~mine])
+    assert not torch.isfinite(got[at:, 1, 7]).any() and not torch.isfinite(fin[0, 1, 7]).any()
