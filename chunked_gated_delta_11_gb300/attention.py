@@ -183,8 +183,9 @@ def kda_cache_reserve(block_table, lens, new_rows, free_pages, free_count, page_
     the free list (free_pages int32 [pages], a place for every page of the pool; the first
     free_count int32 [1] are free) and entered in block_table int32 [N, width], in the order
     of the sequences.  A sequence that the list or its row of the table has no room for
-    gets none.  rows: the new rows of the call's packed tensors, for their slots (None:
-    no slots).  new_lens may be lens, new_free_count free_count; without them the results
+    gets none; its rows must not be appended.  (Without them: the rows with slots >= 0 first,
+    packed by the sums of the new lengths less the old.)  rows: the new rows of the call's
+    packed tensors, for their slots (None: no slots).  new_lens may be lens, new_free_count free_count; without them the results
     are new tensors.  Returns a Reservation."""
     b = _binding or load_binding()
     return Reservation(*_run(stream, "kda_cache_reserve", b.cache_reserve, block_table, lens, new_rows,

@@ -557,11 +557,14 @@ kda_status kda_cache_evict(const kda_cache* cache, const int32_t* block_table, i
  * T_total: the new rows that the call's packed tensors have (2^31 - 1 with slots == NULL
  * where that is not known); a sequence with rows beyond it is refused, and cu_seqlens stays
  * within it.  Rows of a sequence that was refused must not be appended (its table has no
- * pages for them).
+ * pages for them); to go on without them, put the rows that have slots first, in their order, and
+ * pack them by the sums of new_lens - lens (rows behind the last sequence are left alone by every
+ * call here).  slots 16-byte aligned, the others 4.
  *
  * kda_cache_release: the pages behind each sequence's first keep[n] slots (keep == NULL: all
  * pages) go to the end of the free list, in the order of the tables.  A page belongs to the
- * sequence if its lens[n] slots need it; block_table and lens are left as they are.
+ * sequence if its lens[n] slots need it, and to no other; block_table and lens are left as they
+ * are.
  * new_free_count as above.  An id outside the pool becomes -1 in the list. */
 kda_status kda_cache_reserve(int32_t* block_table, int32_t table_width, const int32_t* lens,
                              const int32_t* new_rows, const int32_t* free_pages,
