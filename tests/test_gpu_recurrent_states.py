@@ -123,6 +123,7 @@ def test_the_error_of_a_state_does_not_grow_with_its_length(T, H, P, S, A, whole
     # no bias: the cuts of a chunk's own sum (24 halves of a step of half of it), the weights' functions
     bias = (err.sum() / want.sum()).item()
     assert abs(bias) <= 12 * 2.0 ** -24 + 8 * 2.0 ** -24
+    assert err.norm() <= (ed + 12 * 2.0 ** -24) * want.norm()
 
 
 @pytest.mark.parametrize("lengths,H,G,P,S", [([2048] * 8, 64, 8, 64, 128), ([1500, 700, 2000, 128] * 3, 32, 1, 128, 64),
@@ -178,3 +179,23 @@ def test_what_a_token_that_is_not_finite_reaches(entry, at):
     mine[first:, 1, 7] = True
     assert torch.equal(got[~mine], out[~mine])
     assert not torch.isfinite(got[at:, 1, 7]).any() and not torch.isfinite(fin[0, 1, 7]).any()
+
+
+def test_a_convolution_for_each_of_q_k_and_v():
+    """Columns of the projected rows, where they lie: the tensors that the KDA pass takes, without a copy."""
+    lengths, H, D = [70, 1, 200], 2, 128
+    T, n = sum(lengths), 2 * 128
+    g = gen(76)
+    rows, taps, held = randn(g, T, 3 * n).cuda(), randn(g, 3 * n, 4).cuda(), randn(g, 3, 3, 3 * n).cuda()
+    cu = cu_of(lengths).cuda()
+    out, fin = kda.kda_conv_fwd(rows, taps, initial_state=held, cu_seqlens=cu)
+    parts = [kda.kda_conv_fwd(rows[:, c], taps[c], initial_state=held[..., c].contiguous(), cu_seqlens=cu)
+             for c in (slice(i * n, i * n + n) for i in range(3))]
+    for i, (o, f) in enumerate(parts):
+        assert o.is_contiguous() and torch.equal(o, out[:, i * n:i * n + n]) and torch.equal(f, fin[..., i * n:i * n + n])
+    q, k, v = (o.view(T, H, D) for o, _ in parts)
+    gate, beta = randn(g, T, H, D).cuda(), randn(g, T, H).cuda()
+    got, state = kda.kda_fwd_fused(q, k, v, gate, beta, D ** -0.5, -5.0, cu_seqlens=cu)
+    want, ref_ = kda.kda_fwd_fused(*(t.contiguous() for t in out.view(T, 3, H, D).unbind(1)), gate, beta, D ** -0.5, -5.0,
+                                   cu_seqlens=cu)
+    assert torch.equal(got, want) and torch.equal(state, ref_) and kda.kda_device_status() == 0
