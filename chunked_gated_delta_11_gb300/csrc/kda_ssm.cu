@@ -23,23 +23,25 @@
 // is cut off, not rounded, at each of a chunk's 24 products: added to M itself they drew it toward
 // zero, by 4.2e-5 over 8192 tokens without decay and 2.1e-4 over 32,768.  As it is, M is off by 5e-7
 // of its norm however long the sequence.
-// (M as bf16 upper halves, which the copy is anyway, and lower ones beside them: 250 us for the 16
-// prompts below instead of 195, and the same with the output warps taking half of the columns.)
+// (M as bf16 upper halves, which the copy is anyway, and lower ones beside them: 263 us for 16 other
+// prompts that take 195; 252 with the output warps at half of the columns.)
 // The loops are kept short (rolled, and one copy of what two products share): unrolled,
 // the roles' code outgrew the instruction caches (37 % of fetches missed, 9300 cycles a chunk).
 //
 // Roundings.  x' enters the product with B as the sum of three bf16 numbers, which hold all 24
 // bits, so that a state in fp32 is one.  (Fewer where the caller takes the state in bf16 or not at all
 // gained 3 %, but the outputs of a call then depended on that.)  P and the copy of M that the outputs
-// see are rounded to bf16 once (2^-8 of the value at most, as the output).
+// see are rounded to bf16 once (2^-8 of the value at most, as the output): their error against 64 bits is
+// 1.7e-3 to 1.9e-3, 2.1e-3 for a short prompt from a state, where rounding them alone gives 1.66e-3.
+// A second addend of P has no columns left in tensor memory, one of the copy no room in shared memory.
 //
 // Measured (GB300; heads of 64, states of 128 in fp32): 16 ragged prompts, 33,600 tokens, 64 heads,
-// 239 us, about 6300 cycles a chunk (235 before decays were summed in blocks of 32).  The products themselves are 3100 of them; one lane
-// issues them in order, at 75 to 100 cycles each, because their operands take most of what
+// 245 us, about 6400 cycles and 12,300 warp instructions a chunk.  The products themselves are 3100
+// cycles; one lane issues them in order, at 75 to 100 each, because their operands take most of what
 // shared memory delivers beside what the roles read and write there (5300 of 128 bytes a
-// chunk), and the order S, M C, M' += .., P x waits for each role once.  Tried and slower:
-// two lanes that issue the outputs' and the state's products side by side (291 us), rolled
-// issue loops (247 to 260), 16-token places of x' (266), half of x' before M C (244); no
+// chunk), and the order S, M C, x'^T B, P x waits for each role once.  Tried and slower, while the
+// same prompts took 235: two lanes that issue the outputs' and the state's products side by side (291
+// us), rolled issue loops (247 to 260), 16-token places of x' (266), half of x' before M C (244); no
 // faster: eight warps for the weights or for the state.
 #include <type_traits>
 
@@ -604,7 +606,8 @@ ssm_kernel(const __grid_constant__ SsmMaps maps, SsmArgs a, SsmParts parts, int6
           for (int k = 0; k < 4; ++k) {
             uint32_t word = 0u;
             if (j <= k) {  // (others are behind the diagonal in every lane)
-              // (d is a factor and not part of the exponent: a token's own weight is d whatever l is)
+              // Chosen, not multiplied: S behind the diagonal can hold another sequence's rows, whatever those are.
+              // d is a factor and not part of the exponent: a token's own weight is d whatever l is.
               float x0, x1;
               unpair(mul2(pair(s[k >> 1][4 * j + 2 * (k & 1)], s[k >> 1][4 * j + 2 * (k & 1) + 1]),
                           mul2(pair(ex2_approx(li[k] - f.x), ex2_approx(li[k] - f.z)), pair(f.y, f.w))),
@@ -1035,9 +1038,9 @@ struct Plan {
 // zero takes about half of what the piece itself does, each kernel a few chunks' time to
 // start and to end, and each piece before one half a chunk's (its state is read); the number
 // of pieces is the one of least time under that count.  Whole and cut, in us (heads of 64,
-// states of 128): 8192 tokens, 64 heads 191 and 100 (4 pieces; 5 take a second round: 134);
-// 16384 tokens, 8 heads 364 and 74 (16); 2048 tokens, 16 heads 52 and 35 (8); 1024 tokens, 64
-// heads 30 and 31 (4); four sequences of 2048 tokens, 64 heads 62 and 99 (2, not taken).
+// states of 128): 8192 tokens, 64 heads 190 and 99 (4 pieces; 5 take a second round: 126);
+// 16384 tokens, 8 heads 368 and 65 (16); 2048 tokens, 16 heads 51 and 29 (8); 1024 tokens, 64
+// heads 29 and 26 (4); four sequences of 2048 tokens, 64 heads 60 and 125 (5, not taken).
 Plan plan_of(int64_t T, int H, int G, int N, int P, int S) {
   Plan p{};
   p.units = units_of(H, G, P);
