@@ -32,7 +32,7 @@
 // bits, so that a state in fp32 is one.  (Fewer where the caller takes the state in bf16 or not at all
 // gained 3 %, but the outputs of a call then depended on that.)  P and the copy of M that the outputs
 // see are rounded to bf16 once (2^-8 of the value at most, as the output): their error against 64 bits is
-// 1.7e-3 to 1.9e-3, 2.1e-3 for a short prompt from a state, where rounding them alone gives 1.66e-3.
+// 1.7e-3 to 2.4e-3, where rounding the outputs alone gives 1.66e-3.
 // A second addend of P has no columns left in tensor memory, one of the copy no room in shared memory.
 //
 // Measured (GB300; heads of 64, states of 128 in fp32): 16 ragged prompts, 33,600 tokens, 64 heads,

@@ -57,7 +57,9 @@ def kda_ssm_fwd(x, dt, A, B, C, skip=None, dt_bias=None, initial_state=None, cu_
     not positive.  Per head, with d = softplus(dt + dt_bias): M = exp(A d) M + d x B^T,
     out = M C + skip x.  States [N, H, P, S] fp32 or bf16 (both the same; the final state is
     allocated with the initial state's dtype, fp32 without one); final_state may be
-    initial_state itself.  Returns (out, final_state)."""
+    initial_state itself.  The weights between tokens and the copy of the state that the outputs
+    read are rounded to bf16 once (kda_ssm_step rounds neither); the state and what tokens add to
+    it are fp32 whichever state is taken.  Returns (out, final_state)."""
     b = _attention._binding or _attention.load_binding()
     return _attention._run(stream, "kda_ssm_fwd", b.ssm_fwd, x, dt, A, B, C, skip, dt_bias, initial_state,
                            cu_seqlens, N, out, final_state, output_final_state, workspace)

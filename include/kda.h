@@ -625,8 +625,8 @@ typedef struct {
  *   a token adds to the state keeps all bits of fp32, whichever state the caller takes; an fp32
  *   state is off by about 5e-7 of its norm at any length.  The weights between a chunk's tokens and
  *   the copy of the state that its outputs read are rounded to bf16 once, for the tensor cores;
- *   beside the rounding of the outputs themselves that adds 5 to 25 % to their error (kda_ssm_step
- *   has neither, for any number of tokens).  Rows of other sequences, whatever they hold, reach
+ *   beside the rounding of the outputs themselves (1.7e-3 of their norm) they are off by up to
+ *   2.4e-3 (kda_ssm_step rounds neither, for any number of tokens).  Rows of other sequences, whatever they hold, reach
  *   no result; a non-finite value of x can also spoil its own channel in the up to 127 tokens of its
  *   sequence before it (they share a tile), one of dt, B or C nothing before it.
  *   T_total is below 2^31 - 128, strides of x, B and C below 2^39.  Few sequences are cut into
