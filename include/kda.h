@@ -624,11 +624,12 @@ typedef struct {
  * kda_ssm_fwd: the same result for prompts, in chunks of 128 tokens.  Sums and states are fp32, and what
  *   a token adds to the state keeps all bits of fp32, whichever state the caller takes; an fp32
  *   state is off by about 5e-7 of its norm at any length.  The weights between a chunk's tokens and
- *   the copy of the state that its outputs read are rounded to bf16 once, for the tensor cores;
- *   beside the rounding of the outputs themselves (1.7e-3 of their norm) they are off by up to
- *   2.4e-3 (kda_ssm_step rounds neither, for any number of tokens).  Rows of other sequences, whatever they hold, reach
- *   no result; a non-finite value of x can also spoil its own channel in the up to 127 tokens of its
- *   sequence before it (they share a tile), one of dt, B or C nothing before it.
+ *   the copy of the state that its outputs read are rounded to bf16 once, for the tensor cores
+ *   (kda_ssm_step rounds neither, for any number of tokens): the outputs are off by 1.7e-3 to
+ *   2.4e-3 of their norm, where their own rounding alone gives 1.7e-3.  Rows of other sequences,
+ *   whatever they hold, reach no result; a non-finite value of x can also spoil its own channel in
+ *   the up to 127 tokens of its sequence before it (they share a tile), one of dt, B or C nothing
+ *   before it.
  *   T_total is below 2^31 - 128, strides of x, B and C below 2^39.  Few sequences are cut into
  *   pieces that run at once and are joined through their states, which takes a workspace:
  *   kda_ssm_workspace_size() bytes of device memory (0 where none is cut), 16-byte aligned, or
